@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/pa.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/pa.h and include/pa_cache.h (argument
+marshalling only).
 
 Each ``pa_*`` function here has the name and argument order of the C entry
 point, takes torch tensors (device memory) instead of raw pointers, passes
@@ -26,6 +27,7 @@ PA_OK = 0
 PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE = 1, 2, 3
 PA_NHD, PA_HND = 0, 1
 PA_BF16, PA_FP8_E4M3 = 0, 1
+PA_MX4 = 2   # cache operators only (include/pa_cache.h)
 PA_SCALE_PER_TENSOR, PA_SCALE_PER_ROW = 0, 1
 PA_MODE_DECODE, PA_MODE_PREFILL = 0, 1
 PA_MAP_DECODE_PART = 2   # pa_read_task_map: decode part of a prefill-mode workspace
@@ -38,6 +40,10 @@ EXPORTED = (
     "pa_test_inject_wait_timeout", "pa_static_workspace_size", "pa_static_num_splits",
     "pa_decode_static", "pa_prefill_fp8", "pa_set_task_trace",
 )
+
+# declared in include/pa_cache.h
+EXPORTED_CACHE = ("pa_kv_append", "pa_kv_expand", "pa_mx4_workspace_size", "pa_decode_mx4",
+                  "pa_key_weights", "pa_kv_evict")
 
 PA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # size of the library's fixed scratch
 # pa_problem.unit_cost = 0 takes these (PA_DEFAULT_UNIT_COST_DECODE / _PREFILL)
@@ -110,6 +116,7 @@ def load(build_if_missing: bool = True):
             _build.build()
         lib = ctypes.CDLL(path)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        i64 = ctypes.c_int64
         PP = ctypes.POINTER(PaProblem)
         sig = {
             "pa_status_string": (ctypes.c_char_p, [i32]),
@@ -134,6 +141,12 @@ def load(build_if_missing: bool = True):
                                        vp, vp, vp]),
             "pa_prefill_fp8": (i32, [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz,
                                      vp, vp, vp]),
+            "pa_kv_append": (i32, [PP, vp, vp, i64, i64] + [vp] * 10),
+            "pa_kv_expand": (i32, [PP] + [vp] * 8 + [i32, i32] + [vp] * 4),
+            "pa_mx4_workspace_size": (sz, [PP]),
+            "pa_decode_mx4": (i32, [PP] + [vp] * 9 + [sz] + [vp] * 3),
+            "pa_key_weights": (i32, [PP] + [vp] * 10),
+            "pa_kv_evict": (i32, [PP, i32, i32, i32] + [vp] * 7 + [i32] + [vp] * 5),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -276,6 +289,73 @@ def pa_prefill_fp8(problem, q, q_scale, k_cache, v_cache, block_table, context_l
         _p(context_lens), _p(q_lens), _p(k_scale), _p(v_scale), _p(block_mask), _p(assign_ws),
         _nbytes(assign_ws), _p(partial_ws), _nbytes(partial_ws), _p(out), _p(lse),
         _stream(stream)), "pa_prefill_fp8")
+
+
+# --------------------------------------------- cache operators (pa_cache.h)
+
+def _new_rows(t: torch.Tensor, problem: PaProblem, name: str) -> int:
+    """Elements between the tokens of new K or V rows [tokens, Hkv, D]."""
+    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[0] < problem.total_q_tokens
+            or t.shape[1] != problem.num_kv_heads or t.shape[2] != problem.head_dim
+            or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name} must be bf16 [total_q_tokens, num_kv_heads, head_dim] with "
+                         f"dense heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_kv_append(problem, k_new, v_new, block_table, context_lens, q_lens, k_cache, k_scale,
+                 v_cache, v_scale, key_weights=None, device_error=None, stream=None):
+    """New K/V rows into the cache; the tokens of k_new / v_new may be strided
+    (slices of a fused projection)."""
+    ks, vs = _new_rows(k_new, problem, "k_new"), _new_rows(v_new, problem, "v_new")
+    _check(load().pa_kv_append(
+        ctypes.byref(problem), _p(k_new), _p(v_new), ks, vs, _p(block_table), _p(context_lens),
+        _p(q_lens), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale), _p(key_weights),
+        _p(device_error), _stream(stream)), "pa_kv_append")
+
+
+def pa_kv_expand(problem, k_cache, k_scale, v_cache, v_scale, block_table, context_lens, q_lens,
+                 dst_block_table, dst_num_pages, k_out, v_out, device_error=None, stream=None):
+    """The last q_lens[b] tokens of each sequence of a 4-bit cache as bf16 pages."""
+    _check(load().pa_kv_expand(
+        ctypes.byref(problem), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale),
+        _p(block_table), _p(context_lens), _p(q_lens), _p(dst_block_table),
+        int(dst_block_table.shape[1]), int(dst_num_pages), _p(k_out), _p(v_out),
+        _p(device_error), _stream(stream)), "pa_kv_expand")
+
+
+def pa_mx4_workspace_size(problem: PaProblem) -> int:
+    return int(load().pa_mx4_workspace_size(ctypes.byref(problem)))
+
+
+def pa_decode_mx4(problem, q, k_cache, k_scale, v_cache, v_scale, block_table, context_lens,
+                  q_lens, ws, out, lse, stream=None):
+    """Decode attention over a 4-bit cache (one call, no Assign)."""
+    _check(load().pa_decode_mx4(
+        ctypes.byref(problem), _p(q), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale),
+        _p(block_table), _p(context_lens), _p(q_lens), _p(ws), _nbytes(ws), _p(out), _p(lse),
+        _stream(stream)), "pa_decode_mx4")
+
+
+def pa_key_weights(problem, q, k_cache, k_scale, block_table, context_lens, q_lens, lse,
+                   key_weights, device_error=None, stream=None):
+    """Add the softmax weight of the given queries to every cached key's total."""
+    _check(load().pa_key_weights(
+        ctypes.byref(problem), _p(q), _p(k_cache), _p(k_scale), _p(block_table),
+        _p(context_lens), _p(q_lens), _p(lse), _p(key_weights), _p(device_error),
+        _stream(stream)), "pa_key_weights")
+
+
+def pa_kv_evict(problem, budget, num_first, num_recent, k_cache, k_scale, v_cache, v_scale,
+                key_weights, block_table, dst_block_table, context_lens, kept, new_context_lens,
+                device_error=None, stream=None):
+    """Keep `budget` keys per KV head of every longer sequence, packed into the
+    pages of dst_block_table."""
+    _check(load().pa_kv_evict(
+        ctypes.byref(problem), int(budget), int(num_first), int(num_recent), _p(k_cache),
+        _p(k_scale), _p(v_cache), _p(v_scale), _p(key_weights), _p(block_table),
+        _p(dst_block_table), int(dst_block_table.shape[1]), _p(context_lens), _p(kept),
+        _p(new_context_lens), _p(device_error), _stream(stream)), "pa_kv_evict")
 
 
 def pa_set_task_trace(trace: Optional[torch.Tensor]):

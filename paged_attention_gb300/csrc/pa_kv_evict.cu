@@ -1,0 +1,258 @@
+// pa_kv_evict.cu -- which keys of a paged cache to keep, by their accumulated
+// weights, and moving the kept rows into other pages.
+//
+// Two launches.  Select (one CTA per sequence and KV head): the budget-th
+// largest key by a radix select, eight bits a pass over an order-preserving
+// integer form of the weights, then one ordered pass that lists the kept
+// positions (ties to the lower one).  Move: CTAs copy 64 kept rows of K and V
+// each, 16 bytes a thread; bound by HBM.
+#include "pa_cache_common.cuh"
+
+namespace pa {
+
+struct EvictParams {
+    CacheGeom g;
+    int32_t budget, num_first, num_recent;
+    uint8_t* k;
+    uint8_t* ks;
+    uint8_t* v;
+    uint8_t* vs;
+    float* weights;
+    const int32_t* table;
+    const int32_t* dst_table;
+    int32_t dst_mpps;
+    const int32_t* ctx;
+    int32_t* kept;
+    int32_t* new_ctx;
+    int32_t* err;
+};
+
+namespace {
+
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 256;
+constexpr int kHistBytes = kBins * 32 * 4;   // one histogram per lane: no bank is met twice
+constexpr int kMaxCached = (227 * 1024 - kHistBytes - 2048) / 4;   // keys held in shared memory
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 64;
+
+// Larger weights get larger keys; NaN the smallest, a protected position the largest.
+__device__ __forceinline__ uint32_t order_key(float w) {
+    if (w != w) return 0u;
+    const uint32_t u = __float_as_uint(w + 0.f);   // -0 counts as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelectThreads, 1)
+select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* cached = reinterpret_cast<uint32_t*>(smem + kHistBytes);
+    __shared__ uint32_t bins[kBins];
+    __shared__ uint32_t s_digit, s_left;
+    __shared__ int2 s_count[kSelectWarps];
+    const CacheGeom& g = P.g;
+    const int b = blockIdx.x / g.Hkv, hk = blockIdx.x % g.Hkv;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = P.ctx[b];
+    const bool bad = c < 0 || c > g.max_ctx;
+    if (hk == 0 && tid == 0) {
+        P.new_ctx[b] = bad ? 0 : min(c, P.budget);
+        if (bad) flag_error(P.err, PA_DEV_BAD_LENGTHS);
+    }
+    if (bad || c <= P.budget) return;
+    const int32_t* row = P.table + (int64_t)b * g.mpps;
+    auto key_at = [&](int i) -> uint32_t {
+        if (i < P.num_first || i >= c - P.num_recent) return 0xffffffffu;
+        const int page = row[i >> g.ps_shift];
+        if (page < 0 || page >= g.num_pages) return 0u;   // the move flags it
+        return order_key(P.weights[((int64_t)page * g.Hkv + hk) * g.ps + (i & (g.ps - 1))]);
+    };
+    const bool in_smem = c <= cached_cap;
+    if (in_smem) {
+#pragma unroll 4
+        for (int i = tid; i < c; i += kSelectThreads) cached[i] = key_at(i);
+    }
+    auto key = [&](int i) -> uint32_t { return in_smem ? cached[i] : key_at(i); };
+
+    // ---- the budget-th largest key
+    uint32_t prefix = 0, left = (uint32_t)P.budget;   // rank from the top among equal prefixes
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = tid; i < kBins * 32; i += kSelectThreads) hist[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < c; i += kSelectThreads) {
+            const uint32_t x = key(i);
+            if (shift == 24 || (x >> (shift + 8)) == prefix)
+                atomicAdd(&hist[((x >> shift) & 255u) * 32 + lane], 1u);
+        }
+        __syncthreads();
+        for (int d = warp; d < kBins; d += kSelectWarps) {
+            const uint32_t s = __reduce_add_sync(0xffffffffu, hist[d * 32 + lane]);
+            if (lane == 0) bins[d] = s;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane l holds digits 255 - 8 l downwards
+            uint32_t v[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = bins[255 - 8 * lane - j];
+                sum += v[j];
+            }
+            const uint32_t inc = (uint32_t)warp_inclusive((int)sum, lane);
+            uint32_t above = inc - sum;
+            if (above < left && left <= inc) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (left > above && left <= above + v[j]) {
+                        s_digit = 255 - 8 * lane - j;
+                        s_left = left - above;
+                    }
+                    above += v[j];
+                }
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | s_digit;
+        left = s_left;
+    }
+    // kept: keys above `prefix`, and the first `left` that equal it
+
+    // ---- list the kept positions; a warp owns a run of positions
+    const int per_warp = ((c + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+    const int i0 = min(c, warp * per_warp), i1 = min(c, i0 + per_warp);
+    int above = 0, equal = 0;
+    for (int i = i0; i < i1; i += 32) {
+        const bool on = i + lane < i1;
+        const uint32_t x = on ? key(i + lane) : 0u;
+        above += __popc(__ballot_sync(0xffffffffu, on && x > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, on && x == prefix));
+    }
+    if (lane == 0) s_count[warp] = make_int2(above, equal);
+    __syncthreads();
+    const int2 mine = s_count[lane];
+    const int ea = warp_inclusive(mine.x, lane) - mine.x, ee = warp_inclusive(mine.y, lane) - mine.y;
+    int na = __shfl_sync(0xffffffffu, ea, warp), ne = __shfl_sync(0xffffffffu, ee, warp);
+    int32_t* out = P.kept + (int64_t)blockIdx.x * P.budget;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += 32) {
+        const bool on = i + lane < i1;
+        const uint32_t x = on ? key(i + lane) : 0u;
+        const uint32_t ma = __ballot_sync(0xffffffffu, on && x > prefix);
+        const uint32_t me = __ballot_sync(0xffffffffu, on && x == prefix);
+        const int a = na + __popc(ma & below), e = ne + __popc(me & below);
+        if (on && (x > prefix || (x == prefix && e < (int)left)))
+            out[a + min(e, (int)left)] = i + lane;
+        na += __popc(ma);
+        ne += __popc(me);
+    }
+}
+
+// 16-byte pieces of a row: D / 8 of bf16, D / 32 of 4-bit codes.
+template <int PIECES>
+__global__ void __launch_bounds__(kMoveThreads)
+move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) {
+    __shared__ int64_t s_src[kMoveRows], s_dst[kMoveRows];
+    const CacheGeom& g = P.g;
+    const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+    const int b = unit / g.Hkv, hk = unit % g.Hkv;
+    const int c = P.ctx[b];
+    if (c <= P.budget || c > g.max_ctx) return;
+    const int r0 = chunk * kMoveRows, n = min(kMoveRows, P.budget - r0);
+    const int tid = threadIdx.x;
+    if (tid < n) {
+        const int from = P.kept[(int64_t)unit * P.budget + r0 + tid], to = r0 + tid;
+        const bool listed = from >= 0 && from < c;
+        const int sp = listed ? P.table[(int64_t)b * g.mpps + (from >> g.ps_shift)] : -1;
+        const int dp = P.dst_table[(int64_t)b * P.dst_mpps + (to >> g.ps_shift)];
+        const bool ok = sp >= 0 && sp < g.num_pages && dp >= 0 && dp < g.num_pages;
+        const int ss = from & (g.ps - 1), ds = to & (g.ps - 1);
+        s_src[tid] = ok ? row_of(g, sp, ss, hk) : -1;
+        s_dst[tid] = ok ? row_of(g, dp, ds, hk) : 0;
+        if (ok) {
+            P.weights[((int64_t)dp * g.Hkv + hk) * g.ps + ds] =
+                P.weights[((int64_t)sp * g.Hkv + hk) * g.ps + ss];
+            if (scale_bytes == 4) {
+                const int64_t s = s_src[tid], d = s_dst[tid];
+                reinterpret_cast<uint32_t*>(P.ks)[d] = reinterpret_cast<const uint32_t*>(P.ks)[s];
+                reinterpret_cast<uint32_t*>(P.vs)[d] = reinterpret_cast<const uint32_t*>(P.vs)[s];
+            } else if (scale_bytes == 2) {
+                const int64_t s = s_src[tid], d = s_dst[tid];
+                reinterpret_cast<uint16_t*>(P.ks)[d] = reinterpret_cast<const uint16_t*>(P.ks)[s];
+                reinterpret_cast<uint16_t*>(P.vs)[d] = reinterpret_cast<const uint16_t*>(P.vs)[s];
+            }
+        } else {
+            flag_error(P.err, PA_DEV_BAD_PAGE);
+        }
+    }
+    __syncthreads();
+    // pieces of K, then of V; every load of a thread before its stores
+    constexpr int kPer = (2 * PIECES * kMoveRows + kMoveThreads - 1) / kMoveThreads;
+    uint4 x[kPer];
+    const int items = 2 * PIECES * n;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid + j * kMoveThreads;
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < items) {
+            const int kv = i / (PIECES * n), r = (i / PIECES) % n, p = i % PIECES;
+            const int64_t s = s_src[r];
+            if (s >= 0) x[j] = reinterpret_cast<const uint4*>(kv ? P.v : P.k)[s * PIECES + p];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid + j * kMoveThreads;
+        if (i < items) {
+            const int kv = i / (PIECES * n), r = (i / PIECES) % n, p = i % PIECES;
+            if (s_src[r] >= 0) reinterpret_cast<uint4*>(kv ? P.v : P.k)[s_dst[r] * PIECES + p] = x[j];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first, int num_recent,
+                         void* k, void* ks, void* v, void* vs, float* weights,
+                         const int32_t* table, const int32_t* dst_table, int dst_mpps,
+                         const int32_t* ctx, int32_t* kept, int32_t* new_ctx, int32_t* err,
+                         cudaStream_t stream) {
+    EvictParams P;
+    P.g = g;
+    P.budget = budget;
+    P.num_first = num_first;
+    P.num_recent = num_recent;
+    P.k = (uint8_t*)k;
+    P.ks = (uint8_t*)ks;
+    P.v = (uint8_t*)v;
+    P.vs = (uint8_t*)vs;
+    P.weights = weights;
+    P.table = table;
+    P.dst_table = dst_table;
+    P.dst_mpps = dst_mpps;
+    P.ctx = ctx;
+    P.kept = kept;
+    P.new_ctx = new_ctx;
+    P.err = err;
+    // the longest sequence's keys fit shared memory, or are read from L2 every pass
+    const int cap = g.max_ctx <= kMaxCached ? g.max_ctx : kMaxCached;
+    const int smem = kHistBytes + cap * 4;
+    cudaError_t e =
+        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    select_kernel<<<g.B * g.Hkv, kSelectThreads, smem, stream>>>(P, cap);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (g.max_ctx <= budget) return cudaSuccess;   // nothing can be over the budget
+    const int chunks = (budget + kMoveRows - 1) / kMoveRows;
+    const int64_t grid = (int64_t)g.B * g.Hkv * chunks;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    const int scale_bytes = mx4 ? g.D / 32 : 0;
+    auto kern = mx4 ? (g.D == 128 ? move_kernel<4> : move_kernel<2>)
+                    : (g.D == 128 ? move_kernel<16> : move_kernel<8>);
+    kern<<<(int)grid, kMoveThreads, 0, stream>>>(P, chunks, scale_bytes);
+    return cudaGetLastError();
+}
+
+}  // namespace pa
