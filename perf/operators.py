@@ -345,7 +345,7 @@ def prepare(case, seed):
         if kind == "write":
             s["back_pages"] = s["k_out"].shape[0]
         if kind == "decode":
-            s["ws"] = torch.empty(B.pa_mx4_workspace_size(s["p"]), dtype=torch.uint8, device="cuda")
+            s["ws"] = torch.zeros(B.pa_mx4_workspace_size(s["p"]), dtype=torch.uint8, device="cuda")
             s["out"] = torch.empty((s["total_q"], case["heads"], D), dtype=torch.bfloat16,
                                    device="cuda")
             s["lse_out"] = torch.empty((s["total_q"], case["heads"]), device="cuda")
