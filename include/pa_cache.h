@@ -95,8 +95,13 @@ PA_API pa_status pa_kv_expand(const pa_problem* problem, const void* k_cache, co
  * fp32 sums; the block scales of K are applied in fp32.  A V block adds to the
  * result relative to the largest scale that its 32 columns met so far: what
  * lies more than a factor 2^24 below that is lost to rounding.
- *   ws: >= pa_mx4_workspace_size bytes, 256-byte aligned; needs no
- *     initialisation; the call clears its error word (pa_last_device_error).
+ *   ws: >= pa_mx4_workspace_size bytes, 256-byte aligned, zero-filled by the
+ *     caller before its first use.  Every call that runs to its end leaves it
+ *     ready for the next one, of the same or another problem (a second launch to
+ *     clear it would cost a small call more than its attention); its first 256
+ *     bytes hold the error word that pa_last_device_error reads, which stays
+ *     set until the caller clears them.  Calls that may run at the same time
+ *     need a workspace each.
  *   Other arguments as pa_decode_splitk.
  */
 PA_API size_t pa_mx4_workspace_size(const pa_problem* problem);

@@ -17,6 +17,7 @@ cudaError_t launch_expand(const CacheGeom& g, const void* k_cache, const void* k
                           int dst_mpps, int dst_pages, void* k_out, void* v_out, int32_t* err,
                           int sms, cudaStream_t stream);
 int mx4_row_tiles(int D, int rows);
+int mx4_ctas_per_sm(int D, int nt);
 cudaError_t launch_decode_mx4(const CacheGeom& g, int nt, const void* q, const void* k,
                               const void* ks, const void* v, const void* vs, const int32_t* table,
                               const int32_t* ctx, const int32_t* ql, int32_t* header,
@@ -36,7 +37,7 @@ namespace {
 
 constexpr int kMaxGrid = 1024;          // CTAs of pa_decode_mx4
 constexpr int kMaxHeads = 1 << 15;      // KV heads
-constexpr int kMx4UnitCost = 1;         // a unit's fixed cost, in 64-key tiles
+constexpr int kMx4UnitCost = 8;         // a unit's fixed cost, in 64-key tiles
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -117,7 +118,7 @@ pa_status status_of(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CU
 // partial slots per CTA, each `rows` rows of D + 1 floats.
 struct Mx4Layout {
     int grid, nt, unit_cost;
-    int64_t off_done, clear_bytes, off_part, rows, total;
+    int64_t off_done, off_part, rows, total;
 };
 pa_status mx4_layout(const pa_problem* pp, CacheGeom& g, Mx4Layout& L) {
     pa_status st = geometry(pp, true, g);
@@ -130,13 +131,13 @@ pa_status mx4_layout(const pa_problem* pp, CacheGeom& g, Mx4Layout& L) {
     if (L.grid == 0) {
         L.grid = sm_count();
         if (L.grid <= 0) return PA_ERR_CUDA;
+        L.grid *= mx4_ctas_per_sm(g.D, L.nt);
         if (L.grid > kMaxGrid) L.grid = kMaxGrid;
     }
     L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : kMx4UnitCost;
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
-    L.clear_bytes = L.off_done + (int64_t)L.grid * 4;
-    L.off_part = align256(L.clear_bytes);
+    L.off_part = align256(L.off_done + (int64_t)L.grid * 4);
     L.total = align256(L.off_part + 2 * (int64_t)L.grid * L.rows * (g.D + 1) * 4);
     return PA_OK;
 }
@@ -223,15 +224,13 @@ pa_status pa_decode_mx4(const pa_problem* problem, const void* q, const void* k_
                  !lens_ok(block_table, context_lens, q_lens) || !out || !aligned(out, 16) ||
                  !aligned(lse, 4)))
         return PA_ERR_INVALID_ARG;
-    const cudaStream_t s = (cudaStream_t)stream;
+    if (!rows) return PA_OK;   // no query row: nothing to compute
     char* base = static_cast<char*>(ws);
-    cudaError_t e = cudaMemsetAsync(base, 0, (size_t)L.clear_bytes, s);
-    if (e != cudaSuccess || !rows) return status_of(e);
     float* part_o = reinterpret_cast<float*>(base + L.off_part);
     return status_of(launch_decode_mx4(
         g, L.nt, q, k_cache, k_scale, v_cache, v_scale, block_table, context_lens, q_lens,
         reinterpret_cast<int32_t*>(base), reinterpret_cast<int32_t*>(base + L.off_done), part_o,
-        part_o + 2 * (int64_t)L.grid * L.rows * g.D, out, lse, L.unit_cost, L.grid, s));
+        part_o + 2 * (int64_t)L.grid * L.rows * g.D, out, lse, L.unit_cost, L.grid, (cudaStream_t)stream));
 }
 
 pa_status pa_key_weights(const pa_problem* problem, const void* q, const void* k_cache,

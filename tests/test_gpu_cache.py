@@ -182,7 +182,7 @@ def decode(case, num_ctas=0, stream=None, **kw):
     p = case.problem(B, num_ctas=num_ctas, **kw)
     n = B.pa_mx4_workspace_size(p)
     assert n > 0
-    ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda")     # needs no initialisation
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     out = torch.full((case.total_q, case.heads, case.dim), 9.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((case.total_q, case.heads), 9.0, device="cuda")
     c, q = case.lens()
@@ -297,7 +297,7 @@ def test_decode_is_deterministic_without_splits_and_leaves_other_rows():
     assert torch.equal(a, b) and torch.equal(al, bl)
     # lse may be left out
     p = case.problem(B)
-    ws = torch.empty(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
     out = torch.empty_like(a)
     c, q = case.lens()
     B.pa_decode_mx4(p, case.q.cuda(), dev(case.k), dev(case.ks), dev(case.v), dev(case.vs),
@@ -322,7 +322,7 @@ def test_decode_flags_bad_pages_and_lengths():
     case = R.Case([100, 50], [1, 1], heads=2, kv_heads=1, dim=64, seed=19)
     ql = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
     p = case.problem(B, max_q_len=2)
-    ws = torch.empty(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
     out = torch.full((2, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
     B.pa_decode_mx4(p, case.q.cuda(), dev(case.k), dev(case.ks), dev(case.v), dev(case.vs),
                     dev(case.table), case.lens()[0], ql, ws, out, None)
@@ -594,7 +594,7 @@ def test_a_serving_run(kv):
         cl, qlen = s.lens()
         B.pa_kv_append(p, rows, rows, dev(s.table), cl, qlen, k, ks, v, vs, w, err)
         if kv == MX4:
-            ws = torch.empty(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
+            ws = torch.zeros(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
             out = torch.empty((2, heads, dim), dtype=torch.bfloat16, device="cuda")
             lse = torch.empty((2, heads), device="cuda")
             B.pa_decode_mx4(p, s.q.cuda(), k, ks, v, vs, dev(s.table), cl, qlen, ws, out, lse)
@@ -653,7 +653,7 @@ def test_a_captured_step_replays_on_new_lengths():
     c, q = case.lens()
     t, qs = dev(case.table), case.q.cuda()
     rows = torch.randn((2, 2, 128)).to(torch.bfloat16).cuda()
-    ws = torch.empty(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(B.pa_mx4_workspace_size(p), dtype=torch.uint8, device="cuda")
     out = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda")
     lse = torch.zeros((2, 4), device="cuda")
     w = torch.zeros((10, 2, 16), device="cuda")
