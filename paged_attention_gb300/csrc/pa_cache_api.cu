@@ -30,7 +30,7 @@ cudaError_t launch_key_weights(const CacheGeom& g, bool mx4, const void* q, cons
 cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first, int num_recent,
                          void* k, void* ks, void* v, void* vs, float* weights,
                          const int32_t* table, const int32_t* dst_table, int dst_mpps,
-                         const int32_t* ctx, int32_t* kept, int32_t* new_ctx, int32_t* err,
+                         const int32_t* ctx, int32_t* kept, int32_t* new_ctx, int32_t* err, int sms,
                          cudaStream_t stream);
 
 namespace {
@@ -275,10 +275,12 @@ pa_status pa_kv_evict(const pa_problem* problem, int32_t budget, int32_t num_fir
         !new_context_lens || !aligned(new_context_lens, 4) ||
         (n0 < c0 + len_bytes && c0 < n0 + len_bytes) || !aligned(device_error, 4))
         return PA_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
     return status_of(launch_evict(g, problem->kv_dtype == PA_MX4, budget, num_first, num_recent,
                                   k_cache, k_scale, v_cache, v_scale, key_weights, block_table,
                                   dst_block_table, dst_max_pages_per_seq, context_lens, kept,
-                                  new_context_lens, device_error, (cudaStream_t)stream));
+                                  new_context_lens, device_error, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

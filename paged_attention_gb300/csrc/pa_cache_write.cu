@@ -13,10 +13,30 @@ namespace {
 constexpr int kWriteThreads = 256;
 constexpr int kMaxTokens = 32;   // tokens of one CTA: one per lane of its first warp
 
-// Where a CTA's tokens live: page and slot, page -1 for a token to skip.
+// Where a CTA's tokens live: the rows of their first head (-1: a token to skip),
+// in the cache and, for reading back, in the other pages; and where their key
+// weights of the first head are.
 struct TokenPlace {
-    int page, slot, dst_page;
+    int64_t row, dst_row, weight;
 };
+
+// The thread's items run through token (of the CTA) and position within a token:
+// kWriteThreads further each time, without a division.
+struct Cursor {
+    int t, r;
+    __device__ __forceinline__ void step(int per_token) {
+        r += kWriteThreads;
+        while (r >= per_token) {
+            r -= per_token;
+            ++t;
+        }
+    }
+};
+__device__ __forceinline__ Cursor first_item(int per_token) {
+    Cursor c = {0, (int)threadIdx.x - kWriteThreads};
+    c.step(per_token);
+    return c;
+}
 
 // The first warp finds the places of the CTA's tokens [t0, t0 + n).
 __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* table,
@@ -27,20 +47,22 @@ __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* t
         const int lane = threadIdx.x;
         int start = 0;
         const int b = seq_of_row(g, ql, t0 + min(lane, n - 1), lane, start);
-        TokenPlace p = {-1, 0, -1};
+        TokenPlace p = {-1, -1, 0};
         if (b >= 0 && lane < n) {
             const int q = ql[b], c = ctx[b];
             if (good_lens(g, q, c)) {
                 const int pos = c - q + (t0 + lane - start);
-                const int pi = pos >> g.ps_shift;
-                p.slot = pos & (g.ps - 1);
-                p.page = table[(int64_t)b * g.mpps + pi];
-                if (p.page < 0 || p.page >= g.num_pages) p.page = -1;
-                bool bad = p.page < 0;
+                const int pi = pos >> g.ps_shift, slot = pos & (g.ps - 1);
+                const int page = table[(int64_t)b * g.mpps + pi];
+                bool bad = page < 0 || page >= g.num_pages;
                 if (dst_table != nullptr && !bad) {
-                    p.dst_page = dst_table[(int64_t)b * dst_mpps + pi];
-                    if (p.dst_page < 0 || p.dst_page >= dst_pages) p.page = -1;
-                    bad = p.page < 0;
+                    const int dst = dst_table[(int64_t)b * dst_mpps + pi];
+                    bad = dst < 0 || dst >= dst_pages;
+                    if (!bad) p.dst_row = row_of(g, dst, slot, 0);
+                }
+                if (!bad) {
+                    p.row = row_of(g, page, slot, 0);
+                    p.weight = (int64_t)page * g.Hkv * g.ps + slot;
                 }
                 if (bad) flag_error(err, PA_DEV_BAD_PAGE);
             }
@@ -88,49 +110,60 @@ append_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k_new,
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
     find_places(g, table, ctx, ql, t0, n, nullptr, 0, 0, place, err);
-    const int per_token = 2 * g.Hkv * C;
-    // every lane of a warp takes part in the shuffles: the trip count is uniform
-    const int items = n * per_token;
-    for (int i0 = 0; i0 < items; i0 += kWriteThreads) {
-        const int i = i0 + threadIdx.x;
-        const bool in = i < items;
-        const int t = in ? i / per_token : 0;
-        const int r = in ? i - t * per_token : 0;
-        const int kv = r / (g.Hkv * C), h = (r / C) % g.Hkv, c = r % C;
-        const TokenPlace p = place[t];
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (in && p.page >= 0) {
-            const __nv_bfloat16* src = kv ? v_new + (int64_t)(t0 + t) * v_stride
-                                          : k_new + (int64_t)(t0 + t) * k_stride;
-            x = *reinterpret_cast<const uint4*>(src + h * D + c * 8);
-        }
-        uint32_t codes = 0, scales = 0;
-        if constexpr (MX4) {
-            uint32_t e;
-            codes = quantise8(x, e);
-            // the row's scale bytes, collected in its first lane
-            const int lane = threadIdx.x & 31, base = lane & ~(C - 1);
+    const int half = g.Hkv * C, per_token = 2 * half;
+    // every lane of a warp takes part in the shuffles: the trip count is
+    // uniform; U items' loads are under way at a time
+    constexpr int U = 4;
+    const int rounds = (n * per_token + kWriteThreads - 1) / kWriteThreads;
+    Cursor at = first_item(per_token);
+    for (int i = 0; i < rounds; i += U) {
+        uint4 x[U];
+        Cursor ahead = at;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j)
-                scales |= __shfl_sync(0xffffffffu, e, base + 4 * j) << (8 * j);
-        }
-        if (!in || p.page < 0) continue;
-        const int64_t row = row_of(g, p.page, p.slot, h);
-        void* cache = kv ? v_cache : k_cache;
-        if constexpr (MX4) {
-            reinterpret_cast<uint32_t*>(cache)[row * C + c] = codes;
-            if (c == 0) {
-                uint8_t* sc = kv ? v_scale : k_scale;
-                if constexpr (D == 128)
-                    reinterpret_cast<uint32_t*>(sc)[row] = scales;
-                else
-                    reinterpret_cast<uint16_t*>(sc)[row] = (uint16_t)scales;
+        for (int u = 0; u < U; ++u) {
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (ahead.t < n && place[ahead.t].row >= 0) {
+                const int kv = ahead.r >= half;
+                const __nv_bfloat16* src = kv ? v_new + (int64_t)(t0 + ahead.t) * v_stride
+                                              : k_new + (int64_t)(t0 + ahead.t) * k_stride;
+                x[u] = __ldcs(reinterpret_cast<const uint4*>(src) + (ahead.r - (kv ? half : 0)));
             }
-        } else {
-            reinterpret_cast<uint4*>(cache)[row * C + c] = x;
+            ahead.step(per_token);
         }
-        if (weights != nullptr && kv == 0 && c == 0)
-            weights[((int64_t)p.page * g.Hkv + h) * g.ps + p.slot] = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= rounds) break;
+            const Cursor me = at;
+            at.step(per_token);
+            const int kv = me.r >= half, hc = me.r - (kv ? half : 0), h = hc / C, c = hc % C;
+            uint32_t codes = 0, scales = 0;
+            if constexpr (MX4) {
+                uint32_t e;
+                codes = quantise8(x[u], e);
+                // the row's scale bytes, collected in its first lane
+                const int lane = threadIdx.x & 31, base = lane & ~(C - 1);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    scales |= __shfl_sync(0xffffffffu, e, base + 4 * j) << (8 * j);
+            }
+            if (me.t >= n || place[me.t].row < 0) continue;
+            const int64_t row = place[me.t].row + (int64_t)h * g.head_rows;
+            void* cache = kv ? v_cache : k_cache;
+            if constexpr (MX4) {
+                reinterpret_cast<uint32_t*>(cache)[row * C + c] = codes;
+                if (c == 0) {
+                    uint8_t* sc = kv ? v_scale : k_scale;
+                    if constexpr (D == 128)
+                        reinterpret_cast<uint32_t*>(sc)[row] = scales;
+                    else
+                        reinterpret_cast<uint16_t*>(sc)[row] = (uint16_t)scales;
+                }
+            } else {
+                reinterpret_cast<uint4*>(cache)[row * C + c] = x[u];
+            }
+            if (weights != nullptr && kv == 0 && c == 0)
+                weights[place[me.t].weight + (int64_t)h * g.ps] = 0.f;
+        }
     }
 }
 
@@ -146,37 +179,53 @@ expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
     find_places(g, table, ctx, ql, t0, n, dst_table, dst_mpps, dst_pages, place, err);
-    const int per_token = 2 * g.Hkv * C;
-    const int items = n * per_token;
-    for (int i = threadIdx.x; i < items; i += kWriteThreads) {
-        const int t = i / per_token, r = i - t * per_token;
-        const int kv = r / (g.Hkv * C), h = (r / C) % g.Hkv, c = r % C;
-        const TokenPlace p = place[t];
-        if (p.page < 0) continue;
-        const int64_t row = row_of(g, p.page, p.slot, h);
-        const uint32_t w = (kv ? v_cache : k_cache)[row * C + c];
-        const float s = e8m0_to_f32((kv ? v_scale : k_scale)[row * (D / 32) + c / 4]);
-        uint32_t v[4];
-        e2m1x8_to_f16(w, v[0], v[1], v[2], v[3]);
+    const int half = g.Hkv * C, per_token = 2 * half;
+    constexpr int U = 4;   // items of a thread under way at a time
+    Cursor at = first_item(per_token);
+    while (at.t < n) {
+        uint32_t w[U], e[U];
+        Cursor ahead = at;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-            v[j] = pack_bf16x2(f.x * s, f.y * s);
+        for (int u = 0; u < U; ++u) {
+            w[u] = e[u] = 0;
+            if (ahead.t < n && place[ahead.t].row >= 0) {
+                const int kv = ahead.r >= half, hc = ahead.r - (kv ? half : 0);
+                const int64_t row = place[ahead.t].row + (int64_t)(hc / C) * g.head_rows;
+                w[u] = (kv ? v_cache : k_cache)[row * C + hc % C];
+                e[u] = (kv ? v_scale : k_scale)[row * (D / 32) + hc % C / 4];
+            }
+            ahead.step(per_token);
         }
-        const int64_t out = row_of(g, p.dst_page, p.slot, h);
-        reinterpret_cast<uint4*>(kv ? v_out : k_out)[out * C + c] =
-            make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Cursor me = at;
+            at.step(per_token);
+            if (me.t >= n || place[me.t].row < 0) continue;
+            const int kv = me.r >= half, hc = me.r - (kv ? half : 0);
+            const float f = e8m0_to_f32(e[u]);
+            uint32_t v[4];
+            e2m1x8_to_f16(w[u], v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+                v[j] = pack_bf16x2(x.x * f, x.y * f);
+            }
+            const int64_t out = place[me.t].dst_row + (int64_t)(hc / C) * g.head_rows;
+            reinterpret_cast<uint4*>(kv ? v_out : k_out)[out * C + hc % C] =
+                make_uint4(v[0], v[1], v[2], v[3]);
+        }
     }
 }
 
-// Tokens of a CTA: as few as fill its threads once while that leaves no more
-// CTAs than the GPU runs at a time, else up to four times that, so that a CTA
-// spends less of its life finding its tokens' pages.
+// Tokens of a CTA: as few as fill its threads once, so that a decode step takes
+// one pass, and more on long prompts, so that a CTA spends less of its life
+// finding its tokens' pages; but still 32 CTAs an SM, to keep the last of them
+// short (18000 tokens of 8 heads written and read back: 75 us with 8 an SM, 65
+// with 16, 61 with 32, 64 with 64).
 int tokens_per_cta(const CacheGeom& g, int sms) {
     const int per_token = 2 * g.Hkv * (g.D / 8);
-    const int once = per_token >= kWriteThreads ? 1 : kWriteThreads / per_token;
-    int n = once;
-    while (n < 4 * once && n < kMaxTokens && (int64_t)n * sms * 8 < g.total_q) n *= 2;
+    int n = per_token >= kWriteThreads ? 1 : kWriteThreads / per_token;
+    while (n < kMaxTokens && (int64_t)n * sms * 32 < g.total_q) n *= 2;
     return n < kMaxTokens ? n : kMaxTokens;
 }
 

@@ -84,26 +84,6 @@ struct Mx4Cfg {
 
 namespace {
 
-// Asynchronous copies with an L2 eviction priority; `bytes` 0 writes zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes,
-                                           uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::64B [%0], [%1], 16, %2, %3;" ::"r"(dst),
-                 "l"(src), "r"(bytes), "l"(policy)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes,
-                                          uint64_t policy) {
-    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 4, %2, %3;" ::"r"(dst),
-                 "l"(src), "r"(bytes), "l"(policy)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -129,26 +109,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// Two fp32 products or sums in one instruction.
-__device__ __forceinline__ void fma2(float* d, const float* a, uint64_t b) {
-    asm("{\n\t.reg .b64 x, y;\n\t"
-        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-        "fma.rn.f32x2 x, y, %4, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(d[0]), "+f"(d[1])
-        : "f"(a[0]), "f"(a[1]), "l"(b));
-}
-__device__ __forceinline__ void mul2(float* d, const float* a, uint64_t b) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 y, {%2, %3};\n\t"
-        "mul.rn.f32x2 x, y, %4;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d[0]), "=f"(d[1])
-        : "f"(a[0]), "f"(a[1]), "l"(b));
-}
-__device__ __forceinline__ uint64_t pair2(float x) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
     return d;
 }
 

@@ -2,14 +2,19 @@
 // of queries gives it:  w_j += sum_r exp2(f q_r . k_j - lse_r log2 e), over the
 // rows r (query, q head of the key's group) that see key j.
 //
-// No sum runs over keys, so there is nothing to join: a warp owns 32 keys of
-// one KV head, loads their rows once straight into the operand registers of
-// mma.sync (keys are the rows of the product, the contraction order is free,
-// so a lane takes 16 consecutive bytes of a bf16 row), and passes over the
-// query rows, eight a product, from shared memory.  The sum over rows stays in
-// a thread and its three neighbours: a fixed order, no atomics.
+// No sum runs over keys, so there is nothing to join: a warp owns 32 keys of one
+// KV head at a time, copies their rows into its own shared memory (cp.async) and
+// from there into the operand registers of mma.sync; while it passes over the
+// query rows, eight a product, the next 32 keys' rows are on their way into the
+// same place.  Keys are the rows of the product and the contraction order is
+// free, so a lane takes 16 consecutive bytes of a bf16 row (4 of codes).  The
+// sum over query rows stays in a thread and its three neighbours: a fixed order,
+// no atomics.
 // Bound by HBM (K once) for a decode step's few rows; with many rows by the
-// exponentials and products, which share the SM's issue slots.
+// products and exponentials.
+#include <mutex>
+#include <type_traits>
+
 #include "pa_cache_mma.cuh"
 
 namespace pa {
@@ -31,33 +36,55 @@ namespace {
 
 constexpr int kWeightWarps = 8;
 constexpr int kWeightThreads = 32 * kWeightWarps;
-constexpr int kWeightKeys = 32 * kWeightWarps;   // keys of one item
-constexpr int kQBlock = 128;                     // query rows in shared memory at a time
+
+// How K becomes an operand: bf16 as it is; 4-bit codes as f16, the block scales
+// applied to the block scores (few rows: the least work per key); or 4-bit codes
+// and scales as bf16 values (many rows: the least work per score).
+enum { kFromBf16, kFromCodes, kFromValues };
+
+// Two E2M1 codes as f16, times the block's scale, as bf16 (exact within bf16's range).
+__device__ __forceinline__ uint32_t scaled_bf16(uint32_t h2, float f) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    return pack_bf16x2(x.x * f, x.y * f);
+}
+
+// Bytes of a warp's place for 32 keys' rows (and scale words).
+template <int D, int FROM>
+__host__ __device__ constexpr int weight_stage() {
+    return FROM == kFromBf16 ? 32 * 2 * D : 32 * (D / 2 + 4);
+}
 
 // First key (a multiple of 32) of the items of a sequence, and how many items.
-__device__ __forceinline__ int seq_items(const CacheGeom& g, int c, int q, int& first) {
+__device__ __forceinline__ int seq_items(const CacheGeom& g, int c, int q, int keys, int& first) {
     first = 0;
     if (q <= 0 || !good_lens(g, q, c)) return 0;
     first = window_first_tile(g.window, c - q, 32) * 32;
-    return (c - first + kWeightKeys - 1) / kWeightKeys;
+    return (c - first + keys - 1) / keys;
 }
 
-template <int D, bool MX4>
-__global__ void __launch_bounds__(kWeightThreads)
+// kQBlock: query rows in shared memory at a time.
+template <int D, int FROM, int kQBlock>
+__global__ void __launch_bounds__(kWeightThreads, 2)
 key_weights_kernel(const __grid_constant__ WeightParams P) {
     constexpr int KB = D / 32;                 // blocks of 32 columns
     constexpr int QROW = 2 * D + kQPad;
+    constexpr int MT = 2;                      // 16-key tiles of a warp
+    constexpr int kKeys = 32 * kWeightWarps;   // of one item
+    constexpr bool kMx4 = FROM != kFromBf16;
+    constexpr int ROW = kMx4 ? D / 2 : 2 * D;  // bytes of a key's row
+    constexpr int CH = ROW / 16, RPI = 32 / CH;   // its chunks, rows a copy instruction
     extern __shared__ __align__(128) uint8_t smem[];
-    float* off = reinterpret_cast<float*>(smem + kQBlock * QROW);   // lse * log2 e
+    float* off = reinterpret_cast<float*>(smem + kQBlock * QROW);   // -lse * log2 e
     float* fac = off + kQBlock;                                     // score factor
     int* pos = reinterpret_cast<int*>(fac + kQBlock);               // query position
+    const uint32_t rows = smem_u32(pos + kQBlock) + (threadIdx.x >> 5) * weight_stage<D, FROM>();
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = lane >> 2, t4 = lane & 3;
 
     auto cost = [&](int b) -> int64_t {
         int first;
-        return (int64_t)g.Hkv * seq_items(g, P.ctx[b], P.ql[b], first);
+        return (int64_t)g.Hkv * seq_items(g, P.ctx[b], P.ql[b], kKeys, first);
     };
     const int64_t total = flat_total(g.B, lane, cost);
     if (blockIdx.x == 0 && warp == 0) check_lens(g, P.ctx, P.ql, lane, P.err);
@@ -65,71 +92,169 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
     if (blockIdx.x >= N) return;
     int64_t i = total * blockIdx.x / N;
     const int64_t i_end = total * (blockIdx.x + 1) / N;
-    int64_t start;
-    int row0;
-    int b = flat_find(g.B, lane, i, cost, [&](int x) { return clamp_q(g, P.ql[x]); }, start, row0);
-    int c = P.ctx[b], q = P.ql[b], first;
-    int n = seq_items(g, c, q, first);
-    int hk = (int)((i - start) / n), chunk = (int)((i - start) % n);
-    bool fresh = true;                         // Q of (b, hk) is not in shared memory
+
+    // an item: keys of one KV head of one sequence
+    struct Item {
+        int b, hk, chunk, n, c, q, first, row0;
+    };
+    Item t;
+    {
+        int64_t start;
+        t.b = flat_find(g.B, lane, i, cost, [&](int x) { return clamp_q(g, P.ql[x]); }, start,
+                        t.row0);
+        t.c = P.ctx[t.b];
+        t.q = P.ql[t.b];
+        t.n = seq_items(g, t.c, t.q, kKeys, t.first);
+        t.hk = (int)((i - start) / t.n);
+        t.chunk = (int)((i - start) % t.n);
+    }
+    auto advance = [&](Item& x) {
+        if (++x.chunk < x.n) return;
+        x.chunk = 0;
+        if (++x.hk < g.Hkv) return;
+        x.hk = 0;
+        do {
+            x.row0 += clamp_q(g, x.q);
+            ++x.b;
+            x.c = P.ctx[x.b];
+            x.q = P.ql[x.b];
+            x.n = seq_items(g, x.c, x.q, kKeys, x.first);
+        } while (x.n == 0);
+    };
+    auto first_key = [&](const Item& x) { return x.first + x.chunk * kKeys + 32 * warp; };
+    // the pages of a warp's two runs of 16 keys
+    auto look_up = [&](const Item& x) -> int2 {
+        const int32_t* row = P.table + (int64_t)x.b * g.mpps;
+        const int key = first_key(x);
+        int2 p = make_int2(-1, -1);
+        if (key < x.c) p.x = p.y = row[key >> g.ps_shift];
+        if (g.ps == 16) p.y = key + 16 < x.c ? row[(key >> 4) + 1] : -1;
+        return p;
+    };
+    uint64_t once;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    const int page_rows = g.ps * g.Hkv;
+    // where chunk c of row r goes: eight lanes of a load meet no bank twice
+    auto chunk_at = [&](int r, int c) -> int {
+        if constexpr (CH >= 8) return c ^ ((r & 1) << 2);        // bf16: 64 bytes of two rows
+        else if constexpr (CH == 4) return c ^ ((r >> 1) & 3);   // codes: 16 bytes of eight
+        else return c ^ ((r >> 2) & 1);
+    };
+    // the rows of an item's 32 keys, and their scales, on their way; keys that
+    // do not exist, or whose page does not, become zeros
+    auto issue = [&](const Item& x, int2 p) {
+        const int key = first_key(x), left = x.c - key;
+        const bool oka = (uint32_t)p.x < (uint32_t)g.num_pages;
+        const bool okb = (uint32_t)p.y < (uint32_t)g.num_pages;
+        const int64_t ra = (int64_t)p.x * page_rows +
+                           ((key & (g.ps - 1)) * g.tok_rows + x.hk * g.head_rows);
+        const int64_t rb = g.ps == 16 ? (int64_t)p.y * page_rows + x.hk * g.head_rows
+                                      : ra + 16 * g.tok_rows;
+        if (lane == 0 && ((left > 0 && !oka) || (left > 16 && !okb)))
+            flag_error(P.err, PA_DEV_BAD_PAGE);
+#pragma unroll
+        for (int j = 0; j < 32 / RPI; ++j) {
+            const int r = j * RPI + lane / CH, c = lane % CH;
+            const bool ok = r < left && (r < 16 ? oka : okb);
+            const int64_t row = (r < 16 ? ra : rb) + (r & 15) * g.tok_rows;
+            cp_async16(rows + r * ROW + chunk_at(r, c) * 16, P.k + (ok ? row * ROW + c * 16 : 0),
+                       ok ? 16 : 0, once);
+        }
+        if constexpr (kMx4) {
+            const bool ok = lane < left && (lane < 16 ? oka : okb);
+            const int64_t row = (lane < 16 ? ra : rb) + (lane & 15) * g.tok_rows;
+            // (head_dim 64: the word that holds the key's two bytes)
+            cp_async4(rows + 32 * ROW + lane * 4, P.ks + (ok ? row * KB & ~(int64_t)3 : 0),
+                      ok ? 4 : 0, once);
+        }
+        cp_async_commit();
+    };
+    int2 page = look_up(t);
+    issue(t, page);
+    Item next = t;
+    int2 next_page = make_int2(-1, -1);
+    if (i + 1 < i_end) {
+        advance(next);
+        next_page = look_up(next);
+    }
+    bool fresh = true;                         // Q of the item is not in shared memory
     bool blind = false;                        // some of its rows see nothing (padding, lse -inf)
 
     for (; i < i_end; ++i) {
-        const int R = g.G * q;
-        const bool rows_ok = row0 + q <= g.total_q;
-        // ---- this warp's 32 keys
-        const int tok = first + chunk * kWeightKeys + 32 * warp;
-        const int my_tok = tok + 8 * t4 + gr;  // the key this lane adds up for
-        const bool in = my_tok < c;
-        int page = in ? P.table[(int64_t)b * g.mpps + (my_tok >> g.ps_shift)] : -1;
-        if (in && (page < 0 || page >= g.num_pages)) {
-            flag_error(P.err, PA_DEV_BAD_PAGE);
-            page = -1;
-        }
-        const int slot = my_tok & (g.ps - 1);
-        float* dst = P.weights + ((int64_t)max(page, 0) * g.Hkv + hk) * g.ps + slot;
-        const float before = page >= 0 ? *dst : 0.f;
-        const int64_t my_row = page >= 0 ? row_of(g, page, slot, hk) : -1;
-        uint32_t a[2][KB][2][4];
-        float f[2][2][KB];
+        const int R = g.G * t.q, c = t.c, q = t.q;
+        const bool rows_ok = t.row0 + q <= g.total_q;
+        // ---- this warp's keys; lane (gr, t4) adds up key 8 t4 + gr
+        const int tok = first_key(t), my_tok = tok + 8 * t4 + gr;
+        const int my_page = t4 < 2 ? page.x : page.y;
+        const bool mine_ok = my_tok < c && (uint32_t)my_page < (uint32_t)g.num_pages;
+        float* dst = P.weights + ((int64_t)(mine_ok ? my_page : 0) * g.Hkv + t.hk) * g.ps +
+                     (my_tok & (g.ps - 1));
+        const float before = mine_ok ? *dst : 0.f;
+        cp_async_wait<0>();
+        __syncwarp();
+        uint32_t a[MT][KB][2][4];              // (kFromCodes: a[..][0][hh] only, the codes)
+        uint32_t e[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                // row of key 16 mt + 8 hh + gr, found by lane (gr, 2 mt + hh)
-                const int64_t row = __shfl_sync(0xffffffffu, my_row, gr * 4 + 2 * mt + hh);
-                if constexpr (MX4) {
-                    uint32_t w[KB], e = 0;
+                const int r = 16 * mt + 8 * hh + gr;
+                if constexpr (kMx4) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb)
-                        w[kb] = row >= 0 ? *reinterpret_cast<const uint32_t*>(
-                                               P.k + row * (D / 2) + kb * 16 + t4 * 4)
-                                         : 0u;
-                    if (row >= 0)
-                        e = D == 128 ? *reinterpret_cast<const uint32_t*>(P.ks + row * 4)
-                                     : *reinterpret_cast<const uint16_t*>(P.ks + row * 2);
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        e2m1x8_to_f16(w[kb], a[mt][kb][0][hh], a[mt][kb][0][2 + hh],
-                                      a[mt][kb][1][hh], a[mt][kb][1][2 + hh]);
-                        f[mt][hh][kb] = e8m0_to_f32((e >> (8 * kb)) & 255u);
+                        asm volatile("ld.shared.b32 %0, [%1];"
+                                     : "=r"(a[mt][kb][0][hh])
+                                     : "r"(rows + r * ROW + chunk_at(r, kb) * 16 + t4 * 4));
+                    asm volatile("ld.shared.b32 %0, [%1];"
+                                 : "=r"(e[mt][hh])
+                                 : "r"(rows + 32 * ROW + r * 4));
+                    if constexpr (D == 64) {
+                        const int x = (tok + r) & (g.ps - 1);
+                        e[mt][hh] >>= ((x * g.tok_rows + t.hk * g.head_rows) & 1) * 16;
                     }
                 } else {
 #pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (row >= 0)
-                            x = *reinterpret_cast<const uint4*>(P.k + row * (2 * D) + kb * 64 +
-                                                                t4 * 16);
-                        a[mt][kb][0][hh] = x.x;
-                        a[mt][kb][0][2 + hh] = x.y;
-                        a[mt][kb][1][hh] = x.z;
-                        a[mt][kb][1][2 + hh] = x.w;
-                    }
+                    for (int kb = 0; kb < KB; ++kb)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(a[mt][kb][0][hh]), "=r"(a[mt][kb][0][2 + hh]),
+                                       "=r"(a[mt][kb][1][hh]), "=r"(a[mt][kb][1][2 + hh])
+                                     : "r"(rows + r * ROW + chunk_at(r, 4 * kb + t4) * 16));
                 }
             }
-        float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-        const bool clear = tok + 31 <= c - q && (g.window == 0 || tok > c - 1 - g.window);
+        __syncwarp();
+        // ---- the next item's rows into the same place, the one after's pages
+        const Item done = t;
+        if (i + 1 < i_end) {
+            issue(next, next_page);
+            t = next;
+            page = next_page;
+            if (i + 2 < i_end) {
+                advance(next);
+                next_page = look_up(next);
+            }
+        }
+        if constexpr (FROM == kFromValues) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        e2m1x8_to_f16(a[mt][kb][0][hh], a[mt][kb][0][hh], a[mt][kb][0][2 + hh],
+                                      a[mt][kb][1][hh], a[mt][kb][1][2 + hh]);
+                        const float f = e8m0_to_f32((e[mt][hh] >> (8 * kb)) & 255u);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t& v = a[mt][kb][x >> 1][2 * (x & 1) + hh];
+                            v = scaled_bf16(v, f);
+                        }
+                    }
+        }
+        float w[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) w[mt][0] = w[mt][1] = 0.f;
+        const bool clear =
+            tok + 16 * MT - 1 <= c - q && (g.window == 0 || tok > c - 1 - g.window);
         for (int r0 = 0; r0 < R; r0 += kQBlock) {
             const int nr = min(kQBlock, R - r0);
             if (fresh || R > kQBlock) {
@@ -139,8 +264,8 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
                 for (int r = warp; r < ((nr + 7) & ~7); r += kWeightWarps) {
                     float x[D / 32];
                     const bool real = r < nr && rows_ok;
-                    const int64_t qrow = real ? (int64_t)(row0 + (r0 + r) / g.G) * g.Hq +
-                                                    hk * g.G + (r0 + r) % g.G
+                    const int64_t qrow = real ? (int64_t)(done.row0 + (r0 + r) / g.G) * g.Hq +
+                                                    done.hk * g.G + (r0 + r) % g.G
                                               : 0;
                     float top = 0.f;
 #pragma unroll
@@ -154,24 +279,22 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
                     }
                     float factor = g.sm_scale * kLog2e;
                     float down = 1.f;
-                    if constexpr (MX4) {
+                    if constexpr (FROM == kFromCodes) {
                         // f16 rows with a power of two taken out (as in pa_decode_mx4)
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e = max(8, min(247, (int)(__float_as_uint(top) >> 23)));
-                        down = __uint_as_float((uint32_t)(254 - e) << 23);
-                        factor *= __uint_as_float((uint32_t)e << 23);
+                        const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                        const int ex = max(8, min(247, (int)(tb >> 23)));
+                        down = __uint_as_float((uint32_t)(254 - ex) << 23);
+                        factor *= __uint_as_float((uint32_t)ex << 23);
                     }
 #pragma unroll
                     for (int j = 0; j < D / 64; ++j)
                         *reinterpret_cast<uint32_t*>(smem + r * QROW + 4 * (lane + 32 * j)) =
-                            MX4 ? pack_f16x2(x[2 * j] * down, x[2 * j + 1] * down)
-                                : pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                            FROM == kFromCodes ? pack_f16x2(x[2 * j] * down, x[2 * j + 1] * down)
+                                               : pack_bf16x2(x[2 * j], x[2 * j + 1]);
                     const float v = real ? P.lse[qrow] : -INFINITY;
                     none |= v == -INFINITY;
                     if (lane == 0) {
-                        off[r] = v * kLog2e;
+                        off[r] = -v * kLog2e;
                         fac[r] = factor;
                         pos[r] = v == -INFINITY ? -1 : c - q + (r0 + r) / g.G;
                     }
@@ -179,53 +302,93 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
                 blind = __syncthreads_or(none);
                 fresh = false;
             }
-            const uint32_t qbase = smem_u32(smem);
-            for (int nt = 0; nt < nr; nt += 8) {
-                float s[2][4];
+            const uint32_t qbase = smem_u32(smem) + gr * QROW + t4 * 16;
+            const float factor = g.sm_scale * kLog2e;
+            // eight rows against the warp's keys
+            auto score = [&](int nt, auto mask) {
+                constexpr int U = 1;
+                constexpr bool masked = decltype(mask)::value;
+                float s[U][MT][4];
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    uint32_t b0, b1, b2, b3;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
-                                 : "r"(qbase + (nt + gr) * QROW + kb * 64 + t4 * 16));
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        if constexpr (MX4) {
-                            float x[4];
-                            mma_f16_first(x, a[mt][kb][0], b0, b1);
-                            mma_f16_16816(x, a[mt][kb][1], b2, b3);
+                    for (int u = 0; u < U; ++u) {
+                        uint32_t b0, b1, b2, b3;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                                     : "r"(qbase + (nt + 8 * u) * QROW + kb * 64));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                s[mt][e] = kb == 0 ? x[e] * f[mt][e >> 1][0]
-                                                   : fmaf(x[e], f[mt][e >> 1][kb], s[mt][e]);
-                        } else {
-                            if (kb == 0) s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
-                            mma_bf16_16816(s[mt], a[mt][kb][0], b0, b1);
-                            mma_bf16_16816(s[mt], a[mt][kb][1], b2, b3);
+                        for (int mt = 0; mt < MT; ++mt) {
+                            float* d = s[u][mt];
+                            if constexpr (FROM == kFromCodes) {
+                                // converted anew for every eight rows (few are
+                                // more than that): as f16 for all of them, 128
+                                // registers a thread do not hold a row
+                                uint32_t h[2][4], ex[2];
+#pragma unroll
+                                for (int hh = 0; hh < 2; ++hh) {
+                                    uint32_t code = a[mt][kb][0][hh];
+                                    ex[hh] = e[mt][hh];
+                                    asm volatile("" : "+r"(code), "+r"(ex[hh]));
+                                    e2m1x8_to_f16(code, h[0][hh], h[0][2 + hh], h[1][hh],
+                                                  h[1][2 + hh]);
+                                }
+                                float x[4];
+                                mma_f16_first(x, h[0], b0, b1);
+                                mma_f16_16816(x, h[1], b2, b3);
+#pragma unroll
+                                for (int hh = 0; hh < 2; ++hh) {
+                                    const float f = e8m0_to_f32((ex[hh] >> (8 * kb)) & 255u);
+#pragma unroll
+                                    for (int v = 2 * hh; v < 2 * hh + 2; ++v)
+                                        d[v] = kb == 0 ? x[v] * f : fmaf(x[v], f, d[v]);
+                                }
+                            } else {
+                                if (kb == 0)
+                                    mma_bf16_first(d, a[mt][kb][0], b0, b1);
+                                else
+                                    mma_bf16_16816(d, a[mt][kb][0], b0, b1);
+                                mma_bf16_16816(d, a[mt][kb][1], b2, b3);
+                            }
                         }
                     }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = nt + 8 * u + 2 * t4;
+                    const float2 of = *reinterpret_cast<const float2*>(off + r);
+                    float2 fc = make_float2(factor, factor);
+                    if constexpr (FROM == kFromCodes)
+                        fc = *reinterpret_cast<const float2*>(fac + r);
+                    int2 pp = make_int2(0, 0);
+                    if constexpr (masked) pp = *reinterpret_cast<const int2*>(pos + r);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const float* d = s[u][mt] + 2 * hh;
+                            float p0 = ex2(fmaf(d[0], fc.x, of.x));
+                            float p1 = ex2(fmaf(d[1], fc.y, of.y));
+                            if constexpr (masked) {
+                                const int j = tok + 16 * mt + 8 * hh + gr;
+                                if (j > pp.x || (g.window > 0 && j <= pp.x - g.window)) p0 = 0.f;
+                                if (j > pp.y || (g.window > 0 && j <= pp.y - g.window)) p1 = 0.f;
+                            }
+                            w[mt][hh] += p0 + p1;
+                        }
                 }
-                const float2 fc = *reinterpret_cast<const float2*>(fac + nt + 2 * t4);
-                const float2 of = *reinterpret_cast<const float2*>(off + nt + 2 * t4);
-                const int2 pp = *reinterpret_cast<const int2*>(pos + nt + 2 * t4);
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[mt][e], e & 1 ? fc.y : fc.x, -(e & 1 ? of.y : of.x));
-                        if (!clear || blind) {
-                            const int j = tok + 16 * mt + 8 * (e >> 1) + gr;
-                            const int p = e & 1 ? pp.y : pp.x;
-                            if (j > p || (g.window > 0 && j <= p - g.window)) x = -INFINITY;
-                        }
-                        w[mt][e >> 1] += ex2(x);
-                    }
+            };
+            if (!clear || blind) {
+#pragma unroll 1
+                for (int nt = 0; nt < nr; nt += 8) score(nt, std::true_type());
+            } else {
+#pragma unroll 1
+                for (int nt = 0; nt < nr; nt += 8) score(nt, std::false_type());
             }
         }
         // ---- over the four lanes that hold a key's rows; lane (gr, t4) adds key 8 t4 + gr
         float mine = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 float x = w[mt][hh];
@@ -233,39 +396,43 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 if (t4 == 2 * mt + hh) mine = x;
             }
-        if (page >= 0) *dst = before + mine;
-        // ---- the next item
-        if (++chunk == n) {
-            chunk = 0;
-            fresh = true;
-            if (++hk == g.Hkv) {
-                hk = 0;
-                if (i + 1 < i_end) {
-                    do {
-                        row0 += clamp_q(g, q);
-                        ++b;
-                        c = P.ctx[b];
-                        q = P.ql[b];
-                        n = seq_items(g, c, q, first);
-                    } while (n == 0);
-                }
-            }
-        }
+        if (mine_ok) *dst = before + mine;
+        fresh = t.hk != done.hk || t.b != done.b;
     }
 }
 
-template <int D, bool MX4>
+// Shared-memory opt-in and the CTAs an SM holds, once per device.
+template <int D, int FROM, int kQBlock>
 cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) {
-    constexpr int smem = kQBlock * (2 * D + kQPad) + 3 * kQBlock * 4;
-    auto kern = key_weights_kernel<D, MX4>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = kQBlock * (2 * D + kQPad) + 3 * kQBlock * 4 +
+                         kWeightWarps * weight_stage<D, FROM>();
+    auto kern = key_weights_kernel<D, FROM, kQBlock>;
+    static std::mutex mu;
+    static int per_sm[64] = {0};
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWeightThreads, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<sms * (per_sm > 0 ? per_sm : 1), kWeightThreads, smem, stream>>>(P);
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 64 || per_sm[dev] == 0) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWeightThreads, smem);
+            if (e != cudaSuccess) return e;
+            if (n < 1) n = 1;
+            if (dev < 64) per_sm[dev] = n;
+        } else {
+            n = per_sm[dev];
+        }
+    }
+    kern<<<sms * n, kWeightThreads, smem, stream>>>(P);
     return cudaGetLastError();
 }
+
+// Up to this many query rows (of the longest q_len) the kernel for few rows
+// runs: a small place for Q, 4-bit block scores scaled in fp32.  Above, 128 rows
+// of Q at a time, and 4-bit keys turned into bf16 values once.
+constexpr int kFewRows = 32;
 
 }  // namespace
 
@@ -284,11 +451,19 @@ cudaError_t launch_key_weights(const CacheGeom& g, bool mx4, const void* q, cons
     P.lse = lse;
     P.weights = weights;
     P.err = err;
-    if (g.D == 128)
-        return mx4 ? launch_weights<128, true>(P, sms, stream)
-                   : launch_weights<128, false>(P, sms, stream);
-    return mx4 ? launch_weights<64, true>(P, sms, stream)
-               : launch_weights<64, false>(P, sms, stream);
+    const bool many = g.G * g.max_q_len > kFewRows;
+    if (g.D == 128) {
+        if (!mx4)
+            return many ? launch_weights<128, kFromBf16, 128>(P, sms, stream)
+                        : launch_weights<128, kFromBf16, 32>(P, sms, stream);
+        return many ? launch_weights<128, kFromValues, 128>(P, sms, stream)
+                    : launch_weights<128, kFromCodes, 32>(P, sms, stream);
+    }
+    if (!mx4)
+        return many ? launch_weights<64, kFromBf16, 128>(P, sms, stream)
+                    : launch_weights<64, kFromBf16, 32>(P, sms, stream);
+    return many ? launch_weights<64, kFromValues, 128>(P, sms, stream)
+                : launch_weights<64, kFromCodes, 32>(P, sms, stream);
 }
 
 }  // namespace pa

@@ -1,11 +1,13 @@
 // pa_kv_evict.cu -- which keys of a paged cache to keep, by their accumulated
 // weights, and moving the kept rows into other pages.
 //
-// Two launches.  Select (one CTA per sequence and KV head): the budget-th
-// largest key by a radix select, eight bits a pass over an order-preserving
-// integer form of the weights, then one ordered pass that lists the kept
-// positions (ties to the lower one).  Move: CTAs copy 64 kept rows of K and V
-// each, 16 bytes a thread; bound by HBM.
+// Select, one CTA per sequence and KV head: the budget-th largest key by a radix
+// select, eight bits a pass over an order-preserving integer form of the
+// weights, then one ordered pass that lists the kept positions (ties to the
+// lower one).  Move: 64 kept rows of K and V at a time, 16 bytes a thread; bound
+// by HBM.  Where the (sequence, head) pairs fill the GPU the CTA that selected
+// moves, so that one's selection hides behind another's moves; fewer pairs
+// leave the moves to a second launch that spreads them over all SMs.
 #include "pa_cache_common.cuh"
 
 namespace pa {
@@ -29,13 +31,78 @@ struct EvictParams {
 
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 256;
 constexpr int kHistBytes = kBins * 32 * 4;   // one histogram per lane: no bank is met twice
 constexpr int kMaxCached = (227 * 1024 - kHistBytes - 2048) / 4;   // keys held in shared memory
-constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;
+
+constexpr int kMoveThreads = 256;
+
+// Rows r0 .. r0 + n of the kept list of (b, hk), n <= kMoveRows, into their new
+// pages, by the THREADS of a CTA.  PIECES: 16-byte pieces of a row (D / 8 of bf16,
+// D / 32 of 4-bit codes).
+struct MoveRows {
+    int64_t src[kMoveRows], dst[kMoveRows];
+};
+template <int PIECES, int THREADS>
+__device__ __forceinline__ void move_rows(const EvictParams& P, MoveRows& at, int b, int hk, int c,
+                                          int r0, int n, int scale_bytes) {
+    const CacheGeom& g = P.g;
+    const int tid = threadIdx.x, unit = b * g.Hkv + hk;
+    if (tid < n) {
+        const int from = P.kept[(int64_t)unit * P.budget + r0 + tid], to = r0 + tid;
+        const bool listed = from >= 0 && from < c;
+        const int sp = listed ? P.table[(int64_t)b * g.mpps + (from >> g.ps_shift)] : -1;
+        const int dp = P.dst_table[(int64_t)b * P.dst_mpps + (to >> g.ps_shift)];
+        const bool ok = sp >= 0 && sp < g.num_pages && dp >= 0 && dp < g.num_pages;
+        const int ss = from & (g.ps - 1), ds = to & (g.ps - 1);
+        const int64_t s = ok ? row_of(g, sp, ss, hk) : -1, d = ok ? row_of(g, dp, ds, hk) : 0;
+        at.src[tid] = s;
+        at.dst[tid] = d;
+        if (ok) {
+            P.weights[((int64_t)dp * g.Hkv + hk) * g.ps + ds] =
+                P.weights[((int64_t)sp * g.Hkv + hk) * g.ps + ss];
+            if (scale_bytes == 4) {
+                reinterpret_cast<uint32_t*>(P.ks)[d] = reinterpret_cast<const uint32_t*>(P.ks)[s];
+                reinterpret_cast<uint32_t*>(P.vs)[d] = reinterpret_cast<const uint32_t*>(P.vs)[s];
+            } else if (scale_bytes == 2) {
+                reinterpret_cast<uint16_t*>(P.ks)[d] = reinterpret_cast<const uint16_t*>(P.ks)[s];
+                reinterpret_cast<uint16_t*>(P.vs)[d] = reinterpret_cast<const uint16_t*>(P.vs)[s];
+            }
+        } else {
+            flag_error(P.err, PA_DEV_BAD_PAGE);
+        }
+    }
+    __syncthreads();
+    // pieces of K, then of V; every load of a thread before its stores
+    constexpr int kPer = (2 * PIECES * kMoveRows + THREADS - 1) / THREADS;
+    uint4 x[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid + j * THREADS, kv = i / (PIECES * kMoveRows);
+        const int r = (i / PIECES) % kMoveRows, p = i % PIECES;
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (kv < 2 && r < n && at.src[r] >= 0)
+            x[j] = __ldcs(reinterpret_cast<const uint4*>(kv ? P.v : P.k) + at.src[r] * PIECES + p);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid + j * THREADS, kv = i / (PIECES * kMoveRows);
+        const int r = (i / PIECES) % kMoveRows, p = i % PIECES;
+        if (kv < 2 && r < n && at.src[r] >= 0)
+            __stcs(reinterpret_cast<uint4*>(kv ? P.v : P.k) + at.dst[r] * PIECES + p, x[j]);
+    }
+}
+
+template <int PIECES>
+__global__ void __launch_bounds__(kMoveThreads)
+move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) {
+    __shared__ MoveRows at;
+    const int unit = blockIdx.x / chunks, r0 = blockIdx.x % chunks * kMoveRows;
+    const int b = unit / P.g.Hkv, hk = unit % P.g.Hkv, c = P.ctx[b];
+    if (c <= P.budget || c > P.g.max_ctx) return;
+    move_rows<PIECES, kMoveThreads>(P, at, b, hk, c, r0, min(kMoveRows, P.budget - r0), scale_bytes);
+}
 
 // Larger weights get larger keys; NaN the smallest, a protected position the largest.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -44,8 +111,11 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads, 1)
-select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
+// PIECES 0: select only; else the CTA moves what it selected.
+template <int kSelectThreads, int PIECES>
+__global__ void __launch_bounds__(kSelectThreads)
+select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_bytes) {
+    constexpr int kSelectWarps = kSelectThreads / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
     uint32_t* cached = reinterpret_cast<uint32_t*>(smem + kHistBytes);
@@ -131,7 +201,7 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     }
     if (lane == 0) s_count[warp] = make_int2(above, equal);
     __syncthreads();
-    const int2 mine = s_count[lane];
+    const int2 mine = lane < kSelectWarps ? s_count[lane] : make_int2(0, 0);
     const int ea = warp_inclusive(mine.x, lane) - mine.x, ee = warp_inclusive(mine.y, lane) - mine.y;
     int na = __shfl_sync(0xffffffffu, ea, warp), ne = __shfl_sync(0xffffffffu, ee, warp);
     int32_t* out = P.kept + (int64_t)blockIdx.x * P.budget;
@@ -147,66 +217,13 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
         na += __popc(ma);
         ne += __popc(me);
     }
-}
-
-// 16-byte pieces of a row: D / 8 of bf16, D / 32 of 4-bit codes.
-template <int PIECES>
-__global__ void __launch_bounds__(kMoveThreads)
-move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) {
-    __shared__ int64_t s_src[kMoveRows], s_dst[kMoveRows];
-    const CacheGeom& g = P.g;
-    const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    const int b = unit / g.Hkv, hk = unit % g.Hkv;
-    const int c = P.ctx[b];
-    if (c <= P.budget || c > g.max_ctx) return;
-    const int r0 = chunk * kMoveRows, n = min(kMoveRows, P.budget - r0);
-    const int tid = threadIdx.x;
-    if (tid < n) {
-        const int from = P.kept[(int64_t)unit * P.budget + r0 + tid], to = r0 + tid;
-        const bool listed = from >= 0 && from < c;
-        const int sp = listed ? P.table[(int64_t)b * g.mpps + (from >> g.ps_shift)] : -1;
-        const int dp = P.dst_table[(int64_t)b * P.dst_mpps + (to >> g.ps_shift)];
-        const bool ok = sp >= 0 && sp < g.num_pages && dp >= 0 && dp < g.num_pages;
-        const int ss = from & (g.ps - 1), ds = to & (g.ps - 1);
-        s_src[tid] = ok ? row_of(g, sp, ss, hk) : -1;
-        s_dst[tid] = ok ? row_of(g, dp, ds, hk) : 0;
-        if (ok) {
-            P.weights[((int64_t)dp * g.Hkv + hk) * g.ps + ds] =
-                P.weights[((int64_t)sp * g.Hkv + hk) * g.ps + ss];
-            if (scale_bytes == 4) {
-                const int64_t s = s_src[tid], d = s_dst[tid];
-                reinterpret_cast<uint32_t*>(P.ks)[d] = reinterpret_cast<const uint32_t*>(P.ks)[s];
-                reinterpret_cast<uint32_t*>(P.vs)[d] = reinterpret_cast<const uint32_t*>(P.vs)[s];
-            } else if (scale_bytes == 2) {
-                const int64_t s = s_src[tid], d = s_dst[tid];
-                reinterpret_cast<uint16_t*>(P.ks)[d] = reinterpret_cast<const uint16_t*>(P.ks)[s];
-                reinterpret_cast<uint16_t*>(P.vs)[d] = reinterpret_cast<const uint16_t*>(P.vs)[s];
-            }
-        } else {
-            flag_error(P.err, PA_DEV_BAD_PAGE);
-        }
-    }
-    __syncthreads();
-    // pieces of K, then of V; every load of a thread before its stores
-    constexpr int kPer = (2 * PIECES * kMoveRows + kMoveThreads - 1) / kMoveThreads;
-    uint4 x[kPer];
-    const int items = 2 * PIECES * n;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * kMoveThreads;
-        x[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < items) {
-            const int kv = i / (PIECES * n), r = (i / PIECES) % n, p = i % PIECES;
-            const int64_t s = s_src[r];
-            if (s >= 0) x[j] = reinterpret_cast<const uint4*>(kv ? P.v : P.k)[s * PIECES + p];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * kMoveThreads;
-        if (i < items) {
-            const int kv = i / (PIECES * n), r = (i / PIECES) % n, p = i % PIECES;
-            if (s_src[r] >= 0) reinterpret_cast<uint4*>(kv ? P.v : P.k)[s_dst[r] * PIECES + p] = x[j];
+    if constexpr (PIECES > 0) {
+        // (the kept list and the histograms' place are this CTA's own)
+        MoveRows* at = reinterpret_cast<MoveRows*>(smem);
+        for (int r0 = 0; r0 < P.budget; r0 += kMoveRows) {
+            __syncthreads();
+            move_rows<PIECES, kSelectThreads>(P, at[(r0 / kMoveRows) & 1], b, hk, c, r0,
+                                              min(kMoveRows, P.budget - r0), scale_bytes);
         }
     }
 }
@@ -216,7 +233,7 @@ move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) 
 cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first, int num_recent,
                          void* k, void* ks, void* v, void* vs, float* weights,
                          const int32_t* table, const int32_t* dst_table, int dst_mpps,
-                         const int32_t* ctx, int32_t* kept, int32_t* new_ctx, int32_t* err,
+                         const int32_t* ctx, int32_t* kept, int32_t* new_ctx, int32_t* err, int sms,
                          cudaStream_t stream) {
     EvictParams P;
     P.g = g;
@@ -238,20 +255,32 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     // the longest sequence's keys fit shared memory, or are read from L2 every pass
     const int cap = g.max_ctx <= kMaxCached ? g.max_ctx : kMaxCached;
     const int smem = kHistBytes + cap * 4;
-    cudaError_t e =
-        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int units = g.B * g.Hkv;
+    const int pieces = mx4 ? g.D / 32 : g.D / 8, scale_bytes = mx4 ? g.D / 32 : 0;
+    // many pairs: each CTA its own; short sequences with fewer threads, so that
+    // an SM holds more of them
+    const bool together = units >= 2 * sms, few = cap <= 4096;
+    void (*kern)(EvictParams, int, int) =
+        !together ? (few ? select_kernel<256, 0> : select_kernel<1024, 0>)
+        : pieces == 16 ? (few ? select_kernel<256, 16> : select_kernel<512, 16>)
+        : pieces == 8  ? (few ? select_kernel<256, 8> : select_kernel<512, 8>)
+        : pieces == 4  ? (few ? select_kernel<256, 4> : select_kernel<512, 4>)
+                       : (few ? select_kernel<256, 2> : select_kernel<512, 2>);
+    const int threads = few ? 256 : together ? 512 : 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    select_kernel<<<g.B * g.Hkv, kSelectThreads, smem, stream>>>(P, cap);
+    kern<<<units, threads, smem, stream>>>(P, cap, scale_bytes);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (g.max_ctx <= budget) return cudaSuccess;   // nothing can be over the budget
+    if (together || g.max_ctx <= budget) return cudaSuccess;
     const int chunks = (budget + kMoveRows - 1) / kMoveRows;
-    const int64_t grid = (int64_t)g.B * g.Hkv * chunks;
+    const int64_t grid = (int64_t)units * chunks;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    const int scale_bytes = mx4 ? g.D / 32 : 0;
-    auto kern = mx4 ? (g.D == 128 ? move_kernel<4> : move_kernel<2>)
-                    : (g.D == 128 ? move_kernel<16> : move_kernel<8>);
-    kern<<<(int)grid, kMoveThreads, 0, stream>>>(P, chunks, scale_bytes);
+    auto move = pieces == 16  ? move_kernel<16>
+                : pieces == 8 ? move_kernel<8>
+                : pieces == 4 ? move_kernel<4>
+                              : move_kernel<2>;
+    move<<<(int)grid, kMoveThreads, 0, stream>>>(P, chunks, scale_bytes);
     return cudaGetLastError();
 }
 
