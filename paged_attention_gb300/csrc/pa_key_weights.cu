@@ -1,6 +1,7 @@
 // pa_key_weights.cu -- adds to every cached key the softmax weight that a set
 // of queries gives it:  w_j += sum_r exp2(f q_r . k_j - lse_r log2 e), over the
-// rows r (query, q head of the key's group) that see key j.
+// rows r (query, q head of the key's group) that see key j.  This is the kernel
+// for up to 32 such rows; pa_key_weights_tc.cu has the one for more.
 //
 // No sum runs over keys, so there is nothing to join: a warp owns 32 keys of one
 // KV head at a time, copies their rows into its own shared memory (cp.async) and
@@ -10,8 +11,7 @@
 // free, so a lane takes 16 consecutive bytes of a bf16 row (4 of codes).  The
 // sum over query rows stays in a thread and its three neighbours: a fixed order,
 // no atomics.
-// Bound by HBM (K once) for a decode step's few rows; with many rows by the
-// products and exponentials.
+// Bound by HBM (K once).
 #include <mutex>
 #include <type_traits>
 
@@ -37,21 +37,14 @@ namespace {
 constexpr int kWeightWarps = 8;
 constexpr int kWeightThreads = 32 * kWeightWarps;
 
-// How K becomes an operand: bf16 as it is; 4-bit codes as f16, the block scales
-// applied to the block scores (few rows: the least work per key); or 4-bit codes
-// and scales as bf16 values (many rows: the least work per score).
-enum { kFromBf16, kFromCodes, kFromValues };
-
-// Two E2M1 codes as f16, times the block's scale, as bf16 (exact within bf16's range).
-__device__ __forceinline__ uint32_t scaled_bf16(uint32_t h2, float f) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    return pack_bf16x2(x.x * f, x.y * f);
-}
+// Up to this many query rows (of the longest q_len) this kernel runs; above,
+// the one on tcgen05.
+constexpr int kFewRows = 32;
 
 // Bytes of a warp's place for 32 keys' rows (and scale words).
-template <int D, int FROM>
+template <int D, bool MX4>
 __host__ __device__ constexpr int weight_stage() {
-    return FROM == kFromBf16 ? 32 * 2 * D : 32 * (D / 2 + 4);
+    return MX4 ? 32 * (D / 2 + 4) : 32 * 2 * D;
 }
 
 // First key (a multiple of 32) of the items of a sequence, and how many items.
@@ -62,22 +55,22 @@ __device__ __forceinline__ int seq_items(const CacheGeom& g, int c, int q, int k
     return (c - first + keys - 1) / keys;
 }
 
-// kQBlock: query rows in shared memory at a time.
-template <int D, int FROM, int kQBlock>
+// K becomes an operand as it is (bf16), or as f16 codes, the block scales
+// applied to the block scores.
+template <int D, bool MX4>
 __global__ void __launch_bounds__(kWeightThreads, 2)
 key_weights_kernel(const __grid_constant__ WeightParams P) {
     constexpr int KB = D / 32;                 // blocks of 32 columns
     constexpr int QROW = 2 * D + kQPad;
     constexpr int MT = 2;                      // 16-key tiles of a warp
     constexpr int kKeys = 32 * kWeightWarps;   // of one item
-    constexpr bool kMx4 = FROM != kFromBf16;
-    constexpr int ROW = kMx4 ? D / 2 : 2 * D;  // bytes of a key's row
+    constexpr int ROW = MX4 ? D / 2 : 2 * D;  // bytes of a key's row
     constexpr int CH = ROW / 16, RPI = 32 / CH;   // its chunks, rows a copy instruction
     extern __shared__ __align__(128) uint8_t smem[];
-    float* off = reinterpret_cast<float*>(smem + kQBlock * QROW);   // -lse * log2 e
-    float* fac = off + kQBlock;                                     // score factor
-    int* pos = reinterpret_cast<int*>(fac + kQBlock);               // query position
-    const uint32_t rows = smem_u32(pos + kQBlock) + (threadIdx.x >> 5) * weight_stage<D, FROM>();
+    float* off = reinterpret_cast<float*>(smem + kFewRows * QROW);   // -lse * log2 e
+    float* fac = off + kFewRows;                                     // score factor
+    int* pos = reinterpret_cast<int*>(fac + kFewRows);               // query position
+    const uint32_t rows = smem_u32(pos + kFewRows) + (threadIdx.x >> 5) * weight_stage<D, MX4>();
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = lane >> 2, t4 = lane & 3;
@@ -160,7 +153,7 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
             cp_async16(rows + r * ROW + chunk_at(r, c) * 16, P.k + (ok ? row * ROW + c * 16 : 0),
                        ok ? 16 : 0, once);
         }
-        if constexpr (kMx4) {
+        if constexpr (MX4) {
             const bool ok = lane < left && (lane < 16 ? oka : okb);
             const int64_t row = (lane < 16 ? ra : rb) + (lane & 15) * g.tok_rows;
             // (head_dim 64: the word that holds the key's two bytes)
@@ -192,14 +185,14 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
         const float before = mine_ok ? *dst : 0.f;
         cp_async_wait<0>();
         __syncwarp();
-        uint32_t a[MT][KB][2][4];              // (kFromCodes: a[..][0][hh] only, the codes)
+        uint32_t a[MT][KB][2][4];              // (4-bit: a[..][0][hh] only, the codes)
         uint32_t e[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const int r = 16 * mt + 8 * hh + gr;
-                if constexpr (kMx4) {
+                if constexpr (MX4) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb)
                         asm volatile("ld.shared.b32 %0, [%1];"
@@ -233,157 +226,128 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
                 next_page = look_up(next);
             }
         }
-        if constexpr (FROM == kFromValues) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        e2m1x8_to_f16(a[mt][kb][0][hh], a[mt][kb][0][hh], a[mt][kb][0][2 + hh],
-                                      a[mt][kb][1][hh], a[mt][kb][1][2 + hh]);
-                        const float f = e8m0_to_f32((e[mt][hh] >> (8 * kb)) & 255u);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t& v = a[mt][kb][x >> 1][2 * (x & 1) + hh];
-                            v = scaled_bf16(v, f);
-                        }
-                    }
-        }
         float w[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) w[mt][0] = w[mt][1] = 0.f;
         const bool clear =
             tok + 16 * MT - 1 <= c - q && (g.window == 0 || tok > c - 1 - g.window);
-        for (int r0 = 0; r0 < R; r0 += kQBlock) {
-            const int nr = min(kQBlock, R - r0);
-            if (fresh || R > kQBlock) {
-                // ---- query rows r0 .. r0 + nr, padded to a multiple of 8
-                __syncthreads();
-                bool none = false;
-                for (int r = warp; r < ((nr + 7) & ~7); r += kWeightWarps) {
-                    float x[D / 32];
-                    const bool real = r < nr && rows_ok;
-                    const int64_t qrow = real ? (int64_t)(done.row0 + (r0 + r) / g.G) * g.Hq +
-                                                    done.hk * g.G + (r0 + r) % g.G
-                                              : 0;
-                    float top = 0.f;
+        if (fresh) {
+            // ---- the item's query rows, padded to a multiple of 8
+            __syncthreads();
+            bool none = false;
+            for (int r = warp; r < ((R + 7) & ~7); r += kWeightWarps) {
+                float x[D / 32];
+                const bool real = r < R && rows_ok;
+                const int64_t qrow = real ? (int64_t)(done.row0 + r / g.G) * g.Hq + done.hk * g.G + r % g.G
+                                          : 0;
+                float top = 0.f;
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j) {
-                        const uint32_t v =
-                            real ? reinterpret_cast<const uint32_t*>(P.q + qrow * D)[lane + 32 * j]
-                                 : 0u;
-                        x[2 * j] = __uint_as_float(v << 16);
-                        x[2 * j + 1] = __uint_as_float(v & 0xffff0000u);
-                        top = fmaxf(top, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
-                    }
-                    float factor = g.sm_scale * kLog2e;
-                    float down = 1.f;
-                    if constexpr (FROM == kFromCodes) {
-                        // f16 rows with a power of two taken out (as in pa_decode_mx4)
-                        const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-                        const int ex = max(8, min(247, (int)(tb >> 23)));
-                        down = __uint_as_float((uint32_t)(254 - ex) << 23);
-                        factor *= __uint_as_float((uint32_t)ex << 23);
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-                        *reinterpret_cast<uint32_t*>(smem + r * QROW + 4 * (lane + 32 * j)) =
-                            FROM == kFromCodes ? pack_f16x2(x[2 * j] * down, x[2 * j + 1] * down)
-                                               : pack_bf16x2(x[2 * j], x[2 * j + 1]);
-                    const float v = real ? P.lse[qrow] : -INFINITY;
-                    none |= v == -INFINITY;
-                    if (lane == 0) {
-                        off[r] = -v * kLog2e;
-                        fac[r] = factor;
-                        pos[r] = v == -INFINITY ? -1 : c - q + (r0 + r) / g.G;
-                    }
+                for (int j = 0; j < D / 64; ++j) {
+                    const uint32_t v =
+                        real ? reinterpret_cast<const uint32_t*>(P.q + qrow * D)[lane + 32 * j]
+                             : 0u;
+                    x[2 * j] = __uint_as_float(v << 16);
+                    x[2 * j + 1] = __uint_as_float(v & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
                 }
-                blind = __syncthreads_or(none);
-                fresh = false;
+                float factor = g.sm_scale * kLog2e;
+                float down = 1.f;
+                if constexpr (MX4) {
+                    // f16 rows with a power of two taken out (as in pa_decode_mx4)
+                    const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                    const int ex = max(8, min(247, (int)(tb >> 23)));
+                    down = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    factor *= __uint_as_float((uint32_t)ex << 23);
+                }
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+                    *reinterpret_cast<uint32_t*>(smem + r * QROW + 4 * (lane + 32 * j)) =
+                        MX4 ? pack_f16x2(x[2 * j] * down, x[2 * j + 1] * down)
+                            : pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                const float v = real ? P.lse[qrow] : -INFINITY;
+                none |= v == -INFINITY;
+                if (lane == 0) {
+                    off[r] = -v * kLog2e;
+                    fac[r] = factor;
+                    pos[r] = v == -INFINITY ? -1 : c - q + r / g.G;
+                }
             }
-            const uint32_t qbase = smem_u32(smem) + gr * QROW + t4 * 16;
-            const float factor = g.sm_scale * kLog2e;
-            // eight rows against the warp's keys
-            auto score = [&](int nt, auto mask) {
-                constexpr int U = 1;
-                constexpr bool masked = decltype(mask)::value;
-                float s[U][MT][4];
+            blind = __syncthreads_or(none);
+            fresh = false;
+        }
+        const uint32_t qbase = smem_u32(smem) + gr * QROW + t4 * 16;
+        const float factor = g.sm_scale * kLog2e;
+        // eight rows against the warp's keys
+        auto score = [&](int nt, auto mask) {
+            constexpr bool masked = decltype(mask)::value;
+            float s[MT][4];
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KB; ++kb) {
+                uint32_t b0, b1, b2, b3;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                             : "r"(qbase + nt * QROW + kb * 64));
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        uint32_t b0, b1, b2, b3;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
-                                     : "r"(qbase + (nt + 8 * u) * QROW + kb * 64));
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            float* d = s[u][mt];
-                            if constexpr (FROM == kFromCodes) {
-                                // converted anew for every eight rows (few are
-                                // more than that): as f16 for all of them, 128
-                                // registers a thread do not hold a row
-                                uint32_t h[2][4], ex[2];
-#pragma unroll
-                                for (int hh = 0; hh < 2; ++hh) {
-                                    uint32_t code = a[mt][kb][0][hh];
-                                    ex[hh] = e[mt][hh];
-                                    asm volatile("" : "+r"(code), "+r"(ex[hh]));
-                                    e2m1x8_to_f16(code, h[0][hh], h[0][2 + hh], h[1][hh],
-                                                  h[1][2 + hh]);
-                                }
-                                float x[4];
-                                mma_f16_first(x, h[0], b0, b1);
-                                mma_f16_16816(x, h[1], b2, b3);
-#pragma unroll
-                                for (int hh = 0; hh < 2; ++hh) {
-                                    const float f = e8m0_to_f32((ex[hh] >> (8 * kb)) & 255u);
-#pragma unroll
-                                    for (int v = 2 * hh; v < 2 * hh + 2; ++v)
-                                        d[v] = kb == 0 ? x[v] * f : fmaf(x[v], f, d[v]);
-                                }
-                            } else {
-                                if (kb == 0)
-                                    mma_bf16_first(d, a[mt][kb][0], b0, b1);
-                                else
-                                    mma_bf16_16816(d, a[mt][kb][0], b0, b1);
-                                mma_bf16_16816(d, a[mt][kb][1], b2, b3);
-                            }
-                        }
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = nt + 8 * u + 2 * t4;
-                    const float2 of = *reinterpret_cast<const float2*>(off + r);
-                    float2 fc = make_float2(factor, factor);
-                    if constexpr (FROM == kFromCodes)
-                        fc = *reinterpret_cast<const float2*>(fac + r);
-                    int2 pp = make_int2(0, 0);
-                    if constexpr (masked) pp = *reinterpret_cast<const int2*>(pos + r);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt) {
+                    float* d = s[mt];
+                    if constexpr (MX4) {
+                        // converted anew for every eight rows: a row's codes as
+                        // f16 beside all else do not fit 128 registers
+                        // (64 sequences, 8 rows: 98 us, with 300 bytes spilled 108)
+                        uint32_t h[2][4], ex[2];
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
-                            const float* d = s[u][mt] + 2 * hh;
-                            float p0 = ex2(fmaf(d[0], fc.x, of.x));
-                            float p1 = ex2(fmaf(d[1], fc.y, of.y));
-                            if constexpr (masked) {
-                                const int j = tok + 16 * mt + 8 * hh + gr;
-                                if (j > pp.x || (g.window > 0 && j <= pp.x - g.window)) p0 = 0.f;
-                                if (j > pp.y || (g.window > 0 && j <= pp.y - g.window)) p1 = 0.f;
-                            }
-                            w[mt][hh] += p0 + p1;
+                            uint32_t code = a[mt][kb][0][hh];
+                            ex[hh] = e[mt][hh];
+                            asm volatile("" : "+r"(code), "+r"(ex[hh]));
+                            e2m1x8_to_f16(code, h[0][hh], h[0][2 + hh], h[1][hh], h[1][2 + hh]);
                         }
+                        float x[4];
+                        mma_f16_first(x, h[0], b0, b1);
+                        mma_f16_16816(x, h[1], b2, b3);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const float f = e8m0_to_f32((ex[hh] >> (8 * kb)) & 255u);
+#pragma unroll
+                            for (int v = 2 * hh; v < 2 * hh + 2; ++v)
+                                d[v] = kb == 0 ? x[v] * f : fmaf(x[v], f, d[v]);
+                        }
+                    } else {
+                        if (kb == 0)
+                            mma_bf16_first(d, a[mt][kb][0], b0, b1);
+                        else
+                            mma_bf16_16816(d, a[mt][kb][0], b0, b1);
+                        mma_bf16_16816(d, a[mt][kb][1], b2, b3);
+                    }
                 }
-            };
-            if (!clear || blind) {
-#pragma unroll 1
-                for (int nt = 0; nt < nr; nt += 8) score(nt, std::true_type());
-            } else {
-#pragma unroll 1
-                for (int nt = 0; nt < nr; nt += 8) score(nt, std::false_type());
             }
+            const int r = nt + 2 * t4;
+            const float2 of = *reinterpret_cast<const float2*>(off + r);
+            float2 fc = make_float2(factor, factor);
+            if constexpr (MX4) fc = *reinterpret_cast<const float2*>(fac + r);
+            int2 pp = make_int2(0, 0);
+            if constexpr (masked) pp = *reinterpret_cast<const int2*>(pos + r);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float* d = s[mt] + 2 * hh;
+                    float p0 = ex2(fmaf(d[0], fc.x, of.x));
+                    float p1 = ex2(fmaf(d[1], fc.y, of.y));
+                    if constexpr (masked) {
+                        const int j = tok + 16 * mt + 8 * hh + gr;
+                        if (j > pp.x || (g.window > 0 && j <= pp.x - g.window)) p0 = 0.f;
+                        if (j > pp.y || (g.window > 0 && j <= pp.y - g.window)) p1 = 0.f;
+                    }
+                    w[mt][hh] += p0 + p1;
+                }
+        };
+        if (!clear || blind) {
+#pragma unroll 1
+            for (int nt = 0; nt < R; nt += 8) score(nt, std::true_type());
+        } else {
+#pragma unroll 1
+            for (int nt = 0; nt < R; nt += 8) score(nt, std::false_type());
         }
         // ---- over the four lanes that hold a key's rows; lane (gr, t4) adds key 8 t4 + gr
         float mine = 0.f;
@@ -402,11 +366,11 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
 }
 
 // Shared-memory opt-in and the CTAs an SM holds, once per device.
-template <int D, int FROM, int kQBlock>
+template <int D, bool MX4>
 cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) {
-    constexpr int smem = kQBlock * (2 * D + kQPad) + 3 * kQBlock * 4 +
-                         kWeightWarps * weight_stage<D, FROM>();
-    auto kern = key_weights_kernel<D, FROM, kQBlock>;
+    constexpr int smem = kFewRows * (2 * D + kQPad) + 3 * kFewRows * 4 +
+                         kWeightWarps * weight_stage<D, MX4>();
+    auto kern = key_weights_kernel<D, MX4>;
     static std::mutex mu;
     static int per_sm[64] = {0};
     int dev = 0, n = 0;
@@ -429,17 +393,20 @@ cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) 
     return cudaGetLastError();
 }
 
-// Up to this many query rows (of the longest q_len) the kernel for few rows
-// runs: a small place for Q, 4-bit block scores scaled in fp32.  Above, 128 rows
-// of Q at a time, and 4-bit keys turned into bf16 values once.
-constexpr int kFewRows = 32;
-
 }  // namespace
+
+cudaError_t launch_key_weights_many(const CacheGeom& g, bool mx4, const void* q, const void* k,
+                                    const void* ks, const int32_t* table, const int32_t* ctx,
+                                    const int32_t* ql, const float* lse, float* weights,
+                                    int32_t* err, int sms, cudaStream_t stream);
 
 cudaError_t launch_key_weights(const CacheGeom& g, bool mx4, const void* q, const void* k,
                                const void* ks, const int32_t* table, const int32_t* ctx,
                                const int32_t* ql, const float* lse, float* weights, int32_t* err,
                                int sms, cudaStream_t stream) {
+    if (g.G * g.max_q_len > kFewRows)
+        return launch_key_weights_many(g, mx4, q, k, ks, table, ctx, ql, lse, weights, err, sms,
+                                       stream);
     WeightParams P;
     P.g = g;
     P.q = (const __nv_bfloat16*)q;
@@ -451,19 +418,11 @@ cudaError_t launch_key_weights(const CacheGeom& g, bool mx4, const void* q, cons
     P.lse = lse;
     P.weights = weights;
     P.err = err;
-    const bool many = g.G * g.max_q_len > kFewRows;
-    if (g.D == 128) {
-        if (!mx4)
-            return many ? launch_weights<128, kFromBf16, 128>(P, sms, stream)
-                        : launch_weights<128, kFromBf16, 32>(P, sms, stream);
-        return many ? launch_weights<128, kFromValues, 128>(P, sms, stream)
-                    : launch_weights<128, kFromCodes, 32>(P, sms, stream);
-    }
-    if (!mx4)
-        return many ? launch_weights<64, kFromBf16, 128>(P, sms, stream)
-                    : launch_weights<64, kFromBf16, 32>(P, sms, stream);
-    return many ? launch_weights<64, kFromValues, 128>(P, sms, stream)
-                : launch_weights<64, kFromCodes, 32>(P, sms, stream);
+    if (g.D == 128)
+        return mx4 ? launch_weights<128, true>(P, sms, stream)
+                   : launch_weights<128, false>(P, sms, stream);
+    return mx4 ? launch_weights<64, true>(P, sms, stream)
+               : launch_weights<64, false>(P, sms, stream);
 }
 
 }  // namespace pa

@@ -412,6 +412,46 @@ def test_weights_many_sequences_and_bad_input():
     assert same(got, good)
 
 
+@pytest.mark.parametrize("kv", [BF16, MX4])
+def test_weights_of_many_rows_that_see_nothing_and_of_nan_keys(kv):
+    """As above with 36 and 200 query rows a head (lengths that differ, one
+    without queries), and a bad page."""
+    case = R.Case([80, 300, 41, 700], [9, 50, 0, 17], heads=8, kv_heads=2, dim=128, kv=kv, seed=24)
+    lse = R.attention(case)[1].float().double()
+    lse[1, 2] = -math.inf
+    lse[20] = -math.inf
+    check_weights(case, lse)
+    for b, key in ((0, 79), (1, 299), (3, 690)):     # seen by the last queries only
+        pg, s = int(case.table[b, key // case.page]), key % case.page
+        if kv == BF16:
+            case.k[pg, s, 1, 5] = math.nan
+        else:
+            case.ks[pg, s, 1, 0] = 255
+    check_weights(case, lse)
+    zero = torch.zeros((case.num_pages, 2, case.page))
+    good, err = run_weights(case, lse, zero)
+    assert err == 0
+    page = int(case.table[3, 2])
+    case.table[3, 2] = case.num_pages
+    got, err = run_weights(case, lse, zero)
+    assert err == B.PA_DEV_BAD_PAGE
+    good[page] = 0
+    assert same(got, good)
+
+
+@pytest.mark.parametrize("kv,dim,heads,kv_heads,page,ctx,ql,window", [
+    (BF16, 128, 7, 1, 32, [1000, 5, 513], [300, 5, 129], 0),      # all chunks, partly masked
+    (MX4, 64, 6, 3, 16, [900, 257], [200, 257], 100),             # a window shorter than the tile
+    (BF16, 64, 2, 2, 64, [2000], [700], 33),
+    (MX4, 128, 16, 1, 256, [256, 1024], [256, 8], 0),
+    (MX4, 128, 4, 2, 16, [130] * 200, [20] * 200, 0),             # more items than CTAs
+    (BF16, 128, 33, 1, 16, [1, 300, 1], [1, 1, 1], 0),            # one token, 33 heads
+])
+def test_weights_of_many_rows(kv, dim, heads, kv_heads, page, ctx, ql, window):
+    check_weights(R.Case(ctx, ql, heads=heads, kv_heads=kv_heads, dim=dim, page=page,
+                         kv=kv, window=window, seed=25))
+
+
 # -------------------------------------------------------------------- evict
 
 def run_evict(case, w, budget, first, recent, dst, **kw):
