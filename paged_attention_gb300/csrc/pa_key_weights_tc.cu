@@ -1,16 +1,19 @@
 // pa_key_weights_tc.cu -- pa_key_weights for many query rows, on tcgen05:
 //     w_j += sum_r exp2(f q_r . k_j - lse_r log2 e).
 //
-// The scores of 256 keys (two accumulators of 128) by up to 128 query rows are
+// The scores of 256 keys (two halves of 128) by up to 128 query rows are
 // computed transposed, keys as the rows of the product.  A key is then a lane
 // of tensor memory: one thread sums all its exponentials, over all chunks of
 // query rows, with no exchange between threads and no sum over keys to join.
-// K stays in shared memory for all rows of an item; Q comes in chunks of 128
-// rows, and stays from item to item where a head's rows fit in one chunk.
+// 4-bit keys are turned into bf16 values by the thread that holds their lane,
+// which stores them into tensor memory: the product then reads only Q from
+// shared memory (whose bandwidth bound it with both operands there).  bf16 keys
+// stay in shared memory.  Q comes in chunks of 128 rows, and stays from item to
+// item where a head's rows fit in one chunk.
 //
-// Roles (21 warps): 8 take the accumulators (two groups of four, one for each
-// 128 keys), 8 bring K (bf16 by cp.async; 4-bit codes through registers, as
-// bf16 values), 4 bring Q, 1 issues the products.  All waits are bounded.
+// Roles: two groups of 4 warps take the accumulators, one group for each half;
+// two groups of 4 bring K, 2 warps bring Q, 2 issue the products.  All waits
+// are bounded.
 #include <mutex>
 
 #include "pa_cache_mma.cuh"
@@ -20,8 +23,10 @@ namespace pa {
 namespace {
 
 constexpr int kTileKeys = 256, kChunk = 128;
-constexpr int kEpiWarps = 8, kKWarps = 8, kQWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + kKWarps + kQWarps + 1);
+constexpr int kEpiWarps = 8, kKWarps = 8, kQWarps = 2;
+constexpr int kMmaWarp = kEpiWarps + kKWarps + kQWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 2);
+constexpr int kAccs = 3;        // accumulators of 128 x 128, taken in turn
 constexpr int kQRing = 4;       // of row offsets, positions and full barriers (Q itself has 2)
 
 struct ManyParams {
@@ -37,17 +42,23 @@ struct ManyParams {
     int32_t* err;
 };
 
-template <int D>
+template <int D, bool MX4>
 struct ManySmem {
-    static constexpr int kKBlock = kTileKeys * 128;     // 64 columns of K
+    static constexpr int kKBlock = 128 * 128;           // 128 keys, 64 columns of K
     static constexpr int kQBlock = kChunk * 128;
-    static constexpr int kK = 0;                        // two slots
-    static constexpr int kQ = kK + 2 * (D / 64) * kKBlock;
+    static constexpr int kSlots = MX4 ? 1 : 2;          // of a half of K
+    static constexpr int kHalf = (D / 64) * kKBlock;
+    // bf16: K's slots [slot][half]; 4-bit: each K warp's ring of places for 32
+    // keys' rows and scale words
+    static constexpr int kRing = 3, kPlace = 32 * (D / 2 + 4);
+    static constexpr int kK = 0;
+    static constexpr int kQ = kK + (MX4 ? (kKWarps * kRing * kPlace + 1023) / 1024 * 1024
+                                        : kSlots * 2 * kHalf);
     static constexpr int kOff = kQ + 2 * (D / 64) * kQBlock;
     static constexpr int kPos = kOff + kQRing * kChunk * 4;
     static constexpr int kBlind = kPos + kQRing * kChunk * 4;
-    static constexpr int kBars = kBlind + kQRing * kQWarps * 4;
-    static constexpr int kNumBars = 2 + 2 + kQRing + 2 + 4 + 4 + 1;
+    static constexpr int kBars = kBlind + kQRing * 16;
+    static constexpr int kNumBars = 4 + 4 + kQRing + 2 + 4 * kAccs + 1;
     static constexpr int kTmem = kBars + 8 * kNumBars;
     static constexpr int kBytes = kTmem + 16 + 1024;    // and the alignment of the slots
 };
@@ -66,30 +77,46 @@ __device__ __forceinline__ int many_chunks(const CacheGeom& g, int q) {
 
 // The CTA's items -- (sequence, KV head, tile of keys) -- in order.  Their cost
 // is their chunks of rows; an item belongs to the CTA in whose share of the
-// line it starts.
+// line it starts.  Within the tiles of one head, the next item is a matter of
+// two additions: every role walks the items by itself, many of them in a single
+// thread or warp, where each instruction costs its latency.
 struct Walk {
-    int64_t at, end;           // position of the item, end of the CTA's share
-    int b, hk, tile, n, c, q, first, row0;
+    int left;                  // items of this head that are the CTA's, this one included
+    int key0;                  // first key of the tile
+    int nch;                   // chunks of the head's rows
     bool same;                 // the item before had the same rows, in one chunk
+    int b, hk, c, q, row0;
+    int64_t at, end;           // position behind the items of this head; end of the share
 
-    __device__ __forceinline__ bool more() const { return at < end; }
-    __device__ __forceinline__ void read(const ManyParams& P) {
-        c = P.ctx[b];
-        q = P.ql[b];
-        n = many_tiles(P.g, c, q, first);
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    // enter a head at one of its n tiles, whose position is `at`
+    __device__ __forceinline__ void enter(int tile, int n, int first) {
+        const int64_t mine = (end - at + nch - 1) / nch;
+        left = (int)min((int64_t)(n - tile), mine);
+        key0 = first + tile * kTileKeys;
+        at += (int64_t)left * nch;
+        same = false;
     }
-    // the next sequence with items; false when there is none
-    __device__ __forceinline__ bool next_seq(const ManyParams& P) {
-        do {
-            row0 += clamp_q(P.g, q);
-            if (++b >= P.g.B) {
-                at = end;
-                return false;
-            }
-            read(P);
-        } while (n == 0);
-        hk = tile = 0;
-        return true;
+    // the next head with items of this CTA
+    __device__ __forceinline__ void next_head(const ManyParams& P) {
+        const CacheGeom& g = P.g;
+        left = 0;
+        if (at >= end) return;
+        if (++hk == g.Hkv) {
+            hk = 0;
+            do {
+                row0 += clamp_q(g, q);
+                if (++b >= g.B) return;
+                c = P.ctx[b];
+                q = P.ql[b];
+                int f;
+                nch = many_tiles(g, c, q, f);
+            } while (nch == 0);
+        }
+        int first;
+        const int n = many_tiles(g, c, q, first);
+        nch = many_chunks(g, q);
+        enter(0, n, first);
     }
     __device__ __forceinline__ void init(const ManyParams& P, int lane) {
         const CacheGeom& g = P.g;
@@ -98,48 +125,50 @@ struct Walk {
             const int q_ = P.ql[x];
             return (int64_t)g.Hkv * many_tiles(g, P.ctx[x], q_, f) * many_chunks(g, q_);
         };
+        left = 0;
         same = false;
         const int64_t total = flat_total(g.B, lane, cost);
         const int64_t N = gridDim.x;
-        const int64_t lo = total * blockIdx.x / N;
+        at = total * blockIdx.x / N;
         end = total * (blockIdx.x + 1) / N;
-        at = end;
-        if (lo >= end) return;
+        if (at >= end) return;
         int64_t start;
-        b = flat_find(g.B, lane, lo, cost, [&](int x) { return clamp_q(g, P.ql[x]); }, start, row0);
-        read(P);
-        const int w = many_chunks(g, q);
-        const int64_t item = (lo - start + w - 1) / w;
-        at = start + item * w;
-        if (item < (int64_t)g.Hkv * n) {
-            hk = (int)(item / n);
-            tile = (int)(item % n);
-        } else if (at < end) {
-            next_seq(P);
+        b = flat_find(g.B, lane, at, cost, [&](int x) { return clamp_q(g, P.ql[x]); }, start, row0);
+        c = P.ctx[b];
+        q = P.ql[b];
+        int first;
+        const int n = many_tiles(g, c, q, first);
+        nch = many_chunks(g, q);
+        const int64_t item = (at - start + nch - 1) / nch;
+        at = start + item * nch;
+        hk = (int)(item / n);
+        if (at >= end) return;
+        if (hk < g.Hkv) {
+            enter((int)(item % n), n, first);
+        } else {
+            hk = g.Hkv - 1;
+            next_head(P);
         }
     }
     __device__ __forceinline__ void advance(const ManyParams& P) {
-        const int w = many_chunks(P.g, q);
-        at += w;
-        same = w == 1;
-        if (++tile < n) return;
-        tile = 0;
-        same = false;
-        if (++hk < P.g.Hkv) return;
-        if (at < end) next_seq(P);
+        key0 += kTileKeys;
+        same = nch == 1;
+        if (--left == 0) next_head(P);
     }
-    __device__ __forceinline__ int key0() const { return first + tile * kTileKeys; }
     // chunks of rows that see some key of the tile
     __device__ __forceinline__ int2 chunks(const CacheGeom& g) const {
-        const int n_ = many_chunks(g, q), p0 = c - q;
-        int lo = 0, hi = n_;
-        if (key0() > p0) lo = (int)((int64_t)(key0() - p0) * g.G / kChunk);
-        if (g.window > 0) {
-            // the last query that sees the tile's last key
-            const int64_t last = (int64_t)key0() + kTileKeys - 1 + g.window - 1 - p0;
-            if (last < q - 1) hi = (int)((max(last, (int64_t)0) * g.G + g.G - 1) / kChunk) + 1;
+        int lo = 0, hi = nch;
+        if (nch > 1) {
+            const int p0 = c - q;
+            if (key0 > p0) lo = (int)((int64_t)(key0 - p0) * g.G / kChunk);
+            if (g.window > 0) {
+                // the last query that sees the tile's last key
+                const int64_t last = (int64_t)key0 + kTileKeys - 1 + g.window - 1 - p0;
+                if (last < q - 1) hi = (int)((max(last, (int64_t)0) * g.G + g.G - 1) / kChunk) + 1;
+            }
+            hi = max(hi, lo + 1);
         }
-        return make_int2(lo, max(hi, lo + 1));
+        return make_int2(lo, hi);
     }
 };
 
@@ -180,58 +209,44 @@ struct ScaledCodes {
     }
 };
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 ldg_once16(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::64B.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 template <int D, bool MX4>
 __global__ void __launch_bounds__(kThreads, 1)
 key_weights_many_kernel(const __grid_constant__ ManyParams P) {
-    using S = ManySmem<D>;
+    using S = ManySmem<D, MX4>;
     constexpr int NB = D / 64;                  // blocks of 64 columns
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     float* off = reinterpret_cast<float*>(smem + S::kOff);      // -lse log2 e
     int* pos = reinterpret_cast<int*>(smem + S::kPos);          // query position, -1: sees nothing
-    int* blind = reinterpret_cast<int*>(smem + S::kBlind);
-    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
-    uint64_t* k_empty = k_full + 2;
-    uint64_t* q_full = k_empty + 2;
+    int* blind = reinterpret_cast<int*>(smem + S::kBlind);      // of 32 rows each
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kBars);    // [slot][half]
+    uint64_t* k_empty = k_full + 4;
+    uint64_t* q_full = k_empty + 4;
     uint64_t* q_empty = q_full + kQRing;
-    uint64_t* s_full = q_empty + 2;             // [buffer][half]
-    uint64_t* s_empty = s_full + 4;
-    uint64_t* done = s_empty + 4;
+    uint64_t* s_full = q_empty + 2;
+    uint64_t* s_empty = s_full + 2 * kAccs;                             // [half][accumulator]
+    uint64_t* done = s_empty + 2 * kAccs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kTmem);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 32 * kKWarps);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&q_empty[i], 1);
-        }
-        for (int i = 0; i < kQRing; ++i) mbar_init(&q_full[i], 32 * kQWarps);
         for (int i = 0; i < 4; ++i) {
+            mbar_init(&k_full[i], 128);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&q_empty[i], 2);
+        for (int i = 0; i < kQRing; ++i) mbar_init(&q_full[i], 32 * kQWarps);
+        for (int i = 0; i < 2 * kAccs; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], 128);
         }
-        mbar_init(done, 1);
+        mbar_init(done, 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    constexpr int kMmaWarp = kEpiWarps + kKWarps + kQWarps;
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -243,6 +258,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t kKCol = kAccs * kChunk;  // 4-bit: columns of K's halves, D / 2 each
 
     // true, or the CTA gives up
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -258,46 +274,44 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
 
     if (warp < kEpiWarps) {
         // ------------------------------------------------ exponentials and sums
-        const int half = warp >> 2, quad = warp & 3;
-        const int my = 128 * half + 32 * quad;          // of the tile's keys
+        // Group grp has half grp of every tile; the product of chunk n of all
+        // is in accumulator (2 n + half) % kAccs, after the other half's of
+        // chunk n - 2 + half.  (Barriers of their own for the halves: their
+        // order in time is not fixed.)
+        const int grp = warp >> 2, quad = warp & 3;
+        const int my = 128 * grp + 32 * quad;
         const float factor = g.sm_scale * kLog2e;
         const uint64_t factor2 = pair2(factor);
-        auto page_of = [&](const Walk& x) -> int {
-            const int key = x.key0() + my + lane;
-            return key < x.c ? P.table[(int64_t)x.b * g.mpps + (key >> g.ps_shift)] : -1;
-        };
         uint32_t fill = 0, n = 0;
-        int page = t.more() ? page_of(t) : -1;
         bool ok = true;
-        while (ok && t.more()) {
-            Walk next = t;
-            next.advance(P);
-            const int next_page = next.more() ? page_of(next) : -1;
-            const int tok = t.key0() + my, key = tok + lane, p0 = t.c - t.q;
-            const bool there = t.key0() + 128 * half < t.c;
+        for (; ok && t.more(); t.advance(P)) {
+            const int tok = t.key0 + my, key = tok + lane, p0 = t.c - t.q;
+            const bool there = t.key0 + 128 * grp < t.c;
+            const int page =
+                key < t.c ? P.table[(int64_t)t.b * g.mpps + (key >> g.ps_shift)] : -1;
             const int R = g.G * t.q;
             const int2 ch = t.chunks(g);
             uint64_t sum0 = 0, sum1 = 0;
             if (!t.same) fill += 1;
             for (int k = ch.x; k < ch.y; ++k, ++n) {
                 if (k > ch.x) fill += 1;
-                const uint32_t f = fill - 1;
+                const uint32_t ring = (fill - 1) % kQRing, buf = (2 * n + grp) % kAccs;
                 const int nr = min(kChunk, R - k * kChunk);
-                const int buf = n & 1;
-                ok = warp_wait(&s_full[2 * buf + half], (n >> 1) & 1) &&
-                     warp_wait(&q_full[f % kQRing], (f / kQRing) & 1);
+                ok = warp_wait(&s_full[grp * kAccs + buf], (n / kAccs) & 1) &&
+                     warp_wait(&q_full[ring], ((fill - 1) / kQRing) & 1);
                 if (!ok) break;
                 tc_fence_after();
+                const float* of = off + ring * kChunk;
+                const int* ps = pos + ring * kChunk;
+                const int4 bl = *reinterpret_cast<const int4*>(blind + ring * 4);
+                // all of the chunk's queries see all of the warp's keys
+                const bool clear = (bl.x | bl.y | bl.z | bl.w) == 0 &&
+                                   (tok + 31 <= p0 || tok + 31 <= p0 + k * kChunk / g.G) &&
+                                   (g.window == 0 ||
+                                    tok > p0 + (k * kChunk + nr - 1) / g.G - g.window);
+                const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + buf * kChunk;
                 if (there) {
-                    const float* of = off + (f % kQRing) * kChunk;
-                    const int* ps = pos + (f % kQRing) * kChunk;
-                    const int4 bl = *reinterpret_cast<const int4*>(blind + (f % kQRing) * kQWarps);
-                    const int lo_pos = p0 + k * kChunk / g.G;
-                    const int hi_pos = p0 + (k * kChunk + nr - 1) / g.G;
-                    const bool clear = (bl.x | bl.y | bl.z | bl.w) == 0 && tok + 31 <= lo_pos &&
-                                       (g.window == 0 || tok > hi_pos - g.window);
-                    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) +
-                                         (uint32_t)(2 * half + buf) * kChunk;
+#pragma unroll 1
                     for (int c0 = 0; c0 < nr; c0 += 32) {
                         float v[32];
                         tmem_ld32(acc + c0, v);
@@ -327,220 +341,268 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&s_empty[2 * buf + half]);
+                mbar_arrive(&s_empty[grp * kAccs + buf]);
             }
             if (ok && key < t.c && (uint32_t)page < (uint32_t)g.num_pages) {
                 const float2 a = split2(sum0), b = split2(sum1);
                 atomicAdd(P.weights + ((int64_t)page * g.Hkv + t.hk) * g.ps + (key & (g.ps - 1)),
                           (a.x + a.y) + (b.x + b.y));
             }
-            t = next;
-            page = next_page;
         }
     } else if (warp < kEpiWarps + kKWarps) {
         // ------------------------------------------------------------------- K
+        // Group grp brings half grp of every tile, a warp 32 keys of it.
         constexpr int ROW = MX4 ? D / 2 : 2 * D;        // bytes of a key's row
         constexpr int CH = ROW / 16, RPI = 32 / CH, NI = 32 / RPI;
         constexpr int KB = D / 32;
-        const int kw = warp - kEpiWarps;                // keys 32 kw .. 32 kw + 31
+        const int grp = (warp - kEpiWarps) >> 2, quad = warp & 3;
+        const int my = 128 * grp + 32 * quad;
         const int page_rows = g.ps * g.Hkv;
-        auto look_up = [&](const Walk& x) -> int2 {     // the pages of two runs of 16 keys
+        const int c16 = lane % CH, lr = lane / CH;      // this lane's 16 bytes, and row of RPI
+        uint64_t once;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        // the pages of the warp's two runs of 16 keys; -1: no keys
+        auto look_up = [&](const Walk& x) -> int2 {
             const int32_t* row = P.table + (int64_t)x.b * g.mpps;
-            const int key = x.key0() + 32 * kw;
+            const int key = x.key0 + my;
             int2 p = make_int2(-1, -1);
             if (key < x.c) p.x = p.y = row[key >> g.ps_shift];
             if (g.ps == 16) p.y = key + 16 < x.c ? row[(key >> 4) + 1] : -1;
             return p;
         };
-        const int c16 = lane % CH;                      // this lane's 16 bytes of a row
-        // row r of the warp's 32: its index, or -1
-        auto row_at = [&](const Walk& x, int2 p, int r) -> int64_t {
-            const int key = x.key0() + 32 * kw;
-            const int pg = r < 16 ? p.x : p.y;
-            if (key + r >= x.c || (uint32_t)pg >= (uint32_t)g.num_pages) return -1;
-            return (int64_t)pg * page_rows + (int64_t)((key + r) & (g.ps - 1)) * g.tok_rows +
-                   (int64_t)x.hk * g.head_rows;
+        // Offsets in K of the two runs' first rows.  Keys that do not exist, or
+        // whose page does not, get rows that do: their sums go nowhere.
+        struct Runs {
+            int64_t a, b;
         };
-        auto check_pages = [&](const Walk& x, int2 p) {
-            const int left = x.c - (x.key0() + 32 * kw);
-            if (lane == 0 && ((left > 0 && (uint32_t)p.x >= (uint32_t)g.num_pages) ||
-                              (left > 16 && (uint32_t)p.y >= (uint32_t)g.num_pages)))
+        auto runs_of = [&](const Walk& x, int2 p) -> Runs {
+            const int key = x.key0 + my, left = x.c - key;
+            const bool oka = (uint32_t)p.x < (uint32_t)g.num_pages;
+            const bool okb = (uint32_t)p.y < (uint32_t)g.num_pages;
+            if (lane == 0 && ((left > 0 && !oka) || (left > 16 && !okb)))
                 flag_error(P.err, PA_DEV_BAD_PAGE);
+            const int head = x.hk * g.head_rows;
+            Runs r;
+            r.a = (int64_t)(oka ? p.x : 0) * page_rows + ((key & (g.ps - 1)) * g.tok_rows + head);
+            r.b = (int64_t)(okb ? p.y : 0) * page_rows +
+                  (((key + 16) & (g.ps - 1)) * g.tok_rows + head);
+            return r;
         };
+        // (offsets within a run of 16 rows fit 32 bits)
+        const uint32_t lane_off = (uint32_t)(lr * g.tok_rows) * ROW + c16 * 16;
+        const uint32_t step = (uint32_t)(RPI * g.tok_rows) * ROW;
         int2 page = t.more() ? look_up(t) : make_int2(-1, -1);
         if constexpr (MX4) {
-            uint4 code[2][NI];
-            uint32_t scale[2][NI];
-            auto load = [&](const Walk& x, int2 p, uint4* cd, uint32_t* sc) {
-                check_pages(x, p);
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    const int64_t row = row_at(x, p, j * RPI + lane / CH);
-                    cd[j] = make_uint4(0, 0, 0, 0);
-                    sc[j] = 127;
-                    if (row >= 0) {
-                        cd[j] = ldg_once16(P.k + row * ROW + c16 * 16);
-                        sc[j] = P.ks[row * KB + c16];
-                    }
-                }
+            // Rows come into the warp's ring by cp.async, coalesced, and from
+            // there to the lane that holds the key: 16 bytes of a row (4 words
+            // of codes, one scale) become 16 words of tensor memory.
+            const uint32_t ring =
+                sbase + S::kK + (uint32_t)(warp - kEpiWarps) * S::kRing * S::kPlace;
+            // where chunk c of row r goes: eight lanes of a load meet no bank twice
+            auto chunk_at = [&](int r, int c) -> int {
+                if constexpr (CH == 4) return c ^ ((r >> 1) & 3);
+                else return c ^ ((r >> 2) & 1);
             };
-            if (t.more()) load(t, page, code[0], scale[0]);
-            uint32_t n = 0;
-            bool ok = true;
-            while (ok && t.more()) {
-                Walk next = t;
-                next.advance(P);
-                if (next.more()) load(next, look_up(next), code[1], scale[1]);
-                const int slot = n & 1;
-                ok = wait(&k_empty[slot], ((n >> 1) & 1) ^ 1);
-                if (!ok) break;
-                const int kb = c16 >> 1, turn = c16 & 2;
-                const uint32_t base = sbase + S::kK + (uint32_t)(slot * NB + kb) * S::kKBlock;
+            uint32_t put = 0, get = 0;
+            Walk ahead = t;                             // the item to fetch
+            auto fetch = [&]() {
+                if (ahead.more()) {
+                    const Runs r = runs_of(ahead, page);
+                    const uint32_t place = ring + put * S::kPlace;
+                    const uint8_t* ka = P.k + r.a * ROW;
+                    const uint8_t* kb = P.k + r.b * ROW;
 #pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    const int r = 32 * kw + j * RPI + lane / CH;
-                    const ScaledCodes tab(scale[0][j]);
-                    uint4 w = code[0][j];
-                    // the second block's lanes store in another order: no bank twice
-                    if (turn) w = make_uint4(w.z, w.w, w.x, w.y);
-                    const uint32_t at = base + r * 128;
-                    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sts128(at + ((((c16 & 1) * 4 + (i ^ turn)) ^ (r & 7)) << 4),
-                               tab.eight(word[i]));
+                    for (int j = 0; j < NI; ++j) {
+                        const int x = j * RPI + lr;
+                        cp_async16(place + x * ROW + chunk_at(x, c16) * 16,
+                                   (j * RPI < 16 ? ka : kb) + (lane_off + (j * RPI & 15) / RPI * step),
+                                   16, once);
+                    }
+                    // (head_dim 64: the word that holds the key's two bytes)
+                    const int64_t row = (lane < 16 ? r.a : r.b) + (lane & 15) * g.tok_rows;
+                    cp_async4(place + 32 * ROW + lane * 4, P.ks + (row * KB & ~(int64_t)3), 4, once);
+                    ahead.advance(P);
+                    if (ahead.more()) page = look_up(ahead);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&k_full[slot]);
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    code[0][j] = code[1][j];
-                    scale[0][j] = scale[1][j];
+                cp_async_commit();
+                put = put + 1 == S::kRing ? 0 : put + 1;
+            };
+            for (int i = 0; i < S::kRing - 1; ++i) fetch();
+            const uint32_t dst = tmem + ((uint32_t)(32 * quad) << 16) + kKCol + grp * (D / 2);
+            for (uint32_t n = 0; t.more(); ++n, t.advance(P)) {
+                cp_async_wait<S::kRing - 2>();
+                __syncwarp();
+                fetch();
+                const uint32_t place = ring + get * S::kPlace;
+                get = get + 1 == S::kRing ? 0 : get + 1;
+                uint32_t e;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(e) : "r"(place + 32 * ROW + lane * 4));
+                if constexpr (D == 64) {
+                    const int slot = (t.key0 + my + lane) & (g.ps - 1);
+                    e >>= ((slot * g.tok_rows + t.hk * g.head_rows) & 1) * 16;
                 }
-                t = next;
-                ++n;
+                auto convert = [&](int c, uint32_t* out) {
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(place + lane * ROW + chunk_at(lane, c) * 16));
+                    const ScaledCodes tab((e >> (8 * c)) & 255u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = tab.eight(w[i]);
+                        out[4 * i] = v.x;
+                        out[4 * i + 1] = v.y;
+                        out[4 * i + 2] = v.z;
+                        out[4 * i + 3] = v.w;
+                    }
+                };
+                // all but the last chunk while the item before is still in use
+                uint32_t out[CH - 1][16];
+#pragma unroll
+                for (int c = 0; c < CH - 1; ++c) convert(c, out[c]);
+                if (!warp_wait(&k_empty[grp], (n & 1) ^ 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < CH - 1; ++c) tmem_st16(dst + 16 * c, out[c]);
+                convert(CH - 1, out[0]);
+                tmem_st16(dst + 16 * (CH - 1), out[0]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&k_full[grp]);
             }
         } else {
-            uint64_t once;
-            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-            uint32_t n = 0;
-            while (t.more()) {
-                Walk next = t;
-                next.advance(P);
-                const int2 next_page = next.more() ? look_up(next) : make_int2(-1, -1);
-                const int slot = n & 1;
-                if (!wait(&k_empty[slot], ((n >> 1) & 1) ^ 1)) break;
-                check_pages(t, page);
-                const uint32_t base = sbase + S::kK + (uint32_t)(slot * NB + (c16 >> 3)) * S::kKBlock;
-#pragma unroll
+            for (uint32_t n = 0; t.more(); ++n) {
+                const uint32_t slot = n & 1;
+                const Runs r = runs_of(t, page);
+                t.advance(P);
+                if (t.more()) page = look_up(t);
+                if (!warp_wait(&k_empty[2 * slot + grp], ((n >> 1) & 1) ^ 1)) break;
+                const uint32_t dst =
+                    sbase + S::kK + (uint32_t)((2 * slot + grp) * NB + (c16 >> 3)) * S::kKBlock;
+                const uint8_t* ka = P.k + r.a * ROW;
+                const uint8_t* kb = P.k + r.b * ROW;
+#pragma unroll 8
                 for (int j = 0; j < NI; ++j) {
-                    const int rw = j * RPI + lane / CH, r = 32 * kw + rw;
-                    const int64_t row = row_at(t, page, rw);
-                    cp_async16(base + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
-                               P.k + (row >= 0 ? row * ROW + c16 * 16 : 0), row >= 0 ? 16 : 0, once);
+                    const int y = 32 * quad + j * RPI + lr;
+                    cp_async16(dst + y * 128 + (((c16 & 7) ^ (y & 7)) << 4),
+                               (j * RPI < 16 ? ka : kb) + (lane_off + (j * RPI & 15) / RPI * step),
+                               16, once);
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
-                mbar_arrive(&k_full[slot]);
-                t = next;
-                page = next_page;
-                ++n;
+                mbar_arrive(&k_full[2 * slot + grp]);
             }
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------------- Q
         constexpr int CH = D / 8, RPI = 32 / CH;
-        const int qw = warp - kEpiWarps - kKWarps;      // rows 32 qw .. 32 qw + 31 of a chunk
+        const int qw = warp - kEpiWarps - kKWarps;
         const int c16 = lane % CH;
         uint64_t keep;
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
         uint32_t fill = 0;
         bool ok = true;
-        while (ok && t.more()) {
-            if (!t.same) {
-                const int R = g.G * t.q, p0 = t.c - t.q;
-                const int2 ch = t.chunks(g);
-                const bool rows_ok = t.row0 + t.q <= g.total_q;
-                for (int k = ch.x; k < ch.y; ++k, ++fill) {
-                    const int slot = fill & 1, ring = fill % kQRing;
-                    ok = warp_wait(&q_empty[slot], ((fill >> 1) & 1) ^ 1);
-                    if (!ok) break;
-                    const int r = k * kChunk + 32 * qw + lane;
+        for (; ok && t.more(); t.advance(P)) {
+            if (t.same) continue;
+            const int R = g.G * t.q, p0 = t.c - t.q;
+            const int2 ch = t.chunks(g);
+            const bool rows_ok = t.row0 + t.q <= g.total_q;
+            for (int k = ch.x; k < ch.y; ++k, ++fill) {
+                const int slot = fill & 1, ring = fill % kQRing;
+                ok = warp_wait(&q_empty[slot], ((fill >> 1) & 1) ^ 1);
+                if (!ok) break;
+                const uint32_t base = sbase + S::kQ + (uint32_t)(slot * NB + (c16 >> 3)) * S::kQBlock;
+                constexpr int kParts = kChunk / 32 / kQWarps;   // of 32 rows, a warp
+                int64_t row[kParts];
+                float l[kParts];
+                int tq[kParts];
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) {
+                    const int r = k * kChunk + 32 * (qw * kParts + i) + lane;
                     const bool real = r < R && rows_ok;
-                    const int tq = r / g.G;
-                    const int64_t row =
-                        real ? (int64_t)(t.row0 + tq) * g.Hq + t.hk * g.G + (r - tq * g.G) : -1;
-                    const uint32_t base =
-                        sbase + S::kQ + (uint32_t)(slot * NB + (c16 >> 3)) * S::kQBlock;
+                    tq[i] = r / g.G;
+                    row[i] = real ? (int64_t)(t.row0 + tq[i]) * g.Hq + t.hk * g.G + (r - tq[i] * g.G)
+                                  : -1;
+                    l[i] = real ? P.lse[row[i]] : -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
 #pragma unroll 4
                     for (int j = 0; j < 32 / RPI; ++j) {
-                        const int rw = j * RPI + lane / CH, rr = 32 * qw + rw;
-                        const int64_t x = __shfl_sync(0xffffffffu, row, rw);
+                        const int rw = j * RPI + lane / CH, rr = 32 * (qw * kParts + i) + rw;
+                        const int64_t x = __shfl_sync(0xffffffffu, row[i], rw);
                         cp_async16(base + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4),
                                    P.q + (x >= 0 ? x * 2 * D + c16 * 16 : 0), x >= 0 ? 16 : 0, keep);
                     }
-                    cp_async_commit();
-                    const float l = real ? P.lse[row] : -INFINITY;
-                    off[ring * kChunk + 32 * qw + lane] = -l * kLog2e;
-                    pos[ring * kChunk + 32 * qw + lane] = l == -INFINITY ? -1 : p0 + tq;
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) {
+                    const int r = 32 * (qw * kParts + i) + lane;
+                    off[ring * kChunk + r] = -l[i] * kLog2e;
+                    pos[ring * kChunk + r] = l[i] == -INFINITY ? -1 : p0 + tq[i];
                     // (rows behind the last are left out by their number)
-                    const bool none = __any_sync(0xffffffffu, r < R && l == -INFINITY);
-                    if (lane == 0) blind[ring * kQWarps + qw] = none;
-                    cp_async_wait<0>();
-                    fence_proxy_async_smem();
-                    mbar_arrive(&q_full[ring]);
+                    const bool none =
+                        __any_sync(0xffffffffu, k * kChunk + r < R && l[i] == -INFINITY);
+                    if (lane == 0) blind[ring * 4 + qw * kParts + i] = none;
                 }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                mbar_arrive(&q_full[ring]);
             }
-            t.advance(P);
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------- products
-        uint32_t fill = 0, n = 0, m = 0;
+        // One thread for each half: what lies between its products (waits,
+        // commits, the next item) is as long as the products.
+        // shared-memory descriptors: rows of 128 bytes with the 128-byte swizzle
+        const int half = warp - kMmaWarp;
+        const uint64_t kdesc =
+            smem_desc_sw128(sbase + S::kK, 0, 1024) + half * (S::kHalf >> 4);
+        const uint64_t qdesc = smem_desc_sw128(sbase + S::kQ, 0, 1024);
+        const uint32_t ktmem = tmem + kKCol + half * (D / 2);
+        uint32_t fill = 0, m = 0, n = 0;
         bool ok = true;
-        while (ok && t.more()) {
-            Walk next = t;
-            next.advance(P);
+        for (; ok && t.more(); ++m) {
             const int R = g.G * t.q;
             const int2 ch = t.chunks(g);
-            const bool keep = next.more() && next.same;     // these rows serve the next item too
-            const uint32_t kbase = sbase + S::kK + (uint32_t)((m & 1) * NB) * S::kKBlock;
-            const bool second = t.key0() + 128 < t.c;
-            ok = wait(&k_full[m & 1], (m >> 1) & 1);
+            const bool same = t.same, there = t.key0 + 128 * half < t.c;
+            t.advance(P);
+            const bool keep = t.more() && t.same;     // these rows serve the next item too
+            const uint32_t kslot = m % S::kSlots;
+            const uint64_t kd = kdesc + kslot * (2 * S::kHalf >> 4);
+            ok = wait(&k_full[2 * kslot + half], (m / S::kSlots) & 1);
             for (int k = ch.x; ok && k < ch.y; ++k, ++n) {
-                if (k > ch.x || !t.same) {
+                if (k > ch.x || !same) {
                     ok = wait(&q_full[fill % kQRing], (fill / kQRing) & 1);
                     if (!ok) break;
                     ++fill;
                 }
-                const uint32_t slot = (fill - 1) & 1;
-                const uint32_t qbase = sbase + S::kQ + slot * NB * S::kQBlock;
-                const int cols = (min(kChunk, R - k * kChunk) + 31) & ~31;
-                const uint32_t idesc = idesc_bf16_f32(128, 0, false, false) | ((uint32_t)(cols >> 3) << 17);
-                const int buf = n & 1;
-                for (int half = 0; half < 2; ++half) {
-                    ok = wait(&s_empty[2 * buf + half], ((n >> 1) & 1) ^ 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (half == 0 || second) {
+                const uint32_t qslot = (fill - 1) & 1;
+                const uint64_t qd = qdesc + qslot * (NB * S::kQBlock >> 4);
+                const int cols = (min(kChunk, R - k * kChunk) + 15) & ~15;
+                const uint32_t idesc =
+                    idesc_bf16_f32(128, 0, false, false) | ((uint32_t)(cols >> 3) << 17);
+                const uint32_t buf = (2 * n + half) % kAccs, before = n - 2 + half;
+                if (n + half >= 2) ok = wait(&s_empty[(half ^ 1) * kAccs + buf], (before / kAccs) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (there) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_ss(tmem + (uint32_t)(2 * half + buf) * kChunk,
-                                      smem_desc_sw128(kbase + (kk >> 2) * S::kKBlock +
-                                                          half * 128 * 128 + (kk & 3) * 32,
-                                                      0, 1024),
-                                      smem_desc_sw128(qbase + (kk >> 2) * S::kQBlock + (kk & 3) * 32,
-                                                      0, 1024),
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t q = qd + (((kk >> 2) * S::kQBlock + (kk & 3) * 32) >> 4);
+                        if constexpr (MX4)
+                            tc_mma_ts(tmem + buf * kChunk, ktmem + kk * 8, q, idesc, kk > 0);
+                        else
+                            tc_mma_ss(tmem + buf * kChunk,
+                                      kd + (((kk >> 2) * S::kKBlock + (kk & 3) * 32) >> 4), q,
                                       idesc, kk > 0);
                     }
-                    tc_commit(&s_full[2 * buf + half]);
                 }
-                if (!ok) break;
-                if (k + 1 < ch.y || !keep) tc_commit(&q_empty[slot]);
+                tc_commit(&s_full[half * kAccs + buf]);
+                if (k + 1 == ch.y) tc_commit(&k_empty[2 * kslot + half]);
+                if (k + 1 < ch.y || !keep) tc_commit(&q_empty[qslot]);
             }
-            if (ok) tc_commit(&k_empty[m & 1]);
-            t = next;
-            ++m;
         }
         // every product has ended before tensor memory is given back
         tc_commit(done);
@@ -556,7 +618,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
 template <int D, bool MX4>
 cudaError_t launch_many(const ManyParams& P, int sms, cudaStream_t stream) {
     auto kern = key_weights_many_kernel<D, MX4>;
-    constexpr int smem = ManySmem<D>::kBytes;
+    constexpr int smem = ManySmem<D, MX4>::kBytes;
     static_assert(smem <= 232448, "shared memory of an SM");
     static std::mutex mu;
     static bool ready[64] = {false};
