@@ -1,7 +1,7 @@
 // pa_key_weights.cu -- adds to every cached key the softmax weight that a set
 // of queries gives it:  w_j += sum_r exp2(f q_r . k_j - lse_r log2 e), over the
 // rows r (query, q head of the key's group) that see key j.  This is the kernel
-// for up to 32 such rows; pa_key_weights_tc.cu has the one for more.
+// for up to 16 such rows; pa_key_weights_tc.cu has the one for more.
 //
 // No sum runs over keys, so there is nothing to join: a warp owns 32 keys of one
 // KV head at a time, copies their rows into its own shared memory (cp.async) and
@@ -38,13 +38,22 @@ constexpr int kWeightWarps = 8;
 constexpr int kWeightThreads = 32 * kWeightWarps;
 
 // Up to this many query rows (of the longest q_len) this kernel runs; above,
-// the one on tcgen05.
-constexpr int kFewRows = 32;
+// the one on tcgen05 (16 sequences of 8000 keys, 8 KV heads, here / there: 8 rows
+// bf16 46 / 48 us, 4-bit 35 / 35; 16 rows 49 / 48 and 50 / 55; 24 rows 53 / 48
+// and 64 / 55; 64 rows 88 / 48 and 136 / 51).
+constexpr int kFewRows = 16;
 
 // Bytes of a warp's place for 32 keys' rows (and scale words).
 template <int D, bool MX4>
 __host__ __device__ constexpr int weight_stage() {
     return MX4 ? 32 * (D / 2 + 4) : 32 * 2 * D;
+}
+
+// Where those places begin: behind Q and what belongs to its rows, on a whole
+// line of banks.
+template <int D>
+__host__ __device__ constexpr int weight_rows_at() {
+    return (kFewRows * (2 * D + kQPad + 12) + 127) / 128 * 128;
 }
 
 // First key (a multiple of 32) of the items of a sequence, and how many items.
@@ -70,7 +79,7 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
     float* off = reinterpret_cast<float*>(smem + kFewRows * QROW);   // -lse * log2 e
     float* fac = off + kFewRows;                                     // score factor
     int* pos = reinterpret_cast<int*>(fac + kFewRows);               // query position
-    const uint32_t rows = smem_u32(pos + kFewRows) + (threadIdx.x >> 5) * weight_stage<D, MX4>();
+    const uint32_t rows = smem_u32(smem) + weight_rows_at<D>() + (threadIdx.x >> 5) * weight_stage<D, MX4>();
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = lane >> 2, t4 = lane & 3;
@@ -368,8 +377,7 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
 // Shared-memory opt-in and the CTAs an SM holds, once per device.
 template <int D, bool MX4>
 cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) {
-    constexpr int smem = kFewRows * (2 * D + kQPad) + 3 * kFewRows * 4 +
-                         kWeightWarps * weight_stage<D, MX4>();
+    constexpr int smem = weight_rows_at<D>() + kWeightWarps * weight_stage<D, MX4>();
     auto kern = key_weights_kernel<D, MX4>;
     static std::mutex mu;
     static int per_sm[64] = {0};

@@ -32,8 +32,12 @@ struct EvictParams {
 namespace {
 
 constexpr int kBins = 256;
-constexpr int kHistBytes = kBins * 32 * 4;   // one histogram per lane: no bank is met twice
-constexpr int kMaxCached = (227 * 1024 - kHistBytes - 2048) / 4;   // keys held in shared memory
+// Copies of the histogram, which lanes spread over: fewer are cheaper to clear
+// and to add up, more meet less often.
+constexpr int copies_of(bool few) { return few ? 8 : 32; }
+constexpr int hist_bytes(bool few) { return kBins * copies_of(few) * 4; }
+// Keys whose upper halves shared memory holds
+constexpr int kMaxCached = (227 * 1024 - hist_bytes(false) - 2048) / 2;
 constexpr int kMoveRows = 64;
 
 constexpr int kMoveThreads = 256;
@@ -111,14 +115,16 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// PIECES 0: select only; else the CTA moves what it selected.
-template <int kSelectThreads, int PIECES>
+// PIECES 0: select only; else the CTA moves what it selected.  The upper halves
+// of the keys stay in shared memory; the last two passes and the listing read a
+// weight again where its upper half is the threshold's.
+template <int kSelectThreads, int PIECES, bool FEW>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_bytes) {
-    constexpr int kSelectWarps = kSelectThreads / 32;
+    constexpr int kSelectWarps = kSelectThreads / 32, kCopies = copies_of(FEW);
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
-    uint32_t* cached = reinterpret_cast<uint32_t*>(smem + kHistBytes);
+    uint16_t* cached = reinterpret_cast<uint16_t*>(smem + hist_bytes(FEW));
     __shared__ uint32_t bins[kBins];
     __shared__ uint32_t s_digit, s_left;
     __shared__ int2 s_count[kSelectWarps];
@@ -140,26 +146,50 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
         return order_key(P.weights[((int64_t)page * g.Hkv + hk) * g.ps + (i & (g.ps - 1))]);
     };
     const bool in_smem = c <= cached_cap;
-    if (in_smem) {
-#pragma unroll 4
-        for (int i = tid; i < c; i += kSelectThreads) cached[i] = key_at(i);
-    }
-    auto key = [&](int i) -> uint32_t { return in_smem ? cached[i] : key_at(i); };
+    auto upper = [&](int i) -> uint32_t { return in_smem ? cached[i] : key_at(i) >> 16; };
+    auto clear = [&]() {
+        for (int i = tid; i < kBins * kCopies / 4; i += kSelectThreads)
+            reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    };
+    auto count = [&](uint32_t digit) {
+        atomicAdd(&hist[digit * kCopies + lane % kCopies], 1u);
+    };
 
     // ---- the budget-th largest key
     uint32_t prefix = 0, left = (uint32_t)P.budget;   // rank from the top among equal prefixes
     for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < kBins * 32; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < c; i += kSelectThreads) {
-            const uint32_t x = key(i);
-            if (shift == 24 || (x >> (shift + 8)) == prefix)
-                atomicAdd(&hist[((x >> shift) & 255u) * 32 + lane], 1u);
+        clear();
+        if (shift == 24) {
+#pragma unroll 8
+            for (int i = tid; i < c; i += kSelectThreads) {
+                const uint32_t x = key_at(i);
+                if (in_smem) cached[i] = (uint16_t)(x >> 16);
+                count(x >> 24);
+            }
+        } else if (shift == 16) {
+#pragma unroll 4
+            for (int i = tid; i < c; i += kSelectThreads) {
+                const uint32_t x = upper(i);
+                if (x >> 8 == prefix) count(x & 255u);
+            }
+        } else {
+            for (int i = tid; i < c; i += kSelectThreads)
+                if (upper(i) == prefix >> (8 - shift)) {
+                    const uint32_t x = key_at(i);
+                    if (x >> (shift + 8) == prefix) count((x >> shift) & 255u);
+                }
         }
         __syncthreads();
-        for (int d = warp; d < kBins; d += kSelectWarps) {
-            const uint32_t s = __reduce_add_sync(0xffffffffu, hist[d * 32 + lane]);
-            if (lane == 0) bins[d] = s;
+        if (tid < kBins) {
+            uint32_t s = 0;
+#pragma unroll
+            for (int j = 0; j < kCopies / 4; ++j) {
+                const uint4 v = reinterpret_cast<const uint4*>(
+                    hist)[tid * (kCopies / 4) + (j + tid) % (kCopies / 4)];
+                s += v.x + v.y + v.z + v.w;
+            }
+            bins[tid] = s;
         }
         __syncthreads();
         if (warp == 0) {
@@ -192,12 +222,19 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     // ---- list the kept positions; a warp owns a run of positions
     const int per_warp = ((c + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
     const int i0 = min(c, warp * per_warp), i1 = min(c, i0 + per_warp);
+    // 1: above the threshold, 0: equal, -1: below
+    auto side = [&](int i) -> int {
+        const uint32_t u = upper(i), pu = prefix >> 16;
+        if (u != pu) return u > pu ? 1 : -1;
+        const uint32_t x = key_at(i);
+        return x > prefix ? 1 : x == prefix ? 0 : -1;
+    };
     int above = 0, equal = 0;
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
-        const bool on = i + lane < i1;
-        const uint32_t x = on ? key(i + lane) : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, on && x > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, on && x == prefix));
+        const int x = i + lane < i1 ? side(i + lane) : -1;
+        above += __popc(__ballot_sync(0xffffffffu, x == 1));
+        equal += __popc(__ballot_sync(0xffffffffu, x == 0));
     }
     if (lane == 0) s_count[warp] = make_int2(above, equal);
     __syncthreads();
@@ -206,14 +243,13 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     int na = __shfl_sync(0xffffffffu, ea, warp), ne = __shfl_sync(0xffffffffu, ee, warp);
     int32_t* out = P.kept + (int64_t)blockIdx.x * P.budget;
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
-        const bool on = i + lane < i1;
-        const uint32_t x = on ? key(i + lane) : 0u;
-        const uint32_t ma = __ballot_sync(0xffffffffu, on && x > prefix);
-        const uint32_t me = __ballot_sync(0xffffffffu, on && x == prefix);
+        const int x = i + lane < i1 ? side(i + lane) : -1;
+        const uint32_t ma = __ballot_sync(0xffffffffu, x == 1);
+        const uint32_t me = __ballot_sync(0xffffffffu, x == 0);
         const int a = na + __popc(ma & below), e = ne + __popc(me & below);
-        if (on && (x > prefix || (x == prefix && e < (int)left)))
-            out[a + min(e, (int)left)] = i + lane;
+        if (x == 1 || (x == 0 && e < (int)left)) out[a + min(e, (int)left)] = i + lane;
         na += __popc(ma);
         ne += __popc(me);
     }
@@ -254,19 +290,21 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     P.err = err;
     // the longest sequence's keys fit shared memory, or are read from L2 every pass
     const int cap = g.max_ctx <= kMaxCached ? g.max_ctx : kMaxCached;
-    const int smem = kHistBytes + cap * 4;
     const int units = g.B * g.Hkv;
     const int pieces = mx4 ? g.D / 32 : g.D / 8, scale_bytes = mx4 ? g.D / 32 : 0;
     // many pairs: each CTA its own; short sequences with fewer threads, so that
     // an SM holds more of them
-    const bool together = units >= 2 * sms, few = cap <= 4096;
+    const bool together = units >= 2 * sms, few = cap <= 4096, wide = !few && units <= sms;
+    const int smem = hist_bytes(few) + (cap * 2 + 15) / 16 * 16;
     void (*kern)(EvictParams, int, int) =
-        !together ? (few ? select_kernel<256, 0> : select_kernel<1024, 0>)
-        : pieces == 16 ? (few ? select_kernel<256, 16> : select_kernel<512, 16>)
-        : pieces == 8  ? (few ? select_kernel<256, 8> : select_kernel<512, 8>)
-        : pieces == 4  ? (few ? select_kernel<256, 4> : select_kernel<512, 4>)
-                       : (few ? select_kernel<256, 2> : select_kernel<512, 2>);
-    const int threads = few ? 256 : together ? 512 : 1024;
+        !together ? (few    ? select_kernel<256, 0, true>
+                     : wide ? select_kernel<1024, 0, false>
+                            : select_kernel<512, 0, false>)
+        : pieces == 16 ? (few ? select_kernel<256, 16, true> : select_kernel<512, 16, false>)
+        : pieces == 8  ? (few ? select_kernel<256, 8, true> : select_kernel<512, 8, false>)
+        : pieces == 4  ? (few ? select_kernel<256, 4, true> : select_kernel<512, 4, false>)
+                       : (few ? select_kernel<256, 2, true> : select_kernel<512, 2, false>);
+    const int threads = few ? 256 : wide ? 1024 : 512;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<units, threads, smem, stream>>>(P, cap, scale_bytes);
