@@ -36,8 +36,10 @@ constexpr int kBins = 256;
 // and to add up, more meet less often.
 constexpr int copies_of(bool few) { return few ? 8 : 32; }
 constexpr int hist_bytes(bool few) { return kBins * copies_of(few) * 4; }
+// Keys (as position and value) whose upper half is the threshold's, at most
+constexpr int kListed = 1024;
 // Keys whose upper halves shared memory holds
-constexpr int kMaxCached = (227 * 1024 - hist_bytes(false) - 2048) / 2;
+constexpr int kMaxCached = (227 * 1024 - hist_bytes(false) - kListed * 8 - 4096) / 2;
 constexpr int kMoveRows = 64;
 
 constexpr int kMoveThreads = 256;
@@ -116,15 +118,19 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 // PIECES 0: select only; else the CTA moves what it selected.  The upper halves
-// of the keys stay in shared memory; the last two passes and the listing read a
-// weight again where its upper half is the threshold's.
+// of the keys stay in shared memory.  Where the first two passes leave few keys
+// that share the threshold's upper half, those are read again, all at once, and
+// decide the rest; where many do (equal weights), or the keys do not fit, every
+// later step reads them where they are.
 template <int kSelectThreads, int PIECES, bool FEW>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_bytes) {
     constexpr int kSelectWarps = kSelectThreads / 32, kCopies = copies_of(FEW);
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
-    uint16_t* cached = reinterpret_cast<uint16_t*>(smem + hist_bytes(FEW));
+    uint2* list = reinterpret_cast<uint2*>(smem + hist_bytes(FEW));     // (position, key)
+    uint16_t* cached = reinterpret_cast<uint16_t*>(smem + hist_bytes(FEW) + kListed * 8);
+    __shared__ int s_listed;
     __shared__ uint32_t bins[kBins];
     __shared__ uint32_t s_digit, s_left;
     __shared__ int2 s_count[kSelectWarps];
@@ -139,11 +145,15 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     }
     if (bad || c <= P.budget) return;
     const int32_t* row = P.table + (int64_t)b * g.mpps;
+    // (no branches: the loads of a loop's iterations run together; a page that
+    // is none counts as the smallest key, and the move flags it)
     auto key_at = [&](int i) -> uint32_t {
-        if (i < P.num_first || i >= c - P.num_recent) return 0xffffffffu;
         const int page = row[i >> g.ps_shift];
-        if (page < 0 || page >= g.num_pages) return 0u;   // the move flags it
-        return order_key(P.weights[((int64_t)page * g.Hkv + hk) * g.ps + (i & (g.ps - 1))]);
+        const bool ok = (uint32_t)page < (uint32_t)g.num_pages;
+        const float w =
+            P.weights[((int64_t)(ok ? page : 0) * g.Hkv + hk) * g.ps + (i & (g.ps - 1))];
+        const uint32_t x = ok ? order_key(w) : 0u;
+        return i < P.num_first || i >= c - P.num_recent ? 0xffffffffu : x;
     };
     const bool in_smem = c <= cached_cap;
     auto upper = [&](int i) -> uint32_t { return in_smem ? cached[i] : key_at(i) >> 16; };
@@ -157,6 +167,8 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     };
 
     // ---- the budget-th largest key
+    bool listed = false;
+    if (tid == 0) s_listed = 0;
     uint32_t prefix = 0, left = (uint32_t)P.budget;   // rank from the top among equal prefixes
     for (int shift = 24; shift >= 0; shift -= 8) {
         clear();
@@ -172,6 +184,11 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
             for (int i = tid; i < c; i += kSelectThreads) {
                 const uint32_t x = upper(i);
                 if (x >> 8 == prefix) count(x & 255u);
+            }
+        } else if (listed) {
+            for (int i = tid; i < s_listed; i += kSelectThreads) {
+                const uint32_t x = list[i].y;
+                if (x >> (shift + 8) == prefix) count((x >> shift) & 255u);
             }
         } else {
             for (int i = tid; i < c; i += kSelectThreads)
@@ -216,6 +233,27 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
         __syncthreads();
         prefix = (prefix << 8) | s_digit;
         left = s_left;
+        if (shift == 16 && in_smem) {
+            listed = bins[prefix & 255u] <= kListed;
+            if (listed) {
+#pragma unroll 4
+                for (int i = tid; i < c; i += kSelectThreads)
+                    if (cached[i] == prefix) list[atomicAdd(&s_listed, 1)].x = i;
+                __syncthreads();
+                for (int i = tid; i < s_listed; i += kSelectThreads)
+                    list[i].y = key_at((int)list[i].x);
+                // (read after the next barrier)
+            }
+        }
+    }
+    if (listed) {
+        // from now on an upper half tells a key's side of the threshold: 0xffff
+        // and 0 are the halves of one key each, the largest and the smallest
+        for (int i = tid; i < s_listed; i += kSelectThreads) {
+            const uint2 x = list[i];
+            if (x.y != prefix) cached[x.x] = x.y > prefix ? 0xffffu : 0u;
+        }
+        __syncthreads();
     }
     // kept: keys above `prefix`, and the first `left` that equal it
 
@@ -229,29 +267,43 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
         const uint32_t x = key_at(i);
         return x > prefix ? 1 : x == prefix ? 0 : -1;
     };
-    int above = 0, equal = 0;
-#pragma unroll 4
-    for (int i = i0; i < i1; i += 32) {
-        const int x = i + lane < i1 ? side(i + lane) : -1;
-        above += __popc(__ballot_sync(0xffffffffu, x == 1));
-        equal += __popc(__ballot_sync(0xffffffffu, x == 0));
-    }
-    if (lane == 0) s_count[warp] = make_int2(above, equal);
-    __syncthreads();
-    const int2 mine = lane < kSelectWarps ? s_count[lane] : make_int2(0, 0);
-    const int ea = warp_inclusive(mine.x, lane) - mine.x, ee = warp_inclusive(mine.y, lane) - mine.y;
-    int na = __shfl_sync(0xffffffffu, ea, warp), ne = __shfl_sync(0xffffffffu, ee, warp);
+    int na, ne;                                       // kept before this warp's run
     int32_t* out = P.kept + (int64_t)blockIdx.x * P.budget;
     const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int i = i0; i < i1; i += 32) {
-        const int x = i + lane < i1 ? side(i + lane) : -1;
-        const uint32_t ma = __ballot_sync(0xffffffffu, x == 1);
-        const uint32_t me = __ballot_sync(0xffffffffu, x == 0);
-        const int a = na + __popc(ma & below), e = ne + __popc(me & below);
-        if (x == 1 || (x == 0 && e < (int)left)) out[a + min(e, (int)left)] = i + lane;
-        na += __popc(ma);
-        ne += __popc(me);
+    auto sweep = [&](auto side_of) {
+        int above = 0, equal = 0;
+#pragma unroll 8
+        for (int i = i0; i < i1; i += 32) {
+            const int x = i + lane < i1 ? side_of(i + lane) : -1;
+            above += __popc(__ballot_sync(0xffffffffu, x == 1));
+            equal += __popc(__ballot_sync(0xffffffffu, x == 0));
+        }
+        if (lane == 0) s_count[warp] = make_int2(above, equal);
+        __syncthreads();
+        const int2 mine = lane < kSelectWarps ? s_count[lane] : make_int2(0, 0);
+        const int ea = warp_inclusive(mine.x, lane) - mine.x;
+        const int ee = warp_inclusive(mine.y, lane) - mine.y;
+        na = __shfl_sync(0xffffffffu, ea, warp);
+        ne = __shfl_sync(0xffffffffu, ee, warp);
+#pragma unroll 8
+        for (int i = i0; i < i1; i += 32) {
+            const int x = i + lane < i1 ? side_of(i + lane) : -1;
+            const uint32_t ma = __ballot_sync(0xffffffffu, x == 1);
+            const uint32_t me = __ballot_sync(0xffffffffu, x == 0);
+            const int a = na + __popc(ma & below), e = ne + __popc(me & below);
+            if (x == 1 || (x == 0 && e < (int)left)) out[a + min(e, (int)left)] = i + lane;
+            na += __popc(ma);
+            ne += __popc(me);
+        }
+    };
+    if (listed) {
+        const uint32_t pu = prefix >> 16;
+        sweep([&](int i) -> int {
+            const uint32_t u = cached[i];
+            return (u > pu) - (u < pu);
+        });
+    } else {
+        sweep(side);
     }
     if constexpr (PIECES > 0) {
         // (the kept list and the histograms' place are this CTA's own)
@@ -295,7 +347,7 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     // many pairs: each CTA its own; short sequences with fewer threads, so that
     // an SM holds more of them
     const bool together = units >= 2 * sms, few = cap <= 4096, wide = !few && units <= sms;
-    const int smem = hist_bytes(few) + (cap * 2 + 15) / 16 * 16;
+    const int smem = hist_bytes(few) + kListed * 8 + (cap * 2 + 15) / 16 * 16;
     void (*kern)(EvictParams, int, int) =
         !together ? (few    ? select_kernel<256, 0, true>
                      : wide ? select_kernel<1024, 0, false>
