@@ -4,10 +4,9 @@
 // Select, one CTA per sequence and KV head: the budget-th largest key by a radix
 // select, eight bits a pass over an order-preserving integer form of the
 // weights, then one ordered pass that lists the kept positions (ties to the
-// lower one).  Move: 64 kept rows of K and V at a time, 16 bytes a thread; bound
-// by HBM.  Where the (sequence, head) pairs fill the GPU the CTA that selected
-// moves, so that one's selection hides behind another's moves; fewer pairs
-// leave the moves to a second launch that spreads them over all SMs.
+// lower one).  Move, a second launch over all SMs: 64 kept rows of K and V a
+// CTA, 16 bytes a thread.  The move is bound by HBM, the selection by the
+// latency of its passes.
 #include "pa_cache_common.cuh"
 
 namespace pa {
@@ -44,17 +43,20 @@ constexpr int kMoveRows = 64;
 
 constexpr int kMoveThreads = 256;
 
-// Rows r0 .. r0 + n of the kept list of (b, hk), n <= kMoveRows, into their new
-// pages, by the THREADS of a CTA.  PIECES: 16-byte pieces of a row (D / 8 of bf16,
-// D / 32 of 4-bit codes).
-struct MoveRows {
-    int64_t src[kMoveRows], dst[kMoveRows];
-};
-template <int PIECES, int THREADS>
-__device__ __forceinline__ void move_rows(const EvictParams& P, MoveRows& at, int b, int hk, int c,
-                                          int r0, int n, int scale_bytes) {
+// kMoveRows rows of a kept list into their new pages.  PIECES: 16-byte pieces of a
+// row (D / 8 of bf16, D / 32 of 4-bit codes).
+template <int PIECES>
+__global__ void __launch_bounds__(kMoveThreads)
+move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) {
+    __shared__ struct {
+        int64_t src[kMoveRows], dst[kMoveRows];
+    } at;
     const CacheGeom& g = P.g;
-    const int tid = threadIdx.x, unit = b * g.Hkv + hk;
+    grid_dependency_wait();                     // (launched while the selection runs)
+    const int unit = blockIdx.x / chunks, r0 = blockIdx.x % chunks * kMoveRows;
+    const int b = unit / g.Hkv, hk = unit % g.Hkv, c = P.ctx[b], tid = threadIdx.x;
+    if (c <= P.budget || c > g.max_ctx) return;
+    const int n = min(kMoveRows, P.budget - r0);
     if (tid < n) {
         const int from = P.kept[(int64_t)unit * P.budget + r0 + tid], to = r0 + tid;
         const bool listed = from >= 0 && from < c;
@@ -81,11 +83,11 @@ __device__ __forceinline__ void move_rows(const EvictParams& P, MoveRows& at, in
     }
     __syncthreads();
     // pieces of K, then of V; every load of a thread before its stores
-    constexpr int kPer = (2 * PIECES * kMoveRows + THREADS - 1) / THREADS;
+    constexpr int kPer = (2 * PIECES * kMoveRows + kMoveThreads - 1) / kMoveThreads;
     uint4 x[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * THREADS, kv = i / (PIECES * kMoveRows);
+        const int i = tid + j * kMoveThreads, kv = i / (PIECES * kMoveRows);
         const int r = (i / PIECES) % kMoveRows, p = i % PIECES;
         x[j] = make_uint4(0u, 0u, 0u, 0u);
         if (kv < 2 && r < n && at.src[r] >= 0)
@@ -93,21 +95,11 @@ __device__ __forceinline__ void move_rows(const EvictParams& P, MoveRows& at, in
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * THREADS, kv = i / (PIECES * kMoveRows);
+        const int i = tid + j * kMoveThreads, kv = i / (PIECES * kMoveRows);
         const int r = (i / PIECES) % kMoveRows, p = i % PIECES;
         if (kv < 2 && r < n && at.src[r] >= 0)
             __stcs(reinterpret_cast<uint4*>(kv ? P.v : P.k) + at.dst[r] * PIECES + p, x[j]);
     }
-}
-
-template <int PIECES>
-__global__ void __launch_bounds__(kMoveThreads)
-move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) {
-    __shared__ MoveRows at;
-    const int unit = blockIdx.x / chunks, r0 = blockIdx.x % chunks * kMoveRows;
-    const int b = unit / P.g.Hkv, hk = unit % P.g.Hkv, c = P.ctx[b];
-    if (c <= P.budget || c > P.g.max_ctx) return;
-    move_rows<PIECES, kMoveThreads>(P, at, b, hk, c, r0, min(kMoveRows, P.budget - r0), scale_bytes);
 }
 
 // Larger weights get larger keys; NaN the smallest, a protected position the largest.
@@ -117,14 +109,13 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// PIECES 0: select only; else the CTA moves what it selected.  The upper halves
-// of the keys stay in shared memory.  Where the first two passes leave few keys
+// The upper halves of the keys stay in shared memory.  Where the first two passes leave few keys
 // that share the threshold's upper half, those are read again, all at once, and
 // decide the rest; where many do (equal weights), or the keys do not fit, every
 // later step reads them where they are.
-template <int kSelectThreads, int PIECES, bool FEW>
+template <int kSelectThreads, bool FEW>
 __global__ void __launch_bounds__(kSelectThreads)
-select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_bytes) {
+select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     constexpr int kSelectWarps = kSelectThreads / 32, kCopies = copies_of(FEW);
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
@@ -144,6 +135,7 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
         if (bad) flag_error(P.err, PA_DEV_BAD_LENGTHS);
     }
     if (bad || c <= P.budget) return;
+    grid_launch_dependents();
     const int32_t* row = P.table + (int64_t)b * g.mpps;
     // (no branches: the loads of a loop's iterations run together; a page that
     // is none counts as the smallest key, and the move flags it)
@@ -172,18 +164,47 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     uint32_t prefix = 0, left = (uint32_t)P.budget;   // rank from the top among equal prefixes
     for (int shift = 24; shift >= 0; shift -= 8) {
         clear();
+        // (eight keys are read before the first is counted: no load passes an
+        // atomic operation by itself)
         if (shift == 24) {
-#pragma unroll 8
-            for (int i = tid; i < c; i += kSelectThreads) {
-                const uint32_t x = key_at(i);
-                if (in_smem) cached[i] = (uint16_t)(x >> 16);
-                count(x >> 24);
+            // a warp takes 256 keys at a time; lane l < 16 has the page of their
+            // l-th run of 16, looked up a turn ahead
+            auto look_up = [&](int i) -> int {
+                const int k = i + 16 * (lane & 15);
+                return k < c ? row[k >> g.ps_shift] : -1;
+            };
+            int page = look_up(256 * warp);
+            for (int i = 256 * warp; i < c; i += 8 * kSelectThreads) {
+                const int now = page;
+                page = look_up(i + 8 * kSelectThreads);
+                float w[8];
+                bool ok[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int p = __shfl_sync(0xffffffffu, now, 2 * j + (lane >> 4));
+                    ok[j] = (uint32_t)p < (uint32_t)g.num_pages;
+                    w[j] = P.weights[((int64_t)(ok[j] ? p : 0) * g.Hkv + hk) * g.ps +
+                                     ((i + 32 * j + lane) & (g.ps - 1))];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = i + 32 * j + lane;
+                    if (k < c) {
+                        uint32_t x = ok[j] ? order_key(w[j]) : 0u;
+                        if (k < P.num_first || k >= c - P.num_recent) x = 0xffffffffu;
+                        if (in_smem) cached[k] = (uint16_t)(x >> 16);
+                        count(x >> 24);
+                    }
+                }
             }
         } else if (shift == 16) {
-#pragma unroll 4
-            for (int i = tid; i < c; i += kSelectThreads) {
-                const uint32_t x = upper(i);
-                if (x >> 8 == prefix) count(x & 255u);
+            for (int i = tid; i < c; i += 8 * kSelectThreads) {
+                uint32_t x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = upper(min(i + j * kSelectThreads, c - 1));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (i + j * kSelectThreads < c && x[j] >> 8 == prefix) count(x[j] & 255u);
             }
         } else if (listed) {
             for (int i = tid; i < s_listed; i += kSelectThreads) {
@@ -236,9 +257,15 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
         if (shift == 16 && in_smem) {
             listed = bins[prefix & 255u] <= kListed;
             if (listed) {
-#pragma unroll 4
-                for (int i = tid; i < c; i += kSelectThreads)
-                    if (cached[i] == prefix) list[atomicAdd(&s_listed, 1)].x = i;
+                for (int i = tid; i < c; i += 8 * kSelectThreads) {
+                    uint32_t x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = cached[min(i + j * kSelectThreads, c - 1)];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (i + j * kSelectThreads < c && x[j] == prefix)
+                            list[atomicAdd(&s_listed, 1)].x = i + j * kSelectThreads;
+                }
                 __syncthreads();
                 for (int i = tid; i < s_listed; i += kSelectThreads)
                     list[i].y = key_at((int)list[i].x);
@@ -305,15 +332,6 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap, int scale_b
     } else {
         sweep(side);
     }
-    if constexpr (PIECES > 0) {
-        // (the kept list and the histograms' place are this CTA's own)
-        MoveRows* at = reinterpret_cast<MoveRows*>(smem);
-        for (int r0 = 0; r0 < P.budget; r0 += kMoveRows) {
-            __syncthreads();
-            move_rows<PIECES, kSelectThreads>(P, at[(r0 / kMoveRows) & 1], b, hk, c, r0,
-                                              min(kMoveRows, P.budget - r0), scale_bytes);
-        }
-    }
 }
 
 }  // namespace
@@ -344,25 +362,18 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     const int cap = g.max_ctx <= kMaxCached ? g.max_ctx : kMaxCached;
     const int units = g.B * g.Hkv;
     const int pieces = mx4 ? g.D / 32 : g.D / 8, scale_bytes = mx4 ? g.D / 32 : 0;
-    // many pairs: each CTA its own; short sequences with fewer threads, so that
-    // an SM holds more of them
-    const bool together = units >= 2 * sms, few = cap <= 4096, wide = !few && units <= sms;
+    // short sequences take few threads, so that an SM holds many of them
+    // (MEASURED)
+    const bool few = cap <= 4096, wide = !few && units <= sms;
     const int smem = hist_bytes(few) + kListed * 8 + (cap * 2 + 15) / 16 * 16;
-    void (*kern)(EvictParams, int, int) =
-        !together ? (few    ? select_kernel<256, 0, true>
-                     : wide ? select_kernel<1024, 0, false>
-                            : select_kernel<512, 0, false>)
-        : pieces == 16 ? (few ? select_kernel<256, 16, true> : select_kernel<512, 16, false>)
-        : pieces == 8  ? (few ? select_kernel<256, 8, true> : select_kernel<512, 8, false>)
-        : pieces == 4  ? (few ? select_kernel<256, 4, true> : select_kernel<512, 4, false>)
-                       : (few ? select_kernel<256, 2, true> : select_kernel<512, 2, false>);
-    const int threads = few ? 256 : wide ? 1024 : 512;
+    void (*kern)(EvictParams, int) = few    ? select_kernel<256, true>
+                                     : wide ? select_kernel<1024, false>
+                                            : select_kernel<512, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<units, threads, smem, stream>>>(P, cap, scale_bytes);
+    kern<<<units, few ? 256 : wide ? 1024 : 512, smem, stream>>>(P, cap);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (together || g.max_ctx <= budget) return cudaSuccess;
+    if (e != cudaSuccess || g.max_ctx <= budget) return e;
     const int chunks = (budget + kMoveRows - 1) / kMoveRows;
     const int64_t grid = (int64_t)units * chunks;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
@@ -370,8 +381,8 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
                 : pieces == 8 ? move_kernel<8>
                 : pieces == 4 ? move_kernel<4>
                               : move_kernel<2>;
-    move<<<(int)grid, kMoveThreads, 0, stream>>>(P, chunks, scale_bytes);
-    return cudaGetLastError();
+    return launch_dependent(move, dim3((unsigned)grid), dim3(kMoveThreads), 0, stream, P, chunks,
+                            scale_bytes);
 }
 
 }  // namespace pa
