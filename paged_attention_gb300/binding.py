@@ -163,7 +163,7 @@ def status_string(status: int) -> str:
 def _p(t: Optional[torch.Tensor]):
     if t is None:
         return None
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _nbytes(t: Optional[torch.Tensor]) -> int:
@@ -173,8 +173,8 @@ def _nbytes(t: Optional[torch.Tensor]) -> int:
 def _stream(stream):
     if stream is None:
         # (torch.cuda.current_stream() builds an object: 3 us of every call)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(status: int, where: str):
@@ -296,12 +296,14 @@ def pa_prefill_fp8(problem, q, q_scale, k_cache, v_cache, block_table, context_l
 
 def _new_rows(t: torch.Tensor, problem: PaProblem, name: str) -> int:
     """Elements between the tokens of new K or V rows [tokens, Hkv, D]."""
-    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[0] < problem.total_q_tokens
-            or t.shape[1] != problem.num_kv_heads or t.shape[2] != problem.head_dim
-            or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    shape, stride = t.shape, t.stride()
+    heads, dim = problem.num_kv_heads, problem.head_dim
+    if (len(shape) != 3 or t.dtype != torch.bfloat16 or shape[0] < problem.total_q_tokens
+            or shape[1] != heads or shape[2] != dim
+            or stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{name} must be bf16 [total_q_tokens, num_kv_heads, head_dim] with "
                          f"dense heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def pa_kv_append(problem, k_new, v_new, block_table, context_lens, q_lens, k_cache, k_scale,

@@ -3,6 +3,8 @@
 // device, and the E2M1 / E8M0 conversions of the PA_MX4 cache.
 #pragma once
 
+#include <atomic>
+
 #include "pa_cache.h"
 #include "pa_internal.cuh"
 
@@ -88,6 +90,21 @@ __device__ __forceinline__ void check_lens(const CacheGeom& g, const int32_t* ct
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (__any_sync(0xffffffffu, bad || sum != g.total_q) && lane == 0)
         flag_error(err, PA_DEV_BAD_LENGTHS);
+}
+
+// Lets a kernel take up to `bytes` (the same in every call) of dynamic shared
+// memory on the current device; asked of the runtime once per kernel and device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};          // a bit per device
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    const cudaError_t f =
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (f == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return f;
 }
 
 // ------------------------------------------------------------- E2M1 / E8M0

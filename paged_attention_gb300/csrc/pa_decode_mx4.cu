@@ -880,11 +880,9 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
 template <int D, int NT>
 cudaError_t launch_mx4(const Mx4Params& P, int grid, cudaStream_t stream) {
     using Cfg = Mx4Cfg<D, NT>;
-    auto kern = decode_mx4_kernel<D, NT>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    const cudaError_t e = allow_smem<decode_mx4_kernel<D, NT>>(Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(P);
+    decode_mx4_kernel<D, NT><<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(P);
     return cudaGetLastError();
 }
 

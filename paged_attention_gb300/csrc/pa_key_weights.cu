@@ -12,7 +12,6 @@
 // sum over query rows stays in a thread and its three neighbours: a fixed order,
 // no atomics.
 // Bound by HBM (K once).
-#include <mutex>
 #include <type_traits>
 
 #include "pa_cache_mma.cuh"
@@ -34,7 +33,7 @@ struct WeightParams {
 
 namespace {
 
-constexpr int kWeightWarps = 8;
+constexpr int kWeightWarps = 8, kCtas = 2;    // of an SM
 constexpr int kWeightThreads = 32 * kWeightWarps;
 
 // Up to this many query rows (of the longest q_len) this kernel runs; above,
@@ -67,7 +66,7 @@ __device__ __forceinline__ int seq_items(const CacheGeom& g, int c, int q, int k
 // K becomes an operand as it is (bf16), or as f16 codes, the block scales
 // applied to the block scores.
 template <int D, bool MX4>
-__global__ void __launch_bounds__(kWeightThreads, 2)
+__global__ void __launch_bounds__(kWeightThreads, kCtas)
 key_weights_kernel(const __grid_constant__ WeightParams P) {
     constexpr int KB = D / 32;                 // blocks of 32 columns
     constexpr int QROW = 2 * D + kQPad;
@@ -374,30 +373,12 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
     }
 }
 
-// Shared-memory opt-in and the CTAs an SM holds, once per device.
 template <int D, bool MX4>
 cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) {
     constexpr int smem = weight_rows_at<D>() + kWeightWarps * weight_stage<D, MX4>();
-    auto kern = key_weights_kernel<D, MX4>;
-    static std::mutex mu;
-    static int per_sm[64] = {0};
-    int dev = 0, n = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem<key_weights_kernel<D, MX4>>(smem);
     if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (dev >= 64 || per_sm[dev] == 0) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWeightThreads, smem);
-            if (e != cudaSuccess) return e;
-            if (n < 1) n = 1;
-            if (dev < 64) per_sm[dev] = n;
-        } else {
-            n = per_sm[dev];
-        }
-    }
-    kern<<<sms * n, kWeightThreads, smem, stream>>>(P);
+    key_weights_kernel<D, MX4><<<sms * kCtas, kWeightThreads, smem, stream>>>(P);
     return cudaGetLastError();
 }
 

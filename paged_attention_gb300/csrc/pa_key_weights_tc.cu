@@ -14,8 +14,6 @@
 // Roles: two groups of 4 warps take the accumulators, one group for each half;
 // two groups of 4 bring K, 2 warps bring Q, 2 issue the products.  All waits
 // are bounded.
-#include <mutex>
-
 #include "pa_cache_mma.cuh"
 
 namespace pa {
@@ -620,19 +618,8 @@ cudaError_t launch_many(const ManyParams& P, int sms, cudaStream_t stream) {
     auto kern = key_weights_many_kernel<D, MX4>;
     constexpr int smem = ManySmem<D, MX4>::kBytes;
     static_assert(smem <= 232448, "shared memory of an SM");
-    static std::mutex mu;
-    static bool ready[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem<key_weights_many_kernel<D, MX4>>(smem);
     if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (dev >= 64 || !ready[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-            if (dev < 64) ready[dev] = true;
-        }
-    }
     kern<<<sms, kThreads, smem, stream>>>(P);
     return cudaGetLastError();
 }

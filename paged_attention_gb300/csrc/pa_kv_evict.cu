@@ -39,6 +39,7 @@ constexpr int hist_bytes(bool few) { return kBins * copies_of(few) * 4; }
 constexpr int kListed = 1024;
 // Keys whose upper halves shared memory holds
 constexpr int kMaxCached = (227 * 1024 - hist_bytes(false) - kListed * 8 - 4096) / 2;
+constexpr int kFewKeys = 4096;     // longest sequence that few threads select from
 constexpr int kMoveRows = 64;
 
 constexpr int kMoveThreads = 256;
@@ -334,6 +335,15 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     }
 }
 
+template <int kSelectThreads, bool FEW>
+cudaError_t launch_select(const EvictParams& P, int cap, int units, int smem, cudaStream_t stream) {
+    const cudaError_t e = allow_smem<select_kernel<kSelectThreads, FEW>>(
+        hist_bytes(FEW) + kListed * 8 + (FEW ? kFewKeys : kMaxCached) * 2 + 16);
+    if (e != cudaSuccess) return e;
+    select_kernel<kSelectThreads, FEW><<<units, kSelectThreads, smem, stream>>>(P, cap);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first, int num_recent,
@@ -364,15 +374,11 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     const int pieces = mx4 ? g.D / 32 : g.D / 8, scale_bytes = mx4 ? g.D / 32 : 0;
     // short sequences take few threads, so that an SM holds many of them
     // (MEASURED)
-    const bool few = cap <= 4096, wide = !few && units <= sms;
+    const bool few = cap <= kFewKeys, wide = !few && units <= sms;
     const int smem = hist_bytes(few) + kListed * 8 + (cap * 2 + 15) / 16 * 16;
-    void (*kern)(EvictParams, int) = few    ? select_kernel<256, true>
-                                     : wide ? select_kernel<1024, false>
-                                            : select_kernel<512, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<units, few ? 256 : wide ? 1024 : 512, smem, stream>>>(P, cap);
-    e = cudaGetLastError();
+    cudaError_t e = few    ? launch_select<256, true>(P, cap, units, smem, stream)
+                    : wide ? launch_select<1024, false>(P, cap, units, smem, stream)
+                           : launch_select<512, false>(P, cap, units, smem, stream);
     if (e != cudaSuccess || g.max_ctx <= budget) return e;
     const int chunks = (budget + kMoveRows - 1) / kMoveRows;
     const int64_t grid = (int64_t)units * chunks;
