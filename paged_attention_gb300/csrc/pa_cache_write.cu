@@ -11,6 +11,7 @@ namespace pa {
 namespace {
 
 constexpr int kWriteThreads = 256;
+constexpr int kWriteCtas = 5;    // of an SM
 constexpr int kMaxTokens = 32;   // tokens of one CTA: one per lane of its first warp
 
 // Where a CTA's tokens live: the rows of their first head (-1: a token to skip),
@@ -20,22 +21,33 @@ struct TokenPlace {
     int64_t row, dst_row, weight;
 };
 
-// The thread's items run through token (of the CTA) and position within a token:
-// kWriteThreads further each time, without a division.
-struct Cursor {
-    int t, r;
-    __device__ __forceinline__ void step(int per_token) {
-        r += kWriteThreads;
-        while (r >= per_token) {
-            r -= per_token;
-            ++t;
-        }
-    }
+// A thread has one position in a token -- K or V, head, 16 bytes of bf16 -- and
+// takes it of many tokens: narrow tokens share the CTA's threads, wide ones take
+// several CTAs (blockIdx.y).
+struct Position {
+    int first, step;             // the thread's tokens: first, first + step, ...
+    int kv, hc, h, c;            // K or V; position in it; head; position in the row
 };
-__device__ __forceinline__ Cursor first_item(int per_token) {
-    Cursor c = {0, (int)threadIdx.x - kWriteThreads};
-    c.step(per_token);
-    return c;
+template <int C>
+__device__ __forceinline__ Position my_position(const CacheGeom& g) {
+    const int half = g.Hkv * C, per_token = 2 * half;
+    Position p;
+    int r;
+    if (per_token <= kWriteThreads) {
+        p.step = kWriteThreads / per_token;
+        p.first = threadIdx.x / per_token;
+        r = threadIdx.x % per_token;
+        if (p.first >= p.step) p.first = kMaxTokens;       // left over: no tokens
+    } else {
+        p.step = 1;
+        r = blockIdx.y * kWriteThreads + threadIdx.x;
+        p.first = r < per_token ? 0 : kMaxTokens;
+    }
+    p.kv = r >= half;
+    p.hc = r - (p.kv ? half : 0);
+    p.h = p.hc / C;
+    p.c = p.hc % C;
+    return p;
 }
 
 // The first warp finds the places of the CTA's tokens [t0, t0 + n).
@@ -68,7 +80,7 @@ __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* t
             }
         }
         if (lane < n) place[lane] = p;
-        if (blockIdx.x == 0) check_lens(g, ctx, ql, lane, err);
+        if (blockIdx.x == 0 && blockIdx.y == 0) check_lens(g, ctx, ql, lane, err);
     }
     __syncthreads();
 }
@@ -77,12 +89,11 @@ __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* t
 __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     // magnitudes of bf16 order like their bits
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                            __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 1));
+    two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 2));
+    const uint32_t top = max(two & 0xffffu, two >> 16);
     const uint32_t ex = top >> 7;   // biased exponent of the largest magnitude
     e = ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
     if (ex == 255) return 0u;
@@ -97,78 +108,71 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& e) {
     return codes;
 }
 
-// One item: 8 elements (16 source bytes) of one row of K or V.  Bound by HBM
-// on long prompts and by latency on a decode step.
+// A thread quantises 8 elements (16 source bytes) of a row at a time.  Bound by
+// HBM on long prompts and by latency on a decode step.
 template <int D, bool MX4>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, kWriteCtas)
 append_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k_new,
               const __nv_bfloat16* __restrict__ v_new, int64_t k_stride, int64_t v_stride,
               const int32_t* __restrict__ table, const int32_t* __restrict__ ctx,
               const int32_t* __restrict__ ql, void* k_cache, uint8_t* k_scale, void* v_cache,
               uint8_t* v_scale, float* weights, int32_t* err, int tokens) {
-    constexpr int C = D / 8;   // items of a row
+    constexpr int C = D / 8;   // threads of a row
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
     find_places(g, table, ctx, ql, t0, n, nullptr, 0, 0, place, err);
-    const int half = g.Hkv * C, per_token = 2 * half;
+    const Position p = my_position<C>(g);
+    const int64_t stride = p.kv ? v_stride : k_stride;
+    const __nv_bfloat16* src = (p.kv ? v_new : k_new) + (int64_t)t0 * stride + p.hc * 8;
+    void* cache = p.kv ? v_cache : k_cache;
+    uint8_t* scale = p.kv ? v_scale : k_scale;
+    const int64_t head = (int64_t)p.h * g.head_rows;
+    const int lane = threadIdx.x & 31;
     // every lane of a warp takes part in the shuffles: the trip count is
-    // uniform; U items' loads are under way at a time
+    // uniform; U tokens' loads are under way at a time
     constexpr int U = 4;
-    const int rounds = (n * per_token + kWriteThreads - 1) / kWriteThreads;
-    Cursor at = first_item(per_token);
-    for (int i = 0; i < rounds; i += U) {
+    for (int i = 0; i < n; i += U * p.step) {
         uint4 x[U];
-        Cursor ahead = at;
+        int64_t row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int t = i + u * p.step + p.first;
             x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (ahead.t < n && place[ahead.t].row >= 0) {
-                const int kv = ahead.r >= half;
-                const __nv_bfloat16* src = kv ? v_new + (int64_t)(t0 + ahead.t) * v_stride
-                                              : k_new + (int64_t)(t0 + ahead.t) * k_stride;
-                x[u] = __ldcs(reinterpret_cast<const uint4*>(src) + (ahead.r - (kv ? half : 0)));
-            }
-            ahead.step(per_token);
+            row[u] = t < n ? place[t].row : -1;
+            if (row[u] >= 0) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + t * stride));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u >= rounds) break;
-            const Cursor me = at;
-            at.step(per_token);
-            const int kv = me.r >= half, hc = me.r - (kv ? half : 0), h = hc / C, c = hc % C;
             uint32_t codes = 0, scales = 0;
             if constexpr (MX4) {
                 uint32_t e;
                 codes = quantise8(x[u], e);
                 // the row's scale bytes, collected in its first lane
-                const int lane = threadIdx.x & 31, base = lane & ~(C - 1);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
-                    scales |= __shfl_sync(0xffffffffu, e, base + 4 * j) << (8 * j);
+                    scales |= __shfl_sync(0xffffffffu, e, (lane & ~(C - 1)) + 4 * j) << (8 * j);
             }
-            if (me.t >= n || place[me.t].row < 0) continue;
-            const int64_t row = place[me.t].row + (int64_t)h * g.head_rows;
-            void* cache = kv ? v_cache : k_cache;
+            if (row[u] < 0) continue;
+            const int64_t to = row[u] + head;
             if constexpr (MX4) {
-                reinterpret_cast<uint32_t*>(cache)[row * C + c] = codes;
-                if (c == 0) {
-                    uint8_t* sc = kv ? v_scale : k_scale;
+                reinterpret_cast<uint32_t*>(cache)[to * C + p.c] = codes;
+                if (p.c == 0) {
                     if constexpr (D == 128)
-                        reinterpret_cast<uint32_t*>(sc)[row] = scales;
+                        reinterpret_cast<uint32_t*>(scale)[to] = scales;
                     else
-                        reinterpret_cast<uint16_t*>(sc)[row] = (uint16_t)scales;
+                        reinterpret_cast<uint16_t*>(scale)[to] = (uint16_t)scales;
                 }
             } else {
-                reinterpret_cast<uint4*>(cache)[row * C + c] = x[u];
+                reinterpret_cast<uint4*>(cache)[to * C + p.c] = x[u];
             }
-            if (weights != nullptr && kv == 0 && c == 0)
-                weights[place[me.t].weight + (int64_t)h * g.ps] = 0.f;
+            if (weights != nullptr && p.kv == 0 && p.c == 0)
+                weights[place[i + u * p.step + p.first].weight + (int64_t)p.h * g.ps] = 0.f;
         }
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, kWriteCtas)
 expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
               const uint8_t* __restrict__ k_scale, const uint32_t* __restrict__ v_cache,
               const uint8_t* __restrict__ v_scale, const int32_t* __restrict__ table,
@@ -179,29 +183,28 @@ expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
     find_places(g, table, ctx, ql, t0, n, dst_table, dst_mpps, dst_pages, place, err);
-    const int half = g.Hkv * C, per_token = 2 * half;
-    constexpr int U = 4;   // items of a thread under way at a time
-    Cursor at = first_item(per_token);
-    while (at.t < n) {
+    const Position p = my_position<C>(g);
+    const uint32_t* code = p.kv ? v_cache : k_cache;
+    const uint8_t* scale = p.kv ? v_scale : k_scale;
+    uint4* out = reinterpret_cast<uint4*>(p.kv ? v_out : k_out);
+    const int64_t head = (int64_t)p.h * g.head_rows;
+    constexpr int U = 4;       // tokens of a thread under way at a time
+    for (int i = p.first; i < n; i += U * p.step) {
         uint32_t w[U], e[U];
-        Cursor ahead = at;
+        int64_t row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int t = i + u * p.step;
             w[u] = e[u] = 0;
-            if (ahead.t < n && place[ahead.t].row >= 0) {
-                const int kv = ahead.r >= half, hc = ahead.r - (kv ? half : 0);
-                const int64_t row = place[ahead.t].row + (int64_t)(hc / C) * g.head_rows;
-                w[u] = (kv ? v_cache : k_cache)[row * C + hc % C];
-                e[u] = (kv ? v_scale : k_scale)[row * (D / 32) + hc % C / 4];
+            row[u] = t < n ? place[t].row : -1;
+            if (row[u] >= 0) {
+                w[u] = code[(row[u] + head) * C + p.c];
+                e[u] = scale[(row[u] + head) * (D / 32) + p.c / 4];
             }
-            ahead.step(per_token);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Cursor me = at;
-            at.step(per_token);
-            if (me.t >= n || place[me.t].row < 0) continue;
-            const int kv = me.r >= half, hc = me.r - (kv ? half : 0);
+            if (row[u] < 0) continue;
             const float f = e8m0_to_f32(e[u]);
             uint32_t v[4];
             e2m1x8_to_f16(w[u], v[0], v[1], v[2], v[3]);
@@ -210,23 +213,27 @@ expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
                 v[j] = pack_bf16x2(x.x * f, x.y * f);
             }
-            const int64_t out = place[me.t].dst_row + (int64_t)(hc / C) * g.head_rows;
-            reinterpret_cast<uint4*>(kv ? v_out : k_out)[out * C + hc % C] =
+            out[(place[i + u * p.step].dst_row + head) * C + p.c] =
                 make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
 }
 
 // Tokens of a CTA: as few as fill its threads once, so that a decode step takes
-// one pass, and more on long prompts, so that a CTA spends less of its life
-// finding its tokens' pages; but still 32 CTAs an SM, to keep the last of them
-// short (18000 tokens of 8 heads written and read back: 75 us with 8 an SM, 65
-// with 16, 61 with 32, 64 with 64).
-int tokens_per_cta(const CacheGeom& g, int sms) {
+// one pass, and on long prompts as many as make whole waves of CTAs, so that all
+// of them look their pages up at once and none is left over (20000 tokens of 8
+// heads written and read back: 48 us in one wave, 50 in two or three, 56 in four;
+// 4 tokens of a thread under way and 5 CTAs an SM 48 us, 2 and 6 50, 6 and 4 49).
+dim3 write_grid(const CacheGeom& g, int sms, int& tokens) {
     const int per_token = 2 * g.Hkv * (g.D / 8);
-    int n = per_token >= kWriteThreads ? 1 : kWriteThreads / per_token;
-    while (n < kMaxTokens && (int64_t)n * sms * 32 < g.total_q) n *= 2;
-    return n < kMaxTokens ? n : kMaxTokens;
+    const int least = per_token >= kWriteThreads ? 1 : kWriteThreads / per_token;
+    const int wide = (per_token + kWriteThreads - 1) / kWriteThreads;
+    const int64_t resident = max(1, sms * kWriteCtas / wide);
+    const int64_t waves =
+        max((int64_t)1, (g.total_q + resident * kMaxTokens - 1) / (resident * kMaxTokens));
+    const int even = (int)((g.total_q + resident * waves - 1) / (resident * waves));
+    tokens = min(max(least, even), kMaxTokens);
+    return dim3((g.total_q + tokens - 1) / tokens, wide);
 }
 
 }  // namespace
@@ -236,8 +243,8 @@ cudaError_t launch_append(const CacheGeom& g, bool mx4, const void* k_new, const
                           const int32_t* ctx, const int32_t* ql, void* k_cache, void* k_scale,
                           void* v_cache, void* v_scale, float* weights, int32_t* err, int sms,
                           cudaStream_t stream) {
-    const int tokens = tokens_per_cta(g, sms);
-    const int grid = (g.total_q + tokens - 1) / tokens;
+    int tokens;
+    const dim3 grid = write_grid(g, sms, tokens);
     auto kern = g.D == 128 ? (mx4 ? append_kernel<128, true> : append_kernel<128, false>)
                            : (mx4 ? append_kernel<64, true> : append_kernel<64, false>);
     kern<<<grid, kWriteThreads, 0, stream>>>(
@@ -251,8 +258,8 @@ cudaError_t launch_expand(const CacheGeom& g, const void* k_cache, const void* k
                           const int32_t* ctx, const int32_t* ql, const int32_t* dst_table,
                           int dst_mpps, int dst_pages, void* k_out, void* v_out, int32_t* err,
                           int sms, cudaStream_t stream) {
-    const int tokens = tokens_per_cta(g, sms);
-    const int grid = (g.total_q + tokens - 1) / tokens;
+    int tokens;
+    const dim3 grid = write_grid(g, sms, tokens);
     auto kern = g.D == 128 ? expand_kernel<128> : expand_kernel<64>;
     kern<<<grid, kWriteThreads, 0, stream>>>(
         g, (const uint32_t*)k_cache, (const uint8_t*)k_scale, (const uint32_t*)v_cache,

@@ -152,6 +152,62 @@ def test_expand_reads_the_last_tokens_into_other_pages(dim, page, layout):
     assert same(out[0], want[0]) and same(out[1], want[1])
 
 
+@pytest.mark.parametrize("layout", [NHD, HND])
+@pytest.mark.parametrize("dim,kv_heads", [(128, 9), (128, 20), (64, 33), (128, 7)])
+def test_tokens_wider_and_narrower_than_a_cta(dim, kv_heads, layout):
+    """K and V of a token are 2 * kv_heads * dim / 8 threads' work: more than
+    one CTA's, with a remainder, or fewer than it has."""
+    ctx, ql = [45, 18, 3], [45, 1, 2]
+    case = R.Case(ctx, ql, heads=kv_heads, kv_heads=kv_heads, dim=dim, page=16, layout=layout, seed=6)
+    fresh = R.Case(ctx, ql, heads=kv_heads, kv_heads=kv_heads, dim=dim, page=16, layout=layout, seed=6)
+    w = torch.full((case.num_pages, kv_heads, 16), 3.0, device="cuda")
+    k, ks, v, vs, err = append(fresh, new_rows(case, case.kd).cuda(), new_rows(case, case.vd).cuda(),
+                               weights=w)
+    assert err == 0
+    want_w = torch.full((case.num_pages, kv_heads, 16), 3.0)
+    for b, (c, q) in enumerate(zip(ctx, ql)):
+        for got, sc, full, full_sc in ((k, ks, case.k, case.ks), (v, vs, case.v, case.vs)):
+            assert same(case.get(got.cpu(), b, c)[c - q:], case.get(full, b, c)[c - q:])
+            assert same(case.get(sc.cpu(), b, c)[c - q:], case.get(full_sc, b, c)[c - q:])
+        for p in range(c - q, c):
+            want_w[int(case.table[b, p // 16]), :, p % 16] = 0
+    assert same(w, want_w)
+    shape = case.shape(dim)
+    out = [torch.full(shape, 5.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    cl, qq = case.lens()
+    err = error_word()
+    B.pa_kv_expand(case.problem(B), k, ks, v, vs, dev(case.table), cl, qq, dev(case.table),
+                   case.num_pages, out[0], out[1], err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for b, (c, q) in enumerate(zip(ctx, ql)):
+        for got, n in zip(out, "kv"):
+            want = case.rows(n, b)[c - q:].to(torch.bfloat16)
+            assert same(case.get(got.cpu(), b, c)[c - q:], want)
+            assert bool((case.get(got.cpu(), b, c)[:c - q] == 5.0).all())
+
+
+def test_more_tokens_than_one_wave_holds():
+    """70001 tokens of one head: rows i of the new tokens hold the number i."""
+    n, page = 70001, 256
+    pages = -(-n // page)
+    rows = torch.arange(n, dtype=torch.int32).view(n, 1, 1).expand(n, 1, 32)
+    x = rows.contiguous().view(torch.int16).view(torch.bfloat16).cuda()      # [n, 1, 64], any bits
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(3)).int().cuda().view(1, -1)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    p = B.PaProblem(num_seqs=1, num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=page,
+                    num_pages=pages, max_pages_per_seq=pages, total_q_tokens=n, max_q_len=n,
+                    max_context_len=n, kv_dtype=BF16, sm_scale=1.0)
+    k, v = (torch.zeros((pages, page, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    err = error_word()
+    B.pa_kv_append(p, x, x, table, lens, lens, k, None, v, None, None, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for cache in (k, v):
+        got = cache.view(torch.int16)[table[0].long()].reshape(-1, 64)[:n].contiguous()
+        assert torch.equal(got, x.view(torch.int16).view(n, 64))
+
+
 def test_write_skips_what_it_cannot_place():
     """A page outside the pool, lengths that contradict each other, q_lens that
     do not add up: flagged, the rows concerned left out, the others written."""
@@ -304,6 +360,42 @@ def test_decode_is_deterministic_without_splits_and_leaves_other_rows():
                     dev(case.table), c, q, ws, out, None)
     torch.cuda.synchronize()
     assert torch.equal(out, a)
+
+
+def test_one_workspace_serves_problem_after_problem():
+    """Calls of different problems, split over many CTAs, in one workspace, and
+    two streams with a workspace each: bit for bit what a fresh one gives."""
+    cases = [R.Case([900, 5, 300], [1, 1, 1], heads=4, kv_heads=2, dim=64, seed=51),
+             R.Case([40] * 30, [1] * 30, heads=3, kv_heads=1, dim=128, seed=52),
+             R.Case([1500], [3], heads=8, kv_heads=1, dim=128, seed=53)]
+    calls = []
+    for c in cases:
+        p = c.problem(B)
+        calls.append((p, c.q.cuda(), dev(c.k), dev(c.ks), dev(c.v), dev(c.vs), dev(c.table),
+                      *c.lens()))
+    size = max(B.pa_mx4_workspace_size(a[0]) for a in calls)
+
+    def run(a, ws, stream=None):
+        out = torch.full((a[1].shape[0], a[1].shape[1], a[1].shape[2]), 7.0, dtype=torch.bfloat16,
+                         device="cuda")
+        lse = torch.full(out.shape[:2], 7.0, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        B.pa_decode_mx4(a[0], *a[1:], ws, out, lse, stream)
+        return out, lse
+
+    fresh = [run(a, torch.zeros(size, dtype=torch.uint8, device="cuda")) for a in calls]
+    torch.cuda.synchronize()
+    spaces = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(24):
+        got.append((i % 3, run(calls[i % 3], spaces[i % 2], streams[i % 2])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, fresh[i][0]) and torch.equal(lse, fresh[i][1])
+    for ws in spaces:
+        assert B.pa_last_device_error(ws) == 0
 
 
 def test_decode_flags_bad_pages_and_lengths():
@@ -559,6 +651,48 @@ def test_evict_longer_than_shared_memory_holds():
     assert got["kept"][1, 0].tolist() == keep
     rows = case.get(case.k, 1, n)[torch.tensor(keep)]
     assert same(case.get(got["k"].cpu(), 1, budget, dst), rows)
+
+
+@pytest.mark.parametrize("n,kinds", [
+    (5000, 1),          # all equal: more of the threshold's upper half than are listed
+    (5000, 3), (5000, 1 << 20),
+    (3000, 2),          # the same for short sequences
+    (100003, 5), (100003, 1 << 20),     # upper halves do not fit shared memory
+])
+def test_evict_of_many_equal_and_of_very_many_keys(n, kinds):
+    budget, first, recent, page = 1537, 5, 21, 256
+    g = torch.Generator().manual_seed(n + kinds)
+    pages = -(-n // page) + -(-budget // page)
+    perm = torch.randperm(pages, generator=g).int()
+    need = -(-n // page)
+    table, dst = perm[:need].view(1, -1).cuda(), perm[need:].view(1, -1).cuda()
+    # (halves of the mantissa differ, so that upper halves of the keys repeat)
+    w = torch.randint(0, kinds, (pages, 1, page), generator=g).float() * 1e-3 + 2.0
+    k = torch.arange(pages * page * 32, dtype=torch.int32).view(torch.int16).view(torch.bfloat16)
+    k = k.view(pages, page, 1, 64).cuda()
+    v = k.flip(0).contiguous()
+    p = B.PaProblem(num_seqs=1, num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=page,
+                    num_pages=pages, max_pages_per_seq=need, max_context_len=n, kv_dtype=BF16,
+                    sm_scale=1.0)
+    ctx = torch.tensor([n], dtype=torch.int32, device="cuda")
+    new = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = torch.zeros((1, 1, budget), dtype=torch.int32, device="cuda")
+    err, wd = error_word(), w.cuda()
+    old_k = k.view(torch.int16)[table[0].long()].reshape(-1, 64)
+    old_v = v.view(torch.int16)[table[0].long()].reshape(-1, 64)
+    B.pa_kv_evict(p, budget, first, recent, k, None, v, None, wd, table, dst, ctx, kept, new, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and int(new.item()) == budget
+    line = w[table[0].cpu().long()].reshape(-1)[:n].clone()
+    line[:first] = math.inf
+    line[n - recent:] = math.inf
+    want = torch.sort(torch.sort(-line, stable=True).indices[:budget]).values
+    assert torch.equal(kept.cpu().view(-1).long(), want)
+    for cache, old in ((k, old_k), (v, old_v)):
+        got = cache.view(torch.int16)[dst[0].long()].reshape(-1, 64)[:budget]
+        assert torch.equal(got, old[want.cuda()])
+    got = wd[dst[0].long()].reshape(-1)[:budget].cpu()
+    assert torch.equal(got, w[table[0].cpu().long()].reshape(-1)[want])
 
 
 def test_evict_flags_bad_input():
