@@ -6,7 +6,9 @@
 // weights, then one ordered pass that lists the kept positions (ties to the
 // lower one).  Move, a second launch over all SMs: 64 kept rows of K and V a
 // CTA, 16 bytes a thread.  The move is bound by HBM, the selection by the
-// latency of its passes.
+// latency of its passes and, with two CTAs an SM, by their instructions: 32
+// sequences of 8192 .. 32768 keys, 8 heads, 2048 kept: 55 + 86 us, where reading
+// the weights and moving the rows takes 83 us of HBM time.
 #include "pa_cache_common.cuh"
 
 namespace pa {
@@ -39,7 +41,7 @@ constexpr int hist_bytes(bool few) { return kBins * copies_of(few) * 4; }
 constexpr int kListed = 1024;
 // Keys whose upper halves shared memory holds
 constexpr int kMaxCached = (227 * 1024 - hist_bytes(false) - kListed * 8 - 4096) / 2;
-constexpr int kFewKeys = 4096;     // longest sequence that few threads select from
+constexpr int kFewKeys = 12288;    // longest sequence that few threads select from
 constexpr int kMoveRows = 64;
 
 constexpr int kMoveThreads = 256;
@@ -372,9 +374,12 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     const int cap = g.max_ctx <= kMaxCached ? g.max_ctx : kMaxCached;
     const int units = g.B * g.Hkv;
     const int pieces = mx4 ? g.D / 32 : g.D / 8, scale_bytes = mx4 ? g.D / 32 : 0;
-    // short sequences take few threads, so that an SM holds many of them
-    // (MEASURED)
-    const bool few = cap <= kFewKeys, wide = !few && units <= sms;
+    // Few threads a CTA where an SM gets several (512 pairs, 64 keys kept of 1000 /
+    // 4000 / 6000 / 12000: 17 / 25 / 29 / 46 us with 256 threads, 25 / 31 / 38 / 52
+    // with 512), 1024 where it gets one and the sequence is long (64 pairs of 6000:
+    // 18.6 us with 256, 17.4 with 512, 16.6 with 1024; of 20000: 29 with 512, 25
+    // with 1024).
+    const bool one = units <= sms, few = cap <= (one ? 4096 : kFewKeys), wide = !few && one;
     const int smem = hist_bytes(few) + kListed * 8 + (cap * 2 + 15) / 16 * 16;
     cudaError_t e = few    ? launch_select<256, true>(P, cap, units, smem, stream)
                     : wide ? launch_select<1024, false>(P, cap, units, smem, stream)
