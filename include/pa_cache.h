@@ -24,7 +24,9 @@
  *   context_lens that are negative, above the declared maxima, q_lens[b] >
  *   context_lens[b], or a sum of q_lens that is not total_q_tokens;
  *   PA_DEV_BAD_PAGE for a block-table entry outside [0, num_pages).  The rows
- *   concerned are skipped, the rest is done.
+ *   concerned are skipped, the rest is done.  PA_DEV_WAIT_TIMEOUT (only
+ *   pa_key_weights, with more than 16 rows of queries and heads): a pipeline
+ *   wait ran out; the weights are then unspecified.
  *
  * Shapes: head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; any number of
  * KV heads.  pa_problem's mask_q_tiles / mask_kv_tiles must be 0 and q_dtype
@@ -122,7 +124,9 @@ PA_API pa_status pa_decode_mx4(const pa_problem* problem, const void* q, const v
  * tokens of each sequence, any number of them: a decode step's, or the last
  * few of a prompt.  kv_dtype PA_BF16 or PA_MX4 (k_scale for PA_MX4 only; E4M3
  * is PA_ERR_UNSUPPORTED).  Sums are in a fixed order: equal inputs give equal
- * bits.
+ * bits.  (Hq / Hkv) * max_q_len decides between two kernels, whose sums differ
+ * in order; pa_test_inject_wait_timeout reaches the one for more than 16 rows,
+ * where skip_entry counts tiles of 256 keys.
  */
 PA_API pa_status pa_key_weights(const pa_problem* problem, const void* q, const void* k_cache,
                                 const void* k_scale, const int32_t* block_table,

@@ -38,6 +38,10 @@ struct ManyParams {
     const float* lse;
     float* weights;
     int32_t* err;
+    // Test hook: CTA 0 never announces item `skip` of half 0 (-1: none), and waits
+    // are shorter.
+    int32_t skip;
+    uint64_t wait_limit_ns;
 };
 
 template <int D, bool MX4>
@@ -261,7 +265,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
     // true, or the CTA gives up
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
-        if (mbar_wait_or_abort(bar, parity, kWaitLimitNs, abort_flag)) return true;
+        if (mbar_wait_or_abort(bar, parity, P.wait_limit_ns, abort_flag)) return true;
         *abort_flag = 1;
         flag_error(P.err, PA_DEV_WAIT_TIMEOUT);
         return false;
@@ -389,6 +393,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
         // (offsets within a run of 16 rows fit 32 bits)
         const uint32_t lane_off = (uint32_t)(lr * g.tok_rows) * ROW + c16 * 16;
         const uint32_t step = (uint32_t)(RPI * g.tok_rows) * ROW;
+        const int skip = blockIdx.x == 0 && grp == 0 ? P.skip : -1;
         int2 page = t.more() ? look_up(t) : make_int2(-1, -1);
         if constexpr (MX4) {
             // Rows come into the warp's ring by cp.async, coalesced, and from
@@ -466,7 +471,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                 tmem_st16(dst + 16 * (CH - 1), out[0]);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&k_full[grp]);
+                if ((int)n != skip) mbar_arrive(&k_full[grp]);
             }
         } else {
             for (uint32_t n = 0; t.more(); ++n) {
@@ -489,7 +494,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                 cp_async_commit();
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
-                mbar_arrive(&k_full[2 * slot + grp]);
+                if ((int)n != skip) mbar_arrive(&k_full[2 * slot + grp]);
             }
         }
     } else if (warp < kMmaWarp) {
@@ -641,6 +646,7 @@ cudaError_t launch_key_weights_many(const CacheGeom& g, bool mx4, const void* q,
     P.lse = lse;
     P.weights = weights;
     P.err = err;
+    take_test_hook(&P.skip, &P.wait_limit_ns);
     if (g.D == 128)
         return mx4 ? launch_many<128, true>(P, sms, stream) : launch_many<128, false>(P, sms, stream);
     return mx4 ? launch_many<64, true>(P, sms, stream) : launch_many<64, false>(P, sms, stream);

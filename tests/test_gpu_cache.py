@@ -544,6 +544,24 @@ def test_weights_of_many_rows(kv, dim, heads, kv_heads, page, ctx, ql, window):
                          kv=kv, window=window, seed=25))
 
 
+@pytest.mark.parametrize("kv", [BF16, MX4])
+@pytest.mark.parametrize("skip", [0, 2])
+def test_a_weights_wait_that_runs_out_is_reported_and_the_next_call_is_clean(kv, skip):
+    """One CTA's producer leaves a tile unannounced and the waits last 20 ms:
+    the call ends with the error word set, the next one is a normal one."""
+    # (items for more than three tiles of CTA 0, on any number of SMs)
+    case = R.Case([4000], [20], heads=64, kv_heads=32, dim=64, kv=kv, page=256, seed=26)
+    lse = torch.full((20, 64), 9.0).double()
+    zero = torch.zeros((case.num_pages, 32, 256))
+    good, err = run_weights(case, lse, zero)
+    assert err == 0
+    B.pa_test_inject_wait_timeout(skip, 20_000_000)
+    _, err = run_weights(case, lse, zero)
+    assert err == B.PA_DEV_WAIT_TIMEOUT
+    again, err = run_weights(case, lse, zero)
+    assert err == 0 and same(again, good)
+
+
 # -------------------------------------------------------------------- evict
 
 def run_evict(case, w, budget, first, recent, dst, **kw):
