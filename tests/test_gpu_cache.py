@@ -878,3 +878,55 @@ def test_a_captured_step_replays_on_new_lengths():
         # a softmax row's weights sum to one per q head
         assert abs(float(w.sum()) - 8.0) < 1e-4
     assert int(err.item()) == 0
+
+
+def test_a_captured_observation_and_eviction_replay_on_new_lengths():
+    """Weights of many query rows and the eviction that follows, captured once
+    (two kernels of which overlap), replayed with other lengths and queries:
+    bit for bit what eager calls give."""
+    page, budget, hk = 16, 70, 2
+    case = R.Case([400, 290, 130], [12, 12, 12], heads=8, kv_heads=hk, dim=64, page=page, kv=MX4,
+                  seed=61, spare=15)
+    p = case.problem(B)
+    dst = torch.tensor(case.spare, dtype=torch.int32).view(3, 5).cuda()
+    k, ks, v, vs = dev(case.k), dev(case.ks), dev(case.v), dev(case.vs)
+    base = [x.clone() for x in (k, ks, v, vs)]
+    c, q = case.lens()
+    t, qs = dev(case.table), case.q.cuda()
+    lse = torch.full((36, 8), 4.0, device="cuda")
+    w = torch.zeros((case.num_pages, hk, page), device="cuda")
+    kept = torch.zeros((3, hk, budget), dtype=torch.int32, device="cuda")
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    err = error_word()
+
+    def reset():
+        for x, y in zip((k, ks, v, vs), base):
+            x.copy_(y)
+        w.zero_()
+        kept.zero_()
+
+    def step():
+        B.pa_key_weights(p, qs, k, ks, t, c, q, lse, w, err)
+        B.pa_kv_evict(p, budget, 4, 8, k, ks, v, vs, w, t, dst, c, kept, new, err)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([400, 290, 130], [333, 64, 71], [70, 250, 12]):
+        c.copy_(torch.tensor(lens, dtype=torch.int32))
+        qs.copy_(torch.randn(tuple(qs.shape)).to(torch.bfloat16))
+        got = []
+        for run in (graph.replay, step):
+            reset()
+            run()
+            torch.cuda.synchronize()
+            got.append([x.clone() for x in (w, kept, new, k, ks, v, vs)])
+        assert new.tolist() == [min(x, budget) for x in lens]
+        for a, b in zip(*got):
+            assert same(a, b)
+    assert int(err.item()) == 0
