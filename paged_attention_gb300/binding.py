@@ -106,6 +106,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load the shared library (building it first if it is absent)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
