@@ -85,25 +85,38 @@ __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* t
     __syncthreads();
 }
 
+// The larger of two bf16 pairs, NaN if either is; a bf16 pair times another.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Quantise the 8 elements a lane holds of a block spread over 4 lanes.
 __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    // magnitudes of bf16 order like their bits
-    uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                            __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-    two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 1));
-    two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 2));
-    const uint32_t top = max(two & 0xffffu, two >> 16);
-    const uint32_t ex = top >> 7;   // biased exponent of the largest magnitude
+    uint32_t two = max_bf16x2(max_bf16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                              max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    two = max_bf16x2(two, __shfl_xor_sync(0xffffffffu, two, 1));
+    two = max_bf16x2(two, __shfl_xor_sync(0xffffffffu, two, 2));
+    // biased exponent of the largest magnitude (magnitudes order like their bits)
+    const uint32_t ex = max(two & 0xffffu, two >> 16) >> 7;
     e = ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
     if (ex == 255) return 0u;
-    const float inv = __uint_as_float((254u - e) << 23);   // 2^(127 - e), never subnormal
+    // times 2^(127 - e), never subnormal: exact in bf16 but for what is far
+    // below half the smallest code
+    const uint32_t inv = (254u - e) << 7;
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(w[i] << 16) * inv;
-        const float hi = __uint_as_float(w[i] & 0xffff0000u) * inv;
-        codes |= f32x2_to_e2m1x2(lo, hi) << (8 * i);
+        const uint32_t y = mul_bf16x2(w[i], inv | (inv << 16));
+        codes |= f32x2_to_e2m1x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u))
+                 << (8 * i);
     }
     return codes;
 }
@@ -127,7 +140,6 @@ append_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k_new,
     void* cache = p.kv ? v_cache : k_cache;
     uint8_t* scale = p.kv ? v_scale : k_scale;
     const int64_t head = (int64_t)p.h * g.head_rows;
-    const int lane = threadIdx.x & 31;
     // every lane of a warp takes part in the shuffles: the trip count is
     // uniform; U tokens' loads are under way at a time
     constexpr int U = 4;
@@ -143,25 +155,13 @@ append_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k_new,
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            uint32_t codes = 0, scales = 0;
-            if constexpr (MX4) {
-                uint32_t e;
-                codes = quantise8(x[u], e);
-                // the row's scale bytes, collected in its first lane
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j)
-                    scales |= __shfl_sync(0xffffffffu, e, (lane & ~(C - 1)) + 4 * j) << (8 * j);
-            }
+            uint32_t codes = 0, e = 0;
+            if constexpr (MX4) codes = quantise8(x[u], e);
             if (row[u] < 0) continue;
             const int64_t to = row[u] + head;
             if constexpr (MX4) {
                 reinterpret_cast<uint32_t*>(cache)[to * C + p.c] = codes;
-                if (p.c == 0) {
-                    if constexpr (D == 128)
-                        reinterpret_cast<uint32_t*>(scale)[to] = scales;
-                    else
-                        reinterpret_cast<uint16_t*>(scale)[to] = (uint16_t)scales;
-                }
+                if (p.c % 4 == 0) scale[to * (D / 32) + p.c / 4] = (uint8_t)e;
             } else {
                 reinterpret_cast<uint4*>(cache)[to * C + p.c] = x[u];
             }
@@ -205,13 +205,14 @@ expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (row[u] < 0) continue;
-            const float f = e8m0_to_f32(e[u]);
+            // 2^(e - 127) in bf16
+            const uint32_t f = e[u] == 0 ? 0x0040u : e[u] == 255 ? 0x7fc0u : e[u] << 7;
             uint32_t v[4];
             e2m1x8_to_f16(w[u], v[0], v[1], v[2], v[3]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-                v[j] = pack_bf16x2(x.x * f, x.y * f);
+                v[j] = mul_bf16x2(pack_bf16x2(x.x, x.y), f | (f << 16));
             }
             out[(place[i + u * p.step].dst_row + head) * C + p.c] =
                 make_uint4(v[0], v[1], v[2], v[3]);
