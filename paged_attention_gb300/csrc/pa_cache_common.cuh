@@ -26,6 +26,14 @@ __device__ __forceinline__ int64_t row_of(const CacheGeom& g, int page, int slot
     return (int64_t)page * g.ps * g.Hkv + (int64_t)slot * g.tok_rows + (int64_t)head * g.head_rows;
 }
 
+// Every kernel of the cache operators is launched as a dependent of the kernel
+// before it on the stream (launch_dependent) and waits for that kernel, and for
+// what it wrote, before it does anything else: launches of a serving step's row
+// of short kernels then overlap (three short sequences decoded: 8.4 -> 6.9 us a
+// call).  None lets the next one start before it ends: CTAs that wait take room
+// from those that run (evict 32 prompts: 129 us, with an early start 145; decode
+// 64 sequences: 105 and 111).
+
 __device__ __forceinline__ void flag_error(int32_t* err, int code) {
     if (err != nullptr) atomicOr(err, code);
 }

@@ -130,6 +130,7 @@ append_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k_new,
               const int32_t* __restrict__ table, const int32_t* __restrict__ ctx,
               const int32_t* __restrict__ ql, void* k_cache, uint8_t* k_scale, void* v_cache,
               uint8_t* v_scale, float* weights, int32_t* err, int tokens) {
+    grid_dependency_wait();
     constexpr int C = D / 8;   // threads of a row
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
@@ -179,6 +180,7 @@ expand_kernel(const CacheGeom g, const uint32_t* __restrict__ k_cache,
               const int32_t* __restrict__ ctx, const int32_t* __restrict__ ql,
               const int32_t* __restrict__ dst_table, int dst_mpps, int dst_pages, void* k_out,
               void* v_out, int32_t* err, int tokens) {
+    grid_dependency_wait();
     constexpr int C = D / 8;
     __shared__ TokenPlace place[kMaxTokens];
     const int t0 = blockIdx.x * tokens, n = min(tokens, g.total_q - t0);
@@ -248,10 +250,10 @@ cudaError_t launch_append(const CacheGeom& g, bool mx4, const void* k_new, const
     const dim3 grid = write_grid(g, sms, tokens);
     auto kern = g.D == 128 ? (mx4 ? append_kernel<128, true> : append_kernel<128, false>)
                            : (mx4 ? append_kernel<64, true> : append_kernel<64, false>);
-    kern<<<grid, kWriteThreads, 0, stream>>>(
-        g, (const __nv_bfloat16*)k_new, (const __nv_bfloat16*)v_new, k_stride, v_stride, table,
-        ctx, ql, k_cache, (uint8_t*)k_scale, v_cache, (uint8_t*)v_scale, weights, err, tokens);
-    return cudaGetLastError();
+    return launch_dependent(kern, grid, dim3(kWriteThreads), 0, stream, g,
+                            (const __nv_bfloat16*)k_new, (const __nv_bfloat16*)v_new, k_stride,
+                            v_stride, table, ctx, ql, k_cache, (uint8_t*)k_scale, v_cache,
+                            (uint8_t*)v_scale, weights, err, tokens);
 }
 
 cudaError_t launch_expand(const CacheGeom& g, const void* k_cache, const void* k_scale,
@@ -262,11 +264,10 @@ cudaError_t launch_expand(const CacheGeom& g, const void* k_cache, const void* k
     int tokens;
     const dim3 grid = write_grid(g, sms, tokens);
     auto kern = g.D == 128 ? expand_kernel<128> : expand_kernel<64>;
-    kern<<<grid, kWriteThreads, 0, stream>>>(
-        g, (const uint32_t*)k_cache, (const uint8_t*)k_scale, (const uint32_t*)v_cache,
-        (const uint8_t*)v_scale, table, ctx, ql, dst_table, dst_mpps, dst_pages, k_out, v_out, err,
-        tokens);
-    return cudaGetLastError();
+    return launch_dependent(kern, grid, dim3(kWriteThreads), 0, stream, g,
+                            (const uint32_t*)k_cache, (const uint8_t*)k_scale,
+                            (const uint32_t*)v_cache, (const uint8_t*)v_scale, table, ctx, ql,
+                            dst_table, dst_mpps, dst_pages, k_out, v_out, err, tokens);
 }
 
 }  // namespace pa

@@ -196,6 +196,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = lane >> 2, t4 = lane & 3;   // operand row, column pair
     const int cost = P.unit_cost;
+    grid_dependency_wait();
 
     // ---- this CTA's share of the flat line
     auto seq_cost = [&](int b) -> int64_t {
@@ -882,8 +883,8 @@ cudaError_t launch_mx4(const Mx4Params& P, int grid, cudaStream_t stream) {
     using Cfg = Mx4Cfg<D, NT>;
     const cudaError_t e = allow_smem<decode_mx4_kernel<D, NT>>(Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    decode_mx4_kernel<D, NT><<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(decode_mx4_kernel<D, NT>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem,
+                            stream, P);
 }
 
 }  // namespace

@@ -82,6 +82,7 @@ key_weights_kernel(const __grid_constant__ WeightParams P) {
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = lane >> 2, t4 = lane & 3;
+    grid_dependency_wait();
 
     auto cost = [&](int b) -> int64_t {
         int first;
@@ -378,8 +379,8 @@ cudaError_t launch_weights(const WeightParams& P, int sms, cudaStream_t stream) 
     constexpr int smem = weight_rows_at<D>() + kWeightWarps * weight_stage<D, MX4>();
     const cudaError_t e = allow_smem<key_weights_kernel<D, MX4>>(smem);
     if (e != cudaSuccess) return e;
-    key_weights_kernel<D, MX4><<<sms * kCtas, kWeightThreads, smem, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(key_weights_kernel<D, MX4>, dim3(sms * kCtas), dim3(kWeightThreads),
+                            smem, stream, P);
 }
 
 }  // namespace

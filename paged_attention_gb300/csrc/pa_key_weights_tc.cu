@@ -233,6 +233,7 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const CacheGeom& g = P.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
@@ -625,8 +626,7 @@ cudaError_t launch_many(const ManyParams& P, int sms, cudaStream_t stream) {
     static_assert(smem <= 232448, "shared memory of an SM");
     const cudaError_t e = allow_smem<key_weights_many_kernel<D, MX4>>(smem);
     if (e != cudaSuccess) return e;
-    kern<<<sms, kThreads, smem, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(sms), dim3(kThreads), smem, stream, P);
 }
 
 }  // namespace

@@ -7,8 +7,8 @@
 // lower one).  Move, a second launch over all SMs: 64 kept rows of K and V a
 // CTA, 16 bytes a thread.  The move is bound by HBM, the selection by the
 // latency of its passes and, with two CTAs an SM, by their instructions: 32
-// sequences of 8192 .. 32768 keys, 8 heads, 2048 kept: 55 + 86 us, where reading
-// the weights and moving the rows takes 83 us of HBM time.
+// sequences of 8192 .. 32768 keys, 8 heads, 2048 kept: 129 us, 85 of them the move,
+// where reading the weights and moving the rows takes 83 us of HBM time.
 #include "pa_cache_common.cuh"
 
 namespace pa {
@@ -55,7 +55,7 @@ move_kernel(const __grid_constant__ EvictParams P, int chunks, int scale_bytes) 
         int64_t src[kMoveRows], dst[kMoveRows];
     } at;
     const CacheGeom& g = P.g;
-    grid_dependency_wait();                     // (launched while the selection runs)
+    grid_dependency_wait();
     const int unit = blockIdx.x / chunks, r0 = blockIdx.x % chunks * kMoveRows;
     const int b = unit / g.Hkv, hk = unit % g.Hkv, c = P.ctx[b], tid = threadIdx.x;
     if (c <= P.budget || c > g.max_ctx) return;
@@ -119,6 +119,7 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 template <int kSelectThreads, bool FEW>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
+    grid_dependency_wait();
     constexpr int kSelectWarps = kSelectThreads / 32, kCopies = copies_of(FEW);
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
@@ -138,7 +139,6 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
         if (bad) flag_error(P.err, PA_DEV_BAD_LENGTHS);
     }
     if (bad || c <= P.budget) return;
-    grid_launch_dependents();
     const int32_t* row = P.table + (int64_t)b * g.mpps;
     // (no branches: the loads of a loop's iterations run together; a page that
     // is none counts as the smallest key, and the move flags it)
@@ -342,8 +342,8 @@ cudaError_t launch_select(const EvictParams& P, int cap, int units, int smem, cu
     const cudaError_t e = allow_smem<select_kernel<kSelectThreads, FEW>>(
         hist_bytes(FEW) + kListed * 8 + (FEW ? kFewKeys : kMaxCached) * 2 + 16);
     if (e != cudaSuccess) return e;
-    select_kernel<kSelectThreads, FEW><<<units, kSelectThreads, smem, stream>>>(P, cap);
-    return cudaGetLastError();
+    return launch_dependent(select_kernel<kSelectThreads, FEW>, dim3(units), dim3(kSelectThreads),
+                            smem, stream, P, cap);
 }
 
 }  // namespace
