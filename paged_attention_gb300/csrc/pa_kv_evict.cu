@@ -152,6 +152,17 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     };
     const bool in_smem = c <= cached_cap;
     auto upper = [&](int i) -> uint32_t { return in_smem ? cached[i] : key_at(i) >> 16; };
+    // the upper halves of eight keys that shared memory holds (i a multiple of 8;
+    // behind the last key: anything)
+    auto eight = [&](int i, uint32_t* u) {
+        const uint4 v = *reinterpret_cast<const uint4*>(cached + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u[2 * j] = w[j] & 0xffffu;
+            u[2 * j + 1] = w[j] >> 16;
+        }
+    };
     auto clear = [&]() {
         for (int i = tid; i < kBins * kCopies / 4; i += kSelectThreads)
             reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
@@ -260,14 +271,12 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
         if (shift == 16 && in_smem) {
             listed = bins[prefix & 255u] <= kListed;
             if (listed) {
-                for (int i = tid; i < c; i += 8 * kSelectThreads) {
-                    uint32_t x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = cached[min(i + j * kSelectThreads, c - 1)];
+                for (int i = 8 * tid; i < c; i += 8 * kSelectThreads) {
+                    uint32_t u[8];
+                    eight(i, u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (i + j * kSelectThreads < c && x[j] == prefix)
-                            list[atomicAdd(&s_listed, 1)].x = i + j * kSelectThreads;
+                        if (u[j] == prefix && i + j < c) list[atomicAdd(&s_listed, 1)].x = i + j;
                 }
                 __syncthreads();
                 for (int i = tid; i < s_listed; i += kSelectThreads)
@@ -287,53 +296,70 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     }
     // kept: keys above `prefix`, and the first `left` that equal it
 
-    // ---- list the kept positions; a warp owns a run of positions
-    const int per_warp = ((c + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+    // ---- list the kept positions; a warp owns a run of positions, a lane eight
+    // neighbours of it at a time
+    const int per_warp = (c + 256 * kSelectWarps - 1) / (256 * kSelectWarps) * 256;
     const int i0 = min(c, warp * per_warp), i1 = min(c, i0 + per_warp);
-    // 1: above the threshold, 0: equal, -1: below
-    auto side = [&](int i) -> int {
-        const uint32_t u = upper(i), pu = prefix >> 16;
-        if (u != pu) return u > pu ? 1 : -1;
-        const uint32_t x = key_at(i);
-        return x > prefix ? 1 : x == prefix ? 0 : -1;
-    };
-    int na, ne;                                       // kept before this warp's run
     int32_t* out = P.kept + (int64_t)blockIdx.x * P.budget;
-    const uint32_t below = (1u << lane) - 1u;
-    auto sweep = [&](auto side_of) {
+    // sides(i, x): of keys i .. i + 7, 1 above the threshold, 0 equal, -1 below
+    auto sweep = [&](auto sides) {
+        uint32_t mine = 0;                            // above, and equal << 16, of a warp's turn
         int above = 0, equal = 0;
-#pragma unroll 8
-        for (int i = i0; i < i1; i += 32) {
-            const int x = i + lane < i1 ? side_of(i + lane) : -1;
-            above += __popc(__ballot_sync(0xffffffffu, x == 1));
-            equal += __popc(__ballot_sync(0xffffffffu, x == 0));
+        auto tally = [&](const int* x) {
+            mine = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mine += x[j] > 0 ? 1u : x[j] == 0 ? 0x10000u : 0u;
+        };
+        for (int i = i0 + 8 * lane; i < i1; i += 256) {
+            int x[8];
+            sides(i, x);
+            tally(x);
+            above += (int)(mine & 0xffffu);
+            equal += (int)(mine >> 16);
         }
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
         if (lane == 0) s_count[warp] = make_int2(above, equal);
         __syncthreads();
-        const int2 mine = lane < kSelectWarps ? s_count[lane] : make_int2(0, 0);
-        const int ea = warp_inclusive(mine.x, lane) - mine.x;
-        const int ee = warp_inclusive(mine.y, lane) - mine.y;
-        na = __shfl_sync(0xffffffffu, ea, warp);
-        ne = __shfl_sync(0xffffffffu, ee, warp);
-#pragma unroll 8
-        for (int i = i0; i < i1; i += 32) {
-            const int x = i + lane < i1 ? side_of(i + lane) : -1;
-            const uint32_t ma = __ballot_sync(0xffffffffu, x == 1);
-            const uint32_t me = __ballot_sync(0xffffffffu, x == 0);
-            const int a = na + __popc(ma & below), e = ne + __popc(me & below);
-            if (x == 1 || (x == 0 && e < (int)left)) out[a + min(e, (int)left)] = i + lane;
-            na += __popc(ma);
-            ne += __popc(me);
+        const int2 all = lane < kSelectWarps ? s_count[lane] : make_int2(0, 0);
+        const int ea = warp_inclusive(all.x, lane) - all.x;
+        const int ee = warp_inclusive(all.y, lane) - all.y;
+        int na = __shfl_sync(0xffffffffu, ea, warp);  // kept before this warp's turn
+        int ne = __shfl_sync(0xffffffffu, ee, warp);
+        for (int k = i0; k < i1; k += 256) {
+            const int i = k + 8 * lane;
+            int x[8] = {-1, -1, -1, -1, -1, -1, -1, -1};
+            if (i < i1) sides(i, x);
+            tally(x);
+            const uint32_t inc = (uint32_t)warp_inclusive((int)mine, lane);
+            int a = na + (int)((inc - mine) & 0xffffu), e = ne + (int)((inc - mine) >> 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (x[j] > 0 || (x[j] == 0 && e < (int)left)) out[a + min(e, (int)left)] = i + j;
+                a += x[j] > 0;
+                e += x[j] == 0;
+            }
+            const uint32_t turn = __shfl_sync(0xffffffffu, inc, 31);
+            na += (int)(turn & 0xffffu);
+            ne += (int)(turn >> 16);
         }
     };
     if (listed) {
         const uint32_t pu = prefix >> 16;
-        sweep([&](int i) -> int {
-            const uint32_t u = cached[i];
-            return (u > pu) - (u < pu);
+        sweep([&](int i, int* x) {
+            uint32_t u[8];
+            eight(i, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = i + j < c ? (u[j] > pu) - (u[j] < pu) : -1;
         });
     } else {
-        sweep(side);
+        sweep([&](int i, int* x) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t k = key_at(min(i + j, c - 1));
+                x[j] = i + j < c ? (k > prefix) - (k < prefix) : -1;
+            }
+        });
     }
 }
 
