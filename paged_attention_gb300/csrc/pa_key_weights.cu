@@ -38,8 +38,8 @@ constexpr int kWeightThreads = 32 * kWeightWarps;
 
 // Up to this many query rows (of the longest q_len) this kernel runs; above,
 // the one on tcgen05 (16 sequences of 8000 keys, 8 KV heads, here / there: 8 rows
-// bf16 46 / 48 us, 4-bit 35 / 35; 16 rows 49 / 48 and 50 / 55; 24 rows 53 / 48
-// and 64 / 55; 64 rows 88 / 48 and 136 / 51).
+// bf16 46 / 48 us, 4-bit 35 / 35; 16 rows 49 / 48 and 50 / 55; 24 rows 53 / 46
+// and 64 / 51; 64 rows 88 / 46 and 136 / 49).
 constexpr int kFewRows = 16;
 
 // Bytes of a warp's place for 32 keys' rows (and scale words).

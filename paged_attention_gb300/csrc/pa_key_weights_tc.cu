@@ -14,6 +14,13 @@
 // Roles: two groups of 4 warps take the accumulators, one group for each half;
 // two groups of 4 bring K, 2 warps bring Q, 2 issue the products.  All waits
 // are bounded.
+//
+// 8 prompts of 4096 .. 16384 keys, 8 heads, 128 rows: 36 us 4-bit (80 on mma.sync,
+// 41 with both operands in shared memory), of which 9 are the tensor cores', 7 the
+// exponentials'; the conversion of K and the steps between the roles set the pace,
+// about 2 us for 256 keys by 128 rows.  With 512 rows it is 1.5 us.
+#include <type_traits>
+
 #include "pa_cache_mma.cuh"
 
 namespace pa {
@@ -320,7 +327,9 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                         tmem_ld32(acc + c0, v);
                         tmem_wait_ld();
                         reg_fence32(v);
-                        if (clear && c0 + 32 <= nr) {
+                        // (columns behind the last row are left out, not multiplied
+                        // by nothing: their scores can be NaN)
+                        auto take = [&](auto whole) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
                                 const ulonglong2 o =
@@ -328,9 +337,20 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                                 const float2 x = split2(fma2(make2(v[i], v[i + 1]), factor2, o.x));
                                 const float2 y =
                                     split2(fma2(make2(v[i + 2], v[i + 3]), factor2, o.y));
-                                sum0 = add2(sum0, make2(ex2(x.x), ex2(x.y)));
-                                sum1 = add2(sum1, make2(ex2(y.x), ex2(y.y)));
+                                float e[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+                                if constexpr (!decltype(whole)::value) {
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        if (c0 + i + j >= nr) e[j] = 0.f;
+                                }
+                                sum0 = add2(sum0, make2(e[0], e[1]));
+                                sum1 = add2(sum1, make2(e[2], e[3]));
                             }
+                        };
+                        if (clear && c0 + 32 <= nr) {
+                            take(std::true_type());
+                        } else if (clear) {
+                            take(std::false_type());
                         } else {
                             float s = 0.f;
 #pragma unroll
@@ -373,10 +393,11 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
             if (g.ps == 16) p.y = key + 16 < x.c ? row[(key >> 4) + 1] : -1;
             return p;
         };
-        // Offsets in K of the two runs' first rows.  Keys that do not exist, or
-        // whose page does not, get rows that do: their sums go nowhere.
+        // The two runs' pages and first rows in them (a page's rows are fewer
+        // than 2^23, their bytes than 2^32).  Keys that do not exist, or whose
+        // page does not, get rows that do: their sums go nowhere.
         struct Runs {
-            int64_t a, b;
+            uint32_t page_a, page_b, row_a, row_b;
         };
         auto runs_of = [&](const Walk& x, int2 p) -> Runs {
             const int key = x.key0 + my, left = x.c - key;
@@ -386,12 +407,16 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                 flag_error(P.err, PA_DEV_BAD_PAGE);
             const int head = x.hk * g.head_rows;
             Runs r;
-            r.a = (int64_t)(oka ? p.x : 0) * page_rows + ((key & (g.ps - 1)) * g.tok_rows + head);
-            r.b = (int64_t)(okb ? p.y : 0) * page_rows +
-                  (((key + 16) & (g.ps - 1)) * g.tok_rows + head);
+            r.page_a = oka ? p.x : 0;
+            r.page_b = okb ? p.y : 0;
+            r.row_a = (key & (g.ps - 1)) * g.tok_rows + head;
+            r.row_b = ((key + 16) & (g.ps - 1)) * g.tok_rows + head;
             return r;
         };
-        // (offsets within a run of 16 rows fit 32 bits)
+        const uint32_t page_bytes = (uint32_t)page_rows * ROW;
+        auto at_row = [&](uint32_t pg, uint32_t row) -> const uint8_t* {
+            return P.k + ((uint64_t)pg * page_bytes + row * ROW);
+        };
         const uint32_t lane_off = (uint32_t)(lr * g.tok_rows) * ROW + c16 * 16;
         const uint32_t step = (uint32_t)(RPI * g.tok_rows) * ROW;
         const int skip = blockIdx.x == 0 && grp == 0 ? P.skip : -1;
@@ -413,18 +438,21 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                 if (ahead.more()) {
                     const Runs r = runs_of(ahead, page);
                     const uint32_t place = ring + put * S::kPlace;
-                    const uint8_t* ka = P.k + r.a * ROW;
-                    const uint8_t* kb = P.k + r.b * ROW;
+                    const uint8_t* ka = at_row(r.page_a, r.row_a) + lane_off;
+                    const uint8_t* kb = at_row(r.page_b, r.row_b) + lane_off;
 #pragma unroll
                     for (int j = 0; j < NI; ++j) {
                         const int x = j * RPI + lr;
                         cp_async16(place + x * ROW + chunk_at(x, c16) * 16,
-                                   (j * RPI < 16 ? ka : kb) + (lane_off + (j * RPI & 15) / RPI * step),
+                                   (j * RPI < 16 ? ka : kb) + (j * RPI & 15) / RPI * step,
                                    16, once);
                     }
                     // (head_dim 64: the word that holds the key's two bytes)
-                    const int64_t row = (lane < 16 ? r.a : r.b) + (lane & 15) * g.tok_rows;
-                    cp_async4(place + 32 * ROW + lane * 4, P.ks + (row * KB & ~(int64_t)3), 4, once);
+                    const uint32_t row =
+                        (lane < 16 ? r.row_a : r.row_b) + (lane & 15) * (uint32_t)g.tok_rows;
+                    const uint64_t so = (uint64_t)(lane < 16 ? r.page_a : r.page_b) *
+                                            ((uint32_t)page_rows * KB) + (row * KB & ~3u);
+                    cp_async4(place + 32 * ROW + lane * 4, P.ks + so, 4, once);
                     ahead.advance(P);
                     if (ahead.more()) page = look_up(ahead);
                 }
@@ -483,13 +511,13 @@ key_weights_many_kernel(const __grid_constant__ ManyParams P) {
                 if (!warp_wait(&k_empty[2 * slot + grp], ((n >> 1) & 1) ^ 1)) break;
                 const uint32_t dst =
                     sbase + S::kK + (uint32_t)((2 * slot + grp) * NB + (c16 >> 3)) * S::kKBlock;
-                const uint8_t* ka = P.k + r.a * ROW;
-                const uint8_t* kb = P.k + r.b * ROW;
+                const uint8_t* ka = at_row(r.page_a, r.row_a) + lane_off;
+                const uint8_t* kb = at_row(r.page_b, r.row_b) + lane_off;
 #pragma unroll 8
                 for (int j = 0; j < NI; ++j) {
                     const int y = 32 * quad + j * RPI + lr;
                     cp_async16(dst + y * 128 + (((c16 & 7) ^ (y & 7)) << 4),
-                               (j * RPI < 16 ? ka : kb) + (lane_off + (j * RPI & 15) / RPI * step),
+                               (j * RPI < 16 ? ka : kb) + (j * RPI & 15) / RPI * step,
                                16, once);
                 }
                 cp_async_commit();

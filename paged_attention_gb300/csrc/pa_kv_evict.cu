@@ -407,13 +407,13 @@ cudaError_t launch_evict(const CacheGeom& g, bool mx4, int budget, int num_first
     // with 1024).
     const bool one = units <= sms, few = cap <= (one ? 4096 : kFewKeys), wide = !few && one;
     const int smem = hist_bytes(few) + kListed * 8 + (cap * 2 + 15) / 16 * 16;
+    const int chunks = (budget + kMoveRows - 1) / kMoveRows;
+    const int64_t grid = (int64_t)units * chunks;
+    if (g.max_ctx > budget && grid > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = few    ? launch_select<256, true>(P, cap, units, smem, stream)
                     : wide ? launch_select<1024, false>(P, cap, units, smem, stream)
                            : launch_select<512, false>(P, cap, units, smem, stream);
     if (e != cudaSuccess || g.max_ctx <= budget) return e;
-    const int chunks = (budget + kMoveRows - 1) / kMoveRows;
-    const int64_t grid = (int64_t)units * chunks;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
     auto move = pieces == 16  ? move_kernel<16>
                 : pieces == 8 ? move_kernel<8>
                 : pieces == 4 ? move_kernel<4>
