@@ -56,11 +56,12 @@ constexpr int kMinShare = 4;
 template <int D, int NT>
 struct Mx4Cfg {
     // CTAs of an SM: what the registers of a thread (O alone takes NT D / 4)
-    // leave room for.  Measured on 64 sequences of 128 to 32768 tokens, 8 rows,
-    // D = 128: 3 CTAs of 4 warps (168 registers) 114 us, 4 (128 registers, and
-    // spills) 125; with 24 rows 2 CTAs (255 registers) 511 us, 3 spill
+    // leave room for.  Measured on 64 sequences of 128 to 32768 tokens: 8 rows, D =
+    // 128, 3 CTAs of 4 warps (168 registers) 114 us, 4 (128 registers, and spills)
+    // 125; 16 rows, D = 128, 2 CTAs (255 registers) 152 us, 3 (spills) 177; 32
+    // rows, D = 64, 190 and 201
     static constexpr int kPerThread = NT * D;
-    static constexpr int kCtas = kPerThread <= 256 ? 3 : 2;
+    static constexpr int kCtas = kPerThread <= 128 ? 3 : 2;
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = kPerThread <= 128 ? 2 : 3;   // (3 and 4 measured the same)
