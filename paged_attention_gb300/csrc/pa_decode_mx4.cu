@@ -113,9 +113,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// A unit (sequence, KV head) as a CTA meets it.
+// A unit (sequence, KV head, block of query rows) as a CTA meets it.
 struct Unit {
-    int b, hk;
+    int b, hk, blk;
     int ctx, ql, row0;     // lengths, first query row
     int n, first;          // tiles, the first tile any row sees
     int64_t start;         // position of its fixed cost on the flat line
@@ -136,8 +136,11 @@ __device__ __forceinline__ void load_seq(const Mx4Params& P, Unit& u) {
 }
 
 // The unit after u (every lane the same); false past the last sequence.
+template <int RB>
 __device__ __forceinline__ bool next_unit(const Mx4Params& P, Unit& u) {
     u.start += P.unit_cost + u.n;
+    if (RB > 1 && ++u.blk < RB) return true;
+    u.blk = 0;
     if (++u.hk < P.g.Hkv) return true;
     u.hk = 0;
     do {
@@ -184,7 +187,8 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     return D == 128 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
 }
 
-template <int D, int NT>
+// NT row tiles of 8 at a time; RB: blocks of that many rows, each a unit of its own.
+template <int D, int NT, int RB>
 __global__ void __launch_bounds__(Mx4Cfg<D, NT>::kThreads, Mx4Cfg<D, NT>::kCtas)
 decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     using Cfg = Mx4Cfg<D, NT>;
@@ -203,7 +207,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     auto seq_cost = [&](int b) -> int64_t {
         int first;
         const int n = seq_tiles(g, P.ctx[b], P.ql[b], first);
-        return n > 0 ? (int64_t)g.Hkv * (n + cost) : 0;
+        return n > 0 ? (int64_t)g.Hkv * RB * (n + cost) : 0;
     };
     const int64_t C = flat_total(g.B, lane, seq_cost);
     if (blockIdx.x == 0 && warp == 0) check_lens(g, P.ctx, P.ql, lane, P.header + H_ERROR);
@@ -219,8 +223,10 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         rows);
         load_seq(P, u);
         u.row0 = rows;
-        u.hk = (int)((lo - start) / (u.n + cost));
-        u.start = start + (int64_t)u.hk * (u.n + cost);
+        const int i = (int)((lo - start) / (u.n + cost));
+        u.hk = i / RB;
+        u.blk = i % RB;
+        u.start = start + (int64_t)i * (u.n + cost);
     }
 
     const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::kStage;
@@ -253,7 +259,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     int l_b = u.b;
     int win_lo = first_page(ls);             // 32 page ids, the 32 after them, the next unit's
     int win = page_ids(u, win_lo), nxt = page_ids(u, win_lo + 32), lnw = -1;
-    bool ln_ok = next_unit(P, ln) && ln.start < hi;
+    bool ln_ok = next_unit<RB>(P, ln) && ln.start < hi;
     if (ln_ok) lnw = page_ids(ln, first_page(share_of(ln, cost, lo, hi, warp, W)));
     auto issue = [&](int stage) {
         while (more && l_tok >= l_end) {
@@ -268,7 +274,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
             win_lo = first_page(x);
             win = lnw;
             nxt = page_ids(ln, win_lo + 32);
-            ln_ok = next_unit(P, ln) && ln.start < hi;
+            ln_ok = next_unit<RB>(P, ln) && ln.start < hi;
             if (ln_ok) lnw = page_ids(ln, first_page(share_of(ln, cost, lo, hi, warp, W)));
         }
         if (more) {
@@ -343,8 +349,13 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
 
     // ---- Q rows of a unit, one warp a row: read ahead of the unit that needs them
     uint32_t qw[Cfg::kQPerWarp][D / 64];
+    // (rows past total_q_tokens, lengths that do not add up, are not there)
+    auto rows_of = [&](const Unit& x) -> int {
+        const int rows = x.row0 + x.ql <= g.total_q ? g.G * x.ql : 0;
+        return RB > 1 ? max(0, min(Cfg::kRows, rows - x.blk * Cfg::kRows)) : rows;
+    };
     auto load_q = [&](const Unit& x) {
-        const int R = x.row0 + x.ql <= g.total_q ? g.G * x.ql : 0;
+        const int R = rows_of(x), r0 = x.blk * Cfg::kRows;
 #pragma unroll
         for (int k = 0; k < Cfg::kQPerWarp; ++k) {
             const int r = warp + k * W;
@@ -352,7 +363,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
             for (int j = 0; j < D / 64; ++j) qw[k][j] = 0u;
             if (r < R) {
                 const __nv_bfloat16* src =
-                    P.q + ((int64_t)(x.row0 + r / g.G) * g.Hq + x.hk * g.G + r % g.G) * D;
+                    P.q + ((int64_t)(x.row0 + (r0 + r) / g.G) * g.Hq + x.hk * g.G + (r0 + r) % g.G) * D;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j)
                     qw[k][j] = reinterpret_cast<const uint32_t*>(src)[lane + 32 * j];
@@ -363,8 +374,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
 
     // ---- units
     while (true) {
-        // rows past total_q_tokens (lengths that do not add up) are not there
-        const int R = u.row0 + u.ql <= g.total_q ? g.G * u.ql : 0;
+        const int R = rows_of(u), r0 = u.blk * Cfg::kRows;
         const int ctx = u.ctx, pbase = u.ctx - u.ql;
         const Share sh = share_of(u, cost, lo, hi, warp, W);
         // Q rows as f16 with a power of two taken out of each: no element
@@ -397,7 +407,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
         }
         __syncthreads();
         Unit nu = u;
-        const bool has_next = next_unit(P, nu) && nu.start < hi;
+        const bool has_next = next_unit<RB>(P, nu) && nu.start < hi;
         if (has_next) load_q(nu);
 
         float m[NT][2], l[NT][2], fq[NT][2];
@@ -411,7 +421,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                 m[nt][e] = -INFINITY;
                 l[nt][e] = 0.f;
                 fq[nt][e] = info[r];
-                pr[nt][e] = r < R ? pbase + r / g.G : -1;
+                pr[nt][e] = r < R ? pbase + (r0 + r) / g.G : -1;
             }
 #pragma unroll
             for (int i = 0; i < OT; ++i)
@@ -759,7 +769,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                                               : (M == -INFINITY ? den : (M + lg2(den)) * kLn2);
                         if (part < 0) {
                             const int64_t row =
-                                (int64_t)(u.row0 + r / g.G) * g.Hq + u.hk * g.G + r % g.G;
+                                (int64_t)(u.row0 + (r0 + r) / g.G) * g.Hq + u.hk * g.G + (r0 + r) % g.G;
                             __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
                             for (int e = 0; e < DPL; e += 2)
@@ -860,7 +870,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         }
                         const bool none = den == 0.f;
                         const float inv = none ? 0.f : 1.f / den;
-                        const int64_t row = (int64_t)(u.row0 + r / g.G) * g.Hq + u.hk * g.G + r % g.G;
+                        const int64_t row = (int64_t)(u.row0 + (r0 + r) / g.G) * g.Hq + u.hk * g.G + (r0 + r) % g.G;
                         __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
                         for (int e = 0; e < DPL; e += 2)
@@ -879,12 +889,12 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     cp_async_wait<0>();
 }
 
-template <int D, int NT>
+template <int D, int NT, int RB = 1>
 cudaError_t launch_mx4(const Mx4Params& P, int grid, cudaStream_t stream) {
     using Cfg = Mx4Cfg<D, NT>;
-    const cudaError_t e = allow_smem<decode_mx4_kernel<D, NT>>(Cfg::kSmem);
+    const cudaError_t e = allow_smem<decode_mx4_kernel<D, NT, RB>>(Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(decode_mx4_kernel<D, NT>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem,
+    return launch_dependent(decode_mx4_kernel<D, NT, RB>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem,
                             stream, P);
 }
 
@@ -895,7 +905,7 @@ int mx4_ctas_per_sm(int D, int nt) {
     return D == 128 ? (nt == 1 ? Mx4Cfg<128, 1>::kCtas : nt == 2 ? Mx4Cfg<128, 2>::kCtas
                        : nt == 3 ? Mx4Cfg<128, 3>::kCtas : Mx4Cfg<128, 4>::kCtas)
                     : (nt == 1 ? Mx4Cfg<64, 1>::kCtas : nt == 2 ? Mx4Cfg<64, 2>::kCtas
-                       : nt == 4 ? Mx4Cfg<64, 4>::kCtas : Mx4Cfg<64, 8>::kCtas);
+                       : Mx4Cfg<64, 4>::kCtas);
 }
 
 // Row tiles (of 8) that are built: what holds `rows`, -1 if none.
@@ -940,7 +950,8 @@ cudaError_t launch_decode_mx4(const CacheGeom& g, int nt, const void* q, const v
             case 1: return launch_mx4<64, 1>(P, grid, stream);
             case 2: return launch_mx4<64, 2>(P, grid, stream);
             case 4: return launch_mx4<64, 4>(P, grid, stream);
-            case 8: return launch_mx4<64, 8>(P, grid, stream);
+            // (64 rows at a time spill: 64 sequences 575 us, two blocks of 32 340)
+            case 8: return launch_mx4<64, 4, 2>(P, grid, stream);
         }
     }
     return cudaErrorInvalidValue;
