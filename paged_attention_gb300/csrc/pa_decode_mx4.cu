@@ -903,7 +903,7 @@ cudaError_t launch_mx4(const Mx4Params& P, int grid, cudaStream_t stream) {
 // CTAs of an SM that the variant for `nt` row tiles is built for.
 int mx4_ctas_per_sm(int D, int nt) {
     return D == 128 ? (nt == 1 ? Mx4Cfg<128, 1>::kCtas : nt == 2 ? Mx4Cfg<128, 2>::kCtas
-                       : nt == 3 ? Mx4Cfg<128, 3>::kCtas : Mx4Cfg<128, 4>::kCtas)
+                       : nt == 3 ? Mx4Cfg<128, 3>::kCtas : Mx4Cfg<128, 2>::kCtas)
                     : (nt == 1 ? Mx4Cfg<64, 1>::kCtas : nt == 2 ? Mx4Cfg<64, 2>::kCtas
                        : Mx4Cfg<64, 4>::kCtas);
 }
@@ -943,7 +943,8 @@ cudaError_t launch_decode_mx4(const CacheGeom& g, int nt, const void* q, const v
             case 1: return launch_mx4<128, 1>(P, grid, stream);
             case 2: return launch_mx4<128, 2>(P, grid, stream);
             case 3: return launch_mx4<128, 3>(P, grid, stream);
-            case 4: return launch_mx4<128, 4>(P, grid, stream);
+            // (32 rows at a time spill: 64 sequences 302 us, two blocks of 16 256)
+            case 4: return launch_mx4<128, 2, 2>(P, grid, stream);
         }
     } else {
         switch (nt) {

@@ -298,14 +298,17 @@ def test_decode_split_over_any_number_of_ctas(num_ctas):
     check_decode(case, num_ctas=num_ctas, unit_cost=-1)
 
 
-@pytest.mark.parametrize("heads,kv_heads,ctx,ql,window", [
-    (16, 2, [500, 8, 70, 333, 90], [8, 1, 4, 5, 0], 0),      # 64, 8, 32, 40 and no rows
-    (11, 1, [1200, 40], [5, 3], 0),                          # 55 and 33 rows of 11 heads
-    (64, 1, [2500, 1], [1, 1], 0),                           # one token of 64 heads, split
-    (6, 1, [300, 299], [9, 10], 40),                         # 54 and 60 rows, a window
+@pytest.mark.parametrize("dim,heads,kv_heads,ctx,ql,window", [
+    (64, 16, 2, [500, 8, 70, 333, 90], [8, 1, 4, 5, 0], 0),      # 64, 8, 32, 40 and no rows
+    (64, 11, 1, [1200, 40], [5, 3], 0),                          # 55 and 33 rows of 11 heads
+    (64, 64, 1, [2500, 1], [1, 1], 0),                           # one token of 64 heads, split
+    (64, 6, 1, [300, 299], [9, 10], 40),                         # 54 and 60 rows, a window
+    (128, 16, 2, [500, 8, 70, 333, 90], [4, 1, 2, 3, 0], 0),     # 32, 8, 16, 24 and no rows
+    (128, 9, 1, [1200, 40], [3, 2], 0),                          # 27 and 18 rows of 9 heads
+    (128, 32, 1, [2500, 1], [1, 1], 30),
 ])
-def test_decode_of_two_blocks_of_rows(heads, kv_heads, ctx, ql, window):
-    check_decode(R.Case(ctx, ql, heads=heads, kv_heads=kv_heads, dim=64, page=16, window=window,
+def test_decode_of_two_blocks_of_rows(dim, heads, kv_heads, ctx, ql, window):
+    check_decode(R.Case(ctx, ql, heads=heads, kv_heads=kv_heads, dim=dim, page=16, window=window,
                         seed=71))
 
 
