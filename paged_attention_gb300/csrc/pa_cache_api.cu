@@ -117,8 +117,10 @@ bool lens_ok(const int32_t* table, const int32_t* ctx, const int32_t* ql) {
 }
 pa_status status_of(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
-// Workspace of pa_decode_mx4: header (error word) and counters, then two
-// partial slots per CTA, each `rows` rows of D + 1 floats.
+// Workspace of pa_decode_mx4: header (error word) and the counters of as many
+// CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +
+// 1 floats.  The partials begin at the same place whatever the grid: no call
+// writes them where another finds its counters.
 struct Mx4Layout {
     int grid, nt, unit_cost;
     int64_t off_done, off_part, rows, total;
@@ -140,7 +142,7 @@ pa_status mx4_layout(const pa_problem* pp, CacheGeom& g, Mx4Layout& L) {
     L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : mx4_unit_cost(8 * L.nt);
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
-    L.off_part = align256(L.off_done + (int64_t)L.grid * 4);
+    L.off_part = align256(L.off_done + (int64_t)kMaxGrid * 4);
     L.total = align256(L.off_part + 2 * (int64_t)L.grid * L.rows * (g.D + 1) * 4);
     return PA_OK;
 }

@@ -1,0 +1,116 @@
+"""The cache operators (include/pa_cache.h) where they can go wrong quietly:
+workspaces shared by calls of different grids.
+"""
+import math
+
+import pytest
+import torch
+
+from paged_attention_gb300 import binding as B
+
+import cache_ref as R
+from test_gpu_cache import MX4
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------- caches of random codes
+
+class Coded:
+    """A 4-bit cache of random codes and scales on the device; sequence b holds
+    lens[b] tokens in pages of its own."""
+
+    def __init__(self, lens, ql, *, heads, kv_heads, dim, page=64, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens, self.ql = lens, ql
+        self.heads, self.kv_heads, self.dim, self.page = heads, kv_heads, dim, page
+        need = [-(-n // page) for n in lens]
+        self.pages, self.mpps = sum(need), max(need)
+        perm = torch.randperm(self.pages, generator=g, device="cuda").int()
+        self.table = torch.full((len(lens), self.mpps), -1, dtype=torch.int32, device="cuda")
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = perm[at:at + n]
+            at += n
+        shape = (self.pages, page, kv_heads)
+
+        def bytes_(last, lo, hi):
+            return torch.randint(lo, hi, shape + (last,), generator=g, device="cuda",
+                                 dtype=torch.uint8)
+
+        self.k, self.v = bytes_(dim // 2, 0, 256), bytes_(dim // 2, 0, 256)
+        self.ks, self.vs = bytes_(dim // 32, 123, 127), bytes_(dim // 32, 122, 128)
+        self.q = torch.randn((sum(ql), heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.ctx_t, self.ql_t = ints(lens), ints(ql)
+
+    def problem(self, **kw):
+        p = B.PaProblem(num_seqs=len(self.lens), num_q_heads=self.heads,
+                        num_kv_heads=self.kv_heads, head_dim=self.dim, page_size=self.page,
+                        num_pages=self.pages, max_pages_per_seq=self.mpps,
+                        total_q_tokens=sum(self.ql), max_q_len=max(self.ql),
+                        max_context_len=max(self.lens), kv_dtype=MX4, sm_scale=self.dim ** -0.5)
+        for k, v in kw.items():
+            setattr(p, k, v)
+        return p
+
+    def decode(self, ws, **kw):
+        out = torch.full((sum(self.ql), self.heads, self.dim), 7.0, dtype=torch.bfloat16,
+                         device="cuda")
+        lse = torch.full(out.shape[:2], 7.0, device="cuda")
+        B.pa_decode_mx4(self.problem(**kw), self.q, self.k, self.ks, self.v, self.vs, self.table,
+                        self.ctx_t, self.ql_t, ws, out, lse)
+        return out, lse
+
+    def space(self, **kw):
+        return torch.zeros(B.pa_mx4_workspace_size(self.problem(**kw)), dtype=torch.uint8,
+                           device="cuda")
+
+    def rows(self, which, b):
+        cache, sc = (self.k, self.ks) if which == "k" else (self.v, self.vs)
+        pages = self.table[b][:-(-self.lens[b] // self.page)].long()
+        x, s = (t[pages].reshape(-1, self.kv_heads, t.shape[-1])[:self.lens[b]].cpu()
+                for t in (cache, sc))
+        return R.dequantise(x, s).cuda()
+
+    def check(self, out, lse):
+        """Against 64 bits, with test_gpu_cache.check_decode's tolerances."""
+        at, G = 0, self.heads // self.kv_heads
+        for b, (n, ql) in enumerate(zip(self.lens, self.ql)):
+            K, V = (self.rows(w, b).transpose(0, 1).repeat_interleave(G, 0) for w in "kv")
+            q = self.q[at:at + ql].double().transpose(0, 1)
+            hide = (torch.arange(n, device="cuda")[None]
+                    > torch.arange(n - ql, n, device="cuda")[:, None])
+            x = (q @ K.transpose(1, 2) * self.dim ** -0.5).masked_fill(hide, -math.inf)
+            big = (q.abs() @ K.abs().transpose(1, 2)).amax(-1) * self.dim ** -0.5
+            p = torch.softmax(x, -1)
+            ref, mag, rl = p @ V, p @ V.abs(), torch.logsumexp(x, -1)
+            score = (self.dim + 8) * 2.0 ** -24 * big
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -14 + 2 * score[..., None]) * mag
+            d = (out[at:at + ql].double().transpose(0, 1) - ref).abs()
+            assert bool((d <= tol + 1e-30).all()), float((d / tol).max())
+            dl = (lse[at:at + ql].double().t() - rl).abs()
+            assert bool((dl <= score + 2.0 ** -20 + rl.abs() * 2.0 ** -21).all())
+            at += ql
+
+
+# ---------------------------------------------------------------- workspaces
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("grid", [1, 8, 152])
+def test_one_workspace_serves_grids_of_any_size(dim, grid):
+    """A call of few CTAs, then one of the most there can be, in turn in one
+    workspace: every call gives what a fresh workspace gives."""
+    few = Coded([3000, 900], [1, 1], heads=8, kv_heads=1, dim=dim, seed=1)
+    # units that begin in every part of the grid and are split
+    many = Coded([40000], [1], heads=8, kv_heads=8, dim=64, seed=2)
+    a, b = dict(num_ctas=grid, unit_cost=-1), dict(num_ctas=1024, unit_cost=-1)
+    want_few, want_many = few.decode(few.space(**a), **a), many.decode(many.space(**b), **b)
+    ws = torch.zeros(max(few.space(**a).numel(), many.space(**b).numel()), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(3):
+        got = few.decode(ws, **a)
+        assert torch.equal(got[0], want_few[0]) and torch.equal(got[1], want_few[1])
+        got = many.decode(ws, **b)
+        assert torch.equal(got[0], want_many[0]) and torch.equal(got[1], want_many[1])
+    assert B.pa_last_device_error(ws) == 0
