@@ -484,12 +484,13 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                     e2m1x8_to_f16(lds32(at + 16 * mt * ROW), a[0][0], a[0][2], a[1][0], a[1][2]);
                     e2m1x8_to_f16(lds32(at + (16 * mt + 8) * ROW), a[0][1], a[0][3], a[1][1],
                                   a[1][3]);
-                    // 2^(e - 127): the byte in the exponent's place
-                    // (0 for e = 0, infinite for e = 255: put right below)
-                    const uint64_t f0 = pair2(__uint_as_float(
-                        (kb < 3 ? kw[mt][0] << (23 - 8 * kb) : kw[mt][0] >> 1) & 0x7f800000u));
-                    const uint64_t f1 = pair2(__uint_as_float(
-                        (kb < 3 ? kw[mt][1] << (23 - 8 * kb) : kw[mt][1] >> 1) & 0x7f800000u));
+                    // 2^(e - 127): the byte in the exponent's place, and 2^-127 (a
+                    // subnormal) for e = 0 (infinite for e = 255: put right below)
+                    auto power = [&](uint32_t w) {
+                        const uint32_t x = (kb < 3 ? w << (23 - 8 * kb) : w >> 1) & 0x7f800000u;
+                        return pair2(__uint_as_float(max(x, 0x00400000u)));
+                    };
+                    const uint64_t f0 = power(kw[mt][0]), f1 = power(kw[mt][1]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float x[4];

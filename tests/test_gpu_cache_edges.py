@@ -1,5 +1,5 @@
 """The cache operators (include/pa_cache.h) where they can go wrong quietly:
-workspaces shared by calls of different grids.
+workspaces shared by calls of different grids, the smallest scales.
 """
 import math
 
@@ -9,7 +9,7 @@ import torch
 from paged_attention_gb300 import binding as B
 
 import cache_ref as R
-from test_gpu_cache import MX4
+from test_gpu_cache import MX4, check_decode, decode, run_weights, same
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,28 @@ def test_one_workspace_serves_grids_of_any_size(dim, grid):
         got = many.decode(ws, **b)
         assert torch.equal(got[0], want_many[0]) and torch.equal(got[1], want_many[1])
     assert B.pa_last_device_error(ws) == 0
+
+
+# --------------------------------------------------------------------- scales
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_the_smallest_scale_counts(dim):
+    """Blocks of K with scale byte 0 are codes times 2^-127, as the format says,
+    for queries near the top of bf16's range.  (bf16 queries are exact in f16
+    with their power of two taken out; a score's rounding in the subnormal range
+    is 2^-150, times a factor below 2^120: nothing beside the tolerance.)"""
+    case = R.Case([70, 33], [2, 1], heads=4, kv_heads=2, dim=dim, seed=5)
+    g = torch.Generator().manual_seed(5)
+    case.q = (torch.randn(case.q.shape, generator=g).clamp(-3.5, 3.5) * 2.0 ** 125).to(torch.bfloat16)
+    poison = case.ks == 255
+    case.ks = torch.randint(0, 3, case.ks.shape, generator=g, dtype=torch.uint8)
+    case.ks[poison] = 255
+    check_decode(case)
+    # whole rows of scale 0
+    case.ks = torch.where(poison, 255, 0).to(torch.uint8)
+    out, lse = check_decode(case)
+    assert float(lse.std()) > 1e-3                 # scores that are not all 0
+    # the key weights of the same cache agree with that lse
+    _, rl, _, _ = R.attention(case)
+    w, err = run_weights(case, lse.cpu().double(), torch.zeros((case.num_pages, 2, 16)))
+    assert err == 0 and abs(float(w.sum()) - 3 * 4) < 1e-4
