@@ -94,9 +94,15 @@ PA_API pa_status pa_kv_expand(const pa_problem* problem, const void* k_cache, co
  * num_ctas and unit_cost have their pa.h meaning (num_ctas at most 1024);
  * balance_rows is not used.
  * The scores and the products with V are taken in f16 by the tensor cores with
- * fp32 sums; the block scales of K are applied in fp32.  A V block adds to the
- * result relative to the largest scale that its 32 columns met so far: what
- * lies more than a factor 2^24 below that is lost to rounding.
+ * fp32 sums; the block scales of K are applied in fp32.  What f16 rounds:
+ *   - a probability by 2^-11 of itself, or 2^-32 of its row's largest where that
+ *     is more (so that keys up to 22 nats below one that outweighs them all
+ *     still count), in the product with V only: lse and the normalisation take
+ *     it in fp32;
+ *   - an element of q by 2^-25 of its row's largest, below 2^-14 of that (above,
+ *     bf16's eight bits are exact);
+ *   - a V block relative to the largest scale that its 32 columns met so far:
+ *     what lies more than a factor 2^24 below that is lost.
  *   ws: >= pa_mx4_workspace_size bytes, 256-byte aligned, zero-filled by the
  *     caller before its first use.  Every call that runs to its end leaves it
  *     ready for the next one, of the same or another problem (a second launch to

@@ -4,7 +4,7 @@
 //
 // Persistent CTAs, a few per SM, take equal shares of the flat line of
 // (sequence, KV head, 64-token tile); the warps of a CTA cut each unit's tokens
-// between them in 32-token steps, every warp with its own running (m, l, O), its
+// between them in 32-token steps, every warp with its own running (max, sum, O), its
 // own ring of cp.async stages that runs ahead over unit boundaries, and no
 // barrier until the unit ends.  Then the warps' states merge through shared
 // memory; a unit that spans CTAs leaves normalised parts in the workspace, and
@@ -21,7 +21,11 @@
 //     steps), V's multiply the f16 codes, relative to the largest scale its
 //     columns met so far (moved as rarely as the running max);
 //   - the running max moves only when a score passes it by 2^8, decided by one
-//     vote; a row's max is otherwise never reduced over lanes.
+//     vote; a row's max is otherwise never reduced over lanes;
+//   - P carries a factor 2^7, which the division by its sum takes out: below 2^15
+//     in f16, whose normal range then reaches down to 2^-21 of the row's largest
+//     probability.  What is smaller rounds to multiples of 2^-31 of that, so keys
+//     beside one that outweighs them all still count.
 // Masked scores are -inf and V rows past the context are zero codes, so
 // nothing outside a row's sight reaches it; a NaN block (scale 255) reaches
 // exactly the rows that see its key.
@@ -73,7 +77,7 @@ struct Mx4Cfg {
     static constexpr int kQRow = 2 * D + kQPad;
     static constexpr bool kQInRegs = kPerThread <= 128;   // few enough rows to keep
     static constexpr int kMergeRow = D + 4;                // floats
-    static constexpr int kMergeWarp = 8 * kMergeRow + 16;  // 8 rows, then m[8], l[8]
+    static constexpr int kMergeWarp = 8 * kMergeRow + 16;  // 8 rows, then up[8], l[8]
     static constexpr int kOffQ = kWarps * kStages * kStage;
     static constexpr int kOffInfo = kOffQ + kRows * kQRow;  // per row: score factor
     static constexpr int kOffMerge = kOffInfo + kRows * 4;
@@ -84,6 +88,10 @@ struct Mx4Cfg {
 };
 
 namespace {
+
+// A row's state is up = kPBits - running max: P = exp2(score + up), at most 2^(kPBits
+// + kPRise).  kUpNone: no key seen yet, any score passes the max.
+constexpr float kPBits = 7.f, kPRise = 8.f, kUpNone = 3.402823466e38f;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -410,7 +418,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
         const bool has_next = next_unit<RB>(P, nu) && nu.start < hi;
         if (has_next) load_q(nu);
 
-        float m[NT][2], l[NT][2], fq[NT][2];
+        float up[NT][2], l[NT][2], fq[NT][2];
         int pr[NT][2];              // last visible position of the thread's rows
         float o[OT][NT][4];
 #pragma unroll
@@ -418,7 +426,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + 2 * t4 + e;
-                m[nt][e] = -INFINITY;
+                up[nt][e] = kUpNone;
                 l[nt][e] = 0.f;
                 fq[nt][e] = info[r];
                 pr[nt][e] = r < R ? pbase + (r0 + r) / g.G : -1;
@@ -542,8 +550,9 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    odd_step |= fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]),
-                                      s[1][nt][e + 2]) * fq[nt][e] > m[nt][e] + 8.f;
+                    odd_step |= fmaf(fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]),
+                                           s[1][nt][e + 2]),
+                                     fq[nt][e], up[nt][e]) > kPBits + kPRise;
             bool nan_v = false, wide_v = false;
             if (__any_sync(0xffffffffu, odd_step)) {
                 // a NaN block of K: the key's scores are NaN where it is seen
@@ -589,9 +598,9 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         float al = 1.f;
-                        if (x > m[nt][e]) {
-                            al = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
-                            m[nt][e] = x;
+                        if (kPBits - x < up[nt][e]) {
+                            al = ex2(kPBits - x - up[nt][e]);
+                            up[nt][e] = kPBits - x;
                         }
                         l[nt][e] *= al;
                         const float f = al * vfac;
@@ -606,14 +615,12 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float mu0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-                const float mu1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    const float p0 = ex2(fmaf(s[mt][nt][0], fq[nt][0], -mu0));
-                    const float p1 = ex2(fmaf(s[mt][nt][1], fq[nt][1], -mu1));
-                    const float p2 = ex2(fmaf(s[mt][nt][2], fq[nt][0], -mu0));
-                    const float p3 = ex2(fmaf(s[mt][nt][3], fq[nt][1], -mu1));
+                    const float p0 = ex2(fmaf(s[mt][nt][0], fq[nt][0], up[nt][0]));
+                    const float p1 = ex2(fmaf(s[mt][nt][1], fq[nt][1], up[nt][1]));
+                    const float p2 = ex2(fmaf(s[mt][nt][2], fq[nt][0], up[nt][0]));
+                    const float p3 = ex2(fmaf(s[mt][nt][3], fq[nt][1], up[nt][1]));
                     l[nt][0] += p0 + p2;
                     l[nt][1] += p1 + p3;
                     pb[mt][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -726,7 +733,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         x += __shfl_xor_sync(0xffffffffu, x, 16);
                         if (gr == 0) {
                             mw[8 * Cfg::kMergeRow + 2 * t4 + e] =
-                                sh.s1 > sh.s0 ? m[nt][e] : -INFINITY;
+                                sh.s1 > sh.s0 ? up[nt][e] : kUpNone;
                             mw[8 * Cfg::kMergeRow + 8 + 2 * t4 + e] = x;
                         }
                         // the thread's columns are consecutive: OT pairs from gr * D / 8
@@ -744,20 +751,20 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                     for (int mr = warp; mr < 8 && 8 * nt + mr < R; mr += W) {
                         const int r = 8 * nt + mr;
                         constexpr int DPL = D / 32;
-                        float M = -INFINITY;
+                        float U = kUpNone;
 #pragma unroll
                         for (int w = 0; w < W; ++w)
-                            M = fmaxf(M, merge[w * Cfg::kMergeWarp + 8 * Cfg::kMergeRow + mr]);
+                            U = fminf(U, merge[w * Cfg::kMergeWarp + 8 * Cfg::kMergeRow + mr]);
                         float den = 0.f, acc[DPL];
 #pragma unroll
                         for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
 #pragma unroll 4
                         for (int w = 0; w < W; ++w) {
                             const float* b = merge + w * Cfg::kMergeWarp;
-                            const float mv = b[8 * Cfg::kMergeRow + mr];
+                            const float uv = b[8 * Cfg::kMergeRow + mr];
                             const float lv = b[8 * Cfg::kMergeRow + 8 + mr];
-                            if (mv == -INFINITY && lv == 0.f) continue;   // saw nothing
-                            const float f = mv == -INFINITY ? 1.f : ex2(mv - M);
+                            if (uv == kUpNone && lv == 0.f) continue;     // saw nothing
+                            const float f = uv == kUpNone ? 1.f : ex2(U - uv);
                             den += f * lv;
 #pragma unroll
                             for (int e = 0; e < DPL; ++e)
@@ -767,7 +774,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         const bool none = den == 0.f;
                         const float inv = none ? 0.f : 1.f / den;
                         const float ln = none ? -INFINITY
-                                              : (M == -INFINITY ? den : (M + lg2(den)) * kLn2);
+                                              : (U == kUpNone ? den : (lg2(den) - U) * kLn2);
                         if (part < 0) {
                             const int64_t row =
                                 (int64_t)(u.row0 + (r0 + r) / g.G) * g.Hq + u.hk * g.G + (r0 + r) % g.G;

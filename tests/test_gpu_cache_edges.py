@@ -1,5 +1,6 @@
 """The cache operators (include/pa_cache.h) where they can go wrong quietly:
-workspaces shared by calls of different grids, the smallest scales.
+workspaces shared by calls of different grids, the smallest scales, a key that
+outweighs all others.
 """
 import math
 
@@ -139,3 +140,31 @@ def test_the_smallest_scale_counts(dim):
     _, rl, _, _ = R.attention(case)
     w, err = run_weights(case, lse.cpu().double(), torch.zeros((case.num_pages, 2, 16)))
     assert err == 0 and abs(float(w.sum()) - 3 * 4) < 1e-4
+
+
+# ------------------------------------------------------------------- softmax
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("above", [9.0, 12.0, 18.0])
+@pytest.mark.parametrize("where", [0, 40])
+def test_a_key_that_outweighs_the_others_and_has_no_value(dim, above, where):
+    """What is left of the output is the others' values.  A probability rounds
+    to f16 after a factor 2^7 and relative to a maximum that is at most the
+    row's: below f16's normal range it is off by at most 2^-25 / 2^7 = 2^-32 of
+    the largest probability, so the output by 2^-32 of the sum of |v|."""
+    g = torch.Generator().manual_seed(6)
+    case = R.Case([300], [1], heads=1, kv_heads=1, dim=dim, seed=6, kmag=0.02)
+    q = case.q[0, 0].float()
+    case.kd[0][where, 0] = (q * (above * math.sqrt(dim) / float(q @ q))).to(torch.bfloat16)
+    case.vd[0][where] = 0
+    case.fill()
+    out, lse, ws = decode(case)
+    assert B.pa_last_device_error(ws) == 0
+    ref, rl, mag, big = R.attention(case)
+    assert float((R.key_weights(case, rl)[0][0][0, where])) > 0.9
+    score = (dim + 8) * 2.0 ** -24 * big
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -14 + 2 * score[..., None]) * mag
+    tol = tol + 2.0 ** -32 * case.rows("v", 0)[:, 0].abs().sum(0)
+    d = (out.cpu().double() - ref).abs()
+    assert bool((d <= tol).all()), f"out off by {float((d / tol).max())} of its tolerance"
+    assert bool(((lse.cpu().double() - rl).abs() <= score + 2.0 ** -20 + rl.abs() * 2.0 ** -21).all())
