@@ -23,8 +23,10 @@
  *   into it (they never clear it): PA_DEV_BAD_LENGTHS for q_lens or
  *   context_lens that are negative, above the declared maxima, q_lens[b] >
  *   context_lens[b], or a sum of q_lens that is not total_q_tokens;
- *   PA_DEV_BAD_PAGE for a block-table entry outside [0, num_pages).  The rows
- *   concerned are skipped, the rest is done.  PA_DEV_WAIT_TIMEOUT (only
+ *   PA_DEV_BAD_PAGE for a block-table entry outside [0, num_pages) that the
+ *   call has to look up.  The rows concerned are skipped, the rest is done: a
+ *   key on such a page is not written, not read, seen by no query, given no
+ *   weight, and the first to be evicted.  PA_DEV_WAIT_TIMEOUT (only
  *   pa_key_weights, with more than 16 rows of queries and heads): a pipeline
  *   wait ran out; the weights are then unspecified.
  *

@@ -27,8 +27,8 @@
 //     probability.  What is smaller rounds to multiples of 2^-31 of that, so keys
 //     beside one that outweighs them all still count.
 // Masked scores are -inf and V rows past the context are zero codes, so
-// nothing outside a row's sight reaches it; a NaN block (scale 255) reaches
-// exactly the rows that see its key.
+// nothing outside a row's sight reaches it, nor a key whose page is none; a NaN
+// block (scale 255) reaches exactly the rows that see its key.
 #include "pa_cache_mma.cuh"
 
 namespace pa {
@@ -267,6 +267,7 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     int l_b = u.b;
     int win_lo = first_page(ls);             // 32 page ids, the 32 after them, the next unit's
     int win = page_ids(u, win_lo), nxt = page_ids(u, win_lo + 32), lnw = -1;
+    uint32_t bad = 0;                        // two bits a stage: halves whose page is none
     bool ln_ok = next_unit<RB>(P, ln) && ln.start < hi;
     if (ln_ok) lnw = page_ids(ln, first_page(share_of(ln, cost, lo, hi, warp, W)));
     auto issue = [&](int stage) {
@@ -345,8 +346,9 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                 const bool ok = lane < left && (lane < 16 ? oka : okb);
                 cp_async4(dsc, P.ks + (ok ? so : 0), ok ? 4 : 0, again);
                 cp_async4(dsc + 128, P.vs + (ok ? so : 0), ok ? 4 : 0, again);
-                if ((!oka || (left > 16 && !okb)) && lane == 0)
-                    flag_error(P.header + H_ERROR, PA_DEV_BAD_PAGE);
+                const uint32_t none = (oka ? 0u : 1u) | (left > 16 && !okb ? 2u : 0u);
+                bad |= none << (2 * stage);
+                if (none != 0 && lane == 0) flag_error(P.header + H_ERROR, PA_DEV_BAD_PAGE);
             }
         }
         cp_async_commit();
@@ -525,6 +527,18 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                         for (int e = 0; e < 4; ++e)
                             if (!visible(16 * mt + 8 * (e >> 1) + key0, nt, e & 1))
                                 s[mt][nt][e] = -INFINITY;
+            }
+            // nobody sees keys whose page is none
+            if (bad != 0) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+                    if (bad >> (2 * stage + mt) & 1u) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[mt][nt][e] = -INFINITY;
+                    }
+                bad &= ~(3u << (2 * stage));
             }
             // ---- V's scale bytes of the thread's keys and columns
             int ve[2][4];

@@ -1,6 +1,6 @@
 """The cache operators (include/pa_cache.h) where they can go wrong quietly:
 workspaces shared by calls of different grids, the smallest scales, a key that
-outweighs all others.
+outweighs all others, pages that are none.
 """
 import math
 
@@ -10,7 +10,7 @@ import torch
 from paged_attention_gb300 import binding as B
 
 import cache_ref as R
-from test_gpu_cache import MX4, check_decode, decode, run_weights, same
+from test_gpu_cache import HND, MX4, NHD, check_decode, decode, run_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,64 @@ def test_a_key_that_outweighs_the_others_and_has_no_value(dim, above, where):
     d = (out.cpu().double() - ref).abs()
     assert bool((d <= tol).all()), f"out off by {float((d / tol).max())} of its tolerance"
     assert bool(((lse.cpu().double() - rl).abs() <= score + 2.0 ** -20 + rl.abs() * 2.0 ** -21).all())
+
+
+# ------------------------------------------------------------------ bad pages
+
+def attention_without(case, hidden):
+    """R.attention (out, lse, sum p |v|, largest sum |q k|) where sequence b's
+    keys at positions hidden[b] are not there."""
+    T, H, D, G = case.total_q, case.heads, case.dim, case.group
+    out, mag = torch.zeros((2, T, H, D), dtype=torch.float64)
+    lse = torch.full((T, H), -math.inf, dtype=torch.float64)
+    big = torch.zeros((T, H), dtype=torch.float64)
+    at = 0
+    for b, (c, q) in enumerate(zip(case.ctx, case.ql)):
+        K, V = case.rows("k", b), case.rows("v", b)
+        for i in range(q):
+            p = c - q + i
+            lo = max(0, p - case.window + 1) if case.window else 0
+            see = [j for j in range(lo, p + 1) if j not in hidden[b]]
+            for h in range(H):
+                if not see:
+                    continue
+                k, v, x = K[see, h // G], V[see, h // G], case.q[at + i, h].double()
+                s = (k @ x) * case.scale
+                lse[at + i, h] = torch.logsumexp(s, 0)
+                out[at + i, h] = torch.softmax(s, 0) @ v
+                mag[at + i, h] = torch.softmax(s, 0) @ v.abs()
+                big[at + i, h] = (k.abs() @ x.abs()).max() * case.scale
+        at += q
+    return out, lse, mag, big
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads,page,layout,window,bad", [
+    (64, 2, 1, 16, NHD, 0, [(0, 2), (0, 5)]),             # first and second halves of a step
+    (128, 8, 2, 16, HND, 0, [(0, 6), (1, 0), (1, 2), (1, 1)]),
+    (128, 4, 1, 64, NHD, 0, [(0, 1), (1, 0)]),            # sequence 1: every key
+    (64, 4, 4, 32, HND, 40, [(0, 3), (1, 1)]),            # some queries see no other page
+    (128, 16, 1, 16, NHD, 0, [(0, 0), (0, 6)]),           # two blocks of rows
+])
+@pytest.mark.parametrize("entry", [-1, 1 << 30])
+def test_decode_leaves_out_the_keys_of_a_bad_page(dim, heads, kv_heads, page, layout, window, bad,
+                                                  entry):
+    """Keys whose page is outside the pool are not there; a query that sees no
+    other gets zeros and lse -inf; the error word tells."""
+    case = R.Case([100, 50], [2, 2], heads=heads, kv_heads=kv_heads, dim=dim, page=page,
+                  layout=layout, window=window, seed=7)
+    hidden = [set(), set()]
+    for b, i in bad:
+        hidden[b].update(range(i * page, (i + 1) * page))
+    ref, rl, mag, big = attention_without(case, hidden)
+    for b, i in bad:
+        case.table[b, i] = entry
+    score = (dim + 8) * 2.0 ** -24 * big
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -14 + 2 * score[..., None]) * mag
+    for kw in (dict(), dict(num_ctas=1), dict(num_ctas=1024, unit_cost=-1)):
+        out, lse, ws = decode(case, **kw)
+        assert B.pa_last_device_error(ws) == B.PA_DEV_BAD_PAGE
+        assert bool(((out.cpu().double() - ref).abs() <= tol).all())
+        none = rl == -math.inf
+        assert torch.equal(lse.cpu() == -math.inf, none)
+        d = (lse.cpu().double() - rl).abs()[~none]
+        assert bool((d <= (score + 2.0 ** -20 + rl.abs() * 2.0 ** -21)[~none]).all())
