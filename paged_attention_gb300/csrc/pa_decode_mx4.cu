@@ -121,6 +121,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// 2^(e - 127) of the first 2 N bytes of a word as bf16 pairs (exact; e = 255: NaN).
+template <int N>
+__device__ __forceinline__ void e8m0_to_bf16(uint32_t w, uint32_t* d) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(d[i]) : "h"((uint16_t)(w >> (16 * i))));
+}
+
 // A unit (sequence, KV head, block of query rows) as a CTA meets it.
 struct Unit {
     int b, hk, blk;
@@ -469,13 +477,13 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
             // ---- scores of 2 x 16 keys (before the row's factor)
             float s[2][NT][4];
             const int key0 = tile_key<D>(gr);
-            uint32_t kw[2][2];
+            uint32_t kf[2][2][KB / 2];      // K's scales, pairs of blocks
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int key = key0 + 16 * mt + 8 * hh;
-                    kw[mt][hh] = lds32(sks + key * 4) >> scale_shift(key);
+                    e8m0_to_bf16<KB / 2>(lds32(sks + key * 4) >> scale_shift(key), kf[mt][hh]);
                 }
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
@@ -494,13 +502,10 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                     e2m1x8_to_f16(lds32(at + 16 * mt * ROW), a[0][0], a[0][2], a[1][0], a[1][2]);
                     e2m1x8_to_f16(lds32(at + (16 * mt + 8) * ROW), a[0][1], a[0][3], a[1][1],
                                   a[1][3]);
-                    // 2^(e - 127): the byte in the exponent's place, and 2^-127 (a
-                    // subnormal) for e = 0 (infinite for e = 255: put right below)
-                    auto power = [&](uint32_t w) {
-                        const uint32_t x = (kb < 3 ? w << (23 - 8 * kb) : w >> 1) & 0x7f800000u;
-                        return pair2(__uint_as_float(max(x, 0x00400000u)));
-                    };
-                    const uint64_t f0 = power(kw[mt][0]), f1 = power(kw[mt][1]);
+                    const uint64_t f0 = pair2(__uint_as_float(
+                        kb & 1 ? kf[mt][0][kb / 2] & 0xffff0000u : kf[mt][0][kb / 2] << 16));
+                    const uint64_t f1 = pair2(__uint_as_float(
+                        kb & 1 ? kf[mt][1][kb / 2] & 0xffff0000u : kf[mt][1][kb / 2] << 16));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float x[4];
@@ -556,10 +561,8 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                                  min(min(ve[1][1], ve[1][2]), ve[1][3]));
             // ---- what the plain course below does not cover: a score far above
             // its row's running max, a V scale outside [-14, 4] binary orders of
-            // its columns' reference, a NaN scale of K (each lane looks at one key)
-            const uint32_t kn = lds32(sks + lane * 4);
-            bool odd_step = vmax > vref + 4 || vmin < vref - 14 || vmax == 255 ||
-                            (((kn & 0x7f7f7f7fu) + 0x01010101u) & kn & 0x80808080u) != 0;
+            // its columns' reference, or none
+            bool odd_step = vmax > vref + 4 || vmin < vref - 14 || vmax == 255;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -569,22 +572,6 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                                      fq[nt][e], up[nt][e]) > kPBits + kPRise;
             bool nan_v = false, wide_v = false;
             if (__any_sync(0xffffffffu, odd_step)) {
-                // a NaN block of K: the key's scores are NaN where it is seen
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int key = 16 * mt + 8 * hh + key0;
-                        uint32_t w = lds32(sks + key * 4) >> scale_shift(key);
-                        if (D == 64) w &= 0xffffu;
-                        if ((((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u) != 0) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (visible(key, nt, e)) s[mt][nt][2 * hh + e] = NAN;
-                        }
-                    }
                 int top = -1000;
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
