@@ -146,15 +146,17 @@ PA_API pa_status pa_key_weights(const pa_problem* problem, const void* q, const 
  * Evict: of every sequence longer than budget keep, per KV head, budget keys:
  * the first num_first, the last num_recent, and of the others those with the
  * largest weights (equal weights: the lower position; a NaN counts as less
- * than every number).  The kept rows of K, V (with their scales) and their
- * weights are copied in ascending order to the slots 0 .. budget-1 of the
- * pages listed in dst_block_table (int32 [B][dst_max_pages_per_seq]), pages of
- * the same pool that no sequence of the call uses; the old pages are left as
- * they are.  A sequence of at most budget tokens is not touched, and its row
- * of dst_block_table is not read.  After the call attention reads the evicted
- * sequences through their new pages with new_context_lens; the relative order
- * of their keys is kept, so causal attention of tokens appended later is
- * exact over what is left, while a sliding window counts kept keys.
+ * than every number, and so does what a page outside the pool would hold:
+ * where such a key is kept, its row is not copied).  The kept rows of K, V
+ * (with their scales) and their weights are copied in ascending order to the
+ * slots 0 .. budget-1 of the pages listed in dst_block_table (int32
+ * [B][dst_max_pages_per_seq]), pages of the same pool that no sequence of the
+ * call uses; the old pages are left as they are.  A sequence of at most budget
+ * tokens is not touched, and its row of dst_block_table is not read.  After the
+ * call attention reads the evicted sequences through their new pages with
+ * new_context_lens; the relative order of their keys is kept, so causal
+ * attention of tokens appended later is exact over what is left, while a
+ * sliding window counts kept keys.
  *   budget >= 1; num_first, num_recent >= 0 and num_first + num_recent <= budget.
  *   kept: int32 [B][Hkv][budget]: the positions that were kept, ascending;
  *     rows of sequences that were not evicted are left alone.

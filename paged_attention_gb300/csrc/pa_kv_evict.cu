@@ -141,7 +141,7 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
     if (bad || c <= P.budget) return;
     const int32_t* row = P.table + (int64_t)b * g.mpps;
     // (no branches: the loads of a loop's iterations run together; a page that
-    // is none counts as the smallest key, and the move flags it)
+    // is none counts as the smallest key, and the first pass flags it)
     auto key_at = [&](int i) -> uint32_t {
         const int page = row[i >> g.ps_shift];
         const bool ok = (uint32_t)page < (uint32_t)g.num_pages;
@@ -188,8 +188,10 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
                 return k < c ? row[k >> g.ps_shift] : -1;
             };
             int page = look_up(256 * warp);
+            bool none = false;
             for (int i = 256 * warp; i < c; i += 8 * kSelectThreads) {
                 const int now = page;
+                none |= i + 16 * (lane & 15) < c && (uint32_t)now >= (uint32_t)g.num_pages;
                 page = look_up(i + 8 * kSelectThreads);
                 float w[8];
                 bool ok[8];
@@ -211,6 +213,7 @@ select_kernel(const __grid_constant__ EvictParams P, int cached_cap) {
                     }
                 }
             }
+            if (none) flag_error(P.err, PA_DEV_BAD_PAGE);
         } else if (shift == 16) {
             for (int i = tid; i < c; i += 8 * kSelectThreads) {
                 uint32_t x[8];

@@ -10,7 +10,8 @@ import torch
 from paged_attention_gb300 import binding as B
 
 import cache_ref as R
-from test_gpu_cache import HND, MX4, NHD, check_decode, decode, run_weights
+from test_gpu_cache import (BF16, HND, MX4, NHD, check_decode, decode, dst_table, run_evict,
+                            run_weights, same)
 
 pytestmark = pytest.mark.gpu
 
@@ -229,3 +230,29 @@ def test_decode_leaves_out_the_keys_of_a_bad_page(dim, heads, kv_heads, page, la
         assert torch.equal(lse.cpu() == -math.inf, none)
         d = (lse.cpu().double() - rl).abs()[~none]
         assert bool((d <= (score + 2.0 ** -20 + rl.abs() * 2.0 ** -21)[~none]).all())
+
+
+@pytest.mark.parametrize("kv", [BF16, MX4])
+@pytest.mark.parametrize("n,page,where", [(100, 16, 3), (700, 64, 0), (5000, 256, 19)])
+def test_evict_flags_a_bad_page_whose_keys_go(kv, n, page, where):
+    """The keys of a page that is none are the first to go, and nothing of them
+    is moved: the error word tells all the same, and the others are chosen and
+    moved as if those had no weight."""
+    budget = n // 3
+    case = R.Case([n, 20], [0, 0], heads=2, kv_heads=2, dim=64, page=page, kv=kv, seed=8,
+                  spare=-(-budget // page))
+    w = torch.rand((case.num_pages, 2, page), generator=torch.Generator().manual_seed(8)) + 0.1
+    dst = dst_table(case, budget)
+    no_weight = w.clone()
+    no_weight[int(case.table[0, where])] = math.nan
+    clean = run_evict(case, no_weight, budget, 0, 0, dst)
+    assert clean["err"] == 0
+    for entry in (case.num_pages, -5):
+        case.table[0, where] = entry
+        got = run_evict(case, w, budget, 0, 0, dst)
+        assert got["err"] == B.PA_DEV_BAD_PAGE
+        assert torch.equal(got["kept"], clean["kept"]) and torch.equal(got["new"], clean["new"])
+        for name in ("k", "ks", "v", "vs"):
+            if clean[name] is not None:
+                assert same(got[name], clean[name]), name
+        assert same(got["w"][dst[0].long()], clean["w"][dst[0].long()])
