@@ -815,6 +815,8 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                 }
                 if (alone) {
                     last = warp == 0 && __any_sync(0xffffffffu, last);
+                    __syncwarp();      // (a vote orders no memory: what thread 0 has seen
+                                       // written, the warp sees from here on)
                 } else {
                     __syncthreads();
                     last = *flag != 0;

@@ -118,6 +118,27 @@ def test_one_workspace_serves_grids_of_any_size(dim, grid):
     assert B.pa_last_device_error(ws) == 0
 
 
+def test_decode_repeats_itself_bit_for_bit():
+    """Calls after calls of a batch whose units are split over CTAs."""
+    c = Coded([128, 20000, 333, 4500, 64, 9000], [2, 2, 1, 2, 2, 1], heads=32, kv_heads=8, dim=128,
+              seed=3)
+    ws = c.space()
+    first = c.decode(ws)
+    c.check(*first)
+    for i in range(10):
+        got = c.decode(ws if i % 2 else c.space())
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("dim,heads,n", [(64, 1, 20011), (128, 3, 70001), (128, 32, 9001)])
+def test_decode_of_one_unit_over_many_ctas(dim, heads, n):
+    """One KV head: its parts are joined 32 at a time, several times over (32
+    heads: as two blocks of rows)."""
+    c = Coded([n], [1], heads=heads, kv_heads=1, dim=dim, seed=4)
+    c.check(*c.decode(c.space()))
+    c.check(*c.decode(c.space(num_ctas=1024, unit_cost=-1), num_ctas=1024, unit_cost=-1))
+
+
 # --------------------------------------------------------------------- scales
 
 @pytest.mark.parametrize("dim", [64, 128])
