@@ -1,6 +1,8 @@
 """The cache operators (include/pa_cache.h) where they can go wrong quietly:
 workspaces shared by calls of different grids, the smallest scales, a key that
-outweighs all others, pages that are none.
+outweighs all others, pages that are none, and the variants that only many or
+long sequences reach.  References in 64 bits; the tolerances are those of
+test_gpu_cache.py, with what a case adds to them derived beside it.
 """
 import math
 
@@ -10,8 +12,8 @@ import torch
 from paged_attention_gb300 import binding as B
 
 import cache_ref as R
-from test_gpu_cache import (BF16, HND, MX4, NHD, check_decode, decode, dst_table, run_evict,
-                            run_weights, same)
+from test_gpu_cache import (BF16, HND, MX4, NHD, check_decode, check_weights, decode, dst_table,
+                            error_word, run_evict, run_weights, same)
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +279,99 @@ def test_evict_flags_a_bad_page_whose_keys_go(kv, n, page, where):
             if clean[name] is not None:
                 assert same(got[name], clean[name]), name
         assert same(got["w"][dst[0].long()], clean["w"][dst[0].long()])
+
+
+# ------------------------------------------------- eviction of many and of long
+
+def plain_kept(line, n, budget, first, recent):
+    """Positions kept of weights line[..., n], ascending."""
+    x = line.clone()
+    x[..., :first] = math.inf
+    x[..., n - recent:] = math.inf
+    return torch.sort(torch.sort(-x, dim=-1, stable=True).indices[..., :budget]).values
+
+
+@pytest.mark.parametrize("batch,kv_heads,most,budget,page,kinds,kv", [
+    (40, 4, 1100, 700, 64, 1 << 20, BF16),
+    (40, 4, 6000, 1000, 64, 1 << 20, BF16),       # more pairs than SMs, up to 12288 keys
+    (40, 4, 6000, 1000, 64, 3, MX4),
+    (40, 4, 13000, 2000, 64, 1 << 20, MX4),       # and above
+    (40, 4, 13000, 2000, 64, 3, BF16),
+    (3, 3, 100003, 3001, 256, 1 << 20, MX4),      # upper halves that do not fit shared memory
+    (60, 3, 97001, 130, 128, 5, BF16),            # the same, more pairs than SMs
+    (60, 3, 94000, 130, 128, 1 << 20, MX4),       # just past what fits
+])
+def test_evict_of_many_and_of_long_sequences(batch, kv_heads, most, budget, page, kinds, kv):
+    g = torch.Generator(device="cuda").manual_seed(most)
+    first, recent, dim = 4, 40, 64
+    lens = torch.randint(most // 2, most + 1, (batch,), generator=g, device="cuda")
+    lens[0] = most
+    lens[1] = budget                              # one that stays
+    need, keep = -(-most // page), -(-budget // page)
+    pages = batch * (need + keep)
+    perm = torch.randperm(pages, generator=g, device="cuda").int().view(batch, need + keep)
+    table, dst = perm[:, :need].contiguous(), perm[:, need:].contiguous()
+    # (halves of the mantissa differ, so that upper halves of the keys repeat)
+    w = torch.randint(0, kinds, (pages, kv_heads, page), generator=g, device="cuda").float() * 1e-3 + 2
+    row = dim if kv == BF16 else dim // 2
+    t = torch.int16 if kv == BF16 else torch.uint8
+
+    def cache(last):
+        return torch.randint(0, 100, (pages, page, kv_heads, last), generator=g, device="cuda",
+                             dtype=torch.int32).to(t)
+
+    k, v = cache(row), cache(row)
+    ks, vs = (cache(2), cache(2)) if kv == MX4 else (None, None)
+    p = B.PaProblem(num_seqs=batch, num_q_heads=kv_heads, num_kv_heads=kv_heads, head_dim=dim,
+                    page_size=page, num_pages=pages, max_pages_per_seq=need, max_context_len=most,
+                    kv_dtype=kv, sm_scale=1.0)
+    ctx = lens.int()
+    new = torch.full((batch,), -1, dtype=torch.int32, device="cuda")
+    kept = torch.full((batch, kv_heads, budget), -1, dtype=torch.int32, device="cuda")
+    err, old = error_word(), [x.clone() for x in (k, ks, v, vs) if x is not None] + [w.clone()]
+    as_given = (lambda x: x.view(torch.bfloat16)) if kv == BF16 else (lambda x: x)
+    B.pa_kv_evict(p, budget, first, recent, as_given(k), ks, as_given(v), vs, w, table, dst, ctx,
+                  kept, new, err)
+    torch.cuda.synchronize()
+    assert int(err) == 0 and torch.equal(new, ctx.clamp(max=budget))
+    assert bool((kept[1] == -1).all())
+    heads = torch.arange(kv_heads, device="cuda")[:, None]
+    at = torch.arange(budget, device="cuda")
+    now = [x for x in (k, ks, v, vs) if x is not None]
+    for b in range(batch):
+        n = int(lens[b])
+        if n <= budget:
+            continue
+        line = old[-1][table[b].long()].transpose(0, 1).reshape(kv_heads, -1)[:, :n]
+        want = plain_kept(line, n, budget, first, recent)
+        assert torch.equal(kept[b].long(), want)
+        sp, dp = table[b].long()[want // page], dst[b].long()[at // page].expand_as(want)
+        for got, was in zip(now, old):
+            assert torch.equal(got[dp, at % page, heads], was[sp, want % page, heads])
+        assert torch.equal(w[dp, heads, at % page], old[-1][sp, heads, want % page])
+
+
+# ---------------------------------------------------------------- key weights
+
+@pytest.mark.parametrize("kv", [BF16, MX4])
+@pytest.mark.parametrize("layout,dim,heads,kv_heads,page,ctx,ql,window", [
+    (NHD, 128, 16, 1, 16, [300, 41], [1, 1], 0),              # 16 rows
+    (HND, 64, 10, 2, 32, [70, 600, 3], [3, 1, 2], 0),         # 15, 5 and 10 rows
+    (NHD, 64, 9, 1, 16, [257, 256], [1, 0], 100),             # 9 rows, a window
+    (HND, 128, 4, 2, 64, [90, 513], [8, 5], 33),              # 16 and 10 rows, a window
+])
+def test_weights_of_two_products_of_rows(kv, layout, dim, heads, kv_heads, page, ctx, ql, window):
+    check_weights(R.Case(ctx, ql, heads=heads, kv_heads=kv_heads, dim=dim, page=page,
+                         layout=layout, kv=kv, window=window, seed=9))
+
+
+@pytest.mark.parametrize("kv", [BF16, MX4])
+@pytest.mark.parametrize("dim,heads", [(128, 4), (64, 8)])
+def test_weights_of_more_items_than_ctas(kv, dim, heads):
+    """Few query rows, many sequences and heads: a CTA goes on from item to item,
+    over heads and sequences, some of them without queries."""
+    g = torch.Generator().manual_seed(10)
+    ctx = torch.randint(1, 330, (110,), generator=g).tolist()
+    case = R.Case(ctx, [min(c, i % 3) for i, c in enumerate(ctx)], heads=heads, kv_heads=4, dim=dim,
+                  page=16, kv=kv, seed=10)
+    check_weights(case)
