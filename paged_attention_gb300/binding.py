@@ -296,11 +296,49 @@ def pa_prefill_fp8(problem, q, q_scale, k_cache, v_cache, block_table, context_l
 
 # --------------------------------------------- cache operators (pa_cache.h)
 
+# The kernels read every tensor but new K/V rows as dense, so a slice with other
+# strides would be misread, and so would lengths in 64 bits or a cache of another
+# element size than the problem's: these are refused here, where a tensor still
+# has its shape.  (Small problems are bound by a call's time on the host: a look at
+# type and device of every tensor as well costs 0.5 us of 5 more.)
+
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+
+
+def _dense(t: Optional[torch.Tensor]):
+    """Address of a contiguous tensor."""
+    if t is None:
+        return None
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"a tensor of shape {tuple(t.shape)} and strides {tuple(t.stride())} where a "
+                     f"contiguous one belongs")
+
+
+def _ints(t: Optional[torch.Tensor]):
+    """Address of lengths, a block table, positions or an error word."""
+    if t is None:
+        return None
+    if t.dtype is _I32 and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} on "
+                     f"{t.device} where contiguous int32 on the device belongs")
+
+
+def _cache(t: Optional[torch.Tensor], problem: PaProblem):
+    """Address of a K or V cache of the problem's kv_dtype."""
+    if t is None:
+        return None
+    if (t.dtype is _U8) != (problem.kv_dtype == PA_MX4):
+        raise ValueError(f"a {t.dtype} cache for kv_dtype {problem.kv_dtype}")
+    return t.data_ptr() if t.is_contiguous() else _dense(t)
+
+
 def _new_rows(t: torch.Tensor, problem: PaProblem, name: str) -> int:
     """Elements between the tokens of new K or V rows [tokens, Hkv, D]."""
     shape, stride = t.shape, t.stride()
     heads, dim = problem.num_kv_heads, problem.head_dim
-    if (len(shape) != 3 or t.dtype != torch.bfloat16 or shape[0] < problem.total_q_tokens
+    if (t.dtype is not _BF16 or len(shape) != 3 or shape[0] < problem.total_q_tokens
             or shape[1] != heads or shape[2] != dim
             or stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{name} must be bf16 [total_q_tokens, num_kv_heads, head_dim] with "
@@ -313,20 +351,21 @@ def pa_kv_append(problem, k_new, v_new, block_table, context_lens, q_lens, k_cac
     """New K/V rows into the cache; the tokens of k_new / v_new may be strided
     (slices of a fused projection)."""
     ks, vs = _new_rows(k_new, problem, "k_new"), _new_rows(v_new, problem, "v_new")
-    _check(load().pa_kv_append(
-        ctypes.byref(problem), _p(k_new), _p(v_new), ks, vs, _p(block_table), _p(context_lens),
-        _p(q_lens), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale), _p(key_weights),
-        _p(device_error), _stream(stream)), "pa_kv_append")
+    _check((_lib or load()).pa_kv_append(
+        problem, k_new.data_ptr(), v_new.data_ptr(), ks, vs, _ints(block_table),
+        _ints(context_lens), _ints(q_lens), _cache(k_cache, problem), _dense(k_scale),
+        _dense(v_cache), _dense(v_scale), _dense(key_weights), _ints(device_error),
+        _stream(stream)), "pa_kv_append")
 
 
 def pa_kv_expand(problem, k_cache, k_scale, v_cache, v_scale, block_table, context_lens, q_lens,
                  dst_block_table, dst_num_pages, k_out, v_out, device_error=None, stream=None):
     """The last q_lens[b] tokens of each sequence of a 4-bit cache as bf16 pages."""
-    _check(load().pa_kv_expand(
-        ctypes.byref(problem), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale),
-        _p(block_table), _p(context_lens), _p(q_lens), _p(dst_block_table),
-        int(dst_block_table.shape[1]), int(dst_num_pages), _p(k_out), _p(v_out),
-        _p(device_error), _stream(stream)), "pa_kv_expand")
+    _check((_lib or load()).pa_kv_expand(
+        problem, _cache(k_cache, problem), _dense(k_scale), _dense(v_cache), _dense(v_scale),
+        _ints(block_table), _ints(context_lens), _ints(q_lens), _ints(dst_block_table),
+        dst_block_table.shape[1], int(dst_num_pages), _dense(k_out), _dense(v_out),
+        _ints(device_error), _stream(stream)), "pa_kv_expand")
 
 
 def pa_mx4_workspace_size(problem: PaProblem) -> int:
@@ -336,18 +375,18 @@ def pa_mx4_workspace_size(problem: PaProblem) -> int:
 def pa_decode_mx4(problem, q, k_cache, k_scale, v_cache, v_scale, block_table, context_lens,
                   q_lens, ws, out, lse, stream=None):
     """Decode attention over a 4-bit cache (one call, no Assign)."""
-    _check(load().pa_decode_mx4(
-        ctypes.byref(problem), _p(q), _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale),
-        _p(block_table), _p(context_lens), _p(q_lens), _p(ws), _nbytes(ws), _p(out), _p(lse),
-        _stream(stream)), "pa_decode_mx4")
+    _check((_lib or load()).pa_decode_mx4(
+        problem, _dense(q), _cache(k_cache, problem), _dense(k_scale), _dense(v_cache),
+        _dense(v_scale), _ints(block_table), _ints(context_lens), _ints(q_lens), _dense(ws),
+        _nbytes(ws), _dense(out), _dense(lse), _stream(stream)), "pa_decode_mx4")
 
 
 def pa_key_weights(problem, q, k_cache, k_scale, block_table, context_lens, q_lens, lse,
                    key_weights, device_error=None, stream=None):
     """Add the softmax weight of the given queries to every cached key's total."""
-    _check(load().pa_key_weights(
-        ctypes.byref(problem), _p(q), _p(k_cache), _p(k_scale), _p(block_table),
-        _p(context_lens), _p(q_lens), _p(lse), _p(key_weights), _p(device_error),
+    _check((_lib or load()).pa_key_weights(
+        problem, _dense(q), _cache(k_cache, problem), _dense(k_scale), _ints(block_table),
+        _ints(context_lens), _ints(q_lens), _dense(lse), _dense(key_weights), _ints(device_error),
         _stream(stream)), "pa_key_weights")
 
 
@@ -356,11 +395,12 @@ def pa_kv_evict(problem, budget, num_first, num_recent, k_cache, k_scale, v_cach
                 device_error=None, stream=None):
     """Keep `budget` keys per KV head of every longer sequence, packed into the
     pages of dst_block_table."""
-    _check(load().pa_kv_evict(
-        ctypes.byref(problem), int(budget), int(num_first), int(num_recent), _p(k_cache),
-        _p(k_scale), _p(v_cache), _p(v_scale), _p(key_weights), _p(block_table),
-        _p(dst_block_table), int(dst_block_table.shape[1]), _p(context_lens), _p(kept),
-        _p(new_context_lens), _p(device_error), _stream(stream)), "pa_kv_evict")
+    _check((_lib or load()).pa_kv_evict(
+        problem, int(budget), int(num_first), int(num_recent), _cache(k_cache, problem),
+        _dense(k_scale), _dense(v_cache), _dense(v_scale), _dense(key_weights),
+        _ints(block_table), _ints(dst_block_table), dst_block_table.shape[1],
+        _ints(context_lens), _ints(kept), _ints(new_context_lens), _ints(device_error),
+        _stream(stream)), "pa_kv_evict")
 
 
 def pa_set_task_trace(trace: Optional[torch.Tensor]):

@@ -150,6 +150,86 @@ def test_binding_checks_new_rows():
             B._new_rows(t, p, "k_new")
 
 
+def test_binding_refuses_what_the_kernels_would_misread():
+    wide = torch.zeros((4, 6), dtype=torch.float32)
+    assert B._dense(None) is None and B._dense(wide) == wide.data_ptr()
+    assert B._dense(wide[1:3]) == wide[1:3].data_ptr()          # whole rows are dense
+    for t in (wide[:, :4], wide.t(), wide[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            B._dense(t)
+    assert B._ints(None) is None
+    with pytest.raises(ValueError, match="int64"):
+        B._ints(torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="on cpu"):
+        B._ints(torch.zeros(3, dtype=torch.int32))
+    codes, rows = torch.zeros(64, dtype=torch.uint8), torch.zeros(64, dtype=torch.bfloat16)
+    mx4, bf16 = problem(), problem(kv_dtype=B.PA_BF16)
+    assert B._cache(codes, mx4) == codes.data_ptr() and B._cache(rows, bf16) == rows.data_ptr()
+    assert B._cache(None, bf16) is None
+    for t, p in ((codes, bf16), (rows, mx4)):
+        with pytest.raises(ValueError, match="cache for kv_dtype"):
+            B._cache(t, p)
+
+
+def test_binding_refuses_before_the_library_is_called(monkeypatch):
+    """Each entry point, every tensor in turn a slice of a wider one, lengths and
+    tables in 64 bits, a cache of the other type: refused with nothing called."""
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    # (CPU tensors stand for device ones)
+    monkeypatch.setattr(B, "_lib", Library())
+    monkeypatch.setattr(B, "_stream", lambda s: 0)
+    ints = B._ints
+    monkeypatch.setattr(B, "_ints", lambda t: B._dense(t) if t is None or t.dtype is torch.int32
+                        else ints(t))
+
+    def i32(*shape):
+        return torch.zeros(shape, dtype=torch.int32)
+
+    def u8(*shape):
+        return torch.zeros(shape, dtype=torch.uint8)
+
+    bf, f32 = (lambda *s: torch.zeros(s, dtype=torch.bfloat16)), (lambda *s: torch.zeros(s))
+    p, new, q = problem(), bf(3, 2, 128), bf(3, 8, 128)
+    table, lens, err = i32(3, 10), i32(3), i32(1)
+    cache, scale, pages = u8(50, 16, 2, 64), u8(50, 16, 2, 4), bf(50, 16, 2, 128)
+    lse, w = f32(3, 8), f32(50, 2, 16)
+    whole = {
+        "pa_kv_append": [p, new, new, table, lens, lens, cache, scale, cache, scale, w, err],
+        "pa_kv_expand": [p, cache, scale, cache, scale, table, lens, lens, table, 50, pages, pages,
+                         err],
+        "pa_decode_mx4": [p, q, cache, scale, cache, scale, table, lens, lens, u8(1 << 20), q, lse],
+        "pa_key_weights": [p, q, cache, scale, table, lens, lens, lse, w, err],
+        "pa_kv_evict": [p, 9, 1, 2, cache, scale, cache, scale, w, table, table, lens, i32(3, 2, 9),
+                        lens, err],
+    }
+    for name, args in whole.items():
+        fn = getattr(B, name)
+        fn(*args)
+        assert calls == [name]
+        for i, a in enumerate(args):
+            if not isinstance(a, torch.Tensor) or (name == "pa_kv_append" and i in (1, 2)):
+                continue
+            if a.numel() > 1:
+                wider = torch.zeros(a.shape[:-1] + (a.shape[-1] + 1,), dtype=a.dtype)
+                strided = (wider[..., :-1] if a.dim() > 1
+                           else torch.zeros(2 * len(a), dtype=a.dtype)[::2])
+                with pytest.raises(ValueError):
+                    fn(*args[:i], strided, *args[i + 1:])
+            if a.dtype is torch.int32:
+                with pytest.raises(ValueError):
+                    fn(*args[:i], a.long(), *args[i + 1:])
+        if name not in ("pa_kv_expand", "pa_decode_mx4"):      # these take 4-bit caches alone
+            with pytest.raises(ValueError):
+                fn(problem(kv_dtype=B.PA_BF16), *args[1:])
+        assert calls == [name]
+        calls.clear()
+
+
 def test_plain_quantisation_by_hand():
     x = torch.zeros((1, 64), dtype=torch.float64)
     # largest 6.0: exponent 2 - 2 = 0, scale byte 127; the values are their own codes

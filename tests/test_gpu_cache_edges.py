@@ -375,3 +375,26 @@ def test_weights_of_more_items_than_ctas(kv, dim, heads):
     case = R.Case(ctx, [min(c, i % 3) for i, c in enumerate(ctx)], heads=heads, kv_heads=4, dim=dim,
                   page=16, kv=kv, seed=10)
     check_weights(case)
+
+
+# ------------------------------------------------------------------- refusals
+
+def test_what_would_be_misread_is_refused_on_the_device_too():
+    """A strided q, lengths on the host or in 64 bits, a slice of a wider block
+    table: refused, with nothing launched."""
+    c = Coded([100, 30], [1, 1], heads=4, kv_heads=2, dim=64, page=16, seed=11)
+    ws, p = c.space(), c.problem()
+    out = torch.full((2, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    good = dict(q=c.q, table=c.table, ctx=c.ctx_t, ql=c.ql_t)
+    wide_q = torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda")[:, :4]
+    wide_table = torch.zeros((2, c.mpps + 3), dtype=torch.int32, device="cuda")[:, :c.mpps]
+    for name, t in (("q", wide_q), ("table", wide_table), ("table", c.table.cpu()),
+                    ("ctx", c.ctx_t.cpu()), ("ctx", c.ctx_t.long()), ("ql", c.ql_t.long())):
+        a = dict(good, **{name: t})
+        with pytest.raises(ValueError):
+            B.pa_decode_mx4(p, a["q"], c.k, c.ks, c.v, c.vs, a["table"], a["ctx"], a["ql"], ws, out,
+                            None)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+    B.pa_decode_mx4(p, c.q, c.k, c.ks, c.v, c.vs, c.table, c.ctx_t, c.ql_t, ws, out, None)
+    assert torch.equal(out, c.decode(c.space())[0])
