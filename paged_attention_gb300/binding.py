@@ -172,10 +172,17 @@ def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+# torch.cuda.current_stream() builds an object (3 us of every call); what its own code
+# asks for such a stream's handle (of the current device: -1) has no public name, so
+# this goes without where it is not there.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        # (torch.cuda.current_stream() builds an object: 3 us of every call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is not None:
+            return _raw_stream(-1)
+        return torch.cuda.current_stream().cuda_stream
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 

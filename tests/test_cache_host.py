@@ -230,6 +230,19 @@ def test_binding_refuses_before_the_library_is_called(monkeypatch):
         calls.clear()
 
 
+def test_stream_handles(monkeypatch):
+    """The current stream's handle, with torch's unnamed call for it and without."""
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(B.torch.cuda, "current_stream", lambda: Stream())
+    monkeypatch.setattr(B, "_raw_stream", None)
+    assert B._stream(None) == 77
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 100 + dev)
+    assert B._stream(None) == 99                             # -1: the current device
+    assert B._stream(Stream()) == 77 and B._stream(5) == 5
+
+
 def test_plain_quantisation_by_hand():
     x = torch.zeros((1, 64), dtype=torch.float64)
     # largest 6.0: exponent 2 - 2 = 0, scale byte 127; the values are their own codes

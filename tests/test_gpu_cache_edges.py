@@ -398,3 +398,13 @@ def test_what_would_be_misread_is_refused_on_the_device_too():
     assert bool((out == 7.0).all())
     B.pa_decode_mx4(p, c.q, c.k, c.ks, c.v, c.vs, c.table, c.ctx_t, c.ql_t, ws, out, None)
     assert torch.equal(out, c.decode(c.space())[0])
+
+
+def test_the_current_stream_with_and_without_torchs_unnamed_call(monkeypatch):
+    assert B._raw_stream is not None
+    side = torch.cuda.Stream()
+    for raw in (B._raw_stream, None):
+        monkeypatch.setattr(B, "_raw_stream", raw)
+        assert B._stream(None) == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert B._stream(None) == side.cuda_stream
