@@ -30,6 +30,11 @@
  *   pa_key_weights, with more than 16 rows of queries and heads): a pipeline
  *   wait ran out; the weights are then unspecified.
  *
+ * total_q_tokens = 0 (all but pa_kv_evict): there is nothing to do.  The call
+ *   returns PA_OK after its checks of the problem (and of the workspace), takes
+ *   NULL for every other pointer, and launches nothing: lengths are not read, so
+ *   q_lens that add up to more are not reported.
+ *
  * Shapes: head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; any number of
  * KV heads.  pa_problem's mask_q_tiles / mask_kv_tiles must be 0 and q_dtype
  * PA_BF16; fields an operator does not mention are not read by it, but must
@@ -105,6 +110,9 @@ PA_API pa_status pa_kv_expand(const pa_problem* problem, const void* k_cache, co
  *     bf16's eight bits are exact);
  *   - a V block relative to the largest scale that its 32 columns met so far:
  *     what lies more than a factor 2^24 below that is lost.
+ * Scores are summed before a query's power of two is put back (here, and in
+ * pa_key_weights over PA_MX4 up to 16 rows): keys of 2^119 and more may
+ * overflow to infinite scores, whatever the query.
  *   ws: >= pa_mx4_workspace_size bytes, 256-byte aligned, zero-filled by the
  *     caller before its first use.  Every call that runs to its end leaves it
  *     ready for the next one, of the same or another problem (a second launch to

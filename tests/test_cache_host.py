@@ -131,6 +131,17 @@ def test_no_rows_is_no_work(lib):
         assert call(lib, name, p, args) == B.PA_OK
 
 
+def test_no_rows_is_no_work_in_decode(lib):
+    """As above, but the workspace is still looked at."""
+    p = problem(total_q_tokens=0, max_q_len=0)
+    n = B.pa_mx4_workspace_size(p)
+    assert n > 0
+    rest = [None, None, None]                      # out, lse, stream
+    assert call(lib, "pa_decode_mx4", p, [None] * 8 + [FAKE, n] + rest) == B.PA_OK
+    assert call(lib, "pa_decode_mx4", p, [None] * 8 + [FAKE, n - 1] + rest) == B.PA_ERR_WORKSPACE
+    assert call(lib, "pa_decode_mx4", p, [None] * 9 + [n] + rest) == B.PA_ERR_INVALID_ARG
+
+
 def test_attention_entry_points_refuse_a_4_bit_cache(lib):
     p = problem()
     assert B.pa_assign_workspace_size(p, B.PA_MODE_DECODE) == 0
