@@ -38,8 +38,8 @@ namespace {
 constexpr int kMaxGrid = 1024;          // CTAs of pa_decode_mx4
 constexpr int kMaxHeads = 1 << 15;      // KV heads
 // A unit's fixed cost (its first loads, its warps' merge), in 64-key tiles.  64
-// sequences of 128 .. 32768 tokens, 8 rows: 159 us with 0, 115 with 4, 108 with 8,
-// 112 with 12; 128 of 1024 .. 16384 tokens, 24 rows: 550, 529, 513 and 501.
+// sequences of 128 .. 32768 tokens, 8 rows: 154 us with 0, 112 with 4, 105 with 8,
+// 109 with 12; 128 of 1024 .. 16384 tokens, 24 rows: 533, 512, 497 and 492.
 constexpr int mx4_unit_cost(int rows) { return rows > 16 ? 12 : 8; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

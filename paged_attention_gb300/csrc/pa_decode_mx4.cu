@@ -11,7 +11,9 @@
 // the last CTA to finish one joins them.
 //
 // What bounds it: 17/16 D bytes a key and head from HBM (136 at D = 128, K and
-// V), and the instructions that turn 4-bit codes into operands.  So:
+// V; with more rows than a block holds, every block of them reads the cache, two at
+// most, also where a sequence's own rows fit one), and the instructions that
+// turn 4-bit codes into operands.  So:
 //   - products are transposed (mma m16n8k16 with 16 keys, or 16 columns of V,
 //     as rows): R query rows cost ceil(R/8) products, no half-empty tiles;
 //   - the contraction order is free, so each lane takes the bytes of a row as
@@ -53,22 +55,22 @@ struct Mx4Params {
 };
 
 // No CTA takes less than this of the flat line: joining a unit's parts costs more
-// than the tiles it would spread (3 sequences of 37 to 100 tokens: 12.4 us with 1,
-// 6.8 with 4; one of 4000 tokens, 8 heads: 13.7 with 1, 11.9 with 4, 16.7 with 8).
+// than the tiles it would spread (3 sequences of 37 to 100 tokens: 11.7 us with 1,
+// 6.5 with 4, 7.0 with 8; one of 4000 tokens, 8 heads: 13.8, 11.5 and 16.1).
 constexpr int kMinShare = 4;
 
 template <int D, int NT>
 struct Mx4Cfg {
     // CTAs of an SM: what the registers of a thread (O alone takes NT D / 4)
     // leave room for.  Measured on 64 sequences of 128 to 32768 tokens: 8 rows, D =
-    // 128, 3 CTAs of 4 warps (168 registers) 114 us, 4 (128 registers, and spills)
-    // 125; 16 rows, D = 128, 2 CTAs (255 registers) 152 us, 3 (spills) 177; 32
-    // rows, D = 64, 190 and 201
+    // 128, 3 CTAs of 4 warps (168 registers) 105 us, 4 (128 registers, and spills)
+    // 112; 16 rows, D = 128, 2 CTAs (255 registers) 145 us, 3 (spills) 173; 32
+    // rows, D = 64, 182 and 193
     static constexpr int kPerThread = NT * D;
     static constexpr int kCtas = kPerThread <= 128 ? 3 : 2;
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = kPerThread <= 128 ? 2 : 3;   // (3 and 4 measured the same)
+    static constexpr int kStages = kPerThread <= 128 ? 2 : 3;   // (8 rows, 3: 106 us)
     static constexpr int kStep = 32;                       // tokens of a warp's step
     static constexpr int kRow = D / 2;                     // code bytes of a row
     static constexpr int kStage = 2 * kStep * (kRow + 4);  // K, V, their scale words
@@ -255,7 +257,8 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
     constexpr int CH = ROW / 16, RPI = 32 / CH;   // chunks of a row, rows an instruction
     constexpr int HALF = 16 / RPI;                // instructions for 16 rows
     static_assert(RPI % 8 == 0, "the chunk order repeats every 8 rows");
-    uint64_t once, again;   // codes are read once; a sector of scales serves several heads
+    // a block of rows reads codes once; a sector of scales serves several heads
+    uint64_t once, again;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(again));
     const int page_rows = g.ps * g.Hkv;
@@ -954,7 +957,7 @@ cudaError_t launch_decode_mx4(const CacheGeom& g, int nt, const void* q, const v
             case 1: return launch_mx4<128, 1>(P, grid, stream);
             case 2: return launch_mx4<128, 2>(P, grid, stream);
             case 3: return launch_mx4<128, 3>(P, grid, stream);
-            // (32 rows at a time spill: 64 sequences 302 us, two blocks of 16 256)
+            // (32 rows at a time spill: 64 sequences 288 us, two blocks of 16 260)
             case 4: return launch_mx4<128, 2, 2>(P, grid, stream);
         }
     } else {
@@ -962,7 +965,7 @@ cudaError_t launch_decode_mx4(const CacheGeom& g, int nt, const void* q, const v
             case 1: return launch_mx4<64, 1>(P, grid, stream);
             case 2: return launch_mx4<64, 2>(P, grid, stream);
             case 4: return launch_mx4<64, 4>(P, grid, stream);
-            // (64 rows at a time spill: 64 sequences 575 us, two blocks of 32 340)
+            // (64 rows at a time spill: 64 sequences 497 us, two blocks of 32 307)
             case 8: return launch_mx4<64, 4, 2>(P, grid, stream);
         }
     }
