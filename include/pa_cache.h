@@ -49,6 +49,10 @@
 extern "C" {
 #endif
 
+/* pa_decode_mx4 only, beside the PA_DEV_* codes of pa.h: a counter of the workspace
+ * is none that a call leaves behind; rows of out and lse were not written. */
+enum { PA_DEV_BAD_WORKSPACE = 8 };
+
 /* pa_problem.kv_dtype of the operators below (the entry points of pa.h refuse it). */
 enum { PA_MX4 = 2 };
 
@@ -119,7 +123,9 @@ PA_API pa_status pa_kv_expand(const pa_problem* problem, const void* k_cache, co
  *     clear it would cost a small call more than its attention); its first 256
  *     bytes hold the error word that pa_last_device_error reads, which stays
  *     set until the caller clears them.  Calls that may run at the same time
- *     need a workspace each.
+ *     need a workspace each.  A workspace that was never filled, or that two
+ *     calls used at once, is reported (PA_DEV_BAD_WORKSPACE) where its counters
+ *     can no longer come out; it serves again once it is filled with zeros.
  *   Other arguments as pa_decode_splitk.
  */
 PA_API size_t pa_mx4_workspace_size(const pa_problem* problem);

@@ -28,6 +28,7 @@ PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE = 1, 2, 3
 PA_NHD, PA_HND = 0, 1
 PA_BF16, PA_FP8_E4M3 = 0, 1
 PA_MX4 = 2   # cache operators only (include/pa_cache.h)
+PA_DEV_BAD_WORKSPACE = 8   # the same
 PA_SCALE_PER_TENSOR, PA_SCALE_PER_ROW = 0, 1
 PA_MODE_DECODE, PA_MODE_PREFILL = 0, 1
 PA_MAP_DECODE_PART = 2   # pa_read_task_map: decode part of a prefill-mode workspace

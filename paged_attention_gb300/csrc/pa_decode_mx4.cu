@@ -811,8 +811,12 @@ decode_mx4_kernel(const __grid_constant__ Mx4Params P) {
                 bool last = false;
                 if (threadIdx.x == 0) {
                     __threadfence();   // every warp's part is written (barrier above)
-                    last = atomicAdd(P.done + c_first, 1) == c_last - c_first;
+                    const uint32_t before = (uint32_t)atomicAdd(P.done + c_first, 1);
+                    last = before == (uint32_t)(c_last - c_first);
                     if (last) P.done[c_first] = 0;   // as the next call finds it
+                    // (nobody will come last: the workspace did not start as zeros)
+                    if (before > (uint32_t)(c_last - c_first))
+                        flag_error(P.header + H_ERROR, PA_DEV_BAD_WORKSPACE);
                     __threadfence();
                     *flag = last ? 1 : 0;
                 }

@@ -120,6 +120,22 @@ def test_one_workspace_serves_grids_of_any_size(dim, grid):
     assert B.pa_last_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("fill", [0x7F, 0xFF])
+def test_a_workspace_that_does_not_start_as_zeros_is_reported(fill):
+    """Counters that no call leaves behind: reported, where rows would go
+    missing silently; zeros make the workspace good again."""
+    c = Coded([5000], [1], heads=8, kv_heads=1, dim=64, seed=14)
+    want = c.decode(c.space())
+    ws = c.space()
+    ws[256:256 + 4 * 1024] = fill
+    c.decode(ws)
+    assert B.pa_last_device_error(ws) == B.PA_DEV_BAD_WORKSPACE
+    ws.zero_()
+    got = c.decode(ws)
+    assert B.pa_last_device_error(ws) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_decode_repeats_itself_bit_for_bit():
     """Calls after calls of a batch whose units are split over CTAs."""
     c = Coded([128, 20000, 333, 4500, 64, 9000], [2, 2, 1, 2, 2, 1], heads=32, kv_heads=8, dim=128,
