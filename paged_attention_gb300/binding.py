@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in include/pa.h and include/pa_cache.h (argument
-marshalling only).
+"""ctypes binding of the C ABI in include/pa.h, include/pa_cache.h and
+include/pa_step.h (argument marshalling only).
 
 Each ``pa_*`` function here has the name and argument order of the C entry
 point, takes torch tensors (device memory) instead of raw pointers, passes
@@ -29,6 +29,8 @@ PA_NHD, PA_HND = 0, 1
 PA_BF16, PA_FP8_E4M3 = 0, 1
 PA_MX4 = 2   # cache operators only (include/pa_cache.h)
 PA_DEV_BAD_WORKSPACE = 8   # the same
+PA_DEV_NO_PAGES = 16   # pa_pages_take only (include/pa_step.h)
+PA_ROPE_NONE, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(5)
 PA_SCALE_PER_TENSOR, PA_SCALE_PER_ROW = 0, 1
 PA_MODE_DECODE, PA_MODE_PREFILL = 0, 1
 PA_MAP_DECODE_PART = 2   # pa_read_task_map: decode part of a prefill-mode workspace
@@ -45,6 +47,11 @@ EXPORTED = (
 # declared in include/pa_cache.h
 EXPORTED_CACHE = ("pa_kv_append", "pa_kv_expand", "pa_mx4_workspace_size", "pa_decode_mx4",
                   "pa_key_weights", "pa_kv_evict")
+
+# declared in include/pa_step.h
+EXPORTED_STEP = ("pa_pages_take", "pa_pages_return", "pa_rope_inv_freq", "pa_rope_steps",
+                 "pa_rope_append", "pa_page_bounds", "pa_select_pages",
+                 "pa_selected_workspace_size", "pa_decode_selected")
 
 PA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # size of the library's fixed scratch
 # pa_problem.unit_cost = 0 takes these (PA_DEFAULT_UNIT_COST_DECODE / _PREFILL)
@@ -93,6 +100,30 @@ class PaProblem(ctypes.Structure):
         ("q_dtype", ctypes.c_int32),
         ("q_scale_mode", ctypes.c_int32),
         ("unit_cost", ctypes.c_int32),
+    ]
+
+
+class PaRopeScaling(ctypes.Structure):
+    """Field-for-field copy of ``pa_rope_scaling`` in include/pa_step.h."""
+
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_context", ctypes.c_double),
+        ("high_turns", ctypes.c_double),
+        ("low_turns", ctypes.c_double),
+    ]
+
+
+class PaRope(ctypes.Structure):
+    """Field-for-field copy of ``pa_rope`` in include/pa_step.h."""
+
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("cos_sin_scale", ctypes.c_float),
     ]
 
 
@@ -150,6 +181,16 @@ def load(build_if_missing: bool = True):
             "pa_decode_mx4": (i32, [PP] + [vp] * 9 + [sz] + [vp] * 3),
             "pa_key_weights": (i32, [PP] + [vp] * 10),
             "pa_kv_evict": (i32, [PP, i32, i32, i32] + [vp] * 7 + [i32] + [vp] * 5),
+            "pa_pages_take": (i32, [PP] + [vp] * 12),
+            "pa_pages_return": (i32, [PP] + [vp] * 8),
+            "pa_rope_inv_freq": (i32, [ctypes.POINTER(PaRopeScaling), vp, vp]),
+            "pa_rope_steps": (i32, [vp, ctypes.c_int32, vp]),
+            "pa_rope_append": (i32, [PP, ctypes.POINTER(PaRope)] + [vp] * 4 + [i64] * 3
+                               + [vp] * 9),
+            "pa_page_bounds": (i32, [PP] + [vp] * 6),
+            "pa_select_pages": (i32, [PP, i32, i32, i32] + [vp] * 9),
+            "pa_selected_workspace_size": (sz, [PP, ctypes.c_int32]),
+            "pa_decode_selected": (i32, [PP, i32] + [vp] * 8 + [sz] + [vp] * 3),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -409,6 +450,157 @@ def pa_kv_evict(problem, budget, num_first, num_recent, k_cache, k_scale, v_cach
         _ints(block_table), _ints(dst_block_table), dst_block_table.shape[1],
         _ints(context_lens), _ints(kept), _ints(new_context_lens), _ints(device_error),
         _stream(stream)), "pa_kv_evict")
+
+
+# ------------------------------------ operators of a serving step (pa_step.h)
+
+_I8, _F32 = torch.int8, torch.float32
+_device_index = torch.cuda.current_device
+
+
+def _here(t: torch.Tensor):
+    """The library launches on the current device: a tensor elsewhere is refused."""
+    if not t.is_cuda or t.get_device() != _device_index():
+        raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
+
+
+def _typed(t: Optional[torch.Tensor], dtype, name: str):
+    """Address of a contiguous tensor of a type."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous {dtype}, not {t.dtype} of strides "
+                     f"{tuple(t.stride())}")
+
+
+def _room(t: torch.Tensor, n: int, name: str):
+    """Address of int32 on the device, n elements at least."""
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements where {n} belong")
+    return _ints(t)
+
+
+def _table_of(t: torch.Tensor, problem: PaProblem):
+    if t.dim() != 2 or t.shape[0] < problem.num_seqs or t.shape[1] != problem.max_pages_per_seq:
+        raise ValueError(f"a block table of shape {tuple(t.shape)} for num_seqs "
+                         f"{problem.num_seqs} and max_pages_per_seq {problem.max_pages_per_seq}")
+    return _ints(t)
+
+
+def pa_pages_take(problem, seq_lens, q_lens, block_table, free_pages, free_count, context_lens,
+                  row_seq, positions, slots, free_left, device_error=None, stream=None):
+    """Pages for q_lens[b] new tokens of every sequence, and the maps of the step's rows."""
+    n, rows = problem.num_seqs, problem.total_q_tokens
+    _here(seq_lens)
+    _check((_lib or load()).pa_pages_take(
+        problem, _room(seq_lens, n, "seq_lens"), _room(q_lens, n, "q_lens"),
+        _table_of(block_table, problem), _room(free_pages, 1, "free_pages"),
+        _room(free_count, 1, "free_count"), _room(context_lens, n, "context_lens"),
+        _room(row_seq, rows, "row_seq"), _room(positions, rows, "positions"),
+        _room(slots, rows, "slots"), _room(free_left, 1, "free_left"), _ints(device_error),
+        _stream(stream)), "pa_pages_take")
+
+
+def pa_pages_return(problem, seq_lens, keep_lens, block_table, free_pages, free_count, free_left,
+                    device_error=None, stream=None):
+    """The pages of tokens keep_lens[b] .. seq_lens[b] - 1 back on the free stack."""
+    n = problem.num_seqs
+    _here(seq_lens)
+    _check((_lib or load()).pa_pages_return(
+        problem, _room(seq_lens, n, "seq_lens"), _room(keep_lens, n, "keep_lens"),
+        _table_of(block_table, problem), _room(free_pages, problem.num_pages, "free_pages"),
+        _room(free_count, 1, "free_count"), _room(free_left, 1, "free_left"),
+        _ints(device_error), _stream(stream)), "pa_pages_return")
+
+
+def pa_rope_inv_freq(scaling: PaRopeScaling):
+    """(inverse frequencies float64 [rotary_dim / 2] on the host, factor on cos and sin)."""
+    freq = torch.zeros(max(1, scaling.rotary_dim // 2), dtype=torch.float64)
+    factor = ctypes.c_double(0.0)
+    _check(load().pa_rope_inv_freq(ctypes.byref(scaling), freq.data_ptr(), ctypes.byref(factor)),
+           "pa_rope_inv_freq")
+    return freq, float(factor.value)
+
+
+def pa_rope_steps(inv_freq) -> torch.Tensor:
+    """int64 [count] on the host (the bits of C's uint64): the form of pa_rope_append."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+    steps = torch.zeros(freq.numel(), dtype=torch.int64)
+    _check(load().pa_rope_steps(freq.data_ptr(), freq.numel(), steps.data_ptr()),
+           "pa_rope_steps")
+    return steps
+
+
+def _token_rows(t: torch.Tensor, tokens: int, heads: int, dim: int, name: str) -> int:
+    """Elements between the tokens of rows [tokens, heads, dim] with dense heads."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not _BF16 or len(shape) != 3 or shape[0] < tokens or shape[1] != heads
+            or shape[2] != dim or stride[2] != 1 or (heads > 1 and stride[1] != dim)):
+        raise ValueError(f"{name} must be bf16 [total_q_tokens, {heads}, {dim}] with dense heads")
+    return stride[0] if shape[0] > 1 else heads * dim
+
+
+def pa_rope_append(problem, rope, steps, q, k_new, v_new, positions, slots, q_out, k_cache,
+                   k_scale, v_cache, v_scale, device_error=None, stream=None):
+    """Rotary positions on the new tokens' q (into q_out) and k, and k and v into the cache;
+    the tokens of q, k_new and v_new may be strided (slices of a fused projection)."""
+    rows, dim, kv = problem.total_q_tokens, problem.head_dim, problem.num_kv_heads
+    ks, vs = _new_rows(k_new, problem, "k_new"), _new_rows(v_new, problem, "v_new")
+    qs, qp = 0, None
+    if q is not None:
+        qs = _token_rows(q, rows, problem.num_q_heads, dim, "q")
+        qp = q.data_ptr()
+    if steps.numel() < rope.rotary_dim // 2:
+        raise ValueError(f"{steps.numel()} steps for a rotary_dim of {rope.rotary_dim}")
+    _here(positions)
+    _check((_lib or load()).pa_rope_append(
+        problem, rope, _typed(steps, torch.int64, "steps"), qp, k_new.data_ptr(),
+        v_new.data_ptr(), qs, ks, vs, _room(positions, rows, "positions"),
+        _room(slots, rows, "slots"), _typed(q_out, _BF16, "q_out"), _cache(k_cache, problem),
+        _dense(k_scale), _cache(v_cache, problem), _dense(v_scale), _ints(device_error),
+        _stream(stream)), "pa_rope_append")
+
+
+def pa_page_bounds(problem, k_cache, slots, bounds, bound_scale, device_error=None, stream=None):
+    """Each channel's largest and smallest key of the pages that the rows' slots are in."""
+    _here(slots)
+    _check((_lib or load()).pa_page_bounds(
+        problem, _typed(k_cache, _BF16, "k_cache"), _room(slots, problem.total_q_tokens, "slots"),
+        _typed(bounds, _I8, "bounds"), _typed(bound_scale, _F32, "bound_scale"),
+        _ints(device_error), _stream(stream)), "pa_page_bounds")
+
+
+def pa_select_pages(problem, budget, num_first, num_recent, q, bounds, bound_scale, block_table,
+                    row_seq, positions, selected, device_error=None, stream=None):
+    """Per row and KV head the budget's page indices with the highest bound on a logit."""
+    rows = problem.total_q_tokens
+    _here(positions)
+    _check((_lib or load()).pa_select_pages(
+        problem, int(budget), int(num_first), int(num_recent), _typed(q, _BF16, "q"),
+        _typed(bounds, _I8, "bounds"), _typed(bound_scale, _F32, "bound_scale"),
+        _table_of(block_table, problem), _room(row_seq, rows, "row_seq"),
+        _room(positions, rows, "positions"),
+        _room(selected, rows * problem.num_kv_heads * int(budget), "selected"),
+        _ints(device_error), _stream(stream)), "pa_select_pages")
+
+
+def pa_selected_workspace_size(problem: PaProblem, budget: int) -> int:
+    return int(load().pa_selected_workspace_size(ctypes.byref(problem), int(budget)))
+
+
+def pa_decode_selected(problem, budget, q, k_cache, v_cache, block_table, row_seq, positions,
+                       selected, ws, out, lse=None, stream=None):
+    """Attention of every row over the pages listed for it."""
+    rows = problem.total_q_tokens
+    _here(positions)
+    _check((_lib or load()).pa_decode_selected(
+        problem, int(budget), _typed(q, _BF16, "q"), _typed(k_cache, _BF16, "k_cache"),
+        _typed(v_cache, _BF16, "v_cache"), _table_of(block_table, problem),
+        _room(row_seq, rows, "row_seq"), _room(positions, rows, "positions"),
+        _room(selected, rows * problem.num_kv_heads * int(budget), "selected"), _dense(ws),
+        _nbytes(ws), _typed(out, _BF16, "out"), _typed(lse, _F32, "lse"), _stream(stream)),
+        "pa_decode_selected")
 
 
 def pa_set_task_trace(trace: Optional[torch.Tensor]):

@@ -2,7 +2,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "pa_cache_common.cuh"
+#include "pa_cache_host.cuh"
 
 namespace pa {
 
@@ -42,8 +42,7 @@ constexpr int kMaxHeads = 1 << 15;      // KV heads
 // 109 with 12; 128 of 1024 .. 16384 tokens, 24 rows: 533, 512, 497 and 492.
 constexpr int mx4_unit_cost(int rows) { return rows > 16 ? 12 : 8; }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+}  // namespace
 
 int sm_count() {
     constexpr int kMaxDevices = 64;
@@ -61,7 +60,6 @@ int sm_count() {
     return count[dev];
 }
 
-// The fields every cache operator relies on.
 pa_status geometry(const pa_problem* pp, bool queries, CacheGeom& g) {
     if (!pp) return PA_ERR_INVALID_ARG;
     const pa_problem& p = *pp;
@@ -107,15 +105,7 @@ pa_status geometry(const pa_problem* pp, bool queries, CacheGeom& g) {
     return PA_OK;
 }
 
-// A cache and, for PA_MX4, its scales.
-bool cache_ok(const pa_problem& p, const void* cache, const void* scale) {
-    if (!cache || !aligned(cache, 16)) return false;
-    return p.kv_dtype != PA_MX4 || (scale && aligned(scale, 16));
-}
-bool lens_ok(const int32_t* table, const int32_t* ctx, const int32_t* ql) {
-    return table && ctx && ql && aligned(table, 4) && aligned(ctx, 4) && aligned(ql, 4);
-}
-pa_status status_of(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
+namespace {
 
 // Workspace of pa_decode_mx4: header (error word) and the counters of as many
 // CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +

@@ -148,4 +148,39 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t e) {
     return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : e << 23);
 }
 
+// The larger of two bf16 pairs, NaN if either is; a bf16 pair times another.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+
+// The scale byte of a block, from a pair that holds its largest magnitude (NaN if any is).
+__device__ __forceinline__ uint32_t block_scale(uint32_t two) {
+    // biased exponent of the largest magnitude (magnitudes order like their bits)
+    const uint32_t ex = max(two & 0xffffu, two >> 16) >> 7;
+    return ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
+}
+// The codes of 8 bf16 elements of a block with scale byte e.
+__device__ __forceinline__ uint32_t codes8(const uint32_t* w, uint32_t e) {
+    if (e == 255) return 0u;
+    // times 2^(127 - e), never subnormal: exact in bf16 but for what is far
+    // below half the smallest code
+    const uint32_t inv = (254u - e) << 7;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t y = mul_bf16x2(w[i], inv | (inv << 16));
+        codes |= f32x2_to_e2m1x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u))
+                 << (8 * i);
+    }
+    return codes;
+}
+
 }  // namespace pa

@@ -85,18 +85,6 @@ __device__ __forceinline__ void find_places(const CacheGeom& g, const int32_t* t
     __syncthreads();
 }
 
-// The larger of two bf16 pairs, NaN if either is; a bf16 pair times another.
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // Quantise the 8 elements a lane holds of a block spread over 4 lanes.
 __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -104,21 +92,8 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& e) {
                               max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
     two = max_bf16x2(two, __shfl_xor_sync(0xffffffffu, two, 1));
     two = max_bf16x2(two, __shfl_xor_sync(0xffffffffu, two, 2));
-    // biased exponent of the largest magnitude (magnitudes order like their bits)
-    const uint32_t ex = max(two & 0xffffu, two >> 16) >> 7;
-    e = ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
-    if (ex == 255) return 0u;
-    // times 2^(127 - e), never subnormal: exact in bf16 but for what is far
-    // below half the smallest code
-    const uint32_t inv = (254u - e) << 7;
-    uint32_t codes = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t y = mul_bf16x2(w[i], inv | (inv << 16));
-        codes |= f32x2_to_e2m1x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u))
-                 << (8 * i);
-    }
-    return codes;
+    e = block_scale(two);
+    return codes8(w, e);
 }
 
 // A thread quantises 8 elements (16 source bytes) of a row at a time.  Bound by

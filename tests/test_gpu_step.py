@@ -1,0 +1,843 @@
+"""The operators of a serving step (include/pa_step.h) against their 64-bit plain
+forms, and together as a decode loop uses them."""
+import math
+
+import pytest
+import torch
+
+from paged_attention_gb300 import binding as B
+
+import cache_ref as C
+import step_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, HALF = torch.bfloat16, 2.0 ** -8        # a rounding to bf16 is off by half a step at most
+
+
+def ints(x):
+    return torch.as_tensor(x, dtype=torch.int32).cuda()
+
+
+def problem(**kw):
+    d = dict(num_seqs=1, num_q_heads=4, num_kv_heads=2, head_dim=128, page_size=16, num_pages=8,
+             max_pages_per_seq=8, total_q_tokens=1, max_q_len=1, max_context_len=128, layout=0,
+             kv_dtype=B.PA_BF16, sm_scale=0.1)
+    d.update(kw)
+    return B.PaProblem(**d)
+
+
+def no_error(err):
+    assert int(err) == 0
+
+
+# ------------------------------------------------------------------- pages
+
+def run_take(seq, q, table, stack, count, *, page, pages, rows, max_q, max_ctx, kv=B.PA_BF16):
+    width = len(table[0])
+    p = problem(num_seqs=len(seq), page_size=page, num_pages=pages, max_pages_per_seq=width,
+                total_q_tokens=rows, max_q_len=max_q, max_context_len=max_ctx, kv_dtype=kv)
+    t, err = ints(table), ints([0])
+    ctx, left = ints([-9] * len(seq)), ints([-9])
+    maps = [ints([-9] * rows) for _ in range(3)]
+    stack = ints(stack)
+    before = stack.clone()
+    B.pa_pages_take(p, ints(seq), ints(q), t, stack, ints([count]), ctx, *maps, left, err)
+    torch.cuda.synchronize()
+    assert torch.equal(stack, before)
+    return (t.tolist(), ctx.tolist(), list(zip(*(m.tolist() for m in maps))), int(left), int(err))
+
+
+def take_case(seq, q, *, page=16, spare=3, short=0, pad=0, seed=0, holes=()):
+    g = torch.Generator().manual_seed(seed)
+    have = [R.up(n, page) for n in seq]
+    need = [R.up(n + x, page) - h for n, x, h in zip(seq, q, have)]
+    pages = sum(have) + sum(need) + spare
+    perm = torch.randperm(pages, generator=g).tolist()
+    width = max(1, max(h + n for h, n in zip(have, need)))
+    table, at = [], 0
+    for h in have:
+        table.append(perm[at:at + h] + [-1] * (width - h))
+        at += h
+    for b, j in holes:
+        table[b][j] = pages + 5
+    stack = perm[at:] + [-1] * at
+    return dict(table=table, stack=stack, count=len(perm) - at - short), dict(
+        page=page, pages=pages, rows=sum(q) + pad, max_q=max(q), max_ctx=width * page)
+
+
+@pytest.mark.parametrize("seq,q,kw", [
+    ([0], [1], {}), ([15], [1], {}), ([16], [1], {}), ([17], [40], {}), ([5, 0, 31], [1, 1, 1], {}),
+    ([5, 0, 31, 16], [0, 33, 0, 16], dict(page=32)), ([0, 0, 0], [0, 0, 5], {}),
+    ([100, 1, 64, 255], [3, 70, 2, 1], dict(page=64, pad=7)), ([7] * 3, [300, 1, 129], dict(page=256)),
+    ([5, 20, 0, 40], [30, 1, 50, 9], dict(spare=0)), ([5, 20, 0, 40], [30, 1, 50, 9], dict(spare=0, short=1)),
+    ([5, 20, 0, 40], [30, 1, 50, 9], dict(spare=0, short=5)),
+    ([5, 20, 16, 40], [30, 1, 50, 9], dict(holes=[(0, 0), (2, 0)])),
+    (list(range(1300)), [1] * 1300, dict(pad=11)),             # more sequences than a round
+    ([3 * i % 50 for i in range(700)], [i % 5 for i in range(700)], dict(page=16, spare=0, short=100)),
+    ([3 * i % 50 for i in range(700)], [i % 5 for i in range(700)], dict(page=16, spare=0, short=30)),
+    ([0, 9], [5000, 4000], dict(page=16)),                     # more rows than a CTA's first pass
+])
+def test_take(seq, q, kw):
+    x, geo = take_case(seq, q, **kw)
+    got = run_take(seq, q, x["table"], x["stack"], x["count"], **geo)
+    want = R.take(seq, q, x["table"], x["stack"], x["count"], **geo)
+    assert got == tuple(want)
+
+
+def test_take_with_bad_lengths():
+    seq, q = [5, -3, 20, 30, 100, 10], [2, 1, -1, 9, 30, 3]
+    table = [[i * 8 + j for j in range(8)] for i in range(6)]
+    geo = dict(page=16, pages=60, rows=40, max_q=8, max_ctx=128)
+    got = run_take(seq, q, table, list(range(48, 60)) + [0] * 48, 12, **geo)
+    want = R.take(seq, q, table, list(range(48, 60)) + [0] * 48, 12, **geo)
+    assert got == tuple(want) and want[4] & 1
+    # rows that the call has no room for
+    geo["rows"] = 4
+    got = run_take([5, 6], [3, 3], table, list(range(48, 60)) + [0] * 48, 12, **geo)
+    want = R.take([5, 6], [3, 3], table, list(range(48, 60)) + [0] * 48, 12, **geo)
+    assert got == tuple(want) and want[4] == 1
+    # a stack that says it holds more than the pool, or less than nothing
+    for count in (61, -1):
+        out = run_take([5], [1], table[:1], [0] * 60, count, **dict(geo, rows=1))
+        assert out[4] == 1 and out[2] == [(0, 5, 5)]
+
+
+def test_take_passes_on_page_numbers_that_are_none():
+    geo = dict(page=16, pages=10, rows=20, max_q=20, max_ctx=64)
+    got = run_take([0], [20], [[-1] * 4], [0, 1, 99, 3, 0, 0, 0, 0, 0, 0], 4, **geo)
+    assert got[0] == [[3, 99, -1, -1]] and got[4] == 2
+    assert [m[2] for m in got[2]] == list(range(48, 64)) + [-1] * 4
+
+
+@pytest.mark.parametrize("kv", [B.PA_BF16, B.PA_MX4, B.PA_FP8_E4M3])
+def test_take_without_rows_and_for_every_cache(kv):
+    x, geo = take_case([5, 16], [0, 0], spare=4)
+    geo["max_q"] = 1
+    got = run_take([5, 16], [0, 0], x["table"], x["stack"], x["count"], kv=kv, **geo)
+    assert got == (x["table"], [5, 16], [], x["count"], 0)
+
+
+@pytest.mark.parametrize("seq,keep,page", [
+    ([0], [0], 16), ([17], [16], 16), ([17], [0], 16), ([100, 33, 64], [100, 33, 64], 32),
+    ([100, 33, 64], [97, 0, 1], 32), ([500, 5, 255], [3, 5, 0], 64),
+    ([7 * i % 90 for i in range(1200)], [max(0, 7 * i % 90 - i % 40) for i in range(1200)], 16),
+    ([100, 33, -1, 64, 2000], [101, 33, 0, -2, 0], 32),
+])
+def test_return(seq, keep, page):
+    width = max(1, max(R.up(max(n, 0), page) for n in seq if n < 1000))
+    total = sum(R.up(max(n, 0), page) for n in seq if n < 1000)
+    pages = total + 9
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(3)).tolist()
+    table, at = [], 0
+    for n in seq:
+        h = R.up(max(n, 0), page) if n < 1000 else width
+        table.append((perm + perm)[at:at + h] + [-1] * (width - h))
+        at += h if n < 1000 else 0
+    if len(table) > 1 and len(seq) == 3 and page == 64:
+        table[0][2] = -7                      # an entry that is none
+    stack = perm[total:] + [-9] * total
+    p = problem(num_seqs=len(seq), page_size=page, num_pages=pages, max_pages_per_seq=width,
+                total_q_tokens=0, max_context_len=width * page)
+    dev, left, err = ints(stack), ints([-9]), ints([0])
+    B.pa_pages_return(p, ints(seq), ints(keep), ints(table), dev, ints([9]), left, err)
+    want = R.give_back(seq, keep, table, stack, 9, page=page, pages=pages, max_ctx=width * page)
+    assert (dev.tolist(), int(left), int(err)) == want
+
+
+def test_return_past_the_stack():
+    p = problem(num_seqs=2, num_pages=8, max_pages_per_seq=4, max_context_len=64)
+    table = [[0, 1, 2, 3], [4, 5, 6, 7]]
+    dev, left, err = ints([9] * 8 + [77] * 8), ints([0]), ints([0])
+    B.pa_pages_return(p, ints([64, 64]), ints([0, 0]), ints(table), dev, ints([3]), left, err)
+    assert dev.tolist() == [9] * 3 + [0, 1, 2, 3, 4] + [77] * 8
+    assert int(left) == 8 and int(err) == 1
+
+
+# -------------------------------------------------------------------- rope
+
+def rope_case(T, Hq, Hkv, D, page, layout, kv, *, strided, seed, spare=2):
+    g = torch.Generator().manual_seed(seed)
+    width = (Hq + 2 * Hkv) * D + (24 if strided else 0)
+    fused = torch.randn((T, width), generator=g).to(BF16).cuda()
+    if strided:
+        q, k, v = (fused[:, a * D:b * D].unflatten(1, (-1, D))
+                   for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    else:
+        q, k, v = (torch.randn((T, h, D), generator=g).to(BF16).cuda() for h in (Hq, Hkv, Hkv))
+    pages = R.up(T, page) + spare
+    slots = ints(torch.randperm(pages * page, generator=g)[:T].tolist())
+    last = D if kv == B.PA_BF16 else D // 2
+    shape = (pages, page, Hkv) if layout == 0 else (pages, Hkv, page)
+    make = (lambda: torch.full((*shape, D), math.nan, dtype=BF16, device="cuda")) \
+        if kv == B.PA_BF16 else (lambda: torch.full((*shape, last), 0xAA, dtype=torch.uint8,
+                                                    device="cuda"))
+    scales = [None, None] if kv == B.PA_BF16 else [
+        torch.full((*shape, D // 32), 0xBB, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    p = problem(num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, page_size=page, num_pages=pages,
+                max_pages_per_seq=pages, total_q_tokens=T, max_q_len=T,
+                max_context_len=pages * page, layout=layout, kv_dtype=kv)
+    return p, q, k, v, slots, make(), make(), scales
+
+
+def cached(cache, slots, page, layout):
+    s = slots.long()
+    return cache[s // page, s % page] if layout == 0 else cache[s // page, :, s % page]
+
+
+FREQ = torch.tensor([500000.0 ** (-i / 64) for i in range(64)], dtype=torch.float64)
+
+
+def freq_of(rot):
+    return FREQ[:: 128 // rot][:rot // 2] if 128 % rot == 0 else torch.tensor(
+        [1e4 ** (-2 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,layout,rot,inter,far,strided", [
+    (1, 1, 1, 64, 16, 0, 64, 0, 0, False),
+    (1, 8, 2, 128, 16, 1, 128, 1, 0, True),
+    (3, 4, 1, 64, 32, 0, 16, 1, 5, True),
+    (5, 7, 7, 128, 64, 1, 112, 0, 131071, False),
+    (33, 32, 8, 128, 64, 0, 128, 0, 1000000, True),
+    (33, 32, 8, 128, 64, 1, 64, 1, 2 ** 31 - 40, True),
+    (64, 5, 1, 64, 128, 1, 48, 0, 77, True),
+    (700, 3, 3, 64, 16, 0, 32, 1, 4096, False),
+    (2500, 8, 1, 128, 256, 0, 96, 0, 123456, True),
+    (6000, 16, 4, 128, 32, 1, 128, 1, 9, True),
+])
+def test_rope(T, Hq, Hkv, D, page, layout, rot, inter, far, strided):
+    p, q, k, v, slots, kc, vc, _ = rope_case(T, Hq, Hkv, D, page, layout, B.PA_BF16,
+                                             strided=strided, seed=T + rot)
+    pos = ints([far + (i * 7) % 39 if i % 3 else (i * 13) % 50 for i in range(T)])
+    rope = B.PaRope(rotary_dim=rot, interleaved=inter, cos_sin_scale=1.25 if T % 2 else 1.0)
+    f, err = freq_of(rot), ints([0])
+    out = torch.full((T, Hq, D), math.nan, dtype=BF16, device="cuda")
+    before = kc.clone()
+    B.pa_rope_append(p, rope, B.pa_rope_steps(f).cuda(), q, k, v, pos, slots, out, kc, None, vc,
+                     None, err)
+    no_error(err)
+    for got, x in ((out, q), (cached(kc, slots, page, layout), k)):
+        want, size = R.rotate(x.cpu(), pos.cpu(), f, rot, inter, rope.cos_sin_scale)
+        # fp32: cos and sin off by 2^-24 of rounding, 2 ulp of sincospi and 2^-25 half turns of
+        # angle, two products and a sum; then one rounding to bf16
+        tol = HALF * want.abs() + size * (2.0 ** -24 * 6 + math.pi * 2.0 ** -25) * 1.01
+        assert torch.all((got.cpu().double() - want).abs() <= tol)
+        assert torch.equal(got.cpu()[..., rot:], x.cpu()[..., rot:])
+    assert torch.equal(cached(vc, slots, page, layout), v)
+    # nothing else was written
+    touched = torch.zeros(before.shape[0] * page, dtype=torch.bool, device="cuda")
+    touched[slots.long()] = True
+    rest = ~touched.view(-1, page)
+    for cache in (kc, vc):
+        left = cache[rest] if layout == 0 else cache.transpose(1, 2)[rest]
+        assert torch.isnan(left).all()
+
+
+@pytest.mark.parametrize("D,rot,inter,layout,T", [(128, 128, 0, 0, 9), (128, 32, 0, 1, 40),
+                                                  (64, 48, 0, 0, 7), (64, 64, 1, 1, 300),
+                                                  (128, 112, 0, 1, 21), (64, 16, 1, 0, 2)])
+def test_rope_into_a_4_bit_cache(D, rot, inter, layout, T):
+    """Bit for bit what the bf16 cache's rows quantise to."""
+    page, Hq, Hkv = 16, 4, 2
+    f, rope = freq_of(rot), B.PaRope(rotary_dim=rot, interleaved=inter, cos_sin_scale=1.0)
+    got = {}
+    for kv in (B.PA_BF16, B.PA_MX4):
+        p, q, k, v, slots, kc, vc, sc = rope_case(T, Hq, Hkv, D, page, layout, kv, strided=True,
+                                                  seed=5)
+        k[0, 0, 3] = math.inf                 # its block is NaN
+        v[T - 1, 1] = 0.0
+        k[T // 2, 1, D - 1] = 1e-38
+        pos, err = ints(list(range(T))), ints([0])
+        out = torch.zeros((T, Hq, D), dtype=BF16, device="cuda")
+        B.pa_rope_append(p, rope, B.pa_rope_steps(f).cuda(), q, k, v, pos, slots, out, kc, sc[0],
+                         vc, sc[1], err)
+        no_error(err)
+        got[kv] = [out] + [cached(x, slots, page, layout) for x in (kc, vc, *sc) if x is not None]
+    assert torch.equal(got[B.PA_BF16][0].view(torch.int16), got[B.PA_MX4][0].view(torch.int16))
+    for i in (1, 2):
+        codes, scales = C.quantise(got[B.PA_BF16][i].cpu())
+        assert torch.equal(got[B.PA_MX4][i].cpu(), codes)
+        assert torch.equal(got[B.PA_MX4][i + 2].cpu(), scales)
+
+
+def test_rope_rows_that_are_skipped():
+    T, Hq, Hkv, D, page = 8, 2, 1, 128, 16
+    p, q, k, v, slots, kc, vc, _ = rope_case(T, Hq, Hkv, D, page, 0, B.PA_BF16, strided=False,
+                                             seed=1)
+    steps, rope = B.pa_rope_steps(freq_of(128)).cuda(), B.PaRope(128, 0, 1.0)
+    slots[2] = -1                             # padding
+    pos, err = ints([3] * T), ints([0])
+    out = torch.full((T, Hq, D), math.nan, dtype=BF16, device="cuda")
+    B.pa_rope_append(p, rope, steps, q, k, v, pos, slots, out, kc, None, vc, None, err)
+    no_error(err)
+    skipped = torch.isnan(out).flatten(1).all(1)
+    assert skipped.tolist() == [i == 2 for i in range(T)]
+    assert int((~torch.isnan(kc)).flatten(2).all(2).sum()) == T - 1
+    for bad, code in ((p.num_pages * page, 2), (2 ** 31 - 1, 2), (-2, 2)):
+        s = slots.clone()
+        s[5] = bad
+        out.fill_(math.nan)
+        err.zero_()
+        B.pa_rope_append(p, rope, steps, q, k, v, pos, s, out, kc, None, vc, None, err)
+        assert int(err) == code and torch.isnan(out).flatten(1).all(1).tolist() == [
+            i in (2, 5) for i in range(T)]
+    pos[4] = -1
+    err.zero_()
+    out.fill_(math.nan)
+    B.pa_rope_append(p, rope, steps, q, k, v, pos, slots, out, kc, None, vc, None, err)
+    assert int(err) == 1 and torch.isnan(out).flatten(1).all(1).tolist() == [
+        i in (2, 4) for i in range(T)]
+
+
+def test_rope_in_place_without_q_and_at_position_zero():
+    T, Hq, Hkv, D, page = 40, 4, 2, 64, 16
+    p, q, k, v, slots, kc, vc, _ = rope_case(T, Hq, Hkv, D, page, 1, B.PA_BF16, strided=False,
+                                             seed=2)
+    steps, rope = B.pa_rope_steps(freq_of(64)).cuda(), B.PaRope(64, 0, 1.0)
+    pos, err = ints(list(range(100, 100 + T))), ints([0])
+    out = torch.empty_like(q)
+    B.pa_rope_append(p, rope, steps, q, k, v, pos, slots, out, kc, None, vc, None, err)
+    k2, v2 = torch.full_like(kc, math.nan), torch.full_like(vc, math.nan)
+    B.pa_rope_append(p, rope, steps, None, k, v, pos, slots, None, k2, None, v2, None, err)
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    assert same(k2, kc) and same(v2, vc)
+    qq = q.clone()
+    B.pa_rope_append(p, rope, steps, qq, k, v, pos, slots, qq, k2, None, v2, None, err)
+    assert same(qq, out)
+    B.pa_rope_append(p, rope, steps, q, k, v, ints([0] * T), slots, out, kc, None, vc, None, err)
+    assert same(out, q)                       # no turn at position 0
+    no_error(err)
+
+
+# ------------------------------------------------------------------ bounds
+
+def new_slots(ctx, ql, page, pages, seed):
+    """slots of the last ql[b] of ctx[b] tokens over shuffled pages, and the table."""
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(seed)).tolist()
+    table, slots, seq, pos, at = [], [], [], [], 0
+    for b, (c, q) in enumerate(zip(ctx, ql)):
+        row = perm[at:at + R.up(c, page)]
+        at += R.up(c, page)
+        table.append(row)
+        for t in range(c - q, c):
+            slots.append(row[t // page] * page + t % page)
+            seq.append(b)
+            pos.append(t)
+    width = max(len(r) for r in table)
+    return [r + [-1] * (width - len(r)) for r in table], slots, seq, pos
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,ql,page,Hkv,layout,pad", [
+    ([1], [1], 16, 1, 0, 0), ([16], [1], 16, 2, 1, 0), ([17, 40, 9], [1, 1, 1], 16, 3, 0, 2),
+    ([200, 3], [200, 3], 32, 1, 1, 0), ([300, 70, 64, 1], [300, 70, 1, 0], 64, 4, 0, 5),
+    ([700, 257], [600, 257], 256, 2, 1, 0), ([33] * 70, [2] * 70, 16, 2, 0, 0),
+    ([5000], [5000], 128, 1, 0, 0),
+])
+def test_bounds(ctx, ql, page, Hkv, layout, pad, D):
+    pages = sum(R.up(c, page) for c in ctx) + 2
+    _, slots, _, _ = new_slots(ctx, ql, page, pages, 4)
+    g = torch.Generator().manual_seed(D + page)
+    k = torch.randn((pages, page, Hkv, D), generator=g) * torch.exp(
+        2 * torch.randn((pages, 1, Hkv, D), generator=g))
+    k = k.to(BF16)
+    used = {}
+    for s in slots:
+        used[s // page] = s % page + 1
+    for pg in range(pages):                   # what is behind the last key is not looked at
+        k[pg, used.get(pg, 0):] = math.nan
+    rows = len(slots) + pad
+    p = problem(num_kv_heads=Hkv, num_q_heads=Hkv, head_dim=D, page_size=page, num_pages=pages,
+                max_pages_per_seq=pages, total_q_tokens=rows, max_q_len=max(ql),
+                max_context_len=pages * page, layout=layout)
+    bnd = torch.full((pages, Hkv, 2, D), 99, dtype=torch.int8, device="cuda")
+    sc, err = torch.full((pages, Hkv), -1.0, device="cuda"), ints([0])
+    dev = (k if layout == 0 else k.transpose(1, 2)).contiguous().cuda()
+    B.pa_page_bounds(p, dev, ints(slots + [-1] * pad), bnd, sc, err)
+    no_error(err)
+    for pg in range(pages):
+        for h in range(Hkv):
+            if pg not in used:
+                assert torch.all(bnd[pg, h] == 99) and float(sc[pg, h]) == -1.0
+                continue
+            want, s = R.bounds(k[pg, :used[pg], h])
+            assert float(sc[pg, h]) == s and torch.equal(bnd[pg, h].cpu(), want)
+
+
+def test_bounds_of_odd_values():
+    D, page = 64, 16
+    rows = torch.zeros((9, page, 1, D))
+    rows[1, :, 0, :] = 1e-30                  # below the least exponent's step
+    rows[2, 3, 0, 5] = math.nan
+    rows[2, 4, 0, 6] = 3.0
+    rows[3, 3, 0, 5] = math.inf
+    rows[3, 5, 0, 7] = -1e-30
+    rows[4, 0, 0, 0], rows[4, 1, 0, 1] = 127.0, -127.0      # the largest of an exponent
+    rows[5, 0, 0, 0] = 127.5                  # and the next number
+    rows[6, 2, 0, 9] = -3e38
+    rows[7, :, 0, :] = -0.0
+    rows[8, 0, 0, 3] = -math.inf
+    k = rows.to(BF16)
+    p = problem(num_kv_heads=1, num_q_heads=1, head_dim=D, num_pages=9, max_pages_per_seq=9,
+                total_q_tokens=9, max_q_len=9, max_context_len=144)
+    bnd, sc = torch.zeros((9, 1, 2, D), dtype=torch.int8).cuda(), torch.zeros((9, 1)).cuda()
+    err = ints([0])
+    B.pa_page_bounds(p, k.cuda(), ints([i * 16 + 15 for i in range(9)]), bnd, sc, err)
+    no_error(err)
+    for i in range(9):
+        want, s = R.bounds(k[i, :, 0])
+        assert float(sc[i, 0]) == s, i
+        assert torch.equal(bnd[i, 0].cpu(), want), i
+    err.zero_()
+    B.pa_page_bounds(p, k.cuda(), ints([144, -2, 2 ** 31 - 1] + [3] * 6), bnd, sc, err)
+    assert int(err) == 2                      # the others are done
+
+
+# --------------------------------------------------------------- selection
+
+def random_bounds(pages, Hkv, D, seed):
+    g = torch.Generator().manual_seed(seed)
+    mid, half = torch.randn((pages, Hkv, D), generator=g), 2 + torch.rand((pages, Hkv, D), generator=g)
+    top = (mid + half).abs().maximum((mid - half).abs()).amax(-1)
+    e = torch.ceil(torch.log2(top / 127))
+    unit = torch.exp2(e)[..., None]
+    b = torch.stack((torch.ceil((mid + half) / unit), torch.floor((mid - half) / unit)), 2)
+    return b.clamp(-127, 127).to(torch.int8), torch.exp2(e)
+
+
+@pytest.mark.parametrize("D,G,Hkv,page,window,budget,first,recent,ctx,ql", [
+    (128, 4, 2, 16, 0, 4, 1, 1, [1, 64, 65, 200], [1, 1, 1, 1]),
+    (64, 1, 1, 16, 0, 1, 0, 0, [500, 3], [2, 1]),
+    (128, 8, 1, 32, 0, 7, 2, 3, [3000, 100, 40], [1, 2, 0]),
+    (64, 5, 3, 64, 0, 5, 0, 1, [2000, 321], [3, 1]),
+    (128, 16, 1, 16, 0, 20, 1, 2, [4000], [1]),
+    (128, 33, 1, 16, 0, 9, 1, 2, [900], [2]),
+    (64, 64, 1, 32, 0, 3, 0, 0, [700, 90], [1, 1]),
+    (128, 4, 2, 16, 500, 6, 1, 2, [2000, 200], [2, 1]),
+    (64, 7, 2, 16, 17, 1, 0, 1, [300], [4]),
+    (64, 2, 1, 16, 0, 300, 4, 20, [17000, 4800], [1, 1]),
+    (128, 4, 8, 256, 0, 2, 0, 1, [1000] * 20, [1] * 20),
+])
+def test_selection(D, G, Hkv, page, window, budget, first, recent, ctx, ql):
+    pages = sum(R.up(c, page) for c in ctx) + 2
+    table, _, seq, pos = new_slots(ctx, ql, page, pages, 6)
+    T = len(seq)
+    bnd, sc = random_bounds(pages, Hkv, D, 7)
+    q = torch.randn((T, G * Hkv, D), generator=torch.Generator().manual_seed(8)).to(BF16)
+    p = problem(num_seqs=len(ctx), num_q_heads=G * Hkv, num_kv_heads=Hkv, head_dim=D,
+                page_size=page, num_pages=pages, max_pages_per_seq=len(table[0]),
+                total_q_tokens=T + 2, max_q_len=max(ql), max_context_len=max(ctx), window=window)
+    sel, err = torch.full((T + 2, Hkv, budget), -7, dtype=torch.int32, device="cuda"), ints([0])
+    qd = torch.cat((q, torch.full((2, G * Hkv, D), math.nan, dtype=BF16))).cuda()
+    args = (qd, bnd.cuda(), sc.cuda(), ints(table), ints(seq + [-1, -1]), ints(pos + [0, 0]))
+    B.pa_select_pages(p, budget, first, recent, *args, sel, err)
+    no_error(err)
+    assert torch.all(sel[T:] == -7)
+    for t in range(T):
+        for h in range(Hkv):
+            want = R.select(q[t, h * G:(h + 1) * G], bnd[:, h], sc[:, h], table[seq[t]], pos[t],
+                            budget=budget, num_first=first, num_recent=recent, page=page,
+                            pages=pages, window=window)
+            assert sel[t, h].tolist() == want, (t, h)
+
+
+def test_selection_of_ties_odd_queries_and_bad_pages():
+    D, page, n, budget = 64, 16, 200, 8
+    table = list(range(n))
+    bnd, sc = random_bounds(n, 1, D, 1)
+    bnd[:], sc[:] = bnd[0], sc[0]             # every page the same: the lowest ones
+    q = torch.randn((6, 2, D), generator=torch.Generator().manual_seed(2)).to(BF16)
+    q[1] = 0.0
+    q[2, 0, 5], q[2, 1, :] = math.nan, math.nan
+    q[3, 1, 7] = -math.inf
+    q[4] = 3e38
+    q[5] = 1e-38
+    bnd[150, 0, 0], sc[60] = 127, 2.0 ** 40
+    table[10], table[199], table[0] = -1, 777, n
+    p = problem(num_q_heads=2, num_kv_heads=1, head_dim=D, num_pages=n, max_pages_per_seq=n,
+                total_q_tokens=6, max_q_len=6, max_context_len=n * page)
+    sel, err = torch.zeros((6, 1, budget), dtype=torch.int32, device="cuda"), ints([0])
+    B.pa_select_pages(p, budget, 0, 2, q.cuda(), bnd.cuda(), sc.cuda(), ints([table]),
+                      ints([0] * 6), ints([n * page - 1] * 6), sel, err)
+    assert int(err) == 2
+    for t in range(6):
+        want = R.select(q[t], bnd[:, 0], sc[:, 0], table, n * page - 1, budget=budget, num_first=0,
+                        num_recent=2, page=page, pages=n, window=0)
+        assert sel[t, 0].tolist() == want, t
+    # rows that cannot be: left as they are
+    sel.fill_(-5)
+    err.zero_()
+    B.pa_select_pages(p, budget, 0, 2, q.cuda(), bnd.cuda(), sc.cuda(), ints([table]),
+                      ints([0, 1, -1, 0, 0, 0]), ints([5, 5, 5, -1, n * page, 31]), sel, err)
+    assert int(err) == 1
+    assert [bool((sel[t] == -5).all()) for t in range(6)] == [False, True, True, True, True, False]
+    assert sel[5, 0].tolist() == [0, 1] + [-1] * 6
+
+
+# --------------------------------------------------------------- attention
+
+def attend_case(D, G, Hkv, page, layout, ctx, ql, seed, spare=2, mag=1.0):
+    pages = sum(R.up(c, page) for c in ctx) + spare
+    table, _, seq, pos = new_slots(ctx, ql, page, pages, seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    k = (torch.randn((pages, page, Hkv, D), generator=g) * mag).to(BF16)
+    v = torch.randn((pages, page, Hkv, D), generator=g).to(BF16)
+    q = torch.randn((len(seq), G * Hkv, D), generator=g).to(BF16)
+    return pages, table, seq, pos, k, v, q
+
+
+def check_attend(p, budget, table, seq, pos, k, v, q, sel, code=0, repeat=1):
+    """Runs the call and compares every row of a sequence; the others stay as they are."""
+    T, H, D = q.shape
+    Hkv, page, pages = p.num_kv_heads, p.page_size, p.num_pages
+    G, layout = H // Hkv, p.layout
+    dev = [(x if layout == 0 else x.transpose(1, 2)).contiguous().cuda() for x in (k, v)]
+    ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
+    out = torch.full((T, H, D), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    args = (q.cuda(), *dev, ints(table), ints(seq), ints(pos), ints(sel), ws)
+    for _ in range(repeat):
+        B.pa_decode_selected(p, budget, *args, out, lse)
+    assert B.pa_last_device_error(ws) == code
+    assert not ws[256:4352].any()             # the counters as the next call finds them
+    for t in range(T):
+        if not (0 <= seq[t] < p.num_seqs and 0 <= pos[t] < p.max_context_len):
+            assert torch.all(out[t] == 7) and torch.all(lse[t] == 7)
+            continue
+        first, n = R.seen_pages(pos[t], page, p.window)
+        for h in range(Hkv):
+            ks, vs, at = [], [], []
+            for s in sel[t][h][:min(budget, n)]:
+                if not 0 <= s <= pos[t] // page:
+                    continue
+                pg = table[seq[t]][s]
+                if 0 <= pg < pages:
+                    ks.append(k[pg, :, h])
+                    vs.append(v[pg, :, h])
+                    at += range(s * page, s * page + page)
+            kk = torch.cat(ks) if ks else torch.zeros((0, D))
+            vv = torch.cat(vs) if vs else torch.zeros((0, D))
+            r = slice(h * G, (h + 1) * G)
+            o, L, size, big = R.attend(q[t, r], kk, vv, at, pos[t], p.window, p.sm_scale)
+            # scores in fp32 sums of D products; probabilities and the result rounded to bf16
+            ds = (D + 16) * 2.0 ** -24 * big[:, None] + 2.0 ** -20
+            tol = (HALF + 2 * ds) * size * 1.01 + HALF * (o.abs() + HALF * size)
+            assert torch.all((out[t, r].cpu().double() - o).abs() <= tol), (t, h)
+            got = lse[t, r].cpu().double()
+            none = torch.isinf(L)
+            assert torch.equal(got[none], L[none])
+            far = (got - L).abs()[~none]
+            assert torch.all(far <= (ds[:, 0] + 2.0 ** -22 * (1 + L.abs()))[~none]), (t, h)
+    return out, lse
+
+
+def lists(seq, pos, Hkv, budget, page, window, seed, mode="plain"):
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    for s, x in zip(seq, pos):
+        first, n = R.seen_pages(max(x, 0), page, window)
+        rows = []
+        for _ in range(Hkv):
+            got = (first + torch.randperm(n, generator=g)[:budget].sort()[0]).tolist()
+            if mode == "holes":
+                got = [y if i % 3 else -1 for i, y in enumerate(got)]
+            elif mode == "shuffled":
+                got = got[::-1]
+            elif mode == "twice":
+                got = (got + got)[:min(budget, n)] if len(got) < budget else got[:-1] + got[:1]
+            elif mode == "none":
+                got = [-1] * len(got)
+            rows.append(got + [-1] * (budget - len(got)))
+        out.append(rows)
+    return out
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 5, 700])
+@pytest.mark.parametrize("D,G,Hkv,page,layout,window,budget,ctx,ql,mode", [
+    (128, 4, 2, 16, 0, 0, 4, [1, 64, 65, 200], [1, 1, 1, 1], "plain"),
+    (64, 1, 1, 16, 1, 0, 1, [500, 3], [2, 1], "plain"),
+    (128, 8, 1, 64, 1, 0, 9, [3000, 100, 40], [1, 2, 0], "plain"),
+    (64, 5, 3, 64, 0, 0, 5, [2000, 321], [3, 1], "holes"),
+    (128, 16, 1, 16, 0, 0, 20, [4000], [1], "shuffled"),
+    (128, 29, 1, 32, 1, 0, 9, [900], [2], "plain"),
+    (64, 64, 1, 32, 0, 0, 3, [700, 90], [1, 1], "plain"),
+    (64, 30, 2, 16, 1, 0, 30, [700, 90], [1, 1], "holes"),
+    (64, 9, 2, 16, 1, 0, 40, [700, 90], [1, 1], "plain"),
+    (128, 4, 2, 16, 0, 500, 40, [2000, 200], [2, 1], "plain"),
+    (64, 7, 2, 16, 0, 17, 2, [300], [4], "plain"),
+    (128, 4, 2, 128, 0, 0, 3, [1000, 129], [1, 1], "twice"),
+    (128, 2, 1, 256, 1, 100, 6, [1025, 200], [2, 1], "plain"),
+    (64, 2, 1, 16, 0, 0, 900, [17000, 4800], [1, 1], "plain"),
+    (128, 3, 2, 16, 0, 0, 5, [100, 20], [1, 1], "none"),
+])
+def test_attention(D, G, Hkv, page, layout, window, budget, ctx, ql, mode, ctas):
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, layout, ctx, ql, 3)
+    sel = lists(seq, pos, Hkv, budget, page, window, 5, mode)
+    # what no row may see is NaN: pages that nobody lists, and keys behind the last position
+    listed = set()
+    for t in range(len(seq)):
+        for h in range(Hkv):
+            listed |= {(table[seq[t]][s], h) for s in sel[t][h] if s >= 0}
+    for pg in range(pages):
+        for h in range(Hkv):
+            if (pg, h) not in listed:
+                k[pg, :, h] = v[pg, :, h] = math.nan
+    for b, c in enumerate(ctx):
+        if c % page:
+            pg = table[b][c // page]
+            k[pg, c % page:] = v[pg, c % page:] = math.nan
+    p = problem(num_seqs=len(ctx), num_q_heads=G * Hkv, num_kv_heads=Hkv, head_dim=D,
+                page_size=page, num_pages=pages, max_pages_per_seq=len(table[0]), layout=layout,
+                total_q_tokens=len(seq), max_q_len=max(ql), max_context_len=max(ctx),
+                window=window, num_ctas=ctas, sm_scale=1.0 / math.sqrt(D))
+    check_attend(p, budget, table, seq, pos, k, v, q, sel, repeat=2)
+
+
+def test_attention_past_bad_entries():
+    D, G, Hkv, page, budget = 128, 2, 1, 16, 6
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 0, [300, 200, 64], [1, 1, 1], 9)
+    sel = lists(seq, pos, Hkv, budget, page, 0, 5)
+    p = problem(num_seqs=3, num_q_heads=G, num_kv_heads=Hkv, num_pages=pages,
+                max_pages_per_seq=len(table[0]), total_q_tokens=6, max_q_len=1,
+                max_context_len=300)
+    q = torch.cat((q, q))
+    rows = dict(seq=seq + [-1, 3, 0], pos=pos + [0, 5, 300])
+    sel = sel + sel
+    # padding is no error, a sequence or position that cannot be is one
+    check_attend(p, budget, table, k=k, v=v, q=q, sel=sel, code=1, **rows)
+    rows = dict(seq=seq + [-1] * 3, pos=pos + [0] * 3)
+    check_attend(p, budget, table, k=k, v=v, q=q, sel=sel, **rows)
+    bad = [[list(x) for x in r] for r in sel]
+    bad[0][0][2] = 19                         # behind the row's own page
+    check_attend(p, budget, table, k=k, v=v, q=q, sel=bad, code=1, **rows)
+    bad[0][0][2] = -2 ** 31
+    check_attend(p, budget, table, k=k, v=v, q=q, sel=bad, code=1, **rows)
+    t2 = [list(r) for r in table]
+    t2[1][sel[1][0][1]], t2[1][sel[1][0][3]] = -1, pages
+    check_attend(p, budget, t2, k=k, v=v, q=q, sel=sel, code=2, **rows)
+
+
+def test_attention_with_large_scores_infinities_and_nan():
+    D, G, Hkv, page, budget = 128, 4, 1, 16, 8
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 0, [500, 400], [1, 1], 9, mag=30)
+    sel = lists(seq, pos, Hkv, budget, page, 0, 5)
+    p = problem(num_seqs=2, num_q_heads=G, num_kv_heads=Hkv, num_pages=pages,
+                max_pages_per_seq=len(table[0]), total_q_tokens=2, max_q_len=1,
+                max_context_len=500, sm_scale=1.0)
+    check_attend(p, budget, table, seq, pos, k, v, q, sel)       # one key outweighs the rest
+    # the first list's first page: an infinite V element reaches its column alone, a NaN key all
+    ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros((2, G, D), dtype=BF16, device="cuda"), torch.zeros((2, G)).cuda()
+    p.sm_scale = 0.001
+    v2, k2 = v.clone(), k.clone()
+    v2[table[0][sel[0][0][0]], 3, 0, 11] = math.inf
+    call = lambda kk, vv: B.pa_decode_selected(  # noqa: E731
+        p, budget, q.cuda(), kk.cuda(), vv.cuda(), ints(table), ints(seq), ints(pos), ints(sel),
+        ws, out, lse)
+    call(k, v2)
+    assert torch.isinf(out[0, :, 11]).all() and torch.isfinite(out[1]).all()
+    assert torch.isfinite(out[0, :, :11]).all() and torch.isfinite(out[0, :, 12:]).all()
+    k2[table[0][sel[0][0][0]], 3, 0, 5] = math.nan
+    call(k2, v)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all() and torch.isfinite(out[1]).all()
+    # nor does what the row does not list reach it
+    p.sm_scale = 0.1
+    call(k, v)
+    before = out.clone()
+    unlisted = next(s for s in range(20) if s not in sel[0][0])
+    k2 = k.clone()
+    k2[table[0][unlisted]] = v[table[0][unlisted]] = math.inf
+    call(k2, v)
+    assert torch.equal(out, before)
+
+
+def test_attention_is_pa_decode_where_every_page_is_listed():
+    """All pages listed: the softmax over the whole context, against the oracle's kernel."""
+    D, G, Hkv, page = 128, 4, 2, 64
+    ctx, ql = [1000, 64, 333], [2, 2, 2]
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 0, ctx, ql, 13)
+    budget = 16
+    sel = lists(seq, pos, Hkv, budget, page, 0, 5)
+    p = problem(num_seqs=3, num_q_heads=G * Hkv, num_kv_heads=Hkv, page_size=page, num_pages=pages,
+                max_pages_per_seq=len(table[0]), total_q_tokens=6, max_q_len=2,
+                max_context_len=1000)
+    out, lse = check_attend(p, budget, table, seq, pos, k, v, q, sel)
+    a = torch.empty(B.pa_assign_workspace_size(p, 0), dtype=torch.uint8, device="cuda")
+    w = torch.empty(B.pa_partial_workspace_size(p, 0), dtype=torch.uint8, device="cuda")
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    c, n, t = ints(ctx), ints(ql), ints(table)
+    B.pa_assign(p, 0, c, n, None, a)
+    B.pa_decode_splitk(p, q.cuda(), k.cuda(), v.cuda(), t, c, n, None, None, a, w, o2, l2)
+    B.pa_combine(p, 0, a, w, o2, l2)
+    assert float((out.float() - o2.float()).abs().max()) <= 2e-2
+    assert float((lse - l2).abs().max()) <= 1e-3
+
+
+def test_a_workspace_that_was_never_filled_is_reported():
+    D, G, Hkv, page, budget = 64, 1, 1, 16, 64
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 0, [1024], [1], 9)
+    sel = lists(seq, pos, Hkv, budget, page, 0, 5)
+    p = problem(num_q_heads=1, num_kv_heads=1, head_dim=D, num_pages=pages, max_pages_per_seq=64,
+                max_context_len=1024, num_ctas=5)
+    ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
+    ws[256:4352] = 1
+    out, lse = torch.zeros((1, 1, D), dtype=BF16, device="cuda"), torch.zeros((1, 1)).cuda()
+    args = (q.cuda(), k.cuda(), v.cuda(), ints(table), ints(seq), ints(pos), ints(sel), ws)
+    B.pa_decode_selected(p, budget, *args, out, lse)
+    assert B.pa_last_device_error(ws) == B.PA_DEV_BAD_WORKSPACE
+    ws.zero_()
+    check_attend(p, budget, table, seq, pos, k, v, q, sel)
+
+
+# ------------------------------------------------------------ all together
+
+class Loop:
+    """A decode loop over a paged cache as a server runs it, all state on the GPU."""
+
+    def __init__(self, B_, Hq, Hkv, D, page, layout, budget, rows, max_ctx, seed=0):
+        self.p = problem(num_seqs=B_, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, page_size=page,
+                         num_pages=B_ * R.up(max_ctx, page) + 3, layout=layout,
+                         max_pages_per_seq=R.up(max_ctx, page), total_q_tokens=rows,
+                         max_q_len=rows, max_context_len=max_ctx, sm_scale=1 / math.sqrt(D))
+        n = self.p.num_pages
+        shape = (n, page, Hkv, D) if layout == 0 else (n, Hkv, page, D)
+        self.k, self.v = (torch.full(shape, math.nan, dtype=BF16, device="cuda") for _ in "kv")
+        self.bnd = torch.zeros((n, Hkv, 2, D), dtype=torch.int8, device="cuda")
+        self.sc = torch.zeros((n, Hkv), device="cuda")
+        self.table = torch.full((B_, self.p.max_pages_per_seq), -1, dtype=torch.int32).cuda()
+        self.free = ints(torch.randperm(n, generator=torch.Generator().manual_seed(seed)).tolist())
+        self.count, self.left = ints([n]), ints([0])
+        self.lens, self.ctx, self.ql = ints([0] * B_), ints([0] * B_), ints([0] * B_)
+        self.seq, self.pos, self.slots = (ints([0] * rows) for _ in range(3))
+        self.budget = budget
+        self.sel = torch.zeros((rows, Hkv, budget), dtype=torch.int32, device="cuda")
+        self.ws = torch.zeros(B.pa_selected_workspace_size(self.p, budget), dtype=torch.uint8,
+                              device="cuda")
+        self.qr, self.out = (torch.zeros((rows, Hq, D), dtype=BF16, device="cuda") for _ in "ab")
+        self.lse, self.err = torch.zeros((rows, Hq), device="cuda"), ints([0])
+        self.freq = freq_of(D)
+        self.steps, self.rope = B.pa_rope_steps(self.freq).cuda(), B.PaRope(D, 0, 1.0)
+        self.fused = torch.zeros((rows, (Hq + 2 * Hkv) * D), dtype=BF16, device="cuda")
+        self.q, self.kn, self.vn = (x.unflatten(1, (-1, D)) for x in self.fused.split(
+            [Hq * D, Hkv * D, Hkv * D], 1))
+
+    def step(self):
+        p = self.p
+        B.pa_pages_take(p, self.lens, self.ql, self.table, self.free, self.count, self.ctx,
+                        self.seq, self.pos, self.slots, self.left, self.err)
+        B.pa_rope_append(p, self.rope, self.steps, self.q, self.kn, self.vn, self.pos, self.slots,
+                         self.qr, self.k, None, self.v, None, self.err)
+        B.pa_page_bounds(p, self.k, self.slots, self.bnd, self.sc, self.err)
+        B.pa_select_pages(p, self.budget, 1, 1, self.qr, self.bnd, self.sc, self.table, self.seq,
+                          self.pos, self.sel, self.err)
+        B.pa_decode_selected(p, self.budget, self.qr, self.k, self.v, self.table, self.seq,
+                             self.pos, self.sel, self.ws, self.out, self.lse)
+        self.count.copy_(self.left)
+        self.lens.copy_(self.ctx)
+
+    def give_back(self, keep):
+        B.pa_pages_return(self.p, self.lens, keep, self.table, self.free, self.count, self.left,
+                          self.err)
+        self.count.copy_(self.left)
+        self.lens.copy_(keep)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,layout,graph", [(8, 2, 128, 16, 0, False),
+                                                        (5, 5, 64, 32, 1, True),
+                                                        (16, 2, 64, 16, 0, True)])
+def test_a_decode_loop(Hq, Hkv, D, page, layout, graph):
+    """Prompts, decode steps, drafts taken back and a finished sequence's pages used again,
+    with one captured step replayed; every step against the definition over the whole history."""
+    N, rows, budget, max_ctx = 3, 24, 5, 320
+    L = Loop(N, Hq, Hkv, D, page, layout, budget, rows, max_ctx)
+    g = torch.Generator().manual_seed(1)
+    G = Hq // Hkv
+    hist = [[] for _ in range(N)]                      # (rotated key, value) of every token
+    run = L.step
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            L.step()                                   # nothing new: no row, no page
+        torch.cuda.current_stream().wait_stream(side)
+        G_ = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(G_):
+            L.step()
+        run = G_.replay
+    plan = [[20, 1, 0], [20, 3, 1]] + [[22, 1, 1]] * 10 + [[1, 1, 1]] * 8 + [[3, 3, 3]] * 4
+    for i, ql in enumerate(plan):
+        if i in (8, 15):
+            # drafts of sequence 0 not accepted; sequence 1 done
+            keep = [len(h) for h in hist]
+            keep[0] -= 3
+            keep[1] = 0 if i == 15 else keep[1]
+            L.give_back(ints(keep))
+            hist = [h[:n] for h, n in zip(hist, keep)]
+        x = torch.randn(L.fused.shape, generator=g).to(BF16)
+        L.fused.copy_(x)
+        L.ql.copy_(ints(ql))
+        L.out.fill_(7.0)
+        run()
+        assert int(L.err) == 0 and B.pa_last_device_error(L.ws) == 0
+        q, kn, vn = L.q.cpu(), L.kn.cpu(), L.vn.cpu()
+        t = 0
+        kd = L.k.cpu() if layout == 0 else L.k.cpu().transpose(1, 2)
+        table, sel = L.table.tolist(), L.sel.tolist()
+        for b, n in enumerate(ql):
+            for _ in range(n):
+                pos = len(hist[b])
+                slot = table[b][pos // page] * page + pos % page
+                k_here = kd[slot // page, slot % page]
+                want, size = R.rotate(kn[t:t + 1], torch.tensor([pos]), L.freq, D, 0, 1.0)
+                assert torch.all((k_here.double() - want[0]).abs()
+                                 <= HALF * want[0].abs() + size[0] * 5e-7)
+                hist[b].append((k_here, vn[t]))
+                t += 1
+        t = 0
+        bnd, sc = L.bnd.cpu(), L.sc.cpu()
+        qr, out = L.qr.cpu(), L.out.cpu()
+        for b, n in enumerate(ql):
+            for j in range(n):
+                pos = len(hist[b]) - n + j
+                for h in range(Hkv):
+                    r = slice(h * G, (h + 1) * G)
+                    want = R.select(qr[t, r], bnd[:, h], sc[:, h], table[b], pos, budget=budget,
+                                    num_first=1, num_recent=1, page=page, pages=L.p.num_pages,
+                                    window=0)
+                    assert sel[t][h] == want
+                    at = [x for s in want if s >= 0 for x in range(s * page, min(s * page + page, pos + 1))]
+                    kk = torch.stack([hist[b][x][0][h] for x in at])
+                    vv = torch.stack([hist[b][x][1][h] for x in at])
+                    o, _, size, big = R.attend(qr[t, r], kk, vv, at, pos, 0, L.p.sm_scale)
+                    ds = (D + 16) * 2.0 ** -24 * big[:, None] + 2.0 ** -20
+                    tol = (HALF + 2 * ds) * size * 1.01 + HALF * (o.abs() + HALF * size)
+                    assert torch.all((out[t, r].double() - o).abs() <= tol)
+                t += 1
+        assert torch.all(out[t:] == 7)
+        # every page is somewhere once
+        free = L.free.tolist()[:int(L.count)]
+        held = [pg for b in range(N) for pg in table[b][:R.up(len(hist[b]), page)]]
+        assert sorted(free + held) == list(range(L.p.num_pages))
+
+
+def test_equal_inputs_give_equal_bits_on_another_stream():
+    D, G, Hkv, page, budget = 128, 4, 8, 64, 12
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 1, [3000] * 5, [2] * 5, 21)
+    sel = ints(lists(seq, pos, Hkv, budget, page, 0, 5))
+    p = problem(num_seqs=5, num_q_heads=G * Hkv, num_kv_heads=Hkv, page_size=page, num_pages=pages,
+                max_pages_per_seq=len(table[0]), total_q_tokens=10, max_q_len=2,
+                max_context_len=3000, layout=1)
+    dev = [x.transpose(1, 2).contiguous().cuda() for x in (k, v)]
+    qd, t, s, x = q.cuda(), ints(table), ints(seq), ints(pos)
+    got = []
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream()):
+        ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
+        out = torch.zeros((10, G * Hkv, D), dtype=BF16, device="cuda")
+        lse = torch.zeros((10, G * Hkv), device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(3):
+            B.pa_decode_selected(p, budget, qd, *dev, t, s, x, sel, ws, out, lse, stream=stream)
+        torch.cuda.synchronize()
+        got.append((out, lse))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
