@@ -195,7 +195,7 @@ PA_API pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache,
  * head h's largest magnitude is at most 127 * 2^e_h, and q8 = q_h / 2^e_h rounded
  * to the nearest whole number, ties to even (NaN: 0; within [-127, 127]),
  *   score = bound_scale * max over h of 2^e_h * sum over channels of
- *           max(q8 * largest, q8 * smallest).
+ *           q8 * (the channel's largest where q8 > 0, its smallest where q8 < 0).
  * Every sum is a whole number below 2^24, so scores, and lists, are exact.
  *   q: bf16 [total_q_tokens][Hq][D], dense, as pa_decode_selected takes it.
  *   selected: int32 [total_q_tokens][Hkv][budget], written: page indices in the
@@ -205,9 +205,9 @@ PA_API pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache,
  *   (PA_DEV_BAD_PAGE, where scores are needed at all).
  *   budget >= 1; num_first, num_recent >= 0, together at most budget.  At most 64
  *   q heads a KV head; a context of at most PA_MAX_SELECT_PAGES pages
- *   (max_context_len / page_size); num_ctas, kv_dtype and sm_scale have no part in it.
+ *   (max_context_len / page_size): 720,896 tokens in pages of 16, 2.9 million of 64; num_ctas, kv_dtype and sm_scale have no part in it.
  */
-#define PA_MAX_SELECT_PAGES 262144
+#define PA_MAX_SELECT_PAGES 45056
 PA_API pa_status pa_select_pages(const pa_problem* problem, int32_t budget, int32_t num_first,
                                  int32_t num_recent, const void* q, const int8_t* bounds,
                                  const float* bound_scale, const int32_t* block_table,
@@ -217,18 +217,21 @@ PA_API pa_status pa_select_pages(const pa_problem* problem, int32_t budget, int3
 /*
  * Attention of every row over the pages listed for it (as pa_select_pages lists
  * them, or any other way): the semantics of pa_decode_splitk with the keys of
- * unlisted pages hidden, in one launch.  The lists' lengths are split over the GPU
- * inside the kernel, and the parts of a split list joined by the last CTA to
- * finish one.
+ * unlisted pages hidden.  The lists' lengths are split over the GPU inside the
+ * kernel, and the parts of a split list joined by the last CTA to finish one.
  *   selected: of row t and KV head h the entries 0 .. n-1, n = min(budget, pages
  *     that the row sees keys of); an entry of -1 among them is passed over, and so
  *     is one outside the row's pages [0, positions[t] / page_size] (PA_DEV_BAD_LENGTHS) or
  *     with a block-table entry outside the pool (PA_DEV_BAD_PAGE).  Order does not
- *     matter but for rounding; a page listed twice counts twice.
+ *     matter but for rounding.  No page should be listed twice for a row: whether it
+ *     then counts once or twice is not said.
+ *   With max_q_len > 1 up to six rows that stand together and are of one sequence
+ *   (drafts, a chunk's tokens) are taken together, by a first launch that joins their
+ *   lists: a page that several of them list is read once.  Nothing a row does not
+ *   list, or sees, reaches its result, infinities and NaN included.
  *   A row with no visible key listed: out = 0, lse = -inf.
  *   kv_dtype PA_BF16 (other: PA_ERR_UNSUPPORTED); at most 32 q heads a KV head for
- *   head_dim 128, 64 for 64.  Every row is a query of its own: a long prompt's rows
- *   each read their pages (pa_prefill's block mask shares them).
+ *   head_dim 128, 64 for 64.
  *   The products are bf16 with fp32 sums, probabilities rounded to bf16 for the
  *   product with V (2^-8 of each); num_ctas and unit_cost have their pa.h meaning
  *   (num_ctas at most 1024).

@@ -454,64 +454,57 @@ def pa_kv_evict(problem, budget, num_first, num_recent, k_cache, k_scale, v_cach
 
 # ------------------------------------ operators of a serving step (pa_step.h)
 
-_I8, _F32 = torch.int8, torch.float32
-_device_index = torch.cuda.current_device
+# What the kernels would misread is refused, as above; sizes are the caller's.  (A
+# step's small calls are bound by their time on the host, half of it in looks at
+# tensors: 0.15 us each.)
+
+_I8, _F32, _I64 = torch.int8, torch.float32, torch.int64
+# (torch.cuda.current_device looks for a CUDA context first)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _here(t: torch.Tensor):
     """The library launches on the current device: a tensor elsewhere is refused."""
-    if not t.is_cuda or t.get_device() != _device_index():
+    if not t.is_cuda or t.get_device() != _current_device():
         raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
 
 
-def _typed(t: Optional[torch.Tensor], dtype, name: str):
+def _i32(t: torch.Tensor):
+    """Address of contiguous int32."""
+    if t.dtype is _I32 and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
+                     f"contiguous int32 belongs")
+
+
+def _typed(t: Optional[torch.Tensor], dtype):
     """Address of a contiguous tensor of a type."""
     if t is None:
         return None
     if t.dtype is dtype and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name} must be contiguous {dtype}, not {t.dtype} of strides "
-                     f"{tuple(t.stride())}")
-
-
-def _room(t: torch.Tensor, n: int, name: str):
-    """Address of int32 on the device, n elements at least."""
-    if t.numel() < n:
-        raise ValueError(f"{name} has {t.numel()} elements where {n} belong")
-    return _ints(t)
-
-
-def _table_of(t: torch.Tensor, problem: PaProblem):
-    if t.dim() != 2 or t.shape[0] < problem.num_seqs or t.shape[1] != problem.max_pages_per_seq:
-        raise ValueError(f"a block table of shape {tuple(t.shape)} for num_seqs "
-                         f"{problem.num_seqs} and max_pages_per_seq {problem.max_pages_per_seq}")
-    return _ints(t)
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
+                     f"contiguous {dtype} belongs")
 
 
 def pa_pages_take(problem, seq_lens, q_lens, block_table, free_pages, free_count, context_lens,
                   row_seq, positions, slots, free_left, device_error=None, stream=None):
     """Pages for q_lens[b] new tokens of every sequence, and the maps of the step's rows."""
-    n, rows = problem.num_seqs, problem.total_q_tokens
     _here(seq_lens)
     _check((_lib or load()).pa_pages_take(
-        problem, _room(seq_lens, n, "seq_lens"), _room(q_lens, n, "q_lens"),
-        _table_of(block_table, problem), _room(free_pages, 1, "free_pages"),
-        _room(free_count, 1, "free_count"), _room(context_lens, n, "context_lens"),
-        _room(row_seq, rows, "row_seq"), _room(positions, rows, "positions"),
-        _room(slots, rows, "slots"), _room(free_left, 1, "free_left"), _ints(device_error),
-        _stream(stream)), "pa_pages_take")
+        problem, _i32(seq_lens), _i32(q_lens), _i32(block_table), _i32(free_pages),
+        _i32(free_count), _i32(context_lens), _i32(row_seq), _i32(positions), _i32(slots),
+        _i32(free_left), _typed(device_error, _I32), _stream(stream)), "pa_pages_take")
 
 
 def pa_pages_return(problem, seq_lens, keep_lens, block_table, free_pages, free_count, free_left,
                     device_error=None, stream=None):
     """The pages of tokens keep_lens[b] .. seq_lens[b] - 1 back on the free stack."""
-    n = problem.num_seqs
     _here(seq_lens)
     _check((_lib or load()).pa_pages_return(
-        problem, _room(seq_lens, n, "seq_lens"), _room(keep_lens, n, "keep_lens"),
-        _table_of(block_table, problem), _room(free_pages, problem.num_pages, "free_pages"),
-        _room(free_count, 1, "free_count"), _room(free_left, 1, "free_left"),
-        _ints(device_error), _stream(stream)), "pa_pages_return")
+        problem, _i32(seq_lens), _i32(keep_lens), _i32(block_table), _i32(free_pages),
+        _i32(free_count), _i32(free_left), _typed(device_error, _I32), _stream(stream)),
+        "pa_pages_return")
 
 
 def pa_rope_inv_freq(scaling: PaRopeScaling):
@@ -532,33 +525,29 @@ def pa_rope_steps(inv_freq) -> torch.Tensor:
     return steps
 
 
-def _token_rows(t: torch.Tensor, tokens: int, heads: int, dim: int, name: str) -> int:
-    """Elements between the tokens of rows [tokens, heads, dim] with dense heads."""
-    shape, stride = t.shape, t.stride()
-    if (t.dtype is not _BF16 or len(shape) != 3 or shape[0] < tokens or shape[1] != heads
-            or shape[2] != dim or stride[2] != 1 or (heads > 1 and stride[1] != dim)):
-        raise ValueError(f"{name} must be bf16 [total_q_tokens, {heads}, {dim}] with dense heads")
-    return stride[0] if shape[0] > 1 else heads * dim
-
-
 def pa_rope_append(problem, rope, steps, q, k_new, v_new, positions, slots, q_out, k_cache,
                    k_scale, v_cache, v_scale, device_error=None, stream=None):
     """Rotary positions on the new tokens' q (into q_out) and k, and k and v into the cache;
     the tokens of q, k_new and v_new may be strided (slices of a fused projection)."""
-    rows, dim, kv = problem.total_q_tokens, problem.head_dim, problem.num_kv_heads
-    ks, vs = _new_rows(k_new, problem, "k_new"), _new_rows(v_new, problem, "v_new")
-    qs, qp = 0, None
-    if q is not None:
-        qs = _token_rows(q, rows, problem.num_q_heads, dim, "q")
-        qp = q.data_ptr()
+    dim, heads, rows = problem.head_dim, problem.num_kv_heads, problem.total_q_tokens
+
+    def stride(t, heads, name):
+        shape, by = t.shape, t.stride()
+        if (t.dtype is not _BF16 or len(shape) != 3 or shape[0] < rows or shape[1] != heads
+                or shape[2] != dim or by[2] != 1 or (by[1] != dim and heads > 1)):
+            raise ValueError(f"{name} must be bf16 [total_q_tokens, {heads}, {dim}] with dense "
+                             f"heads")
+        return by[0] if shape[0] > 1 else heads * dim
+
+    _here(positions)
+    qs, qp = (0, None) if q is None else (stride(q, problem.num_q_heads, "q"), q.data_ptr())
+    ks, vs = stride(k_new, heads, "k_new"), stride(v_new, heads, "v_new")
     if steps.numel() < rope.rotary_dim // 2:
         raise ValueError(f"{steps.numel()} steps for a rotary_dim of {rope.rotary_dim}")
-    _here(positions)
     _check((_lib or load()).pa_rope_append(
-        problem, rope, _typed(steps, torch.int64, "steps"), qp, k_new.data_ptr(),
-        v_new.data_ptr(), qs, ks, vs, _room(positions, rows, "positions"),
-        _room(slots, rows, "slots"), _typed(q_out, _BF16, "q_out"), _cache(k_cache, problem),
-        _dense(k_scale), _cache(v_cache, problem), _dense(v_scale), _ints(device_error),
+        problem, rope, _typed(steps, _I64), qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
+        _i32(positions), _i32(slots), _typed(q_out, _BF16), _cache(k_cache, problem),
+        _dense(k_scale), _cache(v_cache, problem), _dense(v_scale), _typed(device_error, _I32),
         _stream(stream)), "pa_rope_append")
 
 
@@ -566,23 +555,19 @@ def pa_page_bounds(problem, k_cache, slots, bounds, bound_scale, device_error=No
     """Each channel's largest and smallest key of the pages that the rows' slots are in."""
     _here(slots)
     _check((_lib or load()).pa_page_bounds(
-        problem, _typed(k_cache, _BF16, "k_cache"), _room(slots, problem.total_q_tokens, "slots"),
-        _typed(bounds, _I8, "bounds"), _typed(bound_scale, _F32, "bound_scale"),
-        _ints(device_error), _stream(stream)), "pa_page_bounds")
+        problem, _typed(k_cache, _BF16), _i32(slots), _typed(bounds, _I8),
+        _typed(bound_scale, _F32), _typed(device_error, _I32), _stream(stream)),
+        "pa_page_bounds")
 
 
 def pa_select_pages(problem, budget, num_first, num_recent, q, bounds, bound_scale, block_table,
                     row_seq, positions, selected, device_error=None, stream=None):
     """Per row and KV head the budget's page indices with the highest bound on a logit."""
-    rows = problem.total_q_tokens
     _here(positions)
     _check((_lib or load()).pa_select_pages(
-        problem, int(budget), int(num_first), int(num_recent), _typed(q, _BF16, "q"),
-        _typed(bounds, _I8, "bounds"), _typed(bound_scale, _F32, "bound_scale"),
-        _table_of(block_table, problem), _room(row_seq, rows, "row_seq"),
-        _room(positions, rows, "positions"),
-        _room(selected, rows * problem.num_kv_heads * int(budget), "selected"),
-        _ints(device_error), _stream(stream)), "pa_select_pages")
+        problem, budget, num_first, num_recent, _typed(q, _BF16), _typed(bounds, _I8),
+        _typed(bound_scale, _F32), _i32(block_table), _i32(row_seq), _i32(positions),
+        _i32(selected), _typed(device_error, _I32), _stream(stream)), "pa_select_pages")
 
 
 def pa_selected_workspace_size(problem: PaProblem, budget: int) -> int:
@@ -592,14 +577,11 @@ def pa_selected_workspace_size(problem: PaProblem, budget: int) -> int:
 def pa_decode_selected(problem, budget, q, k_cache, v_cache, block_table, row_seq, positions,
                        selected, ws, out, lse=None, stream=None):
     """Attention of every row over the pages listed for it."""
-    rows = problem.total_q_tokens
     _here(positions)
     _check((_lib or load()).pa_decode_selected(
-        problem, int(budget), _typed(q, _BF16, "q"), _typed(k_cache, _BF16, "k_cache"),
-        _typed(v_cache, _BF16, "v_cache"), _table_of(block_table, problem),
-        _room(row_seq, rows, "row_seq"), _room(positions, rows, "positions"),
-        _room(selected, rows * problem.num_kv_heads * int(budget), "selected"), _dense(ws),
-        _nbytes(ws), _typed(out, _BF16, "out"), _typed(lse, _F32, "lse"), _stream(stream)),
+        problem, budget, _typed(q, _BF16), _typed(k_cache, _BF16), _typed(v_cache, _BF16),
+        _i32(block_table), _i32(row_seq), _i32(positions), _i32(selected), _dense(ws),
+        _nbytes(ws), _typed(out, _BF16), _typed(lse, _F32), _stream(stream)),
         "pa_decode_selected")
 
 

@@ -13,10 +13,18 @@
 //
 // What bounds it: 4 D bytes a listed key and head from HBM.  A page is 16 tokens or
 // a multiple, so a step lies in one page, and one look at its list entry tells which
-// of its keys are there: keys that the row does not see, or whose page is none, are
-// not loaded but written as zeros, and their scores are -inf.  Nothing outside a
-// row's sight reaches it.  Products are transposed (mma m16n8k16 with 16 keys, or 16
-// columns of V, as rows): the G heads of a group cost ceil(G / 8) of them.
+// of its keys are there: keys that no row sees, or whose page is none, are not loaded
+// but written as zeros, and their scores are -inf.  Products are transposed (mma
+// m16n8k16 with 16 keys, or 16 columns of V, as rows): R query rows cost ceil(R / 8)
+// of them.
+//
+// Rows of one sequence that stand together (drafts, a chunk's tokens) list mostly the
+// same pages.  Where the problem allows several rows a sequence, up to kMostRows of
+// them are one unit: a first kernel joins their lists into one of pages, each with
+// the set of rows that listed it, and looks the pages up; the second reads every page
+// once and hides its keys from the rows that did not list it.  What is hidden from a
+// row must not reach it as 0 * NaN either: a step that not all rows see in full looks
+// whether V is finite, and multiplies row by row where it is not.
 #include <algorithm>
 
 #include "pa_cache_mma.cuh"
@@ -50,64 +58,108 @@ namespace {
 
 // No CTA takes less than this of the flat line: joining a unit's parts costs more
 // than the tiles it would spread.
-constexpr int kMinShareSel = 2;
+constexpr int kMinShareSel = 4;
+
+constexpr int kMostRows = 6;                  // of a unit: what an entry has bits for
+constexpr int kRowBits = 26;                  // a page index is below 2^26 (a context below 2^30)
 
 constexpr float kUnseen = -3.402823466e38f;   // running max of a row that has seen no key
 constexpr float kRise = 8.f;                  // (log2) how far scores may pass the max before it moves
 
-// A unit (row, KV head) as a CTA meets it.
+// A unit (row or rows of a sequence, KV head) as a CTA meets it.
 struct SelUnit {
     int row, hk;
-    int seq, pos;          // of the row
+    int seq, pos;          // of the (first) row
+    int rows;              // how many
     int n;                 // tiles
-    int tokens;            // of its list
+    int entries;           // of its list
+    int64_t list;          // where that begins
     int64_t start;         // position of its fixed cost on the flat line
+    int c_first, c_last;   // the CTAs that share it
 };
 
-// Tokens of row t's list, 0 if it has none or is none of a sequence's.
-__device__ __forceinline__ int list_tokens(const SelectedParams& P, int seq, int pos) {
-    const CacheGeom& g = P.g;
-    if (seq < 0 || seq >= g.B || pos < 0 || pos >= g.max_ctx) return 0;
-    const int first = g.window > 0 ? max(0, pos - g.window + 1) >> g.ps_shift : 0;
-    return min(P.budget, (pos >> g.ps_shift) + 1 - first) << g.ps_shift;
+__device__ __forceinline__ bool good_row(const CacheGeom& g, int seq, int pos) {
+    return seq >= 0 && seq < g.B && pos >= 0 && pos < g.max_ctx;
 }
-__device__ __forceinline__ int tiles_of(int tokens) {
-    return (tokens + kDecodeTile - 1) / kDecodeTile;
+// Entries of the list of a row at pos.
+__device__ __forceinline__ int list_entries(const SelectedParams& P, int pos) {
+    const CacheGeom& g = P.g;
+    const int first = g.window > 0 ? max(0, pos - g.window + 1) >> g.ps_shift : 0;
+    return min(P.budget, (pos >> g.ps_shift) + 1 - first);
+}
+__device__ __forceinline__ int tiles_of(const CacheGeom& g, int entries) {
+    return (int)((((int64_t)entries << g.ps_shift) + kDecodeTile - 1) / kDecodeTile);
 }
 
-__device__ __forceinline__ void load_row(const SelectedParams& P, SelUnit& u) {
-    u.seq = P.row_seq[u.row];
-    u.pos = P.positions[u.row];
-    u.tokens = list_tokens(P, u.seq, u.pos);
-    u.n = tiles_of(u.tokens);
+// What the rows' units are: from the row maps, or as the first kernel left them.
+template <bool JOINED>
+__device__ __forceinline__ int64_t row_cost(const SelectedParams& P, int t) {
+    if constexpr (JOINED) {
+        const int n = P.row_tiles[t];
+        return n > 0 ? n + (int64_t)P.g.Hkv * P.unit_cost : 0;
+    } else {
+        const int seq = P.row_seq[t], pos = P.positions[t];
+        if (!good_row(P.g, seq, pos)) return 0;
+        return (int64_t)P.g.Hkv * (tiles_of(P.g, list_entries(P, pos)) + P.unit_cost);
+    }
+}
+// The rest of u, whose row and head are set; its row leads a unit.
+template <bool JOINED>
+__device__ __forceinline__ void load_unit(const SelectedParams& P, SelUnit& u, int64_t C,
+                                          int64_t N) {
+    const CacheGeom& g = P.g;
+    if (u.hk == 0 || u.rows == 0) {
+        u.seq = P.row_seq[u.row];
+        u.pos = P.positions[u.row];
+        u.rows = JOINED ? P.row_lead[u.row] : 1;
+    }
+    const int64_t at = (int64_t)u.row * g.Hkv;
+    if constexpr (JOINED) {
+        u.entries = P.unit_entries[at + u.hk];
+        u.list = (at + (int64_t)u.hk * u.rows) * P.budget;
+    } else {
+        u.entries = list_entries(P, u.pos);
+        u.list = (at + u.hk) * P.budget;
+    }
+    u.n = tiles_of(g, u.entries);
+    // a tile belongs to the CTA whose share of the line it is in, but no CTA takes less
+    // than two tiles of a unit, and a short unit is not split
+    const int64_t p0 = u.start + P.unit_cost;
+    auto owner = [&](int64_t x) { return (int)(((x + 1) * N - 1) / C); };
+    u.c_first = owner(u.n < 4 ? p0 + u.n - 1 : p0 + 1);
+    u.c_last = u.n < 4 ? u.c_first : owner(p0 + u.n - 2);
 }
 
 // The unit after u (every lane the same); false past the last row.
-__device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u) {
+template <bool JOINED>
+__device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u, int64_t C,
+                                          int64_t N) {
     u.start += P.unit_cost + u.n;
-    if (++u.hk < P.g.Hkv) return true;
-    u.hk = 0;
-    do {
-        if (++u.row >= P.g.total_q) return false;
-        load_row(P, u);
-    } while (u.n == 0);
+    if (++u.hk >= P.g.Hkv) {
+        u.hk = 0;
+        do {
+            if (++u.row >= P.g.total_q) return false;
+        } while (row_cost<JOINED>(P, u.row) == 0);
+    }
+    load_unit<JOINED>(P, u, C, N);
     return true;
 }
 
-// What warp w of W runs of unit u, of the CTA's share [lo, hi) of the flat line:
-// tokens [a, z) of its list.
+// What warp w of W of a CTA runs of unit u, of the CTA's share [lo, hi) of the flat
+// line: tokens [a, z) of its list.
 struct SelShare {
     int t0, t1;     // tiles of the unit in the CTA's share
     int a, z;
 };
-__device__ __forceinline__ SelShare share_of(const SelUnit& u, int cost, int64_t lo, int64_t hi,
-                                             int w, int W) {
-    SelShare s;
+__device__ __forceinline__ SelShare share_of(const CacheGeom& g, const SelUnit& u, int cost, int cta,
+                                             int64_t lo, int64_t hi, int w, int W) {
+    SelShare s = {0, 0, 0, 0};
+    if (cta < u.c_first || cta > u.c_last) return s;
     const int64_t base = u.start + cost;
-    s.t0 = (int)max((int64_t)0, min((int64_t)u.n, lo - base));
-    s.t1 = (int)max((int64_t)0, min((int64_t)u.n, hi - base));
-    const int tok0 = s.t0 * kDecodeTile, end = min(u.tokens, s.t1 * kDecodeTile);
-    const int steps = s.t1 > s.t0 ? (end - tok0) / 16 : 0;
+    s.t0 = cta == u.c_first ? 0 : (int)(lo - base);
+    s.t1 = cta == u.c_last ? u.n : (int)(hi - base);
+    const int tok0 = s.t0 * kDecodeTile, end = min(u.entries << g.ps_shift, s.t1 * kDecodeTile);
+    const int steps = (end - tok0) / 16;
     s.a = tok0 + 16 * (steps * w / W);
     s.z = tok0 + 16 * (steps * (w + 1) / W);
     return s;
@@ -119,6 +171,118 @@ __device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, in
                  : "memory");
 }
 
+// ---- joins the lists of rows of one sequence (one CTA a row; only a unit's first row's
+// goes on).  A warp a KV head: the set of rows of every page, a byte each, in shared
+// memory, some pages at a time; then the pages that have any, in order.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinPages = 4096;
+
+__global__ void __launch_bounds__(32 * kJoinWarps)
+join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
+    __shared__ __align__(16) uint32_t s_rows[kJoinWarps][kJoinPages / 4];
+    __shared__ int s_tiles[kJoinWarps];
+    const CacheGeom& g = P.g;
+    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    int32_t* err = P.header + H_ERROR;
+    const int seq = P.row_seq[t];
+    int m = 0;                         // rows of the unit that t leads
+    if (seq >= 0 && seq < g.B) {
+        // rows of the sequence before t
+        int before = 0;
+        while (true) {
+            const int r = t - 1 - before - lane;
+            const uint32_t other =
+                __ballot_sync(0xffffffffu, r < 0 || P.row_seq[max(r, 0)] != seq);
+            before += other != 0 ? __ffs(other) - 1 : 32;
+            if (other != 0) break;
+        }
+        if (before % most == 0) {
+            const int r = t + lane;
+            const uint32_t other = __ballot_sync(
+                0xffffffffu, r >= g.total_q || P.row_seq[min(r, g.total_q - 1)] != seq);
+            m = min(most, other != 0 ? __ffs(other) - 1 : 32);
+        }
+    }
+    // lane i < m has row i's position and its list's length; a row with a position that
+    // cannot be has none
+    int pos = -1;
+    if (lane < m) pos = P.positions[t + lane];
+    if (lane < m && (pos < 0 || pos >= g.max_ctx)) pos = -1;
+    const int mine = pos >= 0 ? list_entries(P, pos) : 0;
+    const uint32_t good = __ballot_sync(0xffffffffu, pos >= 0);
+    if (threadIdx.x == 0 && ((seq >= g.B) || __popc(good) != m)) flag_error(err, PA_DEV_BAD_LENGTHS);
+    if (good == 0) {
+        if (threadIdx.x == 0) {
+            P.row_lead[t] = 0;
+            P.row_tiles[t] = 0;
+        }
+        return;                        // (the same for every thread)
+    }
+    const int last = __reduce_max_sync(0xffffffffu, pos) >> g.ps_shift;   // page index
+    int tiles = 0;
+    for (int hk = warp; hk < g.Hkv; hk += kJoinWarps) {
+        int2* to = P.list + ((int64_t)t * g.Hkv + (int64_t)hk * m) * P.budget;
+        int n = 0;
+        for (int p0 = 0; p0 <= last; p0 += kJoinPages) {
+            const int span = min(kJoinPages, last + 1 - p0);
+            for (int i = lane; i < (span + 15) / 16; i += 32)
+                reinterpret_cast<uint4*>(s_rows[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+            for (int r = 0; r < m; ++r) {
+                const int many = __shfl_sync(0xffffffffu, mine, r);
+                const int top = __shfl_sync(0xffffffffu, pos, r) >> g.ps_shift;
+                const int32_t* sel = P.selected + ((int64_t)(t + r) * g.Hkv + hk) * P.budget;
+                for (int i = lane; i < many; i += 32) {
+                    const int s = sel[i];
+                    if (s < -1 || s > top) {
+                        flag_error(err, PA_DEV_BAD_LENGTHS);
+                    } else if (s >= p0 && s < p0 + span) {
+                        const int at = s - p0;
+                        atomicOr(&s_rows[warp][at >> 2], 1u << (8 * (at & 3) + r));
+                    }
+                }
+            }
+            __syncwarp();
+            for (int i0 = 0; i0 < span; i0 += 128) {
+                const int i = i0 + 4 * lane;
+                uint32_t w = i < span ? s_rows[warp][i >> 2] : 0u;
+                int here = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) here += (w >> (8 * j) & 255u) != 0;
+                const int upto = warp_inclusive(here, lane);
+                int k = n + upto - here;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t rows = w >> (8 * j) & 255u;
+                    if (rows == 0) continue;
+                    const int s = p0 + i + j;
+                    const int page = P.table[(int64_t)seq * g.mpps + s];
+                    const bool ok = (uint32_t)page < (uint32_t)g.num_pages;
+                    if (!ok) flag_error(err, PA_DEV_BAD_PAGE);
+                    to[k++] = make_int2(ok ? page : -1, (int)((uint32_t)s | rows << kRowBits));
+                }
+                n += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            __syncwarp();
+        }
+        if (n == 0) {                  // the rows' results are written all the same
+            if (lane == 0) to[0] = make_int2(-1, 0);
+            n = 1;
+        }
+        if (lane == 0) P.unit_entries[(int64_t)t * g.Hkv + hk] = n;
+        tiles += tiles_of(g, n);
+    }
+    if (lane == 0) s_tiles[warp] = tiles;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int all = 0;
+        for (int w = 0; w < kJoinWarps; ++w) all += s_tiles[w];
+        P.row_lead[t] = m;
+        P.row_tiles[t] = all;
+    }
+}
+
 // Byte offset of 16-byte piece c of row r of a step's K or V rows: ldmatrix takes
 // eight rows' piece c, on eight bank groups.
 template <int D>
@@ -126,7 +290,8 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
     return (uint32_t)(r * 2 * D + ((c ^ (r & 7)) << 4));
 }
 
-template <int D, int NT>
+// JOINED: units of several rows, whose lists are joined; else of one.
+template <int D, int NT, bool JOINED>
 __global__ void __launch_bounds__(SelCfg<D, NT>::kThreads, SelCfg<D, NT>::kCtas)
 decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     using Cfg = SelCfg<D, NT>;
@@ -142,16 +307,12 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     grid_dependency_wait();
 
     // ---- this CTA's share of the flat line
-    auto row_cost = [&](int t) -> int64_t {
-        const int n = tiles_of(list_tokens(P, P.row_seq[t], P.positions[t]));
-        return n > 0 ? (int64_t)g.Hkv * (n + cost) : 0;
-    };
-    const int64_t C = flat_total(g.total_q, lane, row_cost);
-    if (blockIdx.x == 0 && warp == 0) {
-        bool bad = false;
+    auto cost_of = [&](int t) { return row_cost<JOINED>(P, t); };
+    const int64_t C = flat_total(g.total_q, lane, cost_of);
+    if (!JOINED && blockIdx.x == 0 && warp == 0) {
         for (int t = lane; t < g.total_q; t += 32)
-            bad |= P.row_seq[t] >= 0 && list_tokens(P, P.row_seq[t], P.positions[t]) == 0;
-        if (bad) flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
+            if (P.row_seq[t] >= 0 && !good_row(g, P.row_seq[t], P.positions[t]))
+                flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
     }
     const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel - 1) / kMinShareSel);
     const int cta = blockIdx.x;
@@ -159,14 +320,13 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     const int64_t lo = C * cta / N, hi = C * (cta + 1) / N;
     SelUnit u;
     {
-        int64_t start;
         int none;
-        u.row = flat_find(g.total_q, lane, lo, row_cost, [](int) { return 0; }, start, none);
-        load_row(P, u);
-        const int i = (int)((lo - start) / (u.n + cost));
-        u.hk = i;
-        u.start = start + (int64_t)i * (u.n + cost);
+        u.row = flat_find(g.total_q, lane, lo, cost_of, [](int) { return 0; }, u.start, none);
+        u.hk = u.rows = 0;
+        load_unit<JOINED>(P, u, C, N);
+        while (u.start + cost + u.n <= lo) next_unit<JOINED>(P, u, C, N);   // (of the same row)
     }
+    auto share = [&](const SelUnit& x) { return share_of(g, x, cost, cta, lo, hi, warp, W); };
 
     const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::kStage;
     const uint32_t qbase = smem_u32(smem + Cfg::kOffQ);
@@ -178,52 +338,79 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     constexpr int INS = 16 / RPI;                 // instructions for a step's K (or V)
     const int page_rows = g.ps * g.Hkv;
     const int r_lane = lane / CH, c_lane = lane % CH;
-    // list entry i + lane of a unit, as (page number, position of its first token); a page
-    // number of -1: nothing is there
-    auto entries = [&](const SelUnit& x, int i, int& base) -> int {
-        base = 0;
-        const int k = i + lane;
-        if (k >= x.tokens >> g.ps_shift) return -1;
-        const int s = P.selected[((int64_t)x.row * g.Hkv + x.hk) * P.budget + k];
-        if (s < 0) {
-            if (s < -1) flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
-            return -1;
+    // A list's entry i + lane: as it lies there (read well ahead), and as a page number
+    // (-1: nothing is there) with its index in the sequence (and its rows' bits).
+    auto read_entry = [&](const SelUnit& x, int i) -> int2 {
+        const bool there = i + lane < x.entries;
+        if constexpr (JOINED)
+            return there ? P.list[x.list + i + lane] : make_int2(-1, 0);
+        else
+            return make_int2(-1, there ? P.selected[x.list + i + lane] : -1);
+    };
+    auto look_up = [&](const SelUnit& x, int2 e) -> int2 {
+        if constexpr (JOINED) return e;
+        const int s = e.y;
+        e.y = 0;
+        if (s < 0 || s > x.pos >> g.ps_shift) {
+            if (s != -1) flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
+            return e;
         }
-        if (s > x.pos >> g.ps_shift) {
-            flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
-            return -1;
-        }
-        base = s << g.ps_shift;
         const int page = P.table[(int64_t)x.seq * g.mpps + s];
-        if ((uint32_t)page < (uint32_t)g.num_pages) return page;
-        flag_error(P.header + H_ERROR, PA_DEV_BAD_PAGE);
-        return -1;
+        if ((uint32_t)page < (uint32_t)g.num_pages)
+            e = make_int2(page, s);
+        else
+            flag_error(P.header + H_ERROR, PA_DEV_BAD_PAGE);
+        return e;
+    };
+    // Positions of a unit's rows (lane i has row i's; -1: none), and their extremes.
+    auto row_pos = [&](const SelUnit& x) -> int {
+        if constexpr (!JOINED) return x.pos;
+        const int p = lane < x.rows ? P.positions[x.row + lane] : -1;
+        return p < g.max_ctx ? max(p, -1) : -1;
+    };
+    auto extremes = [&](int p, int& least, int& most, uint32_t& rows) {
+        least = most = p;
+        rows = 1u;
+        if constexpr (JOINED) {
+            most = __reduce_max_sync(0xffffffffu, p);
+            least = __reduce_min_sync(0xffffffffu, p >= 0 ? p : 0x7fffffff);
+            rows = __ballot_sync(0xffffffffu, p >= 0);
+        }
     };
     SelUnit ln = u;                          // the unit after the one being loaded
     SelUnit lu = u;                          // the one being loaded
-    SelShare ls = share_of(u, cost, lo, hi, warp, W);
     bool more = true;
-    int l_tok = ls.a, l_end = ls.z;
-    int win_lo = l_tok >> g.ps_shift;        // 32 entries, and the next unit's
-    int win_base, lnw_base = 0;
-    int win = entries(u, win_lo, win_base), lnw = -1;
-    uint32_t meta = 0;                       // per stage: the first key there is, and one past the last
-    bool ln_ok = next_unit(P, ln) && ln.start < hi;
-    if (ln_ok) lnw = entries(ln, share_of(ln, cost, lo, hi, warp, W).a >> g.ps_shift, lnw_base);
+    int l_tok, l_end, l_least, l_most;
+    uint32_t l_rows;
+    {
+        const SelShare x = share(u);
+        l_tok = x.a;
+        l_end = x.z;
+    }
+    int win_lo = l_tok >> g.ps_shift;        // 32 entries, the 32 after them, the next unit's
+    int2 win = read_entry(u, win_lo), nxt = read_entry(u, win_lo + 32), lnw = make_int2(-1, 0);
+    bool ln_ok = next_unit<JOINED>(P, ln, C, N) && ln.start < hi;
+    if (ln_ok) lnw = read_entry(ln, share(ln).a >> g.ps_shift);
+    extremes(row_pos(u), l_least, l_most, l_rows);
+    win = look_up(u, win);
+    // per stage: its first key that is there, one past the last, the rows that listed its
+    // page, whether all rows see all of it; where its first key is
+    uint32_t meta = 0;
+    int meta_at = 0;
     auto issue = [&](int stage) {
         while (more && l_tok >= l_end) {
             more = ln_ok;
             if (!more) break;
             lu = ln;
-            const SelShare x = share_of(ln, cost, lo, hi, warp, W);
+            const SelShare x = share(ln);
             l_tok = x.a;
             l_end = x.z;
+            extremes(row_pos(ln), l_least, l_most, l_rows);
             win_lo = l_tok >> g.ps_shift;
-            win = lnw;
-            win_base = lnw_base;
-            ln_ok = next_unit(P, ln) && ln.start < hi;
-            if (ln_ok)
-                lnw = entries(ln, share_of(ln, cost, lo, hi, warp, W).a >> g.ps_shift, lnw_base);
+            win = look_up(ln, lnw);
+            nxt = read_entry(ln, win_lo + 32);
+            ln_ok = next_unit<JOINED>(P, ln, C, N) && ln.start < hi;
+            if (ln_ok) lnw = read_entry(ln, share(ln).a >> g.ps_shift);
         }
         if (more) {
             const int tok = l_tok;
@@ -231,22 +418,29 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             const int p0 = tok >> g.ps_shift;
             if (p0 - win_lo >= 32) {
                 win_lo += 32;
-                win = entries(lu, win_lo, win_base);
+                win = look_up(lu, nxt);
+                nxt = read_entry(lu, win_lo + 32);
             }
-            const int page = __shfl_sync(0xffffffffu, win, p0 - win_lo);
+            const int page = __shfl_sync(0xffffffffu, win.x, p0 - win_lo);
+            const uint32_t entry = (uint32_t)__shfl_sync(0xffffffffu, win.y, p0 - win_lo);
             const int slot = tok & (g.ps - 1);
-            const int at = __shfl_sync(0xffffffffu, win_base, p0 - win_lo) + slot;
-            // keys a .. z - 1 of the step are there and seen
+            const int at = (int)((entry & ((1u << kRowBits) - 1u)) << g.ps_shift) + slot;
+            // keys a .. z - 1 of the step are there, and some row sees them
             int a = 0, z = 0;
             if (page >= 0) {
-                a = g.window > 0 ? max(0, min(16, lu.pos - g.window + 1 - at)) : 0;
-                z = max(a, min(16, lu.pos + 1 - at));
+                a = g.window > 0 ? max(0, min(16, l_least - g.window + 1 - at)) : 0;
+                z = max(a, min(16, l_most + 1 - at));
             }
-            const int sh = 10 * stage;
-            if constexpr (ST <= 3)
-                meta = (meta & ~(1023u << sh)) | (uint32_t)(a | z << 5) << sh;
-            else if (lane == stage)
+            if (lane == stage) {
                 meta = (uint32_t)(a | z << 5);
+                if constexpr (JOINED) {
+                    const uint32_t rows = entry >> kRowBits;
+                    const bool all = rows == l_rows && a == 0 && z == 16 && at + 15 <= l_least &&
+                                     (g.window == 0 || at > l_most - g.window);
+                    meta |= rows << 10 | (all ? 1u << 16 : 0u);
+                    meta_at = at;
+                }
+            }
             const int64_t row0 = (int64_t)max(page, 0) * page_rows + (int64_t)slot * g.tok_rows +
                                  (int64_t)lu.hk * g.head_rows;
             const uint32_t dst = ring + stage * Cfg::kStage;
@@ -287,9 +481,10 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             const int r = warp + i * W;
 #pragma unroll
             for (int j = 0; j < QW; ++j) qw[i][j] = 0u;
-            if (r < g.G) {
+            if (r < x.rows * g.G) {
                 const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                    P.q + ((int64_t)x.row * g.Hq + (int64_t)x.hk * g.G + r) * D);
+                    P.q + (JOINED ? (int64_t)(x.row + r / g.G) * g.Hq + (int64_t)x.hk * g.G + r % g.G
+                                  : (int64_t)x.row * g.Hq + (int64_t)x.hk * g.G + r) * D);
 #pragma unroll
                 for (int j = 0; j < QW; ++j) qw[i][j] = src[lane + 32 * j];
             }
@@ -300,7 +495,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     const float f = g.sm_scale * kLog2e;
     // ---- units
     while (true) {
-        const SelShare sh = share_of(u, cost, lo, hi, warp, W);
+        const SelShare sh = share(u);
+        const int R = u.rows * g.G;
 #pragma unroll
         for (int i = 0; i < QPW; ++i)
 #pragma unroll
@@ -309,7 +505,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                                              4 * (lane + 32 * j)) = qw[i][j];
         __syncthreads();
         SelUnit nu = u;
-        const bool has_next = next_unit(P, nu) && nu.start < hi;
+        const bool has_next = next_unit<JOINED>(P, nu, C, N) && nu.start < hi;
         if (has_next) load_q(nu);
 
         float m[NT][2], l[NT][2];
@@ -321,6 +517,21 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 #pragma unroll
             for (int i = 0; i < OT; ++i)
                 o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+        }
+        // JOINED: where the thread's rows are, and their bits in an entry (none: position -1)
+        int pr[JOINED ? NT : 1][2];
+        uint32_t bit[JOINED ? NT : 1][2];
+        if constexpr (JOINED) {
+            const int p = row_pos(u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * t4 + e, i = r / g.G;
+                    pr[nt][e] = __shfl_sync(0xffffffffu, p, min(i, 31));
+                    bit[nt][e] = r < R ? 1u << i : 0u;
+                    if (r >= R) pr[nt][e] = -1;
+                }
         }
         constexpr bool kQInRegs = NT == 1;
         uint32_t qf[kQInRegs ? KK : 1][2];
@@ -345,11 +556,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         for (int tok = sh.a; tok < sh.z; tok += 16) {
             cp_async_wait<ST - 2>();
             __syncwarp();
-            uint32_t mt;
-            if constexpr (ST <= 3)
-                mt = meta >> (10 * stage);
-            else
-                mt = __shfl_sync(0xffffffffu, meta, stage);
+            const uint32_t mt = __shfl_sync(0xffffffffu, meta, stage);
+            const int at = JOINED ? __shfl_sync(0xffffffffu, meta_at, stage) : 0;
             const int a = (int)(mt & 31u), z = (int)((mt >> 5) & 31u);
             issue(stage == 0 ? ST - 1 : stage - 1);   // into the stage the last step left
             const uint32_t sk = ring + stage * Cfg::kStage, sv = sk + 16 * ROW;
@@ -392,14 +600,23 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     for (int e = 0; e < 4; ++e)
                         s[nt][e] = (kTwo ? s[nt][e] + s1[kTwo ? nt : 0][e] : s[nt][e]) * f;
             }
-            if (a > 0 || z < 16) {
+            const bool part_seen = JOINED ? !(mt >> 16 & 1u) : a > 0 || z < 16;
+            // JOINED: whether row (nt, e) sees key x of the step
+            auto sees = [&](int nt, int e, int x) -> bool {
+                const int p = pr[JOINED ? nt : 0][e];
+                return (mt >> 10 & bit[JOINED ? nt : 0][e]) != 0 && x >= a && x < z && at + x <= p &&
+                       (g.window == 0 || at + x > p - g.window);
+            };
+            if (part_seen) {
                 // keys gr and gr + 8 of the step
                 const bool k0 = gr >= a && gr < z, k1 = gr + 8 >= a && gr + 8 < z;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!(e < 2 ? k0 : k1)) s[nt][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const bool ok = JOINED ? sees(nt, e & 1, gr + 8 * (e >> 1)) : e < 2 ? k0 : k1;
+                        if (!ok) s[nt][e] = -INFINITY;
+                    }
             }
             // ---- the running max moves where a score passes it by far
             bool far = false;
@@ -441,27 +658,81 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 pb[nt][1] = movmatrix_trans(pack_bf16x2(p2, p3));
             }
             // ---- O^T += V^T P
-            {
-                const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+            const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+            bool plain = true;
+            if constexpr (JOINED) {
+                if (part_seen) {
+                    // is V finite?  (the largest magnitude of the lane's share of it)
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < OT; ++i) {
+                        uint32_t x[4];
+                        ldsm_x4(sv + piece_at<D>(vr, 2 * i + vc), x[0], x[1], x[2], x[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = max_bf16x2(top, x[j] & 0x7fff7fffu);
+                    }
+                    const uint32_t m1 = max(top & 0xffffu, top >> 16);
+                    plain = !__any_sync(0xffffffffu, m1 >= 0x7f80u);
+                }
+            }
+            if (plain) {
 #pragma unroll
                 for (int i = 0; i < OT; ++i) {
                     uint32_t x[4];
-                    ldsm_x4_t(sv + piece_at<D>(r, 2 * i + c), x[0], x[1], x[2], x[3]);
+                    ldsm_x4_t(sv + piece_at<D>(vr, 2 * i + vc), x[0], x[1], x[2], x[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[i][nt], x, pb[nt][0], pb[nt][1]);
+                }
+            } else if constexpr (JOINED) {
+                // row by row of the sequence: the keys it does not see are zeros in V, and
+                // the product is added to its own columns only
+                for (int i0 = 0; i0 < u.rows; ++i0) {
+                    const int p = __shfl_sync(0xffffffffu, row_pos(u), i0);
+                    auto word = [&](int key) -> uint32_t {
+                        auto seen = [&](int x) {
+                            return (mt >> (10 + i0) & 1u) != 0 && x >= a && x < z && at + x <= p &&
+                                   (g.window == 0 || at + x > p - g.window);
+                        };
+                        return (seen(key) ? 0xffffu : 0u) | (seen(key + 1) ? 0xffff0000u : 0u);
+                    };
+                    const uint32_t w0 = word(2 * t4), w1 = word(2 * t4 + 8);
+#pragma unroll
+                    for (int i = 0; i < OT; ++i) {
+                        uint32_t x[4];
+                        ldsm_x4_t(sv + piece_at<D>(vr, 2 * i + vc), x[0], x[1], x[2], x[3]);
+                        x[0] &= w0;
+                        x[1] &= w0;
+                        x[2] &= w1;
+                        x[3] &= w1;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float y[4];
+                            mma_bf16_first(y, x, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (bit[nt][e & 1] == 1u << i0) o[i][nt][e] += y[e];
+                        }
+                    }
                 }
             }
         }
 
         // ---- merge the warps, a few rows at a time
         if (sh.t1 > sh.t0) {
-            const int64_t pos0 = u.start + cost;   // the CTAs that hold parts of the unit
-            const int c_first = (int)(((pos0 + 1) * N - 1) / C);
-            const int c_last = (int)(((pos0 + u.n) * N - 1) / C);
+            const int c_first = u.c_first, c_last = u.c_last;
+            // where row r of the unit is among the outputs; -1: nowhere
+            auto out_row = [&](int r) -> int64_t {
+                if constexpr (JOINED) {
+                    const int t = u.row + r / g.G, p = P.positions[t];
+                    if (p < 0 || p >= g.max_ctx) return -1;
+                    return (int64_t)t * g.Hq + (int64_t)u.hk * g.G + r % g.G;
+                }
+                return (int64_t)u.row * g.Hq + (int64_t)u.hk * g.G + r;
+            };
             const int part = c_first == c_last ? -1 : 2 * cta + (cta == c_first ? 1 : 0);
 #pragma unroll
             for (int r0 = 0; r0 < Cfg::kRows; r0 += MR) {
-                if (r0 >= g.G) break;
+                if (r0 >= R) break;
                 const int nt = r0 / 8;
                 float* mw = merge + warp * Cfg::kMergeWarp;
                 // rows r0 .. r0 + 3 are with the lanes whose pairs are these columns
@@ -488,7 +759,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 __syncthreads();
                 // a warp a row
                 static_assert(MR == W, "a warp a row");
-                if (r0 + warp < g.G) {
+                if (r0 + warp < R) {
                     const int mr = warp, r = r0 + warp;
                     constexpr int DPL = D / 32;
                     float M = kUnseen;
@@ -515,13 +786,15 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     const float inv = none ? 0.f : 1.f / den;
                     const float ln2 = none ? -INFINITY : (M == kUnseen ? den : (lg2(den) + M) * kLn2);
                     if (part < 0) {
-                        const int64_t row = (int64_t)u.row * g.Hq + (int64_t)u.hk * g.G + r;
-                        __nv_bfloat16* dst = P.out + row * D + lane * DPL;
+                        const int64_t row = out_row(r);
+                        if (row >= 0) {
+                            __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
-                        for (int e = 0; e < DPL; e += 2)
-                            *reinterpret_cast<uint32_t*>(dst + e) =
-                                pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-                        if (P.lse != nullptr && lane == 0) P.lse[row] = ln2;
+                            for (int e = 0; e < DPL; e += 2)
+                                *reinterpret_cast<uint32_t*>(dst + e) =
+                                    pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+                        }
+                        if (P.lse != nullptr && lane == 0 && row >= 0) P.lse[row] = ln2;
                     } else {
                         const int64_t row = (int64_t)part * Cfg::kRows + r;
                         float* dst = P.part_o + row * D + lane * DPL;
@@ -553,7 +826,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 __threadfence();
                 if (last) {
                     constexpr int DPL = D / 32;
-                    for (int r = warp; r < g.G; r += W) {
+                    for (int r = warp; r < R; r += W) {
                         // part c of the unit is in slot 2 c (the first in 2 c + 1); 32
                         // parts' lse at a time, one a lane
                         auto part_row = [&](int c) {
@@ -597,13 +870,15 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         }
                         const bool none = den == 0.f;
                         const float inv = none ? 0.f : 1.f / den;
-                        const int64_t row = (int64_t)u.row * g.Hq + (int64_t)u.hk * g.G + r;
-                        __nv_bfloat16* dst = P.out + row * D + lane * DPL;
+                        const int64_t row = out_row(r);
+                        if (row >= 0) {
+                            __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
-                        for (int e = 0; e < DPL; e += 2)
-                            *reinterpret_cast<uint32_t*>(dst + e) =
-                                pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-                        if (P.lse != nullptr && lane == 0)
+                            for (int e = 0; e < DPL; e += 2)
+                                *reinterpret_cast<uint32_t*>(dst + e) =
+                                    pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+                        }
+                        if (P.lse != nullptr && lane == 0 && row >= 0)
                             P.lse[row] = none ? -INFINITY : M + lg2(den) * kLn2;
                     }
                 }
@@ -616,37 +891,51 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     cp_async_wait<0>();
 }
 
-template <int D, int NT>
+template <int D, int NT, bool JOINED>
 cudaError_t launch(const SelectedParams& P, int grid, cudaStream_t stream) {
     using Cfg = SelCfg<D, NT>;
-    const cudaError_t e = allow_smem<decode_selected_kernel<D, NT>>(Cfg::kSmem);
+    const cudaError_t e = allow_smem<decode_selected_kernel<D, NT, JOINED>>(Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(decode_selected_kernel<D, NT>, dim3(grid), dim3(Cfg::kThreads),
+    return launch_dependent(decode_selected_kernel<D, NT, JOINED>, dim3(grid), dim3(Cfg::kThreads),
                             Cfg::kSmem, stream, P);
 }
 
 }  // namespace
 
-// Row tiles (of 8) that are built: what holds a group of `heads`, -1 if none.
-int selected_row_tiles(int D, int heads) {
-    if (heads > (D == 128 ? 32 : 64)) return -1;
-    return heads <= 8 ? 1 : heads <= 16 ? 2 : heads <= 32 ? 4 : 8;
+// Rows of a sequence that a unit takes, for groups of `heads` and at most max_q_len rows a
+// sequence.
+int selected_rows(int heads, int max_q_len) {
+    return std::max(1, std::min({kMostRows, max_q_len, 32 / heads}));
+}
+// Row tiles (of 8) that are built: what holds `rows` query rows, -1 if none.
+int selected_row_tiles(int D, int rows) {
+    if (rows > (D == 128 ? 32 : 64)) return -1;
+    return rows <= 32 ? (rows + 7) / 8 : 8;
 }
 int selected_ctas_per_sm() { return SelCfg<128, 1>::kCtas; }
 
-cudaError_t launch_decode_selected(const SelectedParams& P, int nt, int grid, cudaStream_t stream) {
+cudaError_t launch_decode_selected(const SelectedParams& P, int rows, int nt, int grid,
+                                   cudaStream_t stream) {
+    if (rows > 1) {
+        const cudaError_t e = launch_dependent(join_lists_kernel, dim3(P.g.total_q),
+                                               dim3(32 * kJoinWarps), 0, stream, P, rows);
+        if (e != cudaSuccess) return e;
+    }
+    const bool joined = rows > 1;
     if (P.g.D == 128) {
         switch (nt) {
-            case 1: return launch<128, 1>(P, grid, stream);
-            case 2: return launch<128, 2>(P, grid, stream);
-            case 4: return launch<128, 4>(P, grid, stream);
+            case 1: return joined ? launch<128, 1, true>(P, grid, stream) : launch<128, 1, false>(P, grid, stream);
+            case 2: return joined ? launch<128, 2, true>(P, grid, stream) : launch<128, 2, false>(P, grid, stream);
+            case 3: return joined ? launch<128, 3, true>(P, grid, stream) : launch<128, 3, false>(P, grid, stream);
+            case 4: return joined ? launch<128, 4, true>(P, grid, stream) : launch<128, 4, false>(P, grid, stream);
         }
     } else {
         switch (nt) {
-            case 1: return launch<64, 1>(P, grid, stream);
-            case 2: return launch<64, 2>(P, grid, stream);
-            case 4: return launch<64, 4>(P, grid, stream);
-            case 8: return launch<64, 8>(P, grid, stream);
+            case 1: return joined ? launch<64, 1, true>(P, grid, stream) : launch<64, 1, false>(P, grid, stream);
+            case 2: return joined ? launch<64, 2, true>(P, grid, stream) : launch<64, 2, false>(P, grid, stream);
+            case 3: return joined ? launch<64, 3, true>(P, grid, stream) : launch<64, 3, false>(P, grid, stream);
+            case 4: return joined ? launch<64, 4, true>(P, grid, stream) : launch<64, 4, false>(P, grid, stream);
+            case 8: return launch<64, 8, false>(P, grid, stream);
         }
     }
     return cudaErrorInvalidValue;

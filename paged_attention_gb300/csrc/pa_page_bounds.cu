@@ -2,11 +2,11 @@
 // key, rounded outward to 8 bits of a power of two.
 //
 // A row of the call is its page's last where the next row's slot lies in another
-// page; it stands for the page.  A CTA looks through some rows for one head, its
-// warps share the pages it finds, and a warp reads a page's rows once, 16 bytes a
-// lane, many rows under way; maxima and minima are taken of bf16 pairs, exactly.
-// Bound by HBM (2 D bytes a key) where pages are whole, by latency on a decode step,
-// which reads one page a sequence and head.
+// page; it stands for the page.  A CTA looks through some rows for one head and takes
+// the pages it finds one after the other, all its warps on a page: every row of it is
+// read once, 16 bytes a lane, all of a page of 64 under way at a time; maxima and
+// minima are taken of bf16 pairs, exactly.  Bound by HBM (2 D bytes a key) where pages
+// are whole, by latency on a decode step, which reads one page a sequence and head.
 #include <algorithm>
 
 #include "pa_cache_common.cuh"
@@ -15,7 +15,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
@@ -39,11 +39,12 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
               float* __restrict__ scale, int32_t* err, int rows) {
     constexpr int C = D / 8;             // 16-byte pieces of a row
     constexpr int RPI = 32 / C;          // rows of a warp's load
-    constexpr int U = 16;                // loads under way
+    constexpr int U = 8;                 // loads of a lane under way
+    __shared__ uint4 s_part[2][kWarps][2][C];        // a warp's largest and smallest
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = blockIdx.y;
     grid_dependency_wait();
     const int r0 = blockIdx.x * rows, r1 = min(r0 + rows, g.total_q);
-    int found = 0;                       // pages before the chunk
+    int turn = 0;                        // (s_part of one page is read while the next fills the other)
     for (int c = r0; c < r1; c += 32) {
         const int r = c + lane;
         const int slot = r < r1 ? slots[r] : -1;
@@ -51,12 +52,10 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
         // (a next slot that is negative shifts to a negative page: another one)
         bool last = slot >= 0 && (slot >> g.ps_shift) != (next >> g.ps_shift);
         const bool none = slot < -1 || (slot >= 0 && (slot >> g.ps_shift) >= g.num_pages);
-        if (none && hk == 0) flag_error(err, PA_DEV_BAD_PAGE);
+        if (none && hk == 0 && warp == 0) flag_error(err, PA_DEV_BAD_PAGE);
         last = last && !none;
-        uint32_t mine = __ballot_sync(0xffffffffu, last);
-        for (; mine != 0; mine &= mine - 1, ++found) {
-            if (found % kWarps != warp) continue;
-            const int at = __shfl_sync(0xffffffffu, slot, __ffs(mine) - 1);
+        for (uint32_t found = __ballot_sync(0xffffffffu, last); found != 0; found &= found - 1) {
+            const int at = __shfl_sync(0xffffffffu, slot, __ffs(found) - 1);
             const int page = at >> g.ps_shift, used = (at & (g.ps - 1)) + 1;
             const uint4* src = reinterpret_cast<const uint4*>(k) + row_of(g, page, 0, hk) * C;
             uint32_t hi[4], lo[4];
@@ -65,17 +64,19 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
                 hi[i] = 0xff80ff80u;     // -inf
                 lo[i] = 0x7f807f80u;
             }
-            for (int s = 0; s < used; s += U * RPI) {
+            const int k0 = warp * RPI + lane / C;
+            for (int s = 0; s < used; s += U * kWarps * RPI) {
                 uint4 x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     // (behind the last key: that key again)
-                    const int key = min(s + u * RPI + lane / C, used - 1);
-                    if (s + u * RPI < used) x[u] = __ldg(src + (int64_t)key * g.tok_rows * C + lane % C);
+                    const int key = min(s + u * kWarps * RPI + k0, used - 1);
+                    if (s + u * kWarps * RPI < used)
+                        x[u] = __ldg(src + (int64_t)key * g.tok_rows * C + lane % C);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (s + u * RPI < used) {
+                    if (s + u * kWarps * RPI < used) {
                         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -91,6 +92,26 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
                     hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
                     lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
                 }
+            if (lane < C) {
+                s_part[turn][warp][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                s_part[turn][warp][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            __syncthreads();
+            const int now = turn;
+            turn ^= 1;
+            if (warp != 0) continue;     // on to the next page
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const uint4 h = s_part[now][w][0][lane % C], l = s_part[now][w][1][lane % C];
+                hi[0] = max_bf16x2(hi[0], h.x);
+                hi[1] = max_bf16x2(hi[1], h.y);
+                hi[2] = max_bf16x2(hi[2], h.z);
+                hi[3] = max_bf16x2(hi[3], h.w);
+                lo[0] = min_bf16x2(lo[0], l.x);
+                lo[1] = min_bf16x2(lo[1], l.y);
+                lo[2] = min_bf16x2(lo[2], l.z);
+                lo[3] = min_bf16x2(lo[3], l.w);
+            }
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -124,12 +145,11 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
 }  // namespace
 
 cudaError_t launch_page_bounds(const CacheGeom& g, const void* k, const int32_t* slots,
-                               int8_t* bounds, float* scale, int32_t* err, int sms,
+                               int8_t* bounds, float* scale, int32_t* err,
                                cudaStream_t stream) {
-    // rows of a CTA: one a warp for a decode step; for prompts, most of whose rows are
-    // not their page's last, a page a warp
-    const int64_t spread = ((int64_t)g.total_q * g.Hkv + sms * 16 - 1) / (sms * 16);
-    const int rows = (int)std::max<int64_t>(kWarps, std::min<int64_t>(spread, kWarps * g.ps));
+    // rows of a CTA: a sequence's new ones, which lie in a page or two, up to two pages
+    // (most rows of a prompt are not their page's last)
+    const int rows = std::max(1, std::min(g.max_q_len, 2 * g.ps));
     const dim3 grid((g.total_q + rows - 1) / rows, g.Hkv);
     auto kern = g.D == 128 ? bounds_kernel<128> : bounds_kernel<64>;
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, g, (const __nv_bfloat16*)k,

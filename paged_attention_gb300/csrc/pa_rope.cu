@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCtas = 4;                 // of an SM
-constexpr int kMaxTokens = 32;           // of a CTA
+constexpr int kMaxTokens = 4;            // of a CTA
 
 // Two bf16 pairs (x0 y0, ...) turned; cs: (cos, sin) of each pair.
 __device__ __forceinline__ void turn(float x, float y, float2 cs, float& u, float& w) {

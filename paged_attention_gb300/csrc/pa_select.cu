@@ -1,49 +1,41 @@
 // pa_select.cu -- for every row and KV head, the pages with the highest bound on
 // a logit.
 //
-//   score = 2^e_page max_h 2^e_h sum_d max(q8 hi, q8 lo)
+//   score = 2^e_page max_h 2^e_h sum_d (q8 > 0 ? q8 hi : q8 lo)
 //         = 2^e_page max_h 2^e_h [max(q8, 0), min(q8, 0)] . [hi, lo]
 //
-// so a group's scores are products of 8-bit matrices: 16 pages by 8 heads a
-// product (mma m16n8k32, 32-bit whole sums: exact, in any order).  The contraction's
-// order being free, a lane takes 16 bytes of a page's bounds as they lie.
+// so a group's scores are products of whole-number matrices: 16 pages by 8 heads a
+// product.  They are taken in f16 (mma m16n8k16, fp32 sums), whose rate is ten times
+// that of 8-bit integers here (64 rows of up to 459 pages: 11.2 us with those).  A code
+// c becomes the f16 1152 + c by one permutation of bytes a pair; 64 codes a sum stay
+// below 2^24, so every sum is exact, and 1152 times the sum of q8 is taken off it.  The
+// contraction's order being free, a lane takes 16 bytes of a page's bounds as they lie.
 //
-// One cluster of CTAs a row and KV head, each with a part of the pages: scores
-// stay in shared memory as order-preserving integers, the budget-th largest is
-// found by a radix select, eight bits a pass, whose histograms the CTAs add up
-// through distributed shared memory, and every CTA lists its part in order.  As many
-// CTAs a cluster as it takes to fill the GPU.  Bound by HBM (2 D bytes a page and
-// head) for many rows or long contexts, else by the latency of the passes.
+// One cluster of CTAs a row and KV head, each scoring a part of the pages; the scores go,
+// as order-preserving integers, to the first CTA's shared memory, which finds the
+// budget-th largest by a radix select over the bits in which they differ, eight a pass,
+// until a pass decides all, and lists the pages in order.  As many CTAs a cluster as it
+// takes to fill the GPU.  Bound by the latency of its steps (row, page numbers, bounds,
+// two or three passes), by HBM (2 D bytes a page and head) for many rows of long contexts.
 #include <algorithm>
 
+#include "pa_cache_mma.cuh"
 #include "pa_step_common.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr float kBias = 1152.f;  // of a code's f16
 constexpr int kMaxGroup = 64;    // q heads of a KV head
 constexpr int kBins = 256;
-static_assert(kBins == kThreads, "a thread a bin");
+constexpr int kTile = 32;        // pages of a warp at a time: two products' rows, all their loads under way
 
-// D = A * B of 8-bit whole numbers, + D
-__device__ __forceinline__ void mma_s8_16832(int* d, uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+constexpr uint32_t kKept = 0xffffffffu;      // key of a page that is kept whatever its score
 
-__device__ __forceinline__ int ld_dsm_s32(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
+// A query row in shared memory: 2 D f16, and padding (lanes of a 16-byte load meet few banks twice)
+constexpr int q_row_bytes(int D) { return 4 * D + 16; }
 
 // Larger scores (never NaN) get larger keys, all above 0.
 __device__ __forceinline__ uint32_t key_of(float score) {
@@ -51,35 +43,47 @@ __device__ __forceinline__ uint32_t key_of(float score) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Codes of a query row's words (two elements each) with 2^-e as factor.
-__device__ __forceinline__ uint32_t q_codes(uint32_t w0, uint32_t w1, float inv) {
-    uint32_t out = 0;
+// The codes of four elements (two words) of a query row, with 2^-e as factor.
+__device__ __forceinline__ void q_codes(uint32_t w0, uint32_t w1, float inv, float* c) {
     const float x[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
                         __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = x[i] == x[i] ? fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f) : 0.f;
-        out |= (uint32_t)((int)y & 255) << (8 * i);
-    }
-    return out;
+    for (int i = 0; i < 4; ++i)
+        c[i] = x[i] == x[i] ? fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f) : 0.f;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams P) {
+// Four codes as f16 pairs, kBias above their values.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;          // 128 above
+    lo = prmt(u, 0x64646464u, 0x4140u);          // 0x6400 is 1024
+    hi = prmt(u, 0x64646464u, 0x4342u);
+}
+
+__device__ __forceinline__ void st_dsm_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
+select_kernel(const __grid_constant__ SelectParams P) {
+    constexpr int kWarps = kThreads / 32;
+    static_assert(kThreads >= kBins, "a thread a bin");
     constexpr int J = 2 * D / 64;                // 64-byte runs of a page's bounds
-    constexpr int kQRow = 2 * D + 64;            // 8 lanes' 16 bytes (two rows) meet no bank twice
-    extern __shared__ uint32_t s_key[];          // of the CTA's pages
-    __shared__ __align__(16) uint8_t s_q[kMaxGroup * kQRow];
+    constexpr int RT = kTile / 8;                // page rows of a lane
+    constexpr int kQRow = q_row_bytes(D);
+    extern __shared__ __align__(16) uint8_t smem[];      // queries; the cluster's keys
     __shared__ float s_factor[kMaxGroup];
-    __shared__ uint32_t s_hist[4][kBins];        // of each pass
-    __shared__ int s_count[2];                   // keys above, and at, the threshold
-    __shared__ uint32_t s_warp[kWarps];
+    __shared__ float s_bias[kMaxGroup][J];       // what the bias of the codes adds to a run's sum
+    __shared__ __align__(16) uint32_t s_hist[4][kBins];  // of each pass
+    __shared__ uint2 s_range[kWarps];
     __shared__ int2 s_part[kWarps];
-    __shared__ uint32_t s_digit, s_left;
     const CacheGeom& g = P.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, t4 = lane & 3;
     const int C = P.cluster, rank = blockIdx.x % C, unit = blockIdx.x / C;
     const int t = unit / g.Hkv, hk = unit % g.Hkv;
+    const int tiles = (g.G + 7) / 8;
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(smem + 8 * tiles * kQRow);
     grid_dependency_wait();
 
     // (the cluster's CTAs leave together: they all look at the same row)
@@ -98,8 +102,33 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         return;
     }
 
-    // ---- the group's queries in 8 bits, positive and negative parts
-    const int tiles = (g.G + 7) / 8;
+    // ---- the CTA's pages [lo, lo + m); a warp has kTile at a time, whose bounds are under
+    // way while the queries are made ready
+    const int part = (n + C - 1) / C, lo = min(n, rank * part), m = min(part, n - lo);
+    const int32_t* row = P.table + (int64_t)b * g.mpps + first + lo;
+    bool none = false;
+    uint4 a[RT][J];
+    float sc[RT];
+    auto load_tile = [&](int i0, int page) {
+        none |= i0 + lane < m && (uint32_t)page >= (uint32_t)g.num_pages;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int p = __shfl_sync(0xffffffffu, page, gr + 8 * r);
+            const bool ok = (uint32_t)p < (uint32_t)g.num_pages;
+            const int64_t at = (int64_t)(ok ? p : 0) * g.Hkv + hk;
+            const uint4* src = reinterpret_cast<const uint4*>(P.bounds + at * 2 * D) + t4;
+#pragma unroll
+            for (int j = 0; j < J; ++j) a[r][j] = __ldg(src + 4 * j);
+            sc[r] = ok ? P.scale[at] : -1.f;     // (no page has a negative scale)
+        }
+    };
+    auto page_of = [&](int i0) -> int { return i0 < m ? row[min(i0 + lane, m - 1)] : 0; };
+    int i0 = kTile * warp;
+    const int page0 = page_of(i0);
+    int page1 = page_of(i0 + kTile * kWarps);
+    if (i0 < m) load_tile(i0, page0);
+
+    // ---- the group's queries in 8 bits, as f16: positive, then negative parts
     for (int h = warp; h < 8 * tiles; h += kWarps) {
         uint32_t w[D / 64];
         uint32_t top = 0;
@@ -110,192 +139,252 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
                 P.q + ((int64_t)t * g.Hq + (int64_t)hk * g.G + h) * D);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-                // (D = 64: a lane has a word, its neighbour the rest of its four codes)
                 w[i] = src[lane * (D / 64) + i];
                 const uint32_t x = w[i] & 0x7fffu, y = (w[i] >> 16) & 0x7fffu;
                 top = max(top, max(x > 0x7f80u ? 0u : x, y > 0x7f80u ? 0u : y));   // NaN: none
             }
         }
-        const uint32_t m = __reduce_max_sync(0xffffffffu, top);
-        // least e with m <= 127 * 2^e = 1.984375 * 2^(e + 6)
-        const int e = max(-50, min(50, (int)(m >> 7) - 133 + ((m & 127u) == 127u ? 1 : 0)));
+        const uint32_t most = __reduce_max_sync(0xffffffffu, top);
+        // least e with most <= 127 * 2^e = 1.984375 * 2^(e + 6)
+        const int e = max(-50, min(50, (int)(most >> 7) - 133 + ((most & 127u) == 127u ? 1 : 0)));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint32_t w0, w1;
         if constexpr (D == 128) {
             w0 = w[0];
             w1 = w[1];
         } else {
+            // (a lane has a word, its neighbour the rest of its four codes)
             w0 = __shfl_sync(0xffffffffu, w[0], 2 * (lane & 15));
             w1 = __shfl_sync(0xffffffffu, w[0], 2 * (lane & 15) + 1);
         }
-        const uint32_t code = q_codes(w0, w1, inv);
+        float c[4];
+        q_codes(w0, w1, inv, c);
+        float up = 0.f, down = 0.f;              // sums over a run: 16 lanes' codes
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            up += fmaxf(c[i], 0.f);
+            down += fminf(c[i], 0.f);
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            up += __shfl_xor_sync(0xffffffffu, up, o);
+            down += __shfl_xor_sync(0xffffffffu, down, o);
+        }
         if (D == 128 || lane < 16) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(s_q + h * kQRow);
-            dst[lane] = __vmaxs4(code, 0u);
-            dst[D / 4 + lane] = __vmins4(code, 0u);
+            uint2* dst = reinterpret_cast<uint2*>(smem + h * kQRow);
+            dst[lane] = make_uint2(pack_f16x2(fmaxf(c[0], 0.f), fmaxf(c[1], 0.f)),
+                                   pack_f16x2(fmaxf(c[2], 0.f), fmaxf(c[3], 0.f)));
+            dst[D / 4 + lane] = make_uint2(pack_f16x2(fminf(c[0], 0.f), fminf(c[1], 0.f)),
+                                           pack_f16x2(fminf(c[2], 0.f), fminf(c[3], 0.f)));
+            if (lane % 16 == 0) {
+                s_bias[h][lane / 16] = kBias * up;
+                s_bias[h][J / 2 + lane / 16] = kBias * down;
+            }
         }
         if (lane == 0) s_factor[h] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
     for (int i = tid; i < 4 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
-    __syncthreads();
+    // (a cluster's first CTA must have begun before the others write to it)
+    __syncwarp();
+    if (C > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
 
-    // ---- scores of the CTA's pages [lo, lo + m)
-    const int part = (n + C - 1) / C, lo = min(n, rank * part), m = min(part, n - lo);
-    const int32_t* row = P.table + (int64_t)b * g.mpps + first + lo;
-    const int gr = lane >> 2, t4 = lane & 3;
-    bool none = false;
-    for (int i0 = 16 * warp; i0 < m; i0 += 16 * kWarps) {
-        int64_t at[2];
-        float sc[2];
-        bool ok[2];
-        uint4 a[2][J];
+    // ---- scores
+    const uint32_t keys = C > 1 ? mapa_shared(smem_u32(s_key), 0) : smem_u32(s_key);
+#pragma unroll 1
+    for (; i0 < m; i0 += kTile * kWarps) {
+        float best[RT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = i0 + gr + 8 * r;
-            const int page = row[min(i, m - 1)];
-            ok[r] = (uint32_t)page < (uint32_t)g.num_pages;
-            none |= !ok[r] && i < m;
-            at[r] = (int64_t)(ok[r] ? page : 0) * g.Hkv + hk;
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            sc[r] = P.scale[at[r]];
-            const uint4* src = reinterpret_cast<const uint4*>(P.bounds + at[r] * 2 * D) + t4;
-#pragma unroll
-            for (int j = 0; j < J; ++j) a[r][j] = __ldg(src + 4 * j);
-        }
-        float best[2] = {-INFINITY, -INFINITY};
+        for (int r = 0; r < RT; ++r) best[r] = -INFINITY;
         for (int nt = 0; nt < tiles; ++nt) {
-            int d[4] = {0, 0, 0, 0};
-            const uint8_t* qr = s_q + (8 * nt + gr) * kQRow + 16 * t4;
+            float sum[RT / 2][4];
+#pragma unroll
+            for (int r = 0; r < RT / 2; ++r) sum[r][0] = sum[r][1] = sum[r][2] = sum[r][3] = 0.f;
+            const uint8_t* qr = smem + (8 * nt + gr) * kQRow + 32 * t4;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const uint4 q = *reinterpret_cast<const uint4*>(qr + 64 * j);
-                mma_s8_16832(d, a[0][j].x, a[1][j].x, a[0][j].y, a[1][j].y, q.x, q.y);
-                mma_s8_16832(d, a[0][j].z, a[1][j].z, a[0][j].w, a[1][j].w, q.z, q.w);
+                const uint4 q0 = *reinterpret_cast<const uint4*>(qr + 128 * j);
+                const uint4 q1 = *reinterpret_cast<const uint4*>(qr + 128 * j + 16);
+                const float b0 = s_bias[8 * nt + 2 * t4][j], b1 = s_bias[8 * nt + 2 * t4 + 1][j];
+#pragma unroll
+                for (int r = 0; r < RT / 2; ++r) {
+                    const uint4 x = a[2 * r][j], y = a[2 * r + 1][j];
+                    float d[4];
+                    uint32_t f[4];
+                    codes_to_f16(x.x, f[0], f[2]);
+                    codes_to_f16(y.x, f[1], f[3]);
+                    mma_f16_first(d, f, q0.x, q0.y);
+                    codes_to_f16(x.y, f[0], f[2]);
+                    codes_to_f16(y.y, f[1], f[3]);
+                    mma_f16_16816(d, f, q0.z, q0.w);
+                    codes_to_f16(x.z, f[0], f[2]);
+                    codes_to_f16(y.z, f[1], f[3]);
+                    mma_f16_16816(d, f, q1.x, q1.y);
+                    codes_to_f16(x.w, f[0], f[2]);
+                    codes_to_f16(y.w, f[1], f[3]);
+                    mma_f16_16816(d, f, q1.z, q1.w);
+                    sum[r][0] += d[0] - b0;
+                    sum[r][1] += d[1] - b1;
+                    sum[r][2] += d[2] - b0;
+                    sum[r][3] += d[3] - b1;
+                }
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int h = 8 * nt + 2 * t4 + (x & 1);
-                if (h < g.G) best[x >> 1] = fmaxf(best[x >> 1], (float)d[x] * s_factor[h]);
+            for (int x = 0; x < 2; ++x) {
+                const int h = 8 * nt + 2 * t4 + x;
+                const float f = s_factor[h];
+                if (h < g.G)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        best[r] = fmaxf(best[r], sum[r / 2][2 * (r & 1) + x] * f);
             }
         }
+        uint32_t key[RT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RT; ++r) {
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-            const int i = i0 + gr + 8 * r;
-            if (t4 == 0 && i < m) {
-                const bool kept = lo + i < P.num_first || lo + i >= n - P.num_recent;
-                s_key[i] = kept ? 0xffffffffu : ok[r] ? key_of(best[r] * sc[r]) : 0u;
-            }
+            const int i = lo + i0 + gr + 8 * r;
+            const bool kept = i < P.num_first || i >= n - P.num_recent;
+            key[r] = kept ? kKept : sc[r] < 0.f ? 0u : key_of(best[r] * sc[r]);
+        }
+        // lane (gr, t4) writes the key of its row t4
+        static_assert(RT == 4, "a row a lane");
+        const uint32_t mine = t4 == 0 ? key[0] : t4 == 1 ? key[1] : t4 == 2 ? key[2] : key[3];
+        const int i = i0 + gr + 8 * t4;
+        if (i < m) st_dsm_u32(keys + 4u * (uint32_t)(lo + i), mine);
+        const int next = i0 + kTile * kWarps;
+        if (next < m) {
+            load_tile(next, page1);
+            page1 = page_of(next + kTile * kWarps);
         }
     }
     if (none) flag_error(P.err, PA_DEV_BAD_PAGE);
-    __syncthreads();
-
-    // ---- the budget-th largest key of the cluster's
-    uint32_t prefix = 0, left = (uint32_t)P.budget;   // rank from the top among equal prefixes
-#pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int i0 = 32 * warp; i0 < m; i0 += kThreads) {
-            const int i = i0 + lane;
-            const uint32_t x = i < m ? s_key[i] : 0u;
-            const bool in = i < m && (pass == 0 || x >> (shift + 8) == prefix);
-            const uint32_t digit = in ? (x >> shift) & 255u : 256u;
-            // (scores crowd into few bins: one addition for all lanes of a bin)
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            if (in && __ffs(same) - 1 == lane) atomicAdd(&s_hist[pass][digit], __popc(same));
-        }
-        uint32_t mine;
-        __syncwarp();
-        if (C > 1) {
-            cluster_sync_all();
-            mine = 0;
-            const uint32_t addr = smem_u32(&s_hist[pass][tid]);
-            for (int c = 0; c < C; ++c) mine += (uint32_t)ld_dsm_s32(mapa_shared(addr, c));
-        } else {
-            __syncthreads();
-            mine = s_hist[pass][tid];
-        }
-        // keys in this bin and above: bins in descending order along the threads' mirror
-        uint32_t sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_down_sync(0xffffffffu, sum, o);
-            if (lane + o < 32) sum += y;
-        }
-        if (lane == 0) s_warp[warp] = sum;
+    __syncwarp();
+    if (C > 1) {
+        cluster_sync_all();
+        if (rank != 0) return;
+    } else {
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w > warp) sum += s_warp[w];
-        if (sum >= left && sum - mine < left) {       // one thread: the bins are ordered
-            s_digit = (uint32_t)tid;
-            s_left = left - (sum - mine);
-        }
-        __syncthreads();
-        prefix = prefix << 8 | s_digit;
-        left = s_left;
     }
-    const uint32_t limit = prefix;                     // `left` of the keys equal to it are kept
 
-    // ---- how many of its keys each CTA lists, and each of its warps
-    const int seg = (m + kThreads - 1) / kThreads * 32;        // of a warp
-    const int w0 = min(m, warp * seg), w1 = min(m, w0 + seg);
-    int above = 0, equal = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t x = i < w1 ? s_key[i] : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, i < w1 && x > limit));
-        equal += __popc(__ballot_sync(0xffffffffu, i < w1 && x == limit));
+    // ---- between which two keys the bits differ
+    uint32_t least = 0xffffffffu, most = 0u;
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t x = s_key[i];
+        if (x != kKept) {
+            least = min(least, x);
+            most = max(most, x);
+        }
     }
-    if (lane == 0) s_part[warp] = make_int2(above, equal);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_range[warp] = make_uint2(least, most);
     __syncthreads();
-    int before_above = 0, before_equal = 0, all_above = 0, all_equal = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) {
-            before_above += s_part[w].x;
-            before_equal += s_part[w].y;
-        }
-        all_above += s_part[w].x;
-        all_equal += s_part[w].y;
+        least = min(least, s_range[w].x);
+        most = max(most, s_range[w].y);
     }
-    if (C > 1) {
-        if (tid == 0) {
-            s_count[0] = all_above;
-            s_count[1] = all_equal;
+    // ---- the keys to list: those from `from` up, and `take` of those equal to `equal`
+    // (the kept ones, above all others, are the first num_first + num_recent)
+    int take = P.budget - P.num_first - P.num_recent;
+    uint32_t from = kKept, equal = 0u;
+    if (take > 0) {
+        int shift = 32 - __clz(least ^ most);    // bits that differ (0: all keys are equal)
+        uint32_t prefix = shift < 32 ? most >> shift : 0u;
+        for (int pass = 0; shift > 0; ++pass) {
+            const int width = min(8, shift);
+            for (int i = tid; i < n; i += kThreads) {
+                const uint32_t x = s_key[i];
+                if (x != kKept && (shift == 32 || x >> shift == prefix))
+                    atomicAdd(&s_hist[pass][(x >> (shift - width)) & ((1u << width) - 1u)], 1u);
+            }
+            __syncthreads();
+            // every warp by itself: a lane has eight bins; in which one is the take-th from
+            // the top?
+            uint32_t h[8], sum = 0;
+            *reinterpret_cast<uint4*>(h) = reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane];
+            *reinterpret_cast<uint4*>(h + 4) =
+                reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane + 1];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) sum += h[d];
+            uint32_t upto = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
+                if (lane + o < 32) upto += y;
+            }
+            uint32_t above = upto - sum, digit = 0, many = 0;
+            const uint32_t has = __ballot_sync(0xffffffffu, upto >= (uint32_t)take &&
+                                                                above < (uint32_t)take);
+#pragma unroll
+            for (int d = 7; d >= 0; --d)
+                if (many == 0) {
+                    if (above + h[d] >= (uint32_t)take) {
+                        digit = 8 * lane + d;
+                        many = h[d];
+                    } else {
+                        above += h[d];
+                    }
+                }
+            const int src = __ffs(has) - 1;
+            digit = __shfl_sync(0xffffffffu, digit, src);
+            many = __shfl_sync(0xffffffffu, many, src);
+            take -= (int)__shfl_sync(0xffffffffu, above, src);
+            prefix = prefix << width | digit;
+            shift -= width;
+            if ((int)many == take) {             // the whole bin
+                from = prefix << shift;
+                take = 0;
+                break;
+            }
         }
-        __syncwarp();
-        cluster_sync_all();
-        for (int c = 0; c < rank; ++c) {
-            before_above += ld_dsm_s32(mapa_shared(smem_u32(&s_count[0]), c));
-            before_equal += ld_dsm_s32(mapa_shared(smem_u32(&s_count[1]), c));
+        if (take > 0) {
+            equal = shift > 0 ? 0u : prefix;     // (no bits differ: prefix is the one key)
+            from = equal + 1;
         }
     }
+
     // ---- list them: a key's place is the number of listed ones before it
-    const int take = (int)left;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
+    const int seg = (n + kThreads - 1) / kThreads * 32;        // of a warp
+    const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    int above = 0, same = 0;
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+        const int i = j0 + lane;
         const uint32_t x = i < w1 ? s_key[i] : 0u;
-        const uint32_t up = __ballot_sync(0xffffffffu, i < w1 && x > limit);
-        const uint32_t eq = __ballot_sync(0xffffffffu, i < w1 && x == limit);
-        const uint32_t below = (1u << lane) - 1u;
-        const int eq_rank = before_equal + __popc(eq & below);
-        const int place = before_above + __popc(up & below) + min(take, eq_rank);
-        if ((up >> lane & 1u) || ((eq >> lane & 1u) && eq_rank < take)) out[place] = first + lo + i;
-        before_above += __popc(up);
-        before_equal += __popc(eq);
+        above += __popc(__ballot_sync(0xffffffffu, i < w1 && x >= from));
+        same += __popc(__ballot_sync(0xffffffffu, i < w1 && x == equal && x < from));
     }
-    __syncwarp();
-    if (C > 1) cluster_sync_all();                     // nobody leaves while it is read
+    if (lane == 0) s_part[warp] = make_int2(above, same);
+    __syncthreads();
+    above = same = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (w < warp) {
+            above += s_part[w].x;
+            same += s_part[w].y;
+        }
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+        const int i = j0 + lane;
+        const uint32_t x = i < w1 ? s_key[i] : 0u;
+        const uint32_t up = __ballot_sync(0xffffffffu, i < w1 && x >= from);
+        const uint32_t eq = __ballot_sync(0xffffffffu, i < w1 && x == equal && x < from);
+        const uint32_t below = (1u << lane) - 1u;
+        const int rank_eq = same + __popc(eq & below);
+        const int place = above + __popc(up & below) + min(take, rank_eq);
+        if ((up >> lane & 1u) || ((eq >> lane & 1u) && rank_eq < take)) out[place] = first + i;
+        above += __popc(up);
+        same += __popc(eq);
+    }
 }
 
-template <int D>
-cudaError_t launch(const SelectParams& P, int smem, int most, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<select_kernel<D>>(most);
+template <int D, int kThreads>
+cudaError_t launch(const SelectParams& P, int smem, cudaStream_t stream) {
+    const cudaError_t e = allow_smem<select_kernel<D, kThreads>>(
+        kMaxGroup * q_row_bytes(D) + PA_MAX_SELECT_PAGES * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(P.g.total_q * P.g.Hkv * P.cluster));
@@ -311,26 +400,24 @@ cudaError_t launch(const SelectParams& P, int smem, int most, cudaStream_t strea
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = P.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, P);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, kThreads>, P);
 }
 
 }  // namespace
 
-// Pages of a context that a cluster's shared memory has room for.
-static_assert(PA_MAX_SELECT_PAGES <= kMaxCluster * 32768, "keys of a CTA");
-
 cudaError_t launch_select(const SelectParams& P0, int sms, cudaStream_t stream) {
     SelectParams P = P0;
     const int pages = (int)(((int64_t)P.g.max_ctx + P.g.ps - 1) >> P.g.ps_shift);
-    // CTAs of a cluster: until the GPU has two an SM, none with under 64 pages; a part's keys
-    // must fit
+    // CTAs of a cluster: until the GPU has two an SM, none with under 64 pages
     int c = 1;
     const int64_t units = (int64_t)P.g.total_q * P.g.Hkv;
-    while (c < kMaxCluster && ((units * c < 2 * sms && pages >= 128 * c) || pages > 32768 * c)) c *= 2;
+    while (c < kMaxCluster && units * c < 2 * sms && pages >= 128 * c) c *= 2;
     P.cluster = c;
-    const int smem = ((pages + c - 1) / c) * 4;
-    return P.g.D == 128 ? launch<128>(P, smem, 32768 * 4, stream)
-                        : launch<64>(P, smem, 32768 * 4, stream);
+    const int smem = (P.g.G + 7) / 8 * 8 * q_row_bytes(P.g.D) + pages * 4;
+    // (more threads where a CTA scores or selects from many)
+    if (pages > 1024)
+        return P.g.D == 128 ? launch<128, 512>(P, smem, stream) : launch<64, 512>(P, smem, stream);
+    return P.g.D == 128 ? launch<128, 256>(P, smem, stream) : launch<64, 256>(P, smem, stream);
 }
 
 }  // namespace pa

@@ -32,17 +32,21 @@ bool slots_fit(const CacheGeom& g) { return (int64_t)g.num_pages * g.ps <= 0x7ff
 
 // Workspace of pa_decode_selected: header (error word) and the counters of as many
 // CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +
-// 1 floats.
+// 1 floats; where several rows of a sequence may be one unit, the units and their
+// joined lists.
 struct SelLayout {
     int grid, nt, unit_cost;
-    int64_t off_done, off_part, rows, total;
+    int together;        // rows of a sequence in a unit, at most
+    int64_t off_done, off_part, rows, off_lead, off_entries, off_list, total;
 };
 pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& L) {
     const pa_status st = geometry(pp, false, g);
     if (st != PA_OK) return st;
     if (budget < 1) return PA_ERR_INVALID_ARG;
     if (pp->kv_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-    L.nt = selected_row_tiles(g.D, g.G);
+    if (g.G > (g.D == 128 ? 32 : 64)) return PA_ERR_UNSUPPORTED;
+    L.together = selected_rows(g.G, g.max_q_len);
+    L.nt = selected_row_tiles(g.D, g.G * L.together);
     if (L.nt < 0 || pp->num_ctas > kMaxGridSel) return PA_ERR_UNSUPPORTED;
     if ((int64_t)g.total_q * g.Hkv > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     L.grid = pp->num_ctas;
@@ -56,7 +60,14 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
     L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * 4);
-    L.total = align256(L.off_part + 2 * (int64_t)L.grid * L.rows * (g.D + 1) * 4);
+    L.off_lead = align256(L.off_part + 2 * (int64_t)L.grid * L.rows * (g.D + 1) * 4);
+    L.off_entries = L.off_list = L.total = L.off_lead;
+    if (L.together > 1) {
+        const int64_t units = (int64_t)g.total_q * g.Hkv;
+        L.off_entries = align256(L.off_lead + (int64_t)g.total_q * 8);
+        L.off_list = align256(L.off_entries + units * 4);
+        L.total = align256(L.off_list + units * budget * 8);
+    }
     return PA_OK;
 }
 
@@ -234,9 +245,7 @@ pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache, const i
     if (!k_cache || !aligned(k_cache, 16) || !ints_ok(slots) || !bounds || !aligned(bounds, 16) ||
         !bound_scale || !aligned(bound_scale, 4) || !aligned(device_error, 4))
         return PA_ERR_INVALID_ARG;
-    const int sms = sm_count();
-    if (sms <= 0) return PA_ERR_CUDA;
-    return status_of(launch_page_bounds(g, k_cache, slots, bounds, bound_scale, device_error, sms,
+    return status_of(launch_page_bounds(g, k_cache, slots, bounds, bound_scale, device_error,
                                         (cudaStream_t)stream));
 }
 
@@ -317,7 +326,11 @@ pa_status pa_decode_selected(const pa_problem* problem, int32_t budget, const vo
     P.out = (__nv_bfloat16*)out;
     P.lse = lse;
     P.unit_cost = L.unit_cost;
-    return status_of(launch_decode_selected(P, L.nt, L.grid, (cudaStream_t)stream));
+    P.row_lead = reinterpret_cast<int32_t*>(base + L.off_lead);
+    P.row_tiles = P.row_lead + g.total_q;
+    P.unit_entries = reinterpret_cast<int32_t*>(base + L.off_entries);
+    P.list = reinterpret_cast<int2*>(base + L.off_list);
+    return status_of(launch_decode_selected(P, L.together, L.nt, L.grid, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -57,6 +57,12 @@ struct SelectedParams {
     __nv_bfloat16* out;
     float* lse;
     int32_t unit_cost;   // fixed cost of a unit, in tiles
+    // rows of a sequence joined to units: per row, how many it leads (0: none) and its
+    // units' tiles; per row and KV head, the entries of the joined list; and the lists
+    int32_t* row_lead;
+    int32_t* row_tiles;
+    int32_t* unit_entries;
+    int2* list;          // page number, index in the sequence and rows
 };
 
 cudaError_t launch_pages_take(const CacheGeom& g, const int32_t* seq_lens, const int32_t* q_lens,
@@ -70,11 +76,13 @@ cudaError_t launch_pages_return(const CacheGeom& g, const int32_t* seq_lens,
                                 int32_t* err, int sms, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& P, bool mx4, int sms, cudaStream_t stream);
 cudaError_t launch_page_bounds(const CacheGeom& g, const void* k, const int32_t* slots,
-                               int8_t* bounds, float* scale, int32_t* err, int sms,
+                               int8_t* bounds, float* scale, int32_t* err,
                                cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& P, int sms, cudaStream_t stream);
-int selected_row_tiles(int D, int heads);
+int selected_rows(int heads, int max_q_len);
+int selected_row_tiles(int D, int rows);
 int selected_ctas_per_sm();
-cudaError_t launch_decode_selected(const SelectedParams& P, int nt, int grid, cudaStream_t stream);
+cudaError_t launch_decode_selected(const SelectedParams& P, int rows, int nt, int grid,
+                                   cudaStream_t stream);
 
 }  // namespace pa

@@ -129,7 +129,8 @@ def select(q, bnd, scale, table_row, pos, *, budget, num_first, num_recent, page
             score.append(-math.inf)
             continue
         hi, lo = bnd[pg].double()
-        score.append(max(p * float(torch.maximum(c * hi, c * lo).sum())
+        # (where the largest is no less than the smallest, max(c * hi, c * lo) is the same)
+        score.append(max(p * float((c * torch.where(c > 0, hi, lo)).sum())
                          for c, p in zip(codes, power)) * float(scale[pg]))
     order = sorted(range(n), key=lambda j: (-score[j], j))[:budget]
     return [first + j for j in sorted(order)]

@@ -441,6 +441,35 @@ def test_selection(D, G, Hkv, page, window, budget, first, recent, ctx, ql):
             assert sel[t, h].tolist() == want, (t, h)
 
 
+@pytest.mark.parametrize("D,G,page,n,budget", [(128, 3, 16, 90, 7), (64, 9, 32, 1500, 100),
+                                               (128, 1, 16, 45056, 333)])
+def test_selection_of_the_largest_sums_and_contexts(D, G, page, n, budget):
+    """Codes of +-127 against queries of +-127: the largest whole numbers there are."""
+    g = torch.Generator().manual_seed(n)
+    bnd = torch.where(torch.rand((n, 1, 2, D), generator=g) < 0.5, 127, -127).to(torch.int8)
+    bnd[: n // 2, :, 0], bnd[: n // 3, :, 1] = 127, -127
+    bnd[n // 3:, :, :, 0] = torch.randint(-127, 128, (n - n // 3, 1, 2), generator=g).to(torch.int8)
+    sc = torch.ones((n, 1))
+    q = torch.where(torch.rand((2, G, D), generator=g) < 0.5, 127.0, -127.0).to(BF16)
+    q[1, 0] = 127.0
+    table = torch.randperm(n, generator=g).tolist()
+    p = problem(num_q_heads=G, num_kv_heads=1, head_dim=D, page_size=page, num_pages=n,
+                max_pages_per_seq=n, total_q_tokens=2, max_q_len=2, max_context_len=n * page)
+    sel, err = torch.zeros((2, 1, budget), dtype=torch.int32, device="cuda"), ints([0])
+    B.pa_select_pages(p, budget, 2, 3, q.cuda(), bnd.cuda(), sc.cuda(), ints([table]),
+                      ints([0, 0]), ints([n * page - 1] * 2), sel, err)
+    no_error(err)
+    for t in range(2):
+        b = bnd[torch.tensor(table), 0].double()
+        # (some of these bounds have the smallest above the largest, where the larger of the
+        # two products is not the definition's)
+        c = q[t].double()[:, None]
+        score = (c * torch.where(c > 0, b[None, :, 0], b[None, :, 1])).sum(-1).amax(0)
+        score[:2] = score[-3:] = math.inf
+        want = torch.sort(score, descending=True, stable=True)[1][:budget].sort()[0]
+        assert sel[t, 0].tolist() == want.tolist()
+
+
 def test_selection_of_ties_odd_queries_and_bad_pages():
     D, page, n, budget = 64, 16, 200, 8
     table = list(range(n))
@@ -591,6 +620,71 @@ def test_attention(D, G, Hkv, page, layout, window, budget, ctx, ql, mode, ctas)
                 total_q_tokens=len(seq), max_q_len=max(ql), max_context_len=max(ctx),
                 window=window, num_ctas=ctas, sm_scale=1.0 / math.sqrt(D))
     check_attend(p, budget, table, seq, pos, k, v, q, sel, repeat=2)
+
+
+@pytest.mark.parametrize("ctas", [0, 3])
+@pytest.mark.parametrize("D,G,Hkv,page,layout,window,budget,ctx,ql,mode", [
+    (128, 1, 2, 16, 0, 0, 5, [400, 90, 13], [13, 6, 13], "plain"),
+    (128, 4, 2, 16, 1, 0, 7, [400, 90, 7], [4, 0, 7], "plain"),
+    (128, 7, 1, 32, 0, 100, 6, [700, 65], [4, 3], "holes"),
+    (128, 8, 2, 64, 1, 0, 4, [2000, 70, 300], [3, 3, 2], "shuffled"),
+    (128, 16, 1, 16, 0, 0, 9, [500, 33], [2, 5], "plain"),
+    (64, 2, 3, 16, 0, 17, 2, [300, 40], [9, 9], "plain"),
+    (64, 5, 1, 128, 1, 0, 3, [1500, 130], [6, 4], "plain"),
+    (64, 11, 1, 16, 0, 0, 40, [700, 90], [2, 1], "plain"),
+    (64, 20, 2, 32, 0, 0, 4, [700, 90], [3, 1], "plain"),
+    (64, 1, 1, 16, 0, 0, 50, [70000, 90], [5, 1], "plain"),
+    (128, 3, 2, 16, 0, 0, 5, [100, 20], [3, 2], "none"),
+])
+def test_attention_of_rows_of_one_sequence(D, G, Hkv, page, layout, window, budget, ctx, ql, mode,
+                                           ctas):
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, layout, ctx, ql, 3)
+    sel = lists(seq, pos, Hkv, budget, page, window, 5, mode)
+    for t in range(1, len(seq)):              # rows of a sequence share some of their pages
+        if seq[t] == seq[t - 1] and t % 3:
+            sel[t] = [list(x) for x in sel[t - 1]]
+    listed = {(table[seq[t]][s], h) for t in range(len(seq)) for h in range(Hkv)
+              for s in sel[t][h] if s >= 0}
+    for pg in range(pages):
+        for h in range(Hkv):
+            if (pg, h) not in listed:
+                k[pg, :, h] = v[pg, :, h] = math.nan
+    p = problem(num_seqs=len(ctx), num_q_heads=G * Hkv, num_kv_heads=Hkv, head_dim=D,
+                page_size=page, num_pages=pages, max_pages_per_seq=len(table[0]), layout=layout,
+                total_q_tokens=len(seq), max_q_len=max(ql), max_context_len=max(ctx),
+                window=window, num_ctas=ctas, sm_scale=1.0 / math.sqrt(D))
+    check_attend(p, budget, table, seq, pos, k, v, q, sel, repeat=2)
+
+
+def test_what_one_row_lists_does_not_reach_its_neighbour():
+    """Infinities and NaN in a page that only one of two rows lists, and in the later row's
+    own token."""
+    for D, G, page in ((128, 4, 16), (64, 3, 32), (128, 12, 64)):
+        pages, table, seq, pos, k, v, q = attend_case(D, G, 1, page, 0, [520], [2], 9)
+        n = R.up(520, page)
+        sel = [[[0, 2, 3, n - 1]], [[0, 1, 3, n - 1]]]
+        p = problem(num_q_heads=G, num_kv_heads=1, head_dim=D, page_size=page, num_pages=pages,
+                    max_pages_per_seq=n, total_q_tokens=2, max_q_len=2, max_context_len=520)
+        good, glse = check_attend(p, 4, table, seq, pos, k, v, q, sel)
+        ws = torch.zeros(B.pa_selected_workspace_size(p, 4), dtype=torch.uint8, device="cuda")
+        for value in (math.inf, -math.inf, math.nan):
+            for which in ("k", "v"):
+                for pg, slot, hit in ((table[0][1], 5, 1), (table[0][2], 9, 0),
+                                      (table[0][n - 1], 519 % page, 1)):
+                    k2, v2 = k.clone(), v.clone()
+                    (k2 if which == "k" else v2)[pg, slot, 0, 7] = value
+                    out, lse = torch.zeros_like(good), torch.zeros_like(glse)
+                    B.pa_decode_selected(p, 4, q.cuda(), k2.cuda(), v2.cuda(), ints(table),
+                                         ints(seq), ints(pos), ints(sel), ws, out, lse)
+                    miss = 1 - hit
+                    # (the same sums but for how a step's products are grouped)
+                    assert float((out[miss].float() - good[miss].float()).abs().max()) <= 2e-2
+                    assert float((lse[miss] - glse[miss]).abs().max()) <= 1e-3
+                    if which == "v":
+                        bad = ~torch.isfinite(out[hit])
+                        assert bad[:, 7].all() and not bad[:, :7].any() and not bad[:, 8:].any()
+                    elif value != value:
+                        assert torch.isnan(out[hit]).all()
 
 
 def test_attention_past_bad_entries():
