@@ -469,14 +469,6 @@ def _here(t: torch.Tensor):
         raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
 
 
-def _i32(t: torch.Tensor):
-    """Address of contiguous int32."""
-    if t.dtype is _I32 and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
-                     f"contiguous int32 belongs")
-
-
 def _typed(t: Optional[torch.Tensor], dtype):
     """Address of a contiguous tensor of a type."""
     if t is None:
@@ -487,14 +479,36 @@ def _typed(t: Optional[torch.Tensor], dtype):
                      f"contiguous {dtype} belongs")
 
 
+def _i32(t: torch.Tensor):
+    """Address of contiguous int32."""
+    if t.dtype is _I32 and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
+                     f"contiguous int32 belongs")
+
+
 def pa_pages_take(problem, seq_lens, q_lens, block_table, free_pages, free_count, context_lens,
                   row_seq, positions, slots, free_left, device_error=None, stream=None):
     """Pages for q_lens[b] new tokens of every sequence, and the maps of the step's rows."""
     _here(seq_lens)
+    # (ten tensors: looked at without a call each)
+    if not (seq_lens.dtype is _I32 and q_lens.dtype is _I32 and block_table.dtype is _I32
+            and free_pages.dtype is _I32 and free_count.dtype is _I32
+            and context_lens.dtype is _I32 and row_seq.dtype is _I32
+            and positions.dtype is _I32 and slots.dtype is _I32 and free_left.dtype is _I32
+            and seq_lens.is_contiguous() and q_lens.is_contiguous()
+            and block_table.is_contiguous() and free_pages.is_contiguous()
+            and context_lens.is_contiguous() and row_seq.is_contiguous()
+            and positions.is_contiguous() and slots.is_contiguous()):
+        for t in (seq_lens, q_lens, block_table, free_pages, free_count, context_lens, row_seq,
+                  positions, slots, free_left):
+            _i32(t)
     _check((_lib or load()).pa_pages_take(
-        problem, _i32(seq_lens), _i32(q_lens), _i32(block_table), _i32(free_pages),
-        _i32(free_count), _i32(context_lens), _i32(row_seq), _i32(positions), _i32(slots),
-        _i32(free_left), _typed(device_error, _I32), _stream(stream)), "pa_pages_take")
+        problem, seq_lens.data_ptr(), q_lens.data_ptr(), block_table.data_ptr(),
+        free_pages.data_ptr(), free_count.data_ptr(), context_lens.data_ptr(), row_seq.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), free_left.data_ptr(),
+        None if device_error is None else _typed(device_error, _I32), _stream(stream)),
+        "pa_pages_take")
 
 
 def pa_pages_return(problem, seq_lens, keep_lens, block_table, free_pages, free_count, free_left,
@@ -525,30 +539,32 @@ def pa_rope_steps(inv_freq) -> torch.Tensor:
     return steps
 
 
+def _tokens(t: torch.Tensor, rows: int, heads: int, dim: int) -> int:
+    """Elements between the tokens of rows [tokens, heads, dim] with dense heads."""
+    n, h, d = t.shape
+    by, by_head, by_element = t.stride()
+    if (h == heads and d == dim and n >= rows and by_element == 1
+            and (by_head == dim or h == 1) and t.dtype is _BF16):
+        return by if n > 1 else heads * dim
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
+                     f"bf16 [{rows}, {heads}, {dim}] with dense heads belongs")
+
+
 def pa_rope_append(problem, rope, steps, q, k_new, v_new, positions, slots, q_out, k_cache,
                    k_scale, v_cache, v_scale, device_error=None, stream=None):
     """Rotary positions on the new tokens' q (into q_out) and k, and k and v into the cache;
     the tokens of q, k_new and v_new may be strided (slices of a fused projection)."""
     dim, heads, rows = problem.head_dim, problem.num_kv_heads, problem.total_q_tokens
-
-    def stride(t, heads, name):
-        shape, by = t.shape, t.stride()
-        if (t.dtype is not _BF16 or len(shape) != 3 or shape[0] < rows or shape[1] != heads
-                or shape[2] != dim or by[2] != 1 or (by[1] != dim and heads > 1)):
-            raise ValueError(f"{name} must be bf16 [total_q_tokens, {heads}, {dim}] with dense "
-                             f"heads")
-        return by[0] if shape[0] > 1 else heads * dim
-
     _here(positions)
-    qs, qp = (0, None) if q is None else (stride(q, problem.num_q_heads, "q"), q.data_ptr())
-    ks, vs = stride(k_new, heads, "k_new"), stride(v_new, heads, "v_new")
-    if steps.numel() < rope.rotary_dim // 2:
+    qs, qp = (0, None) if q is None else (_tokens(q, rows, problem.num_q_heads, dim), q.data_ptr())
+    ks, vs = _tokens(k_new, rows, heads, dim), _tokens(v_new, rows, heads, dim)
+    if 2 * steps.numel() < rope.rotary_dim:
         raise ValueError(f"{steps.numel()} steps for a rotary_dim of {rope.rotary_dim}")
     _check((_lib or load()).pa_rope_append(
         problem, rope, _typed(steps, _I64), qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
-        _i32(positions), _i32(slots), _typed(q_out, _BF16), _cache(k_cache, problem),
-        _dense(k_scale), _cache(v_cache, problem), _dense(v_scale), _typed(device_error, _I32),
-        _stream(stream)), "pa_rope_append")
+        _i32(positions), _i32(slots), _typed(q_out, _BF16),
+        _cache(k_cache, problem), _dense(k_scale), _cache(v_cache, problem), _dense(v_scale),
+        _typed(device_error, _I32), _stream(stream)), "pa_rope_append")
 
 
 def pa_page_bounds(problem, k_cache, slots, bounds, bound_scale, device_error=None, stream=None):

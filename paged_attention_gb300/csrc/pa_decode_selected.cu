@@ -75,8 +75,12 @@ struct SelUnit {
     int entries;           // of its list
     int64_t list;          // where that begins
     int64_t start;         // position of its fixed cost on the flat line
-    int c_first, c_last;   // the CTAs that share it
 };
+
+// x / y, in 32 bits where they fit (64 bits take ten times as long)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return (((uint64_t)x | (uint64_t)y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
 __device__ __forceinline__ bool good_row(const CacheGeom& g, int seq, int pos) {
     return seq >= 0 && seq < g.B && pos >= 0 && pos < g.max_ctx;
@@ -105,59 +109,56 @@ __device__ __forceinline__ int64_t row_cost(const SelectedParams& P, int t) {
 }
 // The rest of u, whose row and head are set; its row leads a unit.
 template <bool JOINED>
-__device__ __forceinline__ void load_unit(const SelectedParams& P, SelUnit& u, int64_t C,
-                                          int64_t N) {
+__device__ __forceinline__ void load_unit(const SelectedParams& P, SelUnit& u) {
     const CacheGeom& g = P.g;
-    if (u.hk == 0 || u.rows == 0) {
-        u.seq = P.row_seq[u.row];
-        u.pos = P.positions[u.row];
-        u.rows = JOINED ? P.row_lead[u.row] : 1;
-    }
     const int64_t at = (int64_t)u.row * g.Hkv;
     if constexpr (JOINED) {
         u.entries = P.unit_entries[at + u.hk];
         u.list = (at + (int64_t)u.hk * u.rows) * P.budget;
     } else {
-        u.entries = list_entries(P, u.pos);
         u.list = (at + u.hk) * P.budget;
     }
     u.n = tiles_of(g, u.entries);
-    // a tile belongs to the CTA whose share of the line it is in, but no CTA takes less
-    // than two tiles of a unit, and a short unit is not split
-    const int64_t p0 = u.start + P.unit_cost;
-    auto owner = [&](int64_t x) { return (int)(((x + 1) * N - 1) / C); };
-    u.c_first = owner(u.n < 4 ? p0 + u.n - 1 : p0 + 1);
-    u.c_last = u.n < 4 ? u.c_first : owner(p0 + u.n - 2);
+}
+template <bool JOINED>
+__device__ __forceinline__ void load_row(const SelectedParams& P, SelUnit& u) {
+    u.seq = P.row_seq[u.row];
+    u.pos = P.positions[u.row];
+    u.rows = JOINED ? P.row_lead[u.row] : 1;
+    if constexpr (!JOINED) u.entries = list_entries(P, u.pos);
 }
 
 // The unit after u (every lane the same); false past the last row.
 template <bool JOINED>
-__device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u, int64_t C,
-                                          int64_t N) {
+__device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u) {
     u.start += P.unit_cost + u.n;
     if (++u.hk >= P.g.Hkv) {
         u.hk = 0;
         do {
             if (++u.row >= P.g.total_q) return false;
         } while (row_cost<JOINED>(P, u.row) == 0);
+        load_row<JOINED>(P, u);
     }
-    load_unit<JOINED>(P, u, C, N);
+    load_unit<JOINED>(P, u);
     return true;
 }
 
-// What warp w of W of a CTA runs of unit u, of the CTA's share [lo, hi) of the flat
-// line: tokens [a, z) of its list.
+// What warp w of W of the CTA with the share [lo, hi) of the flat line runs of unit u:
+// tokens [a, z) of its list.  A tile belongs to the CTA whose share it is in, but no CTA
+// takes less than two tiles of a unit, and a short unit is not split.
 struct SelShare {
     int t0, t1;     // tiles of the unit in the CTA's share
     int a, z;
 };
-__device__ __forceinline__ SelShare share_of(const CacheGeom& g, const SelUnit& u, int cost, int cta,
+__device__ __forceinline__ SelShare share_of(const CacheGeom& g, const SelUnit& u, int cost,
                                              int64_t lo, int64_t hi, int w, int W) {
     SelShare s = {0, 0, 0, 0};
-    if (cta < u.c_first || cta > u.c_last) return s;
-    const int64_t base = u.start + cost;
-    s.t0 = cta == u.c_first ? 0 : (int)(lo - base);
-    s.t1 = cta == u.c_last ? u.n : (int)(hi - base);
+    const int64_t p0 = u.start + cost;
+    const int64_t x = u.n < 4 ? p0 + u.n - 1 : p0 + 1;           // whose CTA has the first tile
+    const int64_t y = u.n < 4 ? x : p0 + u.n - 2;                // and the last
+    if (x >= hi || y < lo) return s;
+    s.t0 = x >= lo ? 0 : (int)(lo - p0);
+    s.t1 = y < hi ? u.n : (int)(hi - p0);
     const int tok0 = s.t0 * kDecodeTile, end = min(u.entries << g.ps_shift, s.t1 * kDecodeTile);
     const int steps = (end - tok0) / 16;
     s.a = tok0 + 16 * (steps * w / W);
@@ -165,9 +166,10 @@ __device__ __forceinline__ SelShare share_of(const CacheGeom& g, const SelUnit& 
     return s;
 }
 
-__device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(bytes)
+__device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, int bytes,
+                                               uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(src), "r"(bytes), "l"(policy)
                  : "memory");
 }
 
@@ -306,27 +308,70 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     const int cost = P.unit_cost;
     grid_dependency_wait();
 
-    // ---- this CTA's share of the flat line
-    auto cost_of = [&](int t) { return row_cost<JOINED>(P, t); };
-    const int64_t C = flat_total(g.total_q, lane, cost_of);
+    // ---- this CTA's share of the flat line: a lane has a run of rows
+    auto before = [&](int64_t v) -> int64_t {            // sum over the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    };
+    const int run = (g.total_q + 31) / 32, run0 = min(lane * run, g.total_q);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int t = run0; t < min(run0 + run, g.total_q); ++t) mine += row_cost<JOINED>(P, t);
     if (!JOINED && blockIdx.x == 0 && warp == 0) {
         for (int t = lane; t < g.total_q; t += 32)
             if (P.row_seq[t] >= 0 && !good_row(g, P.row_seq[t], P.positions[t]))
                 flag_error(P.header + H_ERROR, PA_DEV_BAD_LENGTHS);
     }
+    const int64_t upto = before(mine);
+    const int64_t C = __shfl_sync(0xffffffffu, upto, 31);
     const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel - 1) / kMinShareSel);
     const int cta = blockIdx.x;
     if (cta >= N) return;
-    const int64_t lo = C * cta / N, hi = C * (cta + 1) / N;
+    const int64_t lo = quotient(C * cta, N), hi = quotient(C * (cta + 1), N);
     SelUnit u;
     {
-        int none;
-        u.row = flat_find(g.total_q, lane, lo, cost_of, [](int) { return 0; }, u.start, none);
-        u.hk = u.rows = 0;
-        load_unit<JOINED>(P, u, C, N);
-        while (u.start + cost + u.n <= lo) next_unit<JOINED>(P, u, C, N);   // (of the same row)
+        const int src = __ffs(__ballot_sync(0xffffffffu, upto > lo)) - 1;
+        u.start = __shfl_sync(0xffffffffu, upto - mine, src);
+        // the row among that lane's, then the head among the row's
+        for (int t0 = src * run;; t0 += 32) {
+            const int64_t c = t0 + lane < g.total_q ? row_cost<JOINED>(P, t0 + lane) : 0;
+            const int64_t to = u.start + before(c);
+            const uint32_t past = __ballot_sync(0xffffffffu, to > lo);
+            if (past != 0) {
+                u.row = t0 + __ffs(past) - 1;
+                u.start = __shfl_sync(0xffffffffu, to - c, __ffs(past) - 1);
+                break;
+            }
+            u.start = __shfl_sync(0xffffffffu, to, 31);
+        }
+        load_row<JOINED>(P, u);
+        if constexpr (JOINED) {
+            for (int h0 = 0;; h0 += 32) {
+                const int64_t c =
+                    h0 + lane < g.Hkv
+                        ? tiles_of(g, P.unit_entries[(int64_t)u.row * g.Hkv + h0 + lane]) + cost
+                        : 0;
+                const int64_t to = u.start + before(c);
+                const uint32_t past = __ballot_sync(0xffffffffu, to > lo);
+                if (past != 0) {
+                    u.hk = h0 + __ffs(past) - 1;
+                    u.start = __shfl_sync(0xffffffffu, to - c, __ffs(past) - 1);
+                    break;
+                }
+                u.start = __shfl_sync(0xffffffffu, to, 31);
+            }
+        } else {
+            const int c = tiles_of(g, u.entries) + cost;
+            u.hk = (int)quotient(lo - u.start, c);
+            u.start += (int64_t)u.hk * c;
+        }
+        load_unit<JOINED>(P, u);
     }
-    auto share = [&](const SelUnit& x) { return share_of(g, x, cost, cta, lo, hi, warp, W); };
+    auto share = [&](const SelUnit& x) { return share_of(g, x, cost, lo, hi, warp, W); };
 
     const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::kStage;
     const uint32_t qbase = smem_u32(smem + Cfg::kOffQ);
@@ -336,6 +381,13 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     // ---- the load side runs ST - 1 steps ahead, over unit boundaries
     constexpr int CH = ROW / 16, RPI = 32 / CH;   // pieces of a row, rows an instruction
     constexpr int INS = 16 / RPI;                 // instructions for a step's K (or V)
+    // Where no other unit reads the same pages they leave L2 first (64 rows of 32 pages of 64:
+    // 59.7 us, without 62.1 and with a prefetch of 128 bytes 63.1; 384 rows of 40: 221, 241, 242).
+    uint64_t policy;
+    if (P.once)
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    else
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     const int page_rows = g.ps * g.Hkv;
     const int r_lane = lane / CH, c_lane = lane % CH;
     // A list's entry i + lane: as it lies there (read well ahead), and as a page number
@@ -389,7 +441,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     }
     int win_lo = l_tok >> g.ps_shift;        // 32 entries, the 32 after them, the next unit's
     int2 win = read_entry(u, win_lo), nxt = read_entry(u, win_lo + 32), lnw = make_int2(-1, 0);
-    bool ln_ok = next_unit<JOINED>(P, ln, C, N) && ln.start < hi;
+    bool ln_ok = next_unit<JOINED>(P, ln) && ln.start < hi;
     if (ln_ok) lnw = read_entry(ln, share(ln).a >> g.ps_shift);
     extremes(row_pos(u), l_least, l_most, l_rows);
     win = look_up(u, win);
@@ -409,7 +461,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             win_lo = l_tok >> g.ps_shift;
             win = look_up(ln, lnw);
             nxt = read_entry(ln, win_lo + 32);
-            ln_ok = next_unit<JOINED>(P, ln, C, N) && ln.start < hi;
+            ln_ok = next_unit<JOINED>(P, ln) && ln.start < hi;
             if (ln_ok) lnw = read_entry(ln, share(ln).a >> g.ps_shift);
         }
         if (more) {
@@ -452,8 +504,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 #pragma unroll
                 for (int i = 0; i < INS; ++i) {
                     const uint32_t to = dst + piece_at<D>(i * RPI + r_lane, c_lane);
-                    cp_async16_row(to, k + i * step, 16);
-                    cp_async16_row(to + 16 * ROW, v + i * step, 16);
+                    cp_async16_row(to, k + i * step, 16, policy);
+                    cp_async16_row(to + 16 * ROW, v + i * step, 16, policy);
                 }
             } else {
 #pragma unroll
@@ -461,8 +513,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     const int r = i * RPI + r_lane;
                     const uint32_t to = dst + piece_at<D>(r, c_lane);
                     const bool ok = r >= a && r < z;
-                    cp_async16_row(to, ok ? k + i * step : P.k, ok ? 16 : 0);
-                    cp_async16_row(to + 16 * ROW, ok ? v + i * step : P.v, ok ? 16 : 0);
+                    cp_async16_row(to, ok ? k + i * step : P.k, ok ? 16 : 0, policy);
+                    cp_async16_row(to + 16 * ROW, ok ? v + i * step : P.v, ok ? 16 : 0, policy);
                 }
             }
         }
@@ -505,7 +557,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                                              4 * (lane + 32 * j)) = qw[i][j];
         __syncthreads();
         SelUnit nu = u;
-        const bool has_next = next_unit<JOINED>(P, nu, C, N) && nu.start < hi;
+        const bool has_next = next_unit<JOINED>(P, nu) && nu.start < hi;
         if (has_next) load_q(nu);
 
         float m[NT][2], l[NT][2];
@@ -719,7 +771,10 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 
         // ---- merge the warps, a few rows at a time
         if (sh.t1 > sh.t0) {
-            const int c_first = u.c_first, c_last = u.c_last;
+            // the CTAs that hold parts of the unit
+            auto owner = [&](int64_t x) { return (int)quotient((x + 1) * N - 1, C); };
+            const int c_first = sh.t0 == 0 ? cta : owner(u.start + cost + 1);
+            const int c_last = sh.t1 == u.n ? cta : owner(u.start + cost + u.n - 2);
             // where row r of the unit is among the outputs; -1: nowhere
             auto out_row = [&](int r) -> int64_t {
                 if constexpr (JOINED) {
@@ -832,40 +887,50 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         auto part_row = [&](int c) {
                             return (int64_t)(2 * c + (c == c_first ? 1 : 0)) * Cfg::kRows + r;
                         };
+                        // the first sixteen parts are under way while the lse are looked at
+                        constexpr int B = 16;
+                        float x[B][DPL];
+                        auto load_parts = [&](int c0) {
+#pragma unroll
+                            for (int j = 0; j < B; ++j) {
+                                const float* src =
+                                    P.part_o + part_row(min(c0 + j, c_last)) * D + lane * DPL;
+#pragma unroll
+                                for (int e = 0; e < DPL; e += 2)
+                                    *reinterpret_cast<float2*>(x[j] + e) =
+                                        __ldcg(reinterpret_cast<const float2*>(src + e));
+                            }
+                        };
+                        load_parts(c_first);
                         float M = -INFINITY;
                         bool poison = false;
                         for (int c = c_first + lane; c <= c_last; c += 32) {
-                            const float x = __ldcg(P.part_lse + part_row(c));
-                            poison |= x != x;
-                            M = fmaxf(M, x);
+                            const float y = __ldcg(P.part_lse + part_row(c));
+                            poison |= y != y;
+                            M = fmaxf(M, y);
                         }
 #pragma unroll
-                        for (int x = 16; x > 0; x >>= 1)
-                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                        for (int y = 16; y > 0; y >>= 1)
+                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
                         poison = __any_sync(0xffffffffu, poison);
                         float den = 0.f, acc[DPL];
 #pragma unroll
                         for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
-                        for (int c0 = c_first; c0 <= c_last; c0 += 32) {
+#pragma unroll 1
+                        for (int c0 = c_first; c0 <= c_last; c0 += B) {
+                            if (c0 > c_first) load_parts(c0);
                             float y = 0.f;
-                            if (c0 + lane <= c_last) {
-                                const float x = __ldcg(P.part_lse + part_row(c0 + lane));
-                                y = poison ? NAN : x == -INFINITY ? 0.f : ex2((x - M) * kLog2e);
+                            if (lane < B && c0 + lane <= c_last) {
+                                const float v = __ldcg(P.part_lse + part_row(c0 + lane));
+                                y = poison ? NAN : v == -INFINITY ? 0.f : ex2((v - M) * kLog2e);
                             }
-                            const int n = min(32, c_last - c0 + 1);
-#pragma unroll 8
-                            for (int j = 0; j < n; ++j) {
-                                const float w = __shfl_sync(0xffffffffu, y, j);
-                                const float* src = P.part_o + part_row(c0 + j) * D + lane * DPL;
-                                float x[DPL];
 #pragma unroll
-                                for (int e = 0; e < DPL; e += 2)
-                                    *reinterpret_cast<float2*>(x + e) =
-                                        __ldcg(reinterpret_cast<const float2*>(src + e));
+                            for (int j = 0; j < B; ++j) {
+                                const float w = __shfl_sync(0xffffffffu, y, j);
                                 den += w;
 #pragma unroll
                                 for (int e = 0; e < DPL; ++e)
-                                    if (w != 0.f) acc[e] = fmaf(w, x[e], acc[e]);
+                                    if (w != 0.f) acc[e] = fmaf(w, x[j][e], acc[e]);
                             }
                         }
                         const bool none = den == 0.f;

@@ -33,7 +33,7 @@ __device__ __forceinline__ int code_of(float x, float inv, bool up) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
               const int32_t* __restrict__ slots, int8_t* __restrict__ bounds,
               float* __restrict__ scale, int32_t* err, int rows) {
@@ -72,7 +72,7 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
                     // (behind the last key: that key again)
                     const int key = min(s + u * kWarps * RPI + k0, used - 1);
                     if (s + u * kWarps * RPI < used)
-                        x[u] = __ldg(src + (int64_t)key * g.tok_rows * C + lane % C);
+                        x[u] = __ldcs(src + (int64_t)key * g.tok_rows * C + lane % C);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -147,9 +147,10 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
 cudaError_t launch_page_bounds(const CacheGeom& g, const void* k, const int32_t* slots,
                                int8_t* bounds, float* scale, int32_t* err,
                                cudaStream_t stream) {
-    // rows of a CTA: a sequence's new ones, which lie in a page or two, up to two pages
-    // (most rows of a prompt are not their page's last)
-    const int rows = std::max(1, std::min(g.max_q_len, 2 * g.ps));
+    // rows of a CTA: a sequence's new ones, which lie in a page or two, up to four pages
+    // (8 prompts of 4096 .. 16384 tokens, pages of 64: 27 us with two or four, 29 with one,
+    // 39 with eight)
+    const int rows = std::max(1, std::min(g.max_q_len, 4 * g.ps));
     const dim3 grid((g.total_q + rows - 1) / rows, g.Hkv);
     auto kern = g.D == 128 ? bounds_kernel<128> : bounds_kernel<64>;
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, g, (const __nv_bfloat16*)k,

@@ -43,6 +43,14 @@ __device__ __forceinline__ uint32_t key_of(float score) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The two halves of a barrier over the cluster: this CTA has begun; all have.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // The codes of four elements (two words) of a query row, with 2^-e as factor.
 __device__ __forceinline__ void q_codes(uint32_t w0, uint32_t w1, float inv, float* c) {
     const float x[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
@@ -77,6 +85,7 @@ select_kernel(const __grid_constant__ SelectParams P) {
     __shared__ __align__(16) uint32_t s_hist[4][kBins];  // of each pass
     __shared__ uint2 s_range[kWarps];
     __shared__ int2 s_part[kWarps];
+    __shared__ int3 s_found;
     const CacheGeom& g = P.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t4 = lane & 3;
@@ -102,6 +111,7 @@ select_kernel(const __grid_constant__ SelectParams P) {
         return;
     }
 
+    if (C > 1) cluster_arrive();
     // ---- the CTA's pages [lo, lo + m); a warp has kTile at a time, whose bounds are under
     // way while the queries are made ready
     const int part = (n + C - 1) / C, lo = min(n, rank * part), m = min(part, n - lo);
@@ -185,11 +195,8 @@ select_kernel(const __grid_constant__ SelectParams P) {
     }
     for (int i = tid; i < 4 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
     // (a cluster's first CTA must have begun before the others write to it)
-    __syncwarp();
-    if (C > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
+    __syncthreads();
+    if (C > 1) cluster_wait();
 
     // ---- scores
     const uint32_t keys = C > 1 ? mapa_shared(smem_u32(s_key), 0) : smem_u32(s_key);
@@ -290,6 +297,13 @@ select_kernel(const __grid_constant__ SelectParams P) {
     }
     // ---- the keys to list: those from `from` up, and `take` of those equal to `equal`
     // (the kept ones, above all others, are the first num_first + num_recent)
+    auto four_keys = [&](int i, uint32_t* x) {   // (behind the last: anything)
+        const uint4 v = *reinterpret_cast<const uint4*>(s_key + i);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[2] = v.z;
+        x[3] = v.w;
+    };
     int take = P.budget - P.num_first - P.num_recent;
     uint32_t from = kKept, equal = 0u;
     if (take > 0) {
@@ -303,40 +317,36 @@ select_kernel(const __grid_constant__ SelectParams P) {
                     atomicAdd(&s_hist[pass][(x >> (shift - width)) & ((1u << width) - 1u)], 1u);
             }
             __syncthreads();
-            // every warp by itself: a lane has eight bins; in which one is the take-th from
-            // the top?
-            uint32_t h[8], sum = 0;
-            *reinterpret_cast<uint4*>(h) = reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane];
-            *reinterpret_cast<uint4*>(h + 4) =
-                reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane + 1];
+            // one warp, eight bins a lane: in which one is the take-th from the top?
+            if (warp == 0) {
+                uint32_t h[8], sum = 0;
+                *reinterpret_cast<uint4*>(h) = reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane];
+                *reinterpret_cast<uint4*>(h + 4) =
+                    reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane + 1];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) sum += h[d];
-            uint32_t upto = sum;
+                for (int d = 0; d < 8; ++d) sum += h[d];
+                uint32_t upto = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
-                if (lane + o < 32) upto += y;
-            }
-            uint32_t above = upto - sum, digit = 0, many = 0;
-            const uint32_t has = __ballot_sync(0xffffffffu, upto >= (uint32_t)take &&
-                                                                above < (uint32_t)take);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
+                    if (lane + o < 32) upto += y;
+                }
+                uint32_t above = upto - sum;
+                if (upto >= (uint32_t)take && above < (uint32_t)take) {
 #pragma unroll
-            for (int d = 7; d >= 0; --d)
-                if (many == 0) {
-                    if (above + h[d] >= (uint32_t)take) {
-                        digit = 8 * lane + d;
-                        many = h[d];
-                    } else {
+                    for (int d = 7; d >= 0; --d) {
+                        if (above < (uint32_t)take && above + h[d] >= (uint32_t)take)
+                            s_found = make_int3(8 * lane + d, (int)h[d], (int)above);
                         above += h[d];
                     }
                 }
-            const int src = __ffs(has) - 1;
-            digit = __shfl_sync(0xffffffffu, digit, src);
-            many = __shfl_sync(0xffffffffu, many, src);
-            take -= (int)__shfl_sync(0xffffffffu, above, src);
-            prefix = prefix << width | digit;
+            }
+            __syncthreads();
+            const int3 found = s_found;
+            take -= found.z;
+            prefix = prefix << width | (uint32_t)found.x;
             shift -= width;
-            if ((int)many == take) {             // the whole bin
+            if (found.y == take) {               // the whole bin
                 from = prefix << shift;
                 take = 0;
                 break;
@@ -348,15 +358,27 @@ select_kernel(const __grid_constant__ SelectParams P) {
         }
     }
 
-    // ---- list them: a key's place is the number of listed ones before it
-    const int seg = (n + kThreads - 1) / kThreads * 32;        // of a warp
+    // ---- list them: a key's place is the number of listed ones before it.  A lane has four
+    // keys at a time; counts of keys from `from` up, and 2^16 times those of equal ones
+    const int seg = (n + 4 * kThreads - 1) / (4 * kThreads) * 128;   // keys of a warp
     const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    auto count = [&](const uint32_t* x, int i) -> uint32_t {
+        uint32_t c = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < w1) c += x[j] >= from ? 1u : x[j] == equal ? 0x10000u : 0u;
+        return c;
+    };
     int above = 0, same = 0;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int i = j0 + lane;
-        const uint32_t x = i < w1 ? s_key[i] : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, i < w1 && x >= from));
-        same += __popc(__ballot_sync(0xffffffffu, i < w1 && x == equal && x < from));
+    for (int i = w0 + 4 * lane; i < w0 + seg; i += 128) {
+        uint32_t x[4], c = 0;
+        if (i < w1) {
+            four_keys(i, x);
+            c = count(x, i);
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        above += (int)(c & 0xffffu);
+        same += (int)(c >> 16);
     }
     if (lane == 0) s_part[warp] = make_int2(above, same);
     __syncthreads();
@@ -367,17 +389,33 @@ select_kernel(const __grid_constant__ SelectParams P) {
             above += s_part[w].x;
             same += s_part[w].y;
         }
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int i = j0 + lane;
-        const uint32_t x = i < w1 ? s_key[i] : 0u;
-        const uint32_t up = __ballot_sync(0xffffffffu, i < w1 && x >= from);
-        const uint32_t eq = __ballot_sync(0xffffffffu, i < w1 && x == equal && x < from);
-        const uint32_t below = (1u << lane) - 1u;
-        const int rank_eq = same + __popc(eq & below);
-        const int place = above + __popc(up & below) + min(take, rank_eq);
-        if ((up >> lane & 1u) || ((eq >> lane & 1u) && rank_eq < take)) out[place] = first + i;
-        above += __popc(up);
-        same += __popc(eq);
+    for (int i = w0 + 4 * lane; i < w0 + seg; i += 128) {
+        uint32_t x[4] = {0u, 0u, 0u, 0u}, c = 0;
+        if (i < w1) {
+            four_keys(i, x);
+            c = count(x, i);
+        }
+        uint32_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        int up = above + (int)((upto - c) & 0xffffu), eq = same + (int)((upto - c) >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < w1) {
+                if (x[j] >= from) {
+                    out[up + min(take, eq)] = first + i + j;
+                    ++up;
+                } else if (x[j] == equal) {
+                    if (eq < take) out[up + eq] = first + i + j;
+                    ++eq;
+                }
+            }
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        above += (int)(all & 0xffffu);
+        same += (int)(all >> 16);
     }
 }
 

@@ -10,7 +10,11 @@ namespace pa {
 namespace {
 
 constexpr int kMaxGridSel = 1024;        // CTAs of pa_decode_selected
-constexpr int kSelUnitCost = 3;          // a unit's fixed cost, in 64-key tiles
+// A unit's fixed cost (its first loads, its warps' merge), in 64-key tiles, which are half
+// the bytes with head_dim 64.  64 rows of up to 32 pages of 64: 61 us with 1 to 8, 62 with
+// 12; head_dim 64 46.8 with 1, 38.9 with 6; 64 sequences of 4 rows (16 query rows a
+// unit) 85 with 3, 80 with 6; 128 sequences of 3 rows (24) 223, 215 with 6, 213 with 12.
+constexpr int sel_unit_cost(int D, int rows) { return (rows > 16 ? 10 : rows > 8 ? 6 : 3) * 128 / D; }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const char* x = static_cast<const char*>(a);
@@ -56,7 +60,7 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
         L.grid *= selected_ctas_per_sm();
         if (L.grid > kMaxGridSel) L.grid = kMaxGridSel;
     }
-    L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : kSelUnitCost;
+    L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : sel_unit_cost(g.D, 8 * L.nt);
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
     L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * 4);
@@ -326,6 +330,7 @@ pa_status pa_decode_selected(const pa_problem* problem, int32_t budget, const vo
     P.out = (__nv_bfloat16*)out;
     P.lse = lse;
     P.unit_cost = L.unit_cost;
+    P.once = g.max_q_len <= L.together;
     P.row_lead = reinterpret_cast<int32_t*>(base + L.off_lead);
     P.row_tiles = P.row_lead + g.total_q;
     P.unit_entries = reinterpret_cast<int32_t*>(base + L.off_entries);

@@ -57,6 +57,7 @@ struct SelectedParams {
     __nv_bfloat16* out;
     float* lse;
     int32_t unit_cost;   // fixed cost of a unit, in tiles
+    int32_t once;        // the rows of a sequence are one unit at most
     // rows of a sequence joined to units: per row, how many it leads (0: none) and its
     // units' tiles; per row and KV head, the entries of the joined list; and the lists
     int32_t* row_lead;

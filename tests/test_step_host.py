@@ -193,7 +193,8 @@ def test_the_binding_refuses_what_would_be_misread():
         B.pa_rope_append(p, ROPE, steps[:63], *rows, i32(3), i32(3), bf(3, 8, 128), k, None, k,
                          None)
     for f in (lambda: B._typed(bf(4, 4).t(), torch.bfloat16), lambda: B._typed(bf(4), torch.int8),
-              lambda: B._here(bf(4)), lambda: B._i32(torch.zeros(4, dtype=torch.int64)),
+              lambda: B._here(bf(4)),
+              lambda: B._i32(torch.zeros(4, dtype=torch.int64)),
               lambda: B._i32(i32(4, 2)[:, 0])):
         with pytest.raises(ValueError):
             f()
