@@ -176,7 +176,7 @@ __device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, in
 // ---- joins the lists of rows of one sequence (one CTA a row; only a unit's first row's
 // goes on).  A warp a KV head: the set of rows of every page, a byte each, in shared
 // memory, some pages at a time; then the pages that have any, in order.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 constexpr int kJoinPages = 4096;
 
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -222,6 +222,7 @@ join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
         return;                        // (the same for every thread)
     }
     const int last = __reduce_max_sync(0xffffffffu, pos) >> g.ps_shift;   // page index
+    const int each = __reduce_max_sync(0xffffffffu, mine);                // the longest list
     int tiles = 0;
     for (int hk = warp; hk < g.Hkv; hk += kJoinWarps) {
         int2* to = P.list + ((int64_t)t * g.Hkv + (int64_t)hk * m) * P.budget;
@@ -231,16 +232,24 @@ join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
             for (int i = lane; i < (span + 15) / 16; i += 32)
                 reinterpret_cast<uint4*>(s_rows[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
             __syncwarp();
-            for (int r = 0; r < m; ++r) {
+            // the rows' lists end to end, so that many entries are under way
+            const int32_t* sel = P.selected + ((int64_t)t * g.Hkv + hk) * P.budget;
+            const int64_t next_row = (int64_t)g.Hkv * P.budget;
+#pragma unroll 4
+            for (int k0 = 0; k0 < m * each; k0 += 32) {
+                const int k = k0 + lane;
+                int r = 0;
+#pragma unroll
+                for (int x = 1; x < kMostRows; ++x) r += x < m && k >= x * each;
+                const int i = k - r * each;
                 const int many = __shfl_sync(0xffffffffu, mine, r);
                 const int top = __shfl_sync(0xffffffffu, pos, r) >> g.ps_shift;
-                const int32_t* sel = P.selected + ((int64_t)(t + r) * g.Hkv + hk) * P.budget;
-                for (int i = lane; i < many; i += 32) {
-                    const int s = sel[i];
-                    if (s < -1 || s > top) {
+                if (i < many) {
+                    const int e = sel[r * next_row + i];
+                    if (e < -1 || e > top) {
                         flag_error(err, PA_DEV_BAD_LENGTHS);
-                    } else if (s >= p0 && s < p0 + span) {
-                        const int at = s - p0;
+                    } else if (e >= p0 && e < p0 + span) {
+                        const int at = e - p0;
                         atomicOr(&s_rows[warp][at >> 2], 1u << (8 * (at & 3) + r));
                     }
                 }

@@ -493,6 +493,13 @@ def test_selection_of_ties_odd_queries_and_bad_pages():
         want = R.select(q[t], bnd[:, 0], sc[:, 0], table, n * page - 1, budget=budget, num_first=0,
                         num_recent=2, page=page, pages=n, window=0)
         assert sel[t, 0].tolist() == want, t
+    # the cache's type has no part in it
+    for kv in (B.PA_FP8_E4M3, B.PA_MX4):
+        p.kv_dtype = kv
+        again = torch.zeros_like(sel)
+        B.pa_select_pages(p, budget, 0, 2, q.cuda(), bnd.cuda(), sc.cuda(), ints([table]),
+                          ints([0] * 6), ints([n * page - 1] * 6), again, err)
+        assert torch.equal(again, sel)
     # rows that cannot be: left as they are
     sel.fill_(-5)
     err.zero_()
@@ -767,6 +774,75 @@ def test_attention_is_pa_decode_where_every_page_is_listed():
     assert float((lse - l2).abs().max()) <= 1e-3
 
 
+def test_one_workspace_for_calls_of_other_shapes():
+    """Calls of other grids, groups and rows a sequence follow one another in one workspace."""
+    cases = [(128, 4, 2, 16, [500, 90], [1, 1], 7, 0), (64, 16, 1, 32, [900], [1], 20, 1000),
+             (128, 3, 1, 16, [700, 30], [4, 2], 9, 17), (128, 8, 1, 16, [2000], [1], 100, 300)]
+    ps = []
+    for D, G, Hkv, page, ctx, ql, budget, ctas in cases:
+        c = attend_case(D, G, Hkv, page, 0, ctx, ql, 3)
+        p = problem(num_seqs=len(ctx), num_q_heads=G * Hkv, num_kv_heads=Hkv, head_dim=D,
+                    page_size=page, num_pages=c[0], max_pages_per_seq=len(c[1][0]),
+                    total_q_tokens=len(c[2]), max_q_len=max(ql), max_context_len=max(ctx),
+                    num_ctas=ctas)
+        ps.append((p, budget, c, lists(c[2], c[3], Hkv, budget, page, 0, 5)))
+    need = max(B.pa_selected_workspace_size(p, budget) for p, budget, _, _ in ps)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for p, budget, (_, table, seq, pos, k, v, q), sel in ps:
+            want, wl = check_attend(p, budget, table, seq, pos, k, v, q, sel)
+            out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+            B.pa_decode_selected(p, budget, q.cuda(), k.cuda(), v.cuda(), ints(table), ints(seq),
+                                 ints(pos), ints(sel), ws, out, lse)
+            assert B.pa_last_device_error(ws) == 0
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_pages_past_2_to_the_32_bytes():
+    """Rope, bounds and attention on the last pages of caches of more than 2^32 bytes (and of
+    more than 2^31 elements)."""
+    D, Hkv, G, page = 128, 8, 2, 64
+    pages = (2 ** 32 // (page * Hkv * D * 2)) + 40
+    k = torch.zeros((pages, page, Hkv, D), dtype=BF16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() > 2 ** 31
+    n = 150
+    table = ints([[pages - 1, 0, pages - 2]])
+    p = problem(num_q_heads=G * Hkv, num_kv_heads=Hkv, page_size=page, num_pages=pages,
+                max_pages_per_seq=3, total_q_tokens=n, max_q_len=n, max_context_len=192)
+    g = torch.Generator().manual_seed(3)
+    q, kn, vn = (torch.randn((n, h, D), generator=g).to(BF16).cuda() for h in (G * Hkv, Hkv, Hkv))
+    pos = ints(list(range(n)))
+    slots = (table[0].long()[pos.long() // page] * page + pos % page).int()
+    err, out = ints([0]), torch.zeros_like(q)
+    B.pa_rope_append(p, B.PaRope(16, 0, 1.0), B.pa_rope_steps(torch.zeros(8)).cuda(), q, kn, vn, pos,
+                     slots, out, k, None, v, None, err)
+    s = slots.long()
+    assert torch.equal(k[s // page, s % page], kn) and torch.equal(v[s // page, s % page], vn)
+    assert int(torch.count_nonzero(k[1:pages - 2])) == 0
+    bnd = torch.zeros((pages, Hkv, 2, D), dtype=torch.int8, device="cuda")
+    sc = torch.zeros((pages, Hkv), device="cuda")
+    B.pa_page_bounds(p, k, slots, bnd, sc, err)
+    no_error(err)
+    for i, used in ((0, 64), (1, 64), (2, 22)):
+        for h in (0, Hkv - 1):
+            want, scale = R.bounds(kn[i * page:i * page + used, h].cpu())
+            pg = int(table[0, i])
+            assert float(sc[pg, h]) == scale and torch.equal(bnd[pg, h].cpu(), want)
+    p.total_q_tokens, p.max_q_len = 1, 1
+    sel = ints([[[0, 1, 2]] * Hkv])
+    ws = torch.zeros(B.pa_selected_workspace_size(p, 3), dtype=torch.uint8, device="cuda")
+    o, lse = torch.zeros((1, G * Hkv, D), dtype=BF16, device="cuda"), torch.zeros((1, G * Hkv)).cuda()
+    B.pa_decode_selected(p, 3, q, k, v, table, ints([0]), ints([n - 1]), sel, ws, o, lse)
+    for h in range(Hkv):
+        r = slice(h * G, (h + 1) * G)
+        want, L, size, big = R.attend(q[0, r].cpu(), kn[:, h].cpu(), vn[:, h].cpu(), list(range(n)),
+                                      n - 1, 0, p.sm_scale)
+        ds = (D + 16) * 2.0 ** -24 * big[:, None] + 2.0 ** -20
+        tol = (HALF + 2 * ds) * size * 1.01 + HALF * (want.abs() + HALF * size)
+        assert torch.all((o[0, r].cpu().double() - want).abs() <= tol)
+
+
 def test_a_workspace_that_was_never_filled_is_reported():
     D, G, Hkv, page, budget = 64, 1, 1, 16, 64
     pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, 0, [1024], [1], 9)
@@ -935,3 +1011,34 @@ def test_equal_inputs_give_equal_bits_on_another_stream():
         got.append((out, lse))
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+def test_two_loops_at_once_on_two_streams():
+    """Every operator of two decode loops, each on a stream of its own, against the same loops
+    one after the other."""
+    def make():
+        loops = [Loop(3, 8, 2, 128, 16, i, 4, 9, 700, seed=i) for i in range(2)]
+        g = torch.Generator().manual_seed(9)
+        data = [[torch.randn(L.fused.shape, generator=g).to(BF16).cuda() for _ in range(60)]
+                for L in loops]
+        return loops, data
+
+    got = []
+    for both in (False, True):
+        loops, data = make()
+        streams = [torch.cuda.Stream() for _ in loops] if both else [torch.cuda.current_stream()] * 2
+        torch.cuda.synchronize()
+        for i in range(60):
+            for L, x, s in zip(loops, data, streams):
+                with torch.cuda.stream(s):
+                    L.fused.copy_(x[i])
+                    L.ql.copy_(torch.tensor([3, 1 + i % 4, 2], dtype=torch.int32, device="cuda"))
+                    L.step()
+        torch.cuda.synchronize()
+        for L in loops:
+            no_error(L.err)
+            assert B.pa_last_device_error(L.ws) == 0
+        got.append([(L.out, L.lse, L.sel, L.table, L.lens) for L in loops])
+    for one, two in zip(*got):
+        for a, b in zip(one, two):
+            assert torch.equal(a, b)
