@@ -535,6 +535,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 
     // ---- Q rows of a unit, one warp a row: read ahead of the unit that needs them
     constexpr int QPW = Cfg::kRows / W, QW = D / 64;
+    constexpr bool kQAhead = NT <= 2;         // (registers that many rows need for O)
     uint32_t qw[QPW][QW];
     auto load_q = [&](const SelUnit& x) {
 #pragma unroll
@@ -551,13 +552,15 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             }
         }
     };
-    load_q(u);
+    if constexpr (kQAhead) load_q(u);
 
-    const float f = g.sm_scale * kLog2e;
+    // (never 0, so that a masked score times it stays -inf)
+    const float f = fmaxf(g.sm_scale * kLog2e, 1.2e-38f);
     // ---- units
     while (true) {
         const SelShare sh = share(u);
         const int R = u.rows * g.G;
+        if constexpr (!kQAhead) load_q(u);
 #pragma unroll
         for (int i = 0; i < QPW; ++i)
 #pragma unroll
@@ -567,7 +570,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         __syncthreads();
         SelUnit nu = u;
         const bool has_next = next_unit<JOINED>(P, nu) && nu.start < hi;
-        if (has_next) load_q(nu);
+        if (kQAhead && has_next) load_q(nu);
 
         float m[NT][2], l[NT][2];
         float o[OT][NT][4];
@@ -579,21 +582,9 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             for (int i = 0; i < OT; ++i)
                 o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
         }
-        // JOINED: where the thread's rows are, and their bits in an entry (none: position -1)
-        int pr[JOINED ? NT : 1][2];
-        uint32_t bit[JOINED ? NT : 1][2];
-        if constexpr (JOINED) {
-            const int p = row_pos(u);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 8 * nt + 2 * t4 + e, i = r / g.G;
-                    pr[nt][e] = __shfl_sync(0xffffffffu, p, min(i, 31));
-                    bit[nt][e] = r < R ? 1u << i : 0u;
-                    if (r >= R) pr[nt][e] = -1;
-                }
-        }
+        // JOINED: lane i has row i's position; query row r is of row r / G = r * inv >> 16
+        const int upos = JOINED ? row_pos(u) : 0;
+        const int inv = JOINED ? 65535 / g.G + 1 : 0;
         constexpr bool kQInRegs = NT == 1;
         uint32_t qf[kQInRegs ? KK : 1][2];
         // the B operands of two contraction steps: rows 8 nt + (lane & 7), piece 2 kk + lane / 8
@@ -655,49 +646,65 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         }
                     }
                 }
+                if constexpr (kTwo) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[nt][e] = (kTwo ? s[nt][e] + s1[kTwo ? nt : 0][e] : s[nt][e]) * f;
+                        for (int e = 0; e < 4; ++e) s[nt][e] += s1[nt][e];
+                }
             }
             const bool part_seen = JOINED ? !(mt >> 16 & 1u) : a > 0 || z < 16;
-            // JOINED: whether row (nt, e) sees key x of the step
-            auto sees = [&](int nt, int e, int x) -> bool {
-                const int p = pr[JOINED ? nt : 0][e];
-                return (mt >> 10 & bit[JOINED ? nt : 0][e]) != 0 && x >= a && x < z && at + x <= p &&
-                       (g.window == 0 || at + x > p - g.window);
-            };
             if (part_seen) {
-                // keys gr and gr + 8 of the step
-                const bool k0 = gr >= a && gr < z, k1 = gr + 8 >= a && gr + 8 < z;
+                if constexpr (JOINED) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool ok = JOINED ? sees(nt, e & 1, gr + 8 * (e >> 1)) : e < 2 ? k0 : k1;
-                        if (!ok) s[nt][e] = -INFINITY;
-                    }
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = 8 * nt + 2 * t4 + e, i = r * inv >> 16;
+                            const int p = __shfl_sync(0xffffffffu, upos, i & 31);
+                            const bool listed = r < R && (mt >> (10 + i) & 1u) != 0;
+                            // of keys gr and gr + 8 of the step
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int x = gr + 8 * h;
+                                if (!(listed && x >= a && x < z && at + x <= p &&
+                                      (g.window == 0 || at + x > p - g.window)))
+                                    s[nt][2 * h + e] = -INFINITY;
+                            }
+                        }
+                } else {
+                    const bool k0 = gr >= a && gr < z, k1 = gr + 8 >= a && gr + 8 < z;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(e < 2 ? k0 : k1)) s[nt][e] = -INFINITY;
+                }
             }
-            // ---- the running max moves where a score passes it by far
-            bool far = false;
+            // ---- exponents below the running max, which moves where one passes it by far
+            float x[NT][4];
+            auto exponents = [&]() -> float {
+                float most = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    far |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kRise;
-            if (__any_sync(0xffffffffu, far)) {
+                    for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], f, -m[nt][e & 1]);
+                    most = fmax3(most, fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3]));
+                }
+                return most;
+            };
+            if (__any_sync(0xffffffffu, exponents() > kRise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(s[nt][e], s[nt][e + 2]);
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        if (x > m[nt][e]) {
-                            const float al = m[nt][e] == kUnseen ? 0.f : ex2(m[nt][e] - x);
-                            m[nt][e] = x;
+                        float y = fmaxf(s[nt][e], s[nt][e + 2]) * f;
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        if (y > m[nt][e]) {
+                            const float al = m[nt][e] == kUnseen ? 0.f : ex2(m[nt][e] - y);
+                            m[nt][e] = y;
                             l[nt][e] *= al;
 #pragma unroll
                             for (int i = 0; i < OT; ++i) {
@@ -706,13 +713,14 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                             }
                         }
                     }
+                exponents();
             }
             // ---- probabilities, and their transposes as the B operand
             uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = ex2(s[nt][0] - m[nt][0]), p1 = ex2(s[nt][1] - m[nt][1]);
-                const float p2 = ex2(s[nt][2] - m[nt][0]), p3 = ex2(s[nt][3] - m[nt][1]);
+                const float p0 = ex2(x[nt][0]), p1 = ex2(x[nt][1]);
+                const float p2 = ex2(x[nt][2]), p3 = ex2(x[nt][3]);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
                 pb[nt][0] = movmatrix_trans(pack_bf16x2(p0, p1));
@@ -727,10 +735,10 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < OT; ++i) {
-                        uint32_t x[4];
-                        ldsm_x4(sv + piece_at<D>(vr, 2 * i + vc), x[0], x[1], x[2], x[3]);
+                        uint32_t y[4];
+                        ldsm_x4(sv + piece_at<D>(vr, 2 * i + vc), y[0], y[1], y[2], y[3]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) top = max_bf16x2(top, x[j] & 0x7fff7fffu);
+                        for (int j = 0; j < 4; ++j) top = max_bf16x2(top, y[j] & 0x7fff7fffu);
                     }
                     const uint32_t m1 = max(top & 0xffffu, top >> 16);
                     plain = !__any_sync(0xffffffffu, m1 >= 0x7f80u);
@@ -748,7 +756,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 // row by row of the sequence: the keys it does not see are zeros in V, and
                 // the product is added to its own columns only
                 for (int i0 = 0; i0 < u.rows; ++i0) {
-                    const int p = __shfl_sync(0xffffffffu, row_pos(u), i0);
+                    const int p = __shfl_sync(0xffffffffu, upos, i0);
                     auto word = [&](int key) -> uint32_t {
                         auto seen = [&](int x) {
                             return (mt >> (10 + i0) & 1u) != 0 && x >= a && x < z && at + x <= p &&
@@ -770,8 +778,10 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                             float y[4];
                             mma_bf16_first(y, x, pb[nt][0], pb[nt][1]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (bit[nt][e & 1] == 1u << i0) o[i][nt][e] += y[e];
+                            for (int e = 0; e < 4; ++e) {
+                                const int r = 8 * nt + 2 * t4 + (e & 1);
+                                if (r < R && r * inv >> 16 == i0) o[i][nt][e] += y[e];
+                            }
                         }
                     }
                 }
