@@ -7,6 +7,8 @@
 // read once, 16 bytes a lane, all of a page of 64 under way at a time; maxima and
 // minima are taken of bf16 pairs, exactly.  Bound by HBM (2 D bytes a key) where pages
 // are whole, by latency on a decode step, which reads one page a sequence and head.
+// 69575 keys of 8 heads: 27 us for 21.8 of HBM time; 64 sequences' last pages 2.8 us in a
+// graph, 5 from the host.
 #include <algorithm>
 
 #include "pa_cache_common.cuh"
@@ -44,7 +46,7 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = blockIdx.y;
     grid_dependency_wait();
     const int r0 = blockIdx.x * rows, r1 = min(r0 + rows, g.total_q);
-    int turn = 0;                        // (s_part of one page is read while the next fills the other)
+    int turn = 0;                        // (one half of s_part is read, the next page fills the other)
     for (int c = r0; c < r1; c += 32) {
         const int r = c + lane;
         const int slot = r < r1 ? slots[r] : -1;
@@ -131,7 +133,8 @@ bounds_kernel(const CacheGeom g, const __nv_bfloat16* __restrict__ k,
                     const uint32_t w = up ? hi[i] : lo[i];
                     const int x = code_of(__uint_as_float(w << 16), inv, up);
                     const int y = code_of(__uint_as_float(w & 0xffff0000u), inv, up);
-                    word[i / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8) << (16 * (i & 1));
+                    word[i / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8)
+                                   << (16 * (i & 1));
                 }
                 const int64_t row = (int64_t)page * g.Hkv + hk;
                 reinterpret_cast<uint2*>(bounds + row * 2 * D + (up ? 0 : D))[lane % C] =

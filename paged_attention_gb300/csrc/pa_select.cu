@@ -5,8 +5,8 @@
 //         = 2^e_page max_h 2^e_h [max(q8, 0), min(q8, 0)] . [hi, lo]
 //
 // so a group's scores are products of whole-number matrices: 16 pages by 8 heads a
-// product.  They are taken in f16 (mma m16n8k16, fp32 sums), whose rate is ten times
-// that of 8-bit integers here (64 rows of up to 459 pages: 11.2 us with those).  A code
+// product.  They are taken in f16 (mma m16n8k16, fp32 sums): products of 8-bit integers
+// are slow here (with them the scores of 64 rows took 2 us more than their loads alone).  A code
 // c becomes the f16 1152 + c by one permutation of bytes a pair; 64 codes a sum stay
 // below 2^24, so every sum is exact, and 1152 times the sum of q8 is taken off it.  The
 // contraction's order being free, a lane takes 16 bytes of a page's bounds as they lie.
@@ -17,6 +17,10 @@
 // until a pass decides all, and lists the pages in order.  As many CTAs a cluster as it
 // takes to fill the GPU.  Bound by the latency of its steps (row, page numbers, bounds,
 // two or three passes), by HBM (2 D bytes a page and head) for many rows of long contexts.
+// 64 rows of up to 459 pages, 8 heads: 10.4 us; one row of 8192 pages 17, 5.5 of them the
+// scores on 64 SMs (clusters of 12 CTAs, which are not portable: 16.2).  Slower here: fewer
+// registers and more CTAs an SM (12.3 to 14.2 and 21 to 23), clusters of 16 (22: one of
+// eight waits for the others), pages pruned by groups' largest scores (11.2 and 19).
 #include <algorithm>
 
 #include "pa_cache_mma.cuh"
@@ -30,11 +34,11 @@ constexpr int kMaxCluster = 8;
 constexpr float kBias = 1152.f;  // of a code's f16
 constexpr int kMaxGroup = 64;    // q heads of a KV head
 constexpr int kBins = 256;
-constexpr int kTile = 32;        // pages of a warp at a time: two products' rows, all their loads under way
+constexpr int kTile = 32;        // pages of a warp at a time: two products' rows
 
 constexpr uint32_t kKept = 0xffffffffu;      // key of a page that is kept whatever its score
 
-// A query row in shared memory: 2 D f16, and padding (lanes of a 16-byte load meet few banks twice)
+// A query row in shared memory: 2 D f16, and padding (so that rows begin on other banks)
 constexpr int q_row_bytes(int D) { return 4 * D + 16; }
 
 // Larger scores (never NaN) get larger keys, all above 0.
@@ -320,9 +324,9 @@ select_kernel(const __grid_constant__ SelectParams P) {
             // one warp, eight bins a lane: in which one is the take-th from the top?
             if (warp == 0) {
                 uint32_t h[8], sum = 0;
-                *reinterpret_cast<uint4*>(h) = reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane];
-                *reinterpret_cast<uint4*>(h + 4) =
-                    reinterpret_cast<const uint4*>(s_hist[pass])[2 * lane + 1];
+                const uint4* bins = reinterpret_cast<const uint4*>(s_hist[pass]) + 2 * lane;
+                *reinterpret_cast<uint4*>(h) = bins[0];
+                *reinterpret_cast<uint4*>(h + 4) = bins[1];
 #pragma unroll
                 for (int d = 0; d < 8; ++d) sum += h[d];
                 uint32_t upto = sum;
@@ -451,7 +455,8 @@ cudaError_t launch_select(const SelectParams& P0, int sms, cudaStream_t stream) 
     const int64_t units = (int64_t)P.g.total_q * P.g.Hkv;
     while (c < kMaxCluster && units * c < 2 * sms && pages >= 128 * c) c *= 2;
     P.cluster = c;
-    const int smem = (P.g.G + 7) / 8 * 8 * q_row_bytes(P.g.D) + pages * 4;
+    // (keys are read four at a time)
+    const int smem = (P.g.G + 7) / 8 * 8 * q_row_bytes(P.g.D) + (pages + 3) / 4 * 16;
     // (more threads where a CTA scores or selects from many)
     if (pages > 1024)
         return P.g.D == 128 ? launch<128, 512>(P, smem, stream) : launch<64, 512>(P, smem, stream);

@@ -14,7 +14,9 @@ constexpr int kMaxGridSel = 1024;        // CTAs of pa_decode_selected
 // the bytes with head_dim 64.  64 rows of up to 32 pages of 64: 61 us with 1 to 8, 62 with
 // 12; head_dim 64 46.8 with 1, 38.9 with 6; 64 sequences of 4 rows (16 query rows a
 // unit) 85 with 3, 80 with 6; 128 sequences of 3 rows (24) 223, 215 with 6, 213 with 12.
-constexpr int sel_unit_cost(int D, int rows) { return (rows > 16 ? 10 : rows > 8 ? 6 : 3) * 128 / D; }
+constexpr int sel_unit_cost(int D, int rows) {
+    return (rows > 16 ? 10 : rows > 8 ? 6 : 3) * 128 / D;
+}
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const char* x = static_cast<const char*>(a);
@@ -60,7 +62,9 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
         L.grid *= selected_ctas_per_sm();
         if (L.grid > kMaxGridSel) L.grid = kMaxGridSel;
     }
-    L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : sel_unit_cost(g.D, 8 * L.nt);
+    L.unit_cost = pp->unit_cost > 0   ? pp->unit_cost
+                  : pp->unit_cost < 0 ? 0
+                                      : sel_unit_cost(g.D, 8 * L.nt);
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
     L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * 4);
