@@ -63,12 +63,11 @@ enum { PA_DEV_NO_PAGES = 16 };
  *   so too, with PA_DEV_BAD_LENGTHS (context_lens[b] is then cut to [0,
  *   max_context_len]).  Its q_lens, cut to [0, max_q_len], still count in where the
  *   rows of the sequences after it are.
- *   kv_dtype may be any; at most PA_MAX_STEP_SEQS sequences.
+ *   kv_dtype may be any.  num_pages * page_size at most 2^31 - 1.
  *   context_lens and free_left must not overlap any input; page numbers outside
  *   the pool on the stack are passed on as they are, with PA_DEV_BAD_PAGE, and
  *   slots of -1.
  */
-#define PA_MAX_STEP_SEQS 65536
 PA_API pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_lens,
                                const int32_t* q_lens, int32_t* block_table,
                                const int32_t* free_pages, const int32_t* free_count,
@@ -202,7 +201,8 @@ PA_API pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache,
  *     sequence (positions / page_size), ascending, then -1: all pages where no
  *     more than budget are seen.  Rows that are skipped are left as they are.
  *   A page whose block-table entry is outside the pool has the lowest score
- *   (PA_DEV_BAD_PAGE, where scores are needed at all).
+ *   (PA_DEV_BAD_PAGE, where scores are needed at all), and so has one whose
+ *   bound_scale is negative or NaN: no bounds were written for it.
  *   budget >= 1; num_first, num_recent >= 0, together at most budget.  At most 64
  *   q heads a KV head; a context of at most PA_MAX_SELECT_PAGES pages
  *   (max_context_len / page_size): 720,896 tokens in pages of 16, 2.9 million of 64; num_ctas, kv_dtype and sm_scale have no part in it.

@@ -196,14 +196,22 @@ join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
     const int seq = P.row_seq[t];
     int m = 0;                         // rows of the unit that t leads
     if (seq >= 0 && seq < g.B) {
-        // rows of the sequence before t
+        // rows of the sequence before t, 128 looked at together
         int before = 0;
-        while (true) {
-            const int r = t - 1 - before - lane;
-            const uint32_t other =
-                __ballot_sync(0xffffffffu, r < 0 || P.row_seq[max(r, 0)] != seq);
-            before += other != 0 ? __ffs(other) - 1 : 32;
-            if (other != 0) break;
+        bool here = true;
+        while (here) {
+            uint32_t other[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = t - 1 - before - 32 * j - lane;
+                other[j] = __ballot_sync(0xffffffffu, r < 0 || P.row_seq[max(r, 0)] != seq);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (here) {
+                    before += other[j] != 0 ? __ffs(other[j]) - 1 : 32;
+                    here = other[j] == 0;
+                }
         }
         if (before % most == 0) {
             const int r = t + lane;

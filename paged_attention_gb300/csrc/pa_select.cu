@@ -41,8 +41,10 @@ constexpr uint32_t kKept = 0xffffffffu;      // key of a page that is kept whate
 // A query row in shared memory: 2 D f16, and padding (so that rows begin on other banks)
 constexpr int q_row_bytes(int D) { return 4 * D + 16; }
 
-// Larger scores (never NaN) get larger keys, all above 0.
+// Larger scores get larger keys, all above 0; NaN (a scale that no bounds were written
+// for) the smallest.
 __device__ __forceinline__ uint32_t key_of(float score) {
+    if (score != score) return 0u;
     const uint32_t u = __float_as_uint(score + 0.f);   // -0 counts as 0
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }

@@ -30,9 +30,7 @@ pa_status page_geometry(const pa_problem* pp, CacheGeom& g) {
     pa_problem p = *pp;
     if (p.kv_dtype == PA_FP8_E4M3) p.kv_dtype = PA_BF16;
     if (p.q_dtype == PA_FP8_E4M3) p.q_dtype = PA_BF16;
-    const pa_status st = geometry(&p, false, g);
-    if (st != PA_OK) return st;
-    return g.B > PA_MAX_STEP_SEQS ? PA_ERR_UNSUPPORTED : PA_OK;
+    return geometry(&p, false, g);
 }
 bool slots_fit(const CacheGeom& g) { return (int64_t)g.num_pages * g.ps <= 0x7fffffff; }
 

@@ -493,6 +493,16 @@ def test_selection_of_ties_odd_queries_and_bad_pages():
         want = R.select(q[t], bnd[:, 0], sc[:, 0], table, n * page - 1, budget=budget, num_first=0,
                         num_recent=2, page=page, pages=n, window=0)
         assert sel[t, 0].tolist() == want, t
+    # a page whose scale is none is the last to be listed
+    odd = sc.clone()
+    odd[3], odd[7, 0], odd[100] = math.nan, -1.0, math.inf
+    got = torch.full_like(sel, -3)
+    B.pa_select_pages(p, budget, 0, 2, q.cuda(), bnd.cuda(), odd.cuda(), ints([table]),
+                      ints([0] * 6), ints([n * page - 1] * 6), got, err)
+    for t in range(6):
+        row = got[t, 0].tolist()
+        assert row == sorted(set(row)) and 0 <= row[0] and row[-2:] == [n - 2, n - 1]
+        assert 3 not in row and 7 not in row
     # the cache's type has no part in it
     for kv in (B.PA_FP8_E4M3, B.PA_MX4):
         p.kv_dtype = kv
@@ -642,6 +652,7 @@ def test_attention(D, G, Hkv, page, layout, window, budget, ctx, ql, mode, ctas)
     (64, 20, 2, 32, 0, 0, 4, [700, 90], [3, 1], "plain"),
     (64, 1, 1, 16, 0, 0, 50, [70000, 90], [5, 1], "plain"),
     (128, 3, 2, 16, 0, 0, 5, [100, 20], [3, 2], "none"),
+    (64, 4, 1, 16, 0, 0, 6, [300, 9], [300, 9], "plain"),
 ])
 def test_attention_of_rows_of_one_sequence(D, G, Hkv, page, layout, window, budget, ctx, ql, mode,
                                            ctas):

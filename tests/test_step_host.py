@@ -129,7 +129,6 @@ def test_refusals_of_their_own(lib):
     for j in (0, 1):                          # the last of three lengths
         last = ctypes.c_void_p(t[j].value + 8)
         assert call(lib, "pa_pages_take", problem(), swap("pa_pages_take", 9, last)) == bad
-    assert call(lib, "pa_pages_take", problem(num_seqs=65537)) == no
     assert call(lib, "pa_pages_return", problem(),
                 swap("pa_pages_return", 5, GOOD["pa_pages_return"][4])) == bad
     r = "pa_rope_append"
