@@ -13,7 +13,7 @@
 //
 // One cluster of CTAs a row and KV head, each scoring a part of the pages; the scores go,
 // as order-preserving integers, to the first CTA's shared memory, which finds the
-// budget-th largest by a radix select over the bits in which they differ, eight a pass,
+// budget-th largest by a radix select over the bits in which they differ, eleven a pass,
 // until a pass decides all, and lists the pages in order.  As many CTAs a cluster as it
 // takes to fill the GPU.  Bound by the latency of its steps (row, page numbers, bounds,
 // two or three passes), by HBM (2 D bytes a page and head) for many rows of long contexts.
@@ -33,7 +33,8 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr float kBias = 1152.f;  // of a code's f16
 constexpr int kMaxGroup = 64;    // q heads of a KV head
-constexpr int kBins = 256;
+constexpr int kBinBits = 11;
+constexpr int kBins = 1 << kBinBits;
 constexpr int kTile = 32;        // pages of a warp at a time: two products' rows
 
 constexpr uint32_t kKept = 0xffffffffu;      // key of a page that is kept whatever its score
@@ -81,14 +82,16 @@ template <int D, int kThreads>
 __global__ void __launch_bounds__(kThreads, 512 / kThreads)
 select_kernel(const __grid_constant__ SelectParams P) {
     constexpr int kWarps = kThreads / 32;
-    static_assert(kThreads >= kBins, "a thread a bin");
+    constexpr int kMine = kBins / kThreads;      // bins of a thread
+    static_assert(kMine % 4 == 0, "read four at a time");
     constexpr int J = 2 * D / 64;                // 64-byte runs of a page's bounds
     constexpr int RT = kTile / 8;                // page rows of a lane
     constexpr int kQRow = q_row_bytes(D);
     extern __shared__ __align__(16) uint8_t smem[];      // queries; the cluster's keys
     __shared__ float s_factor[kMaxGroup];
     __shared__ float s_bias[kMaxGroup][J];       // what the bias of the codes adds to a run's sum
-    __shared__ __align__(16) uint32_t s_hist[4][kBins];  // of each pass
+    __shared__ __align__(16) uint32_t s_hist[2][kBins];    // of one pass and the next
+    __shared__ uint32_t s_warp[kWarps];
     __shared__ uint2 s_range[kWarps];
     __shared__ int2 s_part[kWarps];
     __shared__ int3 s_found;
@@ -99,8 +102,23 @@ select_kernel(const __grid_constant__ SelectParams P) {
     const int t = unit / g.Hkv, hk = unit % g.Hkv;
     const int tiles = (g.G + 7) / 8;
     uint32_t* s_key = reinterpret_cast<uint32_t*>(smem + 8 * tiles * kQRow);
+    for (int i = tid; i < 2 * kBins / 4; i += kThreads)
+        reinterpret_cast<uint4*>(&s_hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     grid_dependency_wait();
 
+    // a warp's head: lane l has the words l * D / 64 .. of its query row (0: no such head)
+    uint32_t q_words[D / 64];
+    auto load_q = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) q_words[i] = 0u;
+        if (h < g.G) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                P.q + ((int64_t)t * g.Hq + (int64_t)hk * g.G + h) * D);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) q_words[i] = src[lane * (D / 64) + i];
+        }
+    };
+    load_q(warp);
     // (the cluster's CTAs leave together: they all look at the same row)
     const int b = P.row_seq[t], pos = P.positions[t];
     if (b < 0) return;
@@ -146,19 +164,12 @@ select_kernel(const __grid_constant__ SelectParams P) {
 
     // ---- the group's queries in 8 bits, as f16: positive, then negative parts
     for (int h = warp; h < 8 * tiles; h += kWarps) {
-        uint32_t w[D / 64];
+        if (h != warp) load_q(h);
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) w[i] = 0u;
-        if (h < g.G) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                P.q + ((int64_t)t * g.Hq + (int64_t)hk * g.G + h) * D);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                w[i] = src[lane * (D / 64) + i];
-                const uint32_t x = w[i] & 0x7fffu, y = (w[i] >> 16) & 0x7fffu;
-                top = max(top, max(x > 0x7f80u ? 0u : x, y > 0x7f80u ? 0u : y));   // NaN: none
-            }
+        for (int i = 0; i < D / 64; ++i) {
+            const uint32_t x = q_words[i] & 0x7fffu, y = (q_words[i] >> 16) & 0x7fffu;
+            top = max(top, max(x > 0x7f80u ? 0u : x, y > 0x7f80u ? 0u : y));   // NaN: none
         }
         const uint32_t most = __reduce_max_sync(0xffffffffu, top);
         // least e with most <= 127 * 2^e = 1.984375 * 2^(e + 6)
@@ -166,12 +177,12 @@ select_kernel(const __grid_constant__ SelectParams P) {
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint32_t w0, w1;
         if constexpr (D == 128) {
-            w0 = w[0];
-            w1 = w[1];
+            w0 = q_words[0];
+            w1 = q_words[1];
         } else {
             // (a lane has a word, its neighbour the rest of its four codes)
-            w0 = __shfl_sync(0xffffffffu, w[0], 2 * (lane & 15));
-            w1 = __shfl_sync(0xffffffffu, w[0], 2 * (lane & 15) + 1);
+            w0 = __shfl_sync(0xffffffffu, q_words[0], 2 * (lane & 15));
+            w1 = __shfl_sync(0xffffffffu, q_words[0], 2 * (lane & 15) + 1);
         }
         float c[4];
         q_codes(w0, w1, inv, c);
@@ -199,7 +210,6 @@ select_kernel(const __grid_constant__ SelectParams P) {
         }
         if (lane == 0) s_factor[h] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
-    for (int i = tid; i < 4 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
     // (a cluster's first CTA must have begun before the others write to it)
     __syncthreads();
     if (C > 1) cluster_wait();
@@ -316,35 +326,46 @@ select_kernel(const __grid_constant__ SelectParams P) {
         int shift = 32 - __clz(least ^ most);    // bits that differ (0: all keys are equal)
         uint32_t prefix = shift < 32 ? most >> shift : 0u;
         for (int pass = 0; shift > 0; ++pass) {
-            const int width = min(8, shift);
+            const int width = min(kBinBits, shift);
+            uint32_t* hist = s_hist[pass & 1];
+            if (pass > 0)                        // (the last one's is read; a third pass has it)
+                for (int i = tid; i < kBins / 4; i += kThreads)
+                    reinterpret_cast<uint4*>(s_hist[pass & 1 ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
             for (int i = tid; i < n; i += kThreads) {
                 const uint32_t x = s_key[i];
                 if (x != kKept && (shift == 32 || x >> shift == prefix))
-                    atomicAdd(&s_hist[pass][(x >> (shift - width)) & ((1u << width) - 1u)], 1u);
+                    atomicAdd(&hist[(x >> (shift - width)) & ((1u << width) - 1u)], 1u);
             }
             __syncthreads();
-            // one warp, eight bins a lane: in which one is the take-th from the top?
-            if (warp == 0) {
-                uint32_t h[8], sum = 0;
-                const uint4* bins = reinterpret_cast<const uint4*>(s_hist[pass]) + 2 * lane;
-                *reinterpret_cast<uint4*>(h) = bins[0];
-                *reinterpret_cast<uint4*>(h + 4) = bins[1];
+            // a thread has kMine bins: in which one is the take-th from the top?
+            uint32_t h[kMine], sum = 0;
 #pragma unroll
-                for (int d = 0; d < 8; ++d) sum += h[d];
-                uint32_t upto = sum;
+            for (int d = 0; d < kMine; d += 4) {
+                const uint4 v = reinterpret_cast<const uint4*>(hist + tid * kMine)[d / 4];
+                h[d] = v.x;
+                h[d + 1] = v.y;
+                h[d + 2] = v.z;
+                h[d + 3] = v.w;
+                sum += v.x + v.y + v.z + v.w;
+            }
+            uint32_t upto = sum;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
-                    if (lane + o < 32) upto += y;
-                }
-                uint32_t above = upto - sum;
-                if (upto >= (uint32_t)take && above < (uint32_t)take) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
+                if (lane + o < 32) upto += y;
+            }
+            if (lane == 0) s_warp[warp] = upto;
+            __syncthreads();
+            uint32_t above = upto - sum;
 #pragma unroll
-                    for (int d = 7; d >= 0; --d) {
-                        if (above < (uint32_t)take && above + h[d] >= (uint32_t)take)
-                            s_found = make_int3(8 * lane + d, (int)h[d], (int)above);
-                        above += h[d];
-                    }
+            for (int w = 1; w < kWarps; ++w)
+                if (w > warp) above += s_warp[w];
+            if (above < (uint32_t)take && above + sum >= (uint32_t)take) {   // one thread
+#pragma unroll
+                for (int d = kMine - 1; d >= 0; --d) {
+                    if (above < (uint32_t)take && above + h[d] >= (uint32_t)take)
+                        s_found = make_int3(tid * kMine + d, (int)h[d], (int)above);
+                    above += h[d];
                 }
             }
             __syncthreads();
