@@ -8,8 +8,8 @@
 // tokens between them in 16-token steps, every warp with its own running (max, sum,
 // O), its own ring of cp.async stages that runs ahead over unit boundaries, and no
 // barrier until the unit ends.  Then the warps' states merge through shared memory;
-// a unit that spans CTAs leaves normalised parts in the workspace, and the last CTA
-// to finish one joins them.
+// a unit that spans CTAs leaves normalised parts in the workspace, and the last warp
+// to leave a part of a query row joins that row's.
 //
 // What bounds it: 4 D bytes a listed key and head from HBM.  A page is 16 tokens or
 // a multiple, so a step lies in one page, and one look at its list entry tells which
@@ -51,12 +51,16 @@ struct SelCfg {
     static constexpr int kMergeRows = 4;                   // rows merged at a time
     static constexpr int kMergeRow = D + 4;                // floats
     static constexpr int kMergeWarp = kMergeRows * kMergeRow + 2 * kMergeRows;
+    // eight rows: every warp has their queries in registers, and merges alternate between
+    // two buffers, so that a unit costs one barrier
+    static constexpr bool kQInRegs = NT == 1;
+    static constexpr int kBuffers = NT == 1 ? 2 : 1;
+    static constexpr int kMergeFloats = kWarps * kMergeWarp;
     static constexpr int kOffQ = kWarps * kStages * kStage;
-    static constexpr int kOffMerge = kOffQ + kRows * kQRow;
-    static constexpr int kOffFlag = kOffMerge + kWarps * kMergeWarp * 4;
-    static constexpr int kSmem = kOffFlag + 16;
+    static constexpr int kOffMerge = kOffQ + (kQInRegs ? 0 : kRows * kQRow);
+    static constexpr int kSmem = kOffMerge + kBuffers * kMergeFloats * 4;
     static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
-    static_assert(kOffQ % 16 == 0 && kOffMerge % 16 == 0 && kOffFlag % 16 == 0, "alignment");
+    static_assert(kOffQ % 16 == 0 && kOffMerge % 16 == 0, "alignment");
 };
 
 namespace {
@@ -66,6 +70,7 @@ namespace {
 // heads: 15.7 us with 2, 14.5 with 3, 13.7 with 4).
 constexpr int kMinShareSel = 4;
 
+constexpr int kDoneRows = kSelDoneRows;       // counters of a CTA: one a query row
 constexpr int kMostRows = 6;                  // of a unit: what an entry has bits for
 constexpr int kRowBits = 26;                  // a page index is below 2^26 (a context below 2^30)
 
@@ -400,7 +405,6 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::kStage;
     const uint32_t qbase = smem_u32(smem + Cfg::kOffQ);
     float* merge = reinterpret_cast<float*>(smem + Cfg::kOffMerge);
-    volatile int* flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffFlag);
 
     // ---- the load side runs ST - 1 steps ahead, over unit boundaries
     constexpr int CH = ROW / 16, RPI = 32 / CH;   // pieces of a row, rows an instruction
@@ -548,26 +552,32 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     for (int s = 0; s < ST - 1; ++s) issue(s);
     int stage = 0;
 
-    // ---- Q rows of a unit, one warp a row: read ahead of the unit that needs them
-    constexpr int QPW = Cfg::kRows / W, QW = D / 64;
-    constexpr bool kQAhead = NT <= 2;         // (registers that many rows need for O)
+    // ---- Q rows of a unit, read ahead of the unit that needs them (not where O needs the
+    // registers): the B operands themselves, or a row of a warp's for shared memory
+    constexpr bool kQInRegs = Cfg::kQInRegs;
+    constexpr bool kQAhead = NT <= 2;
+    constexpr int QPW = kQInRegs ? 1 : Cfg::kRows / W, QW = kQInRegs ? KK * 2 : D / 64;
     uint32_t qw[QPW][QW];
+    auto q_row = [&](const SelUnit& x, int r) -> const uint32_t* {
+        return reinterpret_cast<const uint32_t*>(
+            P.q + (JOINED ? (int64_t)(x.row + r / g.G) * g.Hq + (int64_t)x.hk * g.G + r % g.G
+                          : (int64_t)x.row * g.Hq + (int64_t)x.hk * g.G + r) * D);
+    };
     auto load_q = [&](const SelUnit& x) {
 #pragma unroll
         for (int i = 0; i < QPW; ++i) {
-            const int r = warp + i * W;
+            const int r = kQInRegs ? gr : warp + i * W;
 #pragma unroll
             for (int j = 0; j < QW; ++j) qw[i][j] = 0u;
             if (r < x.rows * g.G) {
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                    P.q + (JOINED ? (int64_t)(x.row + r / g.G) * g.Hq + (int64_t)x.hk * g.G + r % g.G
-                                  : (int64_t)x.row * g.Hq + (int64_t)x.hk * g.G + r) * D);
+                const uint32_t* src = q_row(x, r);
 #pragma unroll
-                for (int j = 0; j < QW; ++j) qw[i][j] = src[lane + 32 * j];
+                for (int j = 0; j < QW; ++j) qw[i][j] = src[kQInRegs ? 4 * j + t4 : lane + 32 * j];
             }
         }
     };
     if constexpr (kQAhead) load_q(u);
+    int buffer = 0;
 
     // (never 0, so that a masked score times it stays -inf)
     const float f = fmaxf(g.sm_scale * kLog2e, 1.2e-38f);
@@ -576,13 +586,19 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         const SelShare sh = share(u);
         const int R = u.rows * g.G;
         if constexpr (!kQAhead) load_q(u);
+        uint32_t qf[kQInRegs ? QW : 1];
+        if constexpr (kQInRegs) {
 #pragma unroll
-        for (int i = 0; i < QPW; ++i)
+            for (int j = 0; j < QW; ++j) qf[j] = qw[0][j];
+        } else {
 #pragma unroll
-            for (int j = 0; j < QW; ++j)
-                *reinterpret_cast<uint32_t*>(smem + Cfg::kOffQ + (warp + i * W) * Cfg::kQRow +
-                                             4 * (lane + 32 * j)) = qw[i][j];
-        __syncthreads();
+            for (int i = 0; i < QPW; ++i)
+#pragma unroll
+                for (int j = 0; j < QW; ++j)
+                    *reinterpret_cast<uint32_t*>(smem + Cfg::kOffQ + (warp + i * W) * Cfg::kQRow +
+                                                 4 * (lane + 32 * j)) = qw[i][j];
+            __syncthreads();
+        }
         SelUnit nu = u;
         const bool has_next = next_unit<JOINED>(P, nu) && nu.start < hi;
         if (kQAhead && has_next) load_q(nu);
@@ -600,24 +616,11 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         // JOINED: lane i has row i's position; query row r is of row r / G = r * inv >> 16
         const int upos = JOINED ? row_pos(u) : 0;
         const int inv = JOINED ? 65535 / g.G + 1 : 0;
-        constexpr bool kQInRegs = NT == 1;
-        uint32_t qf[kQInRegs ? KK : 1][2];
         // the B operands of two contraction steps: rows 8 nt + (lane & 7), piece 2 kk + lane / 8
         auto q_frag = [&](int nt, int kk, uint32_t* x) {
             ldsm_x4(qbase + (8 * nt + (lane & 7)) * Cfg::kQRow + (2 * kk + (lane >> 3)) * 16, x[0],
                     x[1], x[2], x[3]);
         };
-        if constexpr (kQInRegs) {
-#pragma unroll
-            for (int kk = 0; kk < KK; kk += 2) {
-                uint32_t x[4];
-                q_frag(0, kk, x);
-                qf[kk][0] = x[0];
-                qf[kk][1] = x[1];
-                qf[kk + 1][0] = x[2];
-                qf[kk + 1][1] = x[3];
-            }
-        }
 
 #pragma unroll 1
         for (int tok = sh.a; tok < sh.z; tok += 16) {
@@ -651,8 +654,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         if constexpr (kQInRegs) {
-                            mma_bf16_16816(s[nt], x, qf[kk][0], qf[kk][1]);
-                            mma_bf16_16816(s1[nt], y, qf[kk + 1][0], qf[kk + 1][1]);
+                            mma_bf16_16816(s[nt], x, qf[2 * kk], qf[2 * kk + 1]);
+                            mma_bf16_16816(s1[nt], y, qf[2 * kk + 2], qf[2 * kk + 3]);
                         } else {
                             uint32_t b[4];
                             q_frag(nt, kk, b);
@@ -823,7 +826,8 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             for (int r0 = 0; r0 < Cfg::kRows; r0 += MR) {
                 if (r0 >= R) break;
                 const int nt = r0 / 8;
-                float* mw = merge + warp * Cfg::kMergeWarp;
+                float* area = merge + (Cfg::kBuffers > 1 ? buffer * Cfg::kMergeFloats : 0);
+                float* mw = area + warp * Cfg::kMergeWarp;
                 // rows r0 .. r0 + 3 are with the lanes whose pairs are these columns
                 const bool mine = t4 / 2 == (r0 % 8) / 4;
 #pragma unroll
@@ -854,13 +858,13 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     float M = kUnseen;
 #pragma unroll
                     for (int w = 0; w < W; ++w)
-                        M = fmaxf(M, merge[w * Cfg::kMergeWarp + MR * Cfg::kMergeRow + mr]);
+                        M = fmaxf(M, area[w * Cfg::kMergeWarp + MR * Cfg::kMergeRow + mr]);
                     float den = 0.f, acc[DPL];
 #pragma unroll
                     for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        const float* b = merge + w * Cfg::kMergeWarp;
+                        const float* b = area + w * Cfg::kMergeWarp;
                         const float mv = b[MR * Cfg::kMergeRow + mr];
                         const float lv = b[MR * Cfg::kMergeRow + MR + mr];
                         if (mv == kUnseen && lv == 0.f) continue;     // saw nothing
@@ -894,28 +898,34 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         if (lane == 0) P.part_lse[row] = ln2;
                     }
                 }
-                __syncthreads();
+                // (two buffers: the next barrier comes before this one is written again)
+                if constexpr (Cfg::kBuffers > 1)
+                    buffer ^= 1;
+                else
+                    __syncthreads();
             }
             if (part >= 0) {
-                // the last of the unit's CTAs to come here joins the parts (nobody
-                // waits for another CTA)
-                if (threadIdx.x == 0) {
-                    __threadfence();   // every warp's part is written (barrier above)
-                    const uint32_t before = (uint32_t)atomicAdd(P.done + c_first, 1);
-                    const bool last = before == (uint32_t)(c_last - c_first);
-                    if (last) P.done[c_first] = 0;   // as the next call finds it
+                // every row for itself: the last warp to leave a part of it joins them (nobody
+                // waits for another); lane i counts the warp's i-th row
+                const uint32_t others = (uint32_t)(c_last - c_first);
+                bool last = false;
+                __syncwarp();
+                __threadfence();                 // the warp's parts are written
+                if (warp + W * lane < R) {
+                    int32_t* count = P.done + c_first * kDoneRows + warp + W * lane;
+                    const uint32_t earlier = (uint32_t)atomicAdd(count, 1);
+                    last = earlier == others;
+                    if (last) *count = 0;        // as the next call finds it
                     // (nobody will come last: the workspace did not start as zeros)
-                    if (before > (uint32_t)(c_last - c_first))
-                        flag_error(P.header + H_ERROR, PA_DEV_BAD_WORKSPACE);
-                    __threadfence();
-                    *flag = last ? 1 : 0;
+                    if (earlier > others) flag_error(P.header + H_ERROR, PA_DEV_BAD_WORKSPACE);
                 }
-                __syncthreads();
-                const bool last = *flag != 0;
                 __threadfence();
-                if (last) {
+                uint32_t ends = __ballot_sync(0xffffffffu, last);
+                __syncwarp();                    // (a vote orders no memory)
+                {
                     constexpr int DPL = D / 32;
-                    for (int r = warp; r < R; r += W) {
+                    for (; ends != 0; ends &= ends - 1) {
+                        const int r = warp + W * (__ffs(ends) - 1);
                         // part c of the unit is in slot 2 c (the first in 2 c + 1); 32
                         // parts' lse at a time, one a lane
                         auto part_row = [&](int c) {
@@ -984,7 +994,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             }
         }
         if (!has_next) break;
-        if (sh.t1 <= sh.t0) __syncthreads();   // all have read this unit's Q rows
+        if (!kQInRegs && sh.t1 <= sh.t0) __syncthreads();   // all have read this unit's Q rows
         u = nu;
     }
     cp_async_wait<0>();

@@ -34,8 +34,8 @@ pa_status page_geometry(const pa_problem* pp, CacheGeom& g) {
 }
 bool slots_fit(const CacheGeom& g) { return (int64_t)g.num_pages * g.ps <= 0x7fffffff; }
 
-// Workspace of pa_decode_selected: header (error word) and the counters of as many
-// CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +
+// Workspace of pa_decode_selected: header (error word) and the counters, one a query
+// row, of as many CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +
 // 1 floats; where several rows of a sequence may be one unit, the units and their
 // joined lists.
 struct SelLayout {
@@ -65,7 +65,7 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
                                       : sel_unit_cost(g.D, 8 * L.nt);
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
-    L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * 4);
+    L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * kSelDoneRows * 4);
     L.off_lead = align256(L.off_part + 2 * (int64_t)L.grid * L.rows * (g.D + 1) * 4);
     L.off_entries = L.off_list = L.total = L.off_lead;
     if (L.together > 1) {

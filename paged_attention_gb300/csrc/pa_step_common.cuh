@@ -51,7 +51,7 @@ struct SelectedParams {
     const int32_t* positions;
     const int32_t* selected;
     int32_t* header;     // error word at H_ERROR
-    int32_t* done;       // completion counter of the unit a CTA begins
+    int32_t* done;       // completion counters of the rows of the unit a CTA begins
     float* part_o;       // [2 * grid][rows][D]
     float* part_lse;     // [2 * grid][rows]
     __nv_bfloat16* out;
@@ -65,6 +65,8 @@ struct SelectedParams {
     int32_t* unit_entries;
     int2* list;          // page number, index in the sequence and rows
 };
+
+constexpr int kSelDoneRows = 64;     // query rows of a unit of pa_decode_selected, at most
 
 cudaError_t launch_pages_take(const CacheGeom& g, const int32_t* seq_lens, const int32_t* q_lens,
                               int32_t* table, const int32_t* free_pages, const int32_t* free_count,

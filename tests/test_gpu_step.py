@@ -545,7 +545,7 @@ def check_attend(p, budget, table, seq, pos, k, v, q, sel, code=0, repeat=1):
     for _ in range(repeat):
         B.pa_decode_selected(p, budget, *args, out, lse)
     assert B.pa_last_device_error(ws) == code
-    assert not ws[256:4352].any()             # the counters as the next call finds them
+    assert not ws[256:256 + 1024 * 64 * 4].any()   # the counters as the next call finds them
     for t in range(T):
         if not (0 <= seq[t] < p.num_seqs and 0 <= pos[t] < p.max_context_len):
             assert torch.all(out[t] == 7) and torch.all(lse[t] == 7)
@@ -861,7 +861,7 @@ def test_a_workspace_that_was_never_filled_is_reported():
     p = problem(num_q_heads=1, num_kv_heads=1, head_dim=D, num_pages=pages, max_pages_per_seq=64,
                 max_context_len=1024, num_ctas=5)
     ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
-    ws[256:4352] = 1
+    ws[256:256 + 1024 * 64 * 4] = 1
     out, lse = torch.zeros((1, 1, D), dtype=BF16, device="cuda"), torch.zeros((1, 1)).cuda()
     args = (q.cuda(), k.cuda(), v.cuda(), ints(table), ints(seq), ints(pos), ints(sel), ws)
     B.pa_decode_selected(p, budget, *args, out, lse)
