@@ -24,6 +24,7 @@
  *   number, block-table entry or slot outside the pool; PA_DEV_NO_PAGES.  The
  *   rows, pages or sequences concerned are skipped, the rest is done.
  *
+ * total_q_tokens: at most 2^30 (more: PA_ERR_UNSUPPORTED).
  * total_q_tokens = 0 (all but pa_pages_*): returns PA_OK after the checks of the
  *   problem (and of the workspace) and launches nothing; the other pointers may
  *   be NULL.
@@ -81,7 +82,8 @@ PA_API pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_len
  * accepted).  The pages that hold none of those go on top of the stack, sequences
  * in order, a sequence's pages in order: from free_pages[*free_count] up.
  *   free_pages: int32 [num_pages]; what is below *free_count (cut to [0, num_pages],
- *     with PA_DEV_BAD_LENGTHS, where it is outside) is left alone.  A push past its end is not done (PA_DEV_BAD_LENGTHS).
+ *     with PA_DEV_BAD_LENGTHS, where it is outside) is left alone.  A push past its
+ *     end is not done (PA_DEV_BAD_LENGTHS).
  *   free_left: int32 [1], written: the new number of pages on the stack; must not
  *     overlap an input.
  *   block_table is only read; an entry outside the pool is put back as -1
@@ -148,7 +150,8 @@ typedef struct pa_rope {
  *   q: bf16 [total_q_tokens][Hq][D], tokens q_stride elements apart, or NULL with
  *     q_out NULL; k_new, v_new as pa_kv_append's.  Strides: multiples of 8, at
  *     least a token's rows: the three may be slices of a fused projection's output.
- *   q_out: bf16 [total_q_tokens][Hq][D], dense; may be q itself where q is dense.
+ *   q_out: bf16 [total_q_tokens][Hq][D], dense; may be q itself where q is dense (where not:
+ *     PA_ERR_INVALID_ARG).
  *   positions: any int32 >= 0 (max_context_len does not bound them).
  *   A row whose slot is -1 is not cached and its q not written; other slots outside
  *   the pool: neither, and PA_DEV_BAD_PAGE; a negative position: neither, and
@@ -177,8 +180,9 @@ PA_API pa_status pa_rope_append(const pa_problem* problem, const pa_rope* rope,
  *
  * The call rewrites the bounds of every page in which the given rows have slots:
  * over the page's slots up to that of its last row in the call.  Rows of a page
- * stand together, in order (as pa_pages_take maps them).  slots of -1 are passed
- * over.  k_cache: PA_BF16 (other kv_dtype: PA_ERR_UNSUPPORTED), with the new rows.
+ * stand together, in order, with none of another page or of -1 among them (as
+ * pa_pages_take maps them); else which of its rows is the last is not said.  slots of
+ * -1 are passed over.  k_cache: PA_BF16 (other kv_dtype: PA_ERR_UNSUPPORTED), with the new rows.
  * num_pages * page_size at most 2^31 - 1.
  */
 PA_API pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache,
@@ -205,7 +209,8 @@ PA_API pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache,
  *   bound_scale is negative or NaN: no bounds were written for it.
  *   budget >= 1; num_first, num_recent >= 0, together at most budget.  At most 64
  *   q heads a KV head; a context of at most PA_MAX_SELECT_PAGES pages
- *   (max_context_len / page_size): 720,896 tokens in pages of 16, 2.9 million of 64; num_ctas, kv_dtype and sm_scale have no part in it.
+ *   (max_context_len / page_size): 720,896 tokens in pages of 16, 2.9 million of 64;
+ *   num_ctas, kv_dtype and sm_scale have no part in it.
  */
 #define PA_MAX_SELECT_PAGES 45056
 PA_API pa_status pa_select_pages(const pa_problem* problem, int32_t budget, int32_t num_first,
@@ -218,7 +223,7 @@ PA_API pa_status pa_select_pages(const pa_problem* problem, int32_t budget, int3
  * Attention of every row over the pages listed for it (as pa_select_pages lists
  * them, or any other way): the semantics of pa_decode_splitk with the keys of
  * unlisted pages hidden.  The lists' lengths are split over the GPU inside the
- * kernel, and the parts of a split list joined by the last CTA to finish one.
+ * kernel, and the parts of a split list joined by the last to finish one of them.
  *   selected: of row t and KV head h the entries 0 .. n-1, n = min(budget, pages
  *     that the row sees keys of); an entry of -1 among them is passed over, and so
  *     is one outside the row's pages [0, positions[t] / page_size] (PA_DEV_BAD_LENGTHS) or

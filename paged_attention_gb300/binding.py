@@ -456,41 +456,50 @@ def pa_kv_evict(problem, budget, num_first, num_recent, k_cache, k_scale, v_cach
 
 # What the kernels would misread is refused, as above; sizes are the caller's.  (A
 # step's small calls are bound by their time on the host, half of it in looks at
-# tensors: 0.15 us each.)
+# tensors: 0.15 us each for type, strides and device.)
 
 _I8, _F32, _I64 = torch.int8, torch.float32, torch.int64
 # (torch.cuda.current_device looks for a CUDA context first)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(t: torch.Tensor):
-    """The library launches on the current device: a tensor elsewhere is refused."""
-    if not t.is_cuda or t.get_device() != _current_device():
-        raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
+def _here(t: torch.Tensor) -> int:
+    """The current device's index.  The library launches there: a tensor elsewhere (this
+    one, and those that the functions below look at) is refused."""
+    if t.is_cuda and t.get_device() == (dev := _current_device()):
+        return dev
+    raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
 
 
-def _typed(t: Optional[torch.Tensor], dtype):
-    """Address of a contiguous tensor of a type."""
+def _on(t: Optional[torch.Tensor], dev: int):
+    """The tensor, which is on the device."""
+    if t is None or t.get_device() == dev:
+        return t
+    raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
+
+
+def _typed(t: Optional[torch.Tensor], dtype, dev: int = 0):
+    """Address of a contiguous tensor of a type on the device."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_contiguous():
+    if t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
-    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
-                     f"contiguous {dtype} belongs")
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} on "
+                     f"{t.device} where contiguous {dtype} on the current CUDA device belongs")
 
 
-def _i32(t: torch.Tensor):
-    """Address of contiguous int32."""
-    if t.dtype is _I32 and t.is_contiguous():
+def _i32(t: torch.Tensor, dev: int = 0):
+    """Address of contiguous int32 on the device."""
+    if t.dtype is _I32 and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
-    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
-                     f"contiguous int32 belongs")
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} on "
+                     f"{t.device} where contiguous int32 on the current CUDA device belongs")
 
 
 def pa_pages_take(problem, seq_lens, q_lens, block_table, free_pages, free_count, context_lens,
                   row_seq, positions, slots, free_left, device_error=None, stream=None):
     """Pages for q_lens[b] new tokens of every sequence, and the maps of the step's rows."""
-    _here(seq_lens)
+    dev = _here(seq_lens)
     # (ten tensors: looked at without a call each)
     if not (seq_lens.dtype is _I32 and q_lens.dtype is _I32 and block_table.dtype is _I32
             and free_pages.dtype is _I32 and free_count.dtype is _I32
@@ -499,25 +508,31 @@ def pa_pages_take(problem, seq_lens, q_lens, block_table, free_pages, free_count
             and seq_lens.is_contiguous() and q_lens.is_contiguous()
             and block_table.is_contiguous() and free_pages.is_contiguous()
             and context_lens.is_contiguous() and row_seq.is_contiguous()
-            and positions.is_contiguous() and slots.is_contiguous()):
+            and positions.is_contiguous() and slots.is_contiguous()
+            and q_lens.get_device() == dev and block_table.get_device() == dev
+            and free_pages.get_device() == dev and free_count.get_device() == dev
+            and context_lens.get_device() == dev and row_seq.get_device() == dev
+            and positions.get_device() == dev and slots.get_device() == dev
+            and free_left.get_device() == dev):
         for t in (seq_lens, q_lens, block_table, free_pages, free_count, context_lens, row_seq,
                   positions, slots, free_left):
-            _i32(t)
+            _i32(t, dev)
     _check((_lib or load()).pa_pages_take(
         problem, seq_lens.data_ptr(), q_lens.data_ptr(), block_table.data_ptr(),
         free_pages.data_ptr(), free_count.data_ptr(), context_lens.data_ptr(), row_seq.data_ptr(),
         positions.data_ptr(), slots.data_ptr(), free_left.data_ptr(),
-        None if device_error is None else _typed(device_error, _I32), _stream(stream)),
+        None if device_error is None else _typed(device_error, _I32, dev), _stream(stream)),
         "pa_pages_take")
 
 
 def pa_pages_return(problem, seq_lens, keep_lens, block_table, free_pages, free_count, free_left,
                     device_error=None, stream=None):
     """The pages of tokens keep_lens[b] .. seq_lens[b] - 1 back on the free stack."""
-    _here(seq_lens)
+    dev = _here(seq_lens)
     _check((_lib or load()).pa_pages_return(
-        problem, _i32(seq_lens), _i32(keep_lens), _i32(block_table), _i32(free_pages),
-        _i32(free_count), _i32(free_left), _typed(device_error, _I32), _stream(stream)),
+        problem, _i32(seq_lens, dev), _i32(keep_lens, dev), _i32(block_table, dev),
+        _i32(free_pages, dev), _i32(free_count, dev), _i32(free_left, dev),
+        _typed(device_error, _I32, dev), _stream(stream)),
         "pa_pages_return")
 
 
@@ -539,15 +554,16 @@ def pa_rope_steps(inv_freq) -> torch.Tensor:
     return steps
 
 
-def _tokens(t: torch.Tensor, rows: int, heads: int, dim: int) -> int:
+def _tokens(t: torch.Tensor, rows: int, heads: int, dim: int, dev: int) -> int:
     """Elements between the tokens of rows [tokens, heads, dim] with dense heads."""
     n, h, d = t.shape
     by, by_head, by_element = t.stride()
     if (h == heads and d == dim and n >= rows and by_element == 1
-            and (by_head == dim or h == 1) and t.dtype is _BF16):
+            and (by_head == dim or h == 1) and t.dtype is _BF16 and t.get_device() == dev):
         return by if n > 1 else heads * dim
-    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} where "
-                     f"bf16 [{rows}, {heads}, {dim}] with dense heads belongs")
+    raise ValueError(f"{t.dtype} of shape {tuple(t.shape)} and strides {tuple(t.stride())} on "
+                     f"{t.device} where bf16 [{rows}, {heads}, {dim}] with dense heads on the "
+                     f"current CUDA device belongs")
 
 
 def pa_rope_append(problem, rope, steps, q, k_new, v_new, positions, slots, q_out, k_cache,
@@ -555,35 +571,38 @@ def pa_rope_append(problem, rope, steps, q, k_new, v_new, positions, slots, q_ou
     """Rotary positions on the new tokens' q (into q_out) and k, and k and v into the cache;
     the tokens of q, k_new and v_new may be strided (slices of a fused projection)."""
     dim, heads, rows = problem.head_dim, problem.num_kv_heads, problem.total_q_tokens
-    _here(positions)
-    qs, qp = (0, None) if q is None else (_tokens(q, rows, problem.num_q_heads, dim), q.data_ptr())
-    ks, vs = _tokens(k_new, rows, heads, dim), _tokens(v_new, rows, heads, dim)
+    dev = _here(positions)
+    qs, qp = (0, None) if q is None else (
+        _tokens(q, rows, problem.num_q_heads, dim, dev), q.data_ptr())
+    ks, vs = _tokens(k_new, rows, heads, dim, dev), _tokens(v_new, rows, heads, dim, dev)
     if 2 * steps.numel() < rope.rotary_dim:
         raise ValueError(f"{steps.numel()} steps for a rotary_dim of {rope.rotary_dim}")
     _check((_lib or load()).pa_rope_append(
-        problem, rope, _typed(steps, _I64), qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
-        _i32(positions), _i32(slots), _typed(q_out, _BF16),
-        _cache(k_cache, problem), _dense(k_scale), _cache(v_cache, problem), _dense(v_scale),
-        _typed(device_error, _I32), _stream(stream)), "pa_rope_append")
+        problem, rope, _typed(steps, _I64, dev), qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
+        _i32(positions, dev), _i32(slots, dev), _typed(q_out, _BF16, dev),
+        _cache(_on(k_cache, dev), problem), _dense(_on(k_scale, dev)),
+        _cache(_on(v_cache, dev), problem), _dense(_on(v_scale, dev)),
+        _typed(device_error, _I32, dev), _stream(stream)), "pa_rope_append")
 
 
 def pa_page_bounds(problem, k_cache, slots, bounds, bound_scale, device_error=None, stream=None):
     """Each channel's largest and smallest key of the pages that the rows' slots are in."""
-    _here(slots)
+    dev = _here(slots)
     _check((_lib or load()).pa_page_bounds(
-        problem, _typed(k_cache, _BF16), _i32(slots), _typed(bounds, _I8),
-        _typed(bound_scale, _F32), _typed(device_error, _I32), _stream(stream)),
+        problem, _typed(k_cache, _BF16, dev), _i32(slots, dev), _typed(bounds, _I8, dev),
+        _typed(bound_scale, _F32, dev), _typed(device_error, _I32, dev), _stream(stream)),
         "pa_page_bounds")
 
 
 def pa_select_pages(problem, budget, num_first, num_recent, q, bounds, bound_scale, block_table,
                     row_seq, positions, selected, device_error=None, stream=None):
     """Per row and KV head the budget's page indices with the highest bound on a logit."""
-    _here(positions)
+    dev = _here(positions)
     _check((_lib or load()).pa_select_pages(
-        problem, budget, num_first, num_recent, _typed(q, _BF16), _typed(bounds, _I8),
-        _typed(bound_scale, _F32), _i32(block_table), _i32(row_seq), _i32(positions),
-        _i32(selected), _typed(device_error, _I32), _stream(stream)), "pa_select_pages")
+        problem, budget, num_first, num_recent, _typed(q, _BF16, dev), _typed(bounds, _I8, dev),
+        _typed(bound_scale, _F32, dev), _i32(block_table, dev), _i32(row_seq, dev),
+        _i32(positions, dev), _i32(selected, dev), _typed(device_error, _I32, dev),
+        _stream(stream)), "pa_select_pages")
 
 
 def pa_selected_workspace_size(problem: PaProblem, budget: int) -> int:
@@ -593,11 +612,12 @@ def pa_selected_workspace_size(problem: PaProblem, budget: int) -> int:
 def pa_decode_selected(problem, budget, q, k_cache, v_cache, block_table, row_seq, positions,
                        selected, ws, out, lse=None, stream=None):
     """Attention of every row over the pages listed for it."""
-    _here(positions)
+    dev = _here(positions)
     _check((_lib or load()).pa_decode_selected(
-        problem, budget, _typed(q, _BF16), _typed(k_cache, _BF16), _typed(v_cache, _BF16),
-        _i32(block_table), _i32(row_seq), _i32(positions), _i32(selected), _dense(ws),
-        _nbytes(ws), _typed(out, _BF16), _typed(lse, _F32), _stream(stream)),
+        problem, budget, _typed(q, _BF16, dev), _typed(k_cache, _BF16, dev),
+        _typed(v_cache, _BF16, dev), _i32(block_table, dev), _i32(row_seq, dev),
+        _i32(positions, dev), _i32(selected, dev), _dense(_on(ws, dev)), _nbytes(ws),
+        _typed(out, _BF16, dev), _typed(lse, _F32, dev), _stream(stream)),
         "pa_decode_selected")
 
 

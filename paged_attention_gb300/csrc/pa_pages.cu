@@ -114,9 +114,10 @@ take_kernel(const CacheGeom g, const int32_t* __restrict__ seq_lens,
             if (ok && !granted) flag_error(err, PA_DEV_NO_PAGES);
         }
         __syncthreads();
-        for (int i = blockIdx.x * kThreads + tid; i < rows && row0 + i < g.total_q;
-             i += gridDim.x * kThreads) {
-            const int r = row0 + i;
+        // (bad lengths add up to as much as 2^31 - 1 rows: one step further needs the 32nd bit)
+        for (uint32_t i = blockIdx.x * kThreads + tid;
+             i < (uint32_t)rows && row0 + i < (uint32_t)g.total_q; i += gridDim.x * kThreads) {
+            const int r = (int)(row0 + i);
             const int s = first_above(s_end, r);
             const SeqOf x = s_seq[s];
             int seq = -1, pos = 0, slot = -1;
@@ -147,7 +148,8 @@ take_kernel(const CacheGeom g, const int32_t* __restrict__ seq_lens,
         need0 += all;
         __syncthreads();                 // the round's rows are done with s_end and s_seq
     }
-    for (int r = row0 + blockIdx.x * kThreads + tid; r < g.total_q; r += gridDim.x * kThreads) {
+    for (uint32_t r = row0 + blockIdx.x * kThreads + tid; r < (uint32_t)g.total_q;
+         r += gridDim.x * kThreads) {
         row_seq[r] = -1;
         positions[r] = 0;
         slots[r] = -1;

@@ -33,6 +33,8 @@ pa_status page_geometry(const pa_problem* pp, CacheGeom& g) {
     return geometry(&p, false, g);
 }
 bool slots_fit(const CacheGeom& g) { return (int64_t)g.num_pages * g.ps <= 0x7fffffff; }
+// Rows that 32 bits count with room for a grid's step beyond.
+bool rows_fit(const CacheGeom& g) { return g.total_q <= 1 << 30; }
 
 // Workspace of pa_decode_selected: header (error word) and the counters, one a query
 // row, of as many CTAs as a call may have, then two partial slots per CTA, each `rows` rows of D +
@@ -52,7 +54,7 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
     L.together = selected_rows(g.G, g.max_q_len);
     L.nt = selected_row_tiles(g.D, g.G * L.together);
     if (L.nt < 0 || pp->num_ctas > kMaxGridSel) return PA_ERR_UNSUPPORTED;
-    if ((int64_t)g.total_q * g.Hkv > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    if (!rows_fit(g) || (int64_t)g.total_q * g.Hkv > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     L.grid = pp->num_ctas;
     if (L.grid == 0) {
         L.grid = sm_count();
@@ -95,7 +97,7 @@ pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_lens, cons
     CacheGeom g;
     pa_status st = page_geometry(problem, g);
     if (st != PA_OK) return st;
-    if (!slots_fit(g)) return PA_ERR_UNSUPPORTED;
+    if (!slots_fit(g) || !rows_fit(g)) return PA_ERR_UNSUPPORTED;
     const bool rows = g.total_q > 0;
     if (!ints_ok(seq_lens) || !ints_ok(q_lens) || !ints_ok(block_table) || !ints_ok(free_pages) ||
         !ints_ok(free_count) || !ints_ok(context_lens) || !ints_ok(free_left) ||
@@ -206,7 +208,7 @@ pa_status pa_rope_append(const pa_problem* problem, const pa_rope* rope, const u
         rope->rotary_dim > g.D || rope->rotary_dim % 16 != 0 ||
         (rope->interleaved != 0 && rope->interleaved != 1))
         return PA_ERR_INVALID_ARG;
-    if (!slots_fit(g)) return PA_ERR_UNSUPPORTED;
+    if (!slots_fit(g) || !rows_fit(g)) return PA_ERR_UNSUPPORTED;
     if (g.total_q == 0) return PA_OK;   // no new token
     const int64_t kv = (int64_t)g.Hkv * g.D, qd = (int64_t)g.Hq * g.D;
     if (!steps || !aligned(steps, 8) || !k_new || !v_new || !aligned(k_new, 16) ||
@@ -214,7 +216,8 @@ pa_status pa_rope_append(const pa_problem* problem, const pa_rope* rope, const u
         v_stride % 8 != 0 || !ints_ok(positions) || !ints_ok(slots) ||
         !cache_ok(*problem, k_cache, k_scale) || !cache_ok(*problem, v_cache, v_scale) ||
         !aligned(device_error, 4) || (q == nullptr) != (q_out == nullptr) || !aligned(q, 16) ||
-        !aligned(q_out, 16) || (q != nullptr && (q_stride < qd || q_stride % 8 != 0)))
+        !aligned(q_out, 16) || (q != nullptr && (q_stride < qd || q_stride % 8 != 0)) ||
+        (q != nullptr && q == q_out && q_stride != qd && g.total_q > 1))
         return PA_ERR_INVALID_ARG;
     P.rotary = rope->rotary_dim;
     P.interleaved = rope->interleaved;
@@ -246,7 +249,7 @@ pa_status pa_page_bounds(const pa_problem* problem, const void* k_cache, const i
     CacheGeom g;
     pa_status st = geometry(problem, false, g);
     if (st != PA_OK) return st;
-    if (problem->kv_dtype != PA_BF16 || !slots_fit(g)) return PA_ERR_UNSUPPORTED;
+    if (problem->kv_dtype != PA_BF16 || !slots_fit(g) || !rows_fit(g)) return PA_ERR_UNSUPPORTED;
     if (g.total_q == 0) return PA_OK;   // no page got a new token
     if (!k_cache || !aligned(k_cache, 16) || !ints_ok(slots) || !bounds || !aligned(bounds, 16) ||
         !bound_scale || !aligned(bound_scale, 4) || !aligned(device_error, 4))

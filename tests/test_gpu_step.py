@@ -1053,3 +1053,85 @@ def test_two_loops_at_once_on_two_streams():
     for one, two in zip(*got):
         for a, b in zip(one, two):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------- calls at the edge of what is allowed
+
+def test_take_of_lengths_that_add_up_to_2_to_the_31():
+    """No sequence's rows fit; the few rows that there are become padding, and nothing
+    else is written."""
+    B_, most = 3, 715827882                    # B_ * most = 2^31 - 2
+    width = (most + 255) // 256
+    p = problem(num_seqs=B_, num_q_heads=2, page_size=256, num_pages=4, max_pages_per_seq=width,
+                total_q_tokens=5, max_q_len=most, max_context_len=most)
+    table = torch.full((B_, width), -1, dtype=torch.int32, device="cuda")
+    maps = [ints([-9] * 9) for _ in range(3)]
+    ctx, left, err = ints([-9] * B_), ints([-9]), ints([0])
+    B.pa_pages_take(p, ints([0] * B_), ints([most] * B_), table, ints([0, 1, 2, 3]), ints([4]),
+                    ctx, *maps, left, err)
+    for m, x in zip(maps, (-1, 0, -1)):
+        assert m.tolist() == [x] * 5 + [-9] * 4
+    assert ctx.tolist() == [0] * B_ and int(left) == 4 and int(err) == 1
+    assert not (table != -1).any()
+
+
+@pytest.mark.parametrize("most", [1, 3])
+def test_attention_of_few_rows_among_many_of_padding(most):
+    """Rows of no sequence before, between and far behind the others."""
+    ctx, ql = [900, 70, 333], [most, 1, most]
+    pages, table, seq, pos, k, v, q = attend_case(128, 4, 2, 16, 0, ctx, ql, 11)
+    lead, gap, tail = 40, 70, 3000
+    n0 = ql[0]
+    seq = [-1] * lead + seq[:n0] + [-1] * gap + seq[n0:] + [-1] * tail
+    pos = [0] * lead + pos[:n0] + [0] * gap + pos[n0:] + [0] * tail
+    full = torch.zeros((len(seq), *q.shape[1:]), dtype=BF16)
+    full[[i for i, b in enumerate(seq) if b >= 0]] = q
+    sel = lists(seq, pos, 2, 9, 16, 0, 6)
+    p = problem(num_seqs=3, num_q_heads=8, num_pages=pages, max_pages_per_seq=len(table[0]),
+                total_q_tokens=len(seq), max_q_len=most, max_context_len=max(ctx))
+    check_attend(p, 9, table, seq, pos, k, v, full, sel, repeat=2)
+
+
+def test_tensors_on_the_host_are_refused():
+    """Each tensor of each call in turn, before the library sees any."""
+    p = problem(total_q_tokens=2, num_seqs=2)
+    bf = lambda *s: torch.zeros(s, dtype=BF16, device="cuda")  # noqa: E731
+    seq, pos, slots, err = ints([0, 1]), ints([3, 4]), ints([3, 20]), ints([0])
+    table = ints([[0] * 8, [1] * 8])
+    k, v, q = bf(8, 16, 2, 128), bf(8, 16, 2, 128), bf(2, 4, 128)
+    kn, vn, out = bf(2, 2, 128), bf(2, 2, 128), bf(2, 4, 128)
+    bounds = torch.zeros((8, 2, 2, 128), dtype=torch.int8, device="cuda")
+    scale = torch.zeros((8, 2), device="cuda")
+    sel = torch.zeros((2, 2, 1), dtype=torch.int32, device="cuda")
+    steps, rope = B.pa_rope_steps(freq_of(128)).cuda(), B.PaRope(128, 0, 1.0)
+    ws = torch.zeros(B.pa_selected_workspace_size(p, 1), dtype=torch.uint8, device="cuda")
+    lse = torch.zeros((2, 4), device="cuda")
+    stack, count = ints([2, 3, 4, 5, 6, 7, 0, 0]), ints([6])
+    one = lambda: ints([0, 0])  # noqa: E731
+    calls = [
+        (B.pa_pages_take, (p, ints([3, 4]), ints([1, 1]), table, stack, count, one(), one(), one(),
+                           one(), ints([0]), err)),
+        (B.pa_pages_return, (p, ints([3, 4]), ints([3, 4]), table, stack, count, ints([0]), err)),
+        (B.pa_rope_append, (p, rope, steps, q, kn, vn, pos, slots, out, k, None, v, None, err)),
+        (B.pa_page_bounds, (p, k, slots, bounds, scale, err)),
+        (B.pa_select_pages, (p, 1, 0, 0, q, bounds, scale, table, seq, pos, sel, err)),
+        (B.pa_decode_selected, (p, 1, q, k, v, table, seq, pos, sel, ws, out, lse)),
+    ]
+    for f, args in calls:
+        f(*args)
+        for i, a in enumerate(args):
+            if torch.is_tensor(a):
+                with pytest.raises(ValueError):
+                    f(*args[:i], a.cpu(), *args[i + 1:])
+    torch.cuda.synchronize()
+    no_error(err)
+    # a 4-bit cache's scales
+    x = problem(total_q_tokens=2, num_seqs=2, kv_dtype=B.PA_MX4)
+    codes, s4 = (torch.zeros((8, 16, 2, n), dtype=torch.uint8, device="cuda") for n in (64, 4))
+    args = (x, rope, steps, q, kn, vn, pos, slots, out, codes, s4, codes.clone(), s4.clone(), err)
+    B.pa_rope_append(*args)
+    for i in (9, 10, 11, 12):
+        with pytest.raises(ValueError):
+            B.pa_rope_append(*args[:i], args[i].cpu(), *args[i + 1:])
+    torch.cuda.synchronize()
+    no_error(err)

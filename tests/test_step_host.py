@@ -199,6 +199,20 @@ def test_the_binding_refuses_what_would_be_misread():
             f()
 
 
+@pytest.mark.parametrize("name", ["pa_pages_take", "pa_rope_append", "pa_page_bounds",
+                                  "pa_select_pages", "pa_decode_selected"])
+def test_more_rows_than_are_counted_are_refused(lib, name):
+    assert call(lib, name, problem(total_q_tokens=(1 << 30) + 1)) == B.PA_ERR_UNSUPPORTED
+
+
+def test_queries_in_place_are_dense(lib):
+    r = "pa_rope_append"
+    for stride in (1032, 1536):
+        args = swap(r, 5, stride)
+        args[10] = args[2]
+        assert call(lib, r, problem(), args) == B.PA_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------- frequencies
 
 def scaling(kind, dim, **kw):
