@@ -31,6 +31,7 @@
 // (each row by itself: 540).  With 32 query rows a unit the products and the softmax set
 // the pace: 64 sequences of 4 rows, 64 q heads, 103 us for 56.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_cache_mma.cuh"
 #include "pa_step_common.cuh"
@@ -68,7 +69,7 @@ namespace {
 // No CTA takes less than this of the flat line: joining a unit's parts costs more
 // than the tiles it would spread (one sequence of 131071 tokens, 256 pages of 16, 8
 // heads: 15.7 us with 2, 14.5 with 3, 13.7 with 4).
-constexpr int kMinShareSel = 4;
+constexpr int kMinShareSel(int nt) { return nt == 1 ? 4 : 4; }
 
 constexpr int kDoneRows = kSelDoneRows;       // counters of a CTA: one a query row
 constexpr int kMostRows = 6;                  // of a unit: what an entry has bits for
@@ -87,6 +88,9 @@ struct SelUnit {
     int64_t list;          // where that begins
     int64_t start;         // position of its fixed cost on the flat line
 };
+
+template <int N>
+using Const = std::integral_constant<int, N>;
 
 // x / y, in 32 bits where they fit (64 bits take ten times as long)
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
@@ -110,7 +114,8 @@ __device__ __forceinline__ int tiles_of(const CacheGeom& g, int entries) {
 template <bool JOINED>
 __device__ __forceinline__ int64_t row_cost(const SelectedParams& P, int t) {
     if constexpr (JOINED) {
-        const int n = P.row_tiles[t];
+        int64_t n = 0;
+        for (int c = 0; c < P.join_parts; ++c) n += P.row_tiles[t * P.join_parts + c];
         return n > 0 ? n + (int64_t)P.g.Hkv * P.unit_cost : 0;
     } else {
         const int seq = P.row_seq[t], pos = P.positions[t];
@@ -150,7 +155,7 @@ __device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u, i
         u.hk = 0;
         do {
             if (++u.row >= P.g.total_q) return false;
-        } while (row_cost<JOINED>(P, u.row) == 0);
+        } while (JOINED ? P.row_tiles[u.row * P.join_parts] == 0 : row_cost<JOINED>(P, u.row) == 0);
         load_row<JOINED>(P, u);
     }
     load_unit<JOINED>(P, u);
@@ -187,21 +192,26 @@ __device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, in
                  : "memory");
 }
 
-// ---- joins the lists of rows of one sequence (one CTA a row; only a unit's first row's
-// goes on).  A warp a KV head: the set of rows of every page, a byte each, in shared
-// memory, some pages at a time; then the pages that have any, in order.
+// ---- joins the lists of rows of one sequence (the CTAs (t, c) of row t; only a unit's first
+// row's go on).  P.join_team warps a KV head, some pages at a time: the set of rows of every
+// page, and a bit for the pages that have any, in shared memory; the bits before a page tell
+// its place.  Where rows are few their heads are shared out among P.join_parts CTAs.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinPages = 4096;
+constexpr int kJoinPages = 4096;             // a warp
 
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
-    __shared__ __align__(16) uint32_t s_rows[kJoinWarps][kJoinPages / 4];
-    __shared__ int s_tiles[kJoinWarps];
+    __shared__ __align__(16) uint32_t s_rows[kJoinWarps * kJoinPages / 4];    // a byte a page
+    __shared__ __align__(16) uint32_t s_any[kJoinWarps * kJoinPages / 32];    // a bit
+    __shared__ __align__(16) int s_before[kJoinWarps * kJoinPages / 32];
+    __shared__ int s_sum[kJoinWarps], s_tiles[kJoinWarps];
     const CacheGeom& g = P.g;
     const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     int32_t* err = P.header + H_ERROR;
-    const int seq = P.row_seq[t];
+    // (read together: what follows is a chain of loads)
+    const int ahead = min(t + lane, g.total_q - 1);
+    const int seq = P.row_seq[t], seq_ahead = P.row_seq[ahead], pos_ahead = P.positions[ahead];
     int m = 0;                         // rows of the unit that t leads
     if (seq >= 0 && seq < g.B) {
         // rows of the sequence before t, 128 looked at together
@@ -222,98 +232,156 @@ join_lists_kernel(const __grid_constant__ SelectedParams P, int most) {
                 }
         }
         if (before % most == 0) {
-            const int r = t + lane;
-            const uint32_t other = __ballot_sync(
-                0xffffffffu, r >= g.total_q || P.row_seq[min(r, g.total_q - 1)] != seq);
+            const uint32_t other =
+                __ballot_sync(0xffffffffu, t + lane >= g.total_q || seq_ahead != seq);
             m = min(most, other != 0 ? __ffs(other) - 1 : 32);
         }
     }
     // lane i < m has row i's position and its list's length; a row with a position that
     // cannot be has none
     int pos = -1;
-    if (lane < m) pos = P.positions[t + lane];
-    if (lane < m && (pos < 0 || pos >= g.max_ctx)) pos = -1;
+    if (lane < m && pos_ahead >= 0 && pos_ahead < g.max_ctx) pos = pos_ahead;
     const int mine = pos >= 0 ? list_entries(P, pos) : 0;
     const uint32_t good = __ballot_sync(0xffffffffu, pos >= 0);
     if (threadIdx.x == 0 && (seq >= g.B || __popc(good) != m))
         flag_error(err, PA_DEV_BAD_LENGTHS);
+    const int parts = P.join_parts, c = blockIdx.y;
     if (good == 0) {
         if (threadIdx.x == 0) {
             P.row_lead[t] = 0;
-            P.row_tiles[t] = 0;
+            P.row_tiles[t * parts + c] = 0;
         }
         return;                        // (the same for every thread)
     }
     const int last = __reduce_max_sync(0xffffffffu, pos) >> g.ps_shift;   // page index
     const int each = __reduce_max_sync(0xffffffffu, mine);                // the longest list
-    int tiles = 0;
-    for (int hk = warp; hk < g.Hkv; hk += kJoinWarps) {
-        int2* to = P.list + ((int64_t)t * g.Hkv + (int64_t)hk * m) * P.budget;
-        int n = 0;
-        for (int p0 = 0; p0 <= last; p0 += kJoinPages) {
-            const int span = min(kJoinPages, last + 1 - p0);
-            for (int i = lane; i < (span + 15) / 16; i += 32)
-                reinterpret_cast<uint4*>(s_rows[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
+    // the CTA has the heads c, c + parts, ..., its teams one each at a time
+    const int S = P.join_team, teams = kJoinWarps / S, team = warp / S;
+    const int me = threadIdx.x - 32 * S * team, size = 32 * S;            // of the team
+    uint32_t* rows_of = s_rows + team * S * (kJoinPages / 4);
+    uint32_t* any = s_any + team * S * (kJoinPages / 32);
+    int* before_word = s_before + team * S * (kJoinPages / 32);
+    const int64_t chunk = (int64_t)S * kJoinPages;
+    auto team_sync = [&]() {           // (all teams take the same steps)
+        if (S > 1)
+            __syncthreads();
+        else
             __syncwarp();
-            // the rows' lists end to end, so that many entries are under way
-            const int32_t* sel = P.selected + ((int64_t)t * g.Hkv + hk) * P.budget;
-            const int64_t next_row = (int64_t)g.Hkv * P.budget;
-#pragma unroll 4
-            for (int k0 = 0; k0 < m * each; k0 += 32) {
-                const int k = k0 + lane;
-                int r = 0;
+    };
+    int tiles = 0;
+    for (int h0 = c; h0 < g.Hkv; h0 += parts * teams) {
+        const int hk = h0 + parts * team;
+        const bool there = hk < g.Hkv;
+        int2* to = P.list + ((int64_t)t * g.Hkv + (int64_t)hk * m) * P.budget;
+        // The rows' lists end to end, kAhead entries a lane under way: f(entries, their rows),
+        // -1 for none.
+        const int32_t* sel = P.selected + ((int64_t)t * g.Hkv + hk) * P.budget;
+        const int64_t next_row = (int64_t)g.Hkv * P.budget;
+        const int all = there ? m * each : 0;
+        auto entries = [&](auto f) {
+            constexpr int kAhead = 4;
+            for (int k0 = 0; k0 < all; k0 += size * kAhead) {
+                int e[kAhead], of[kAhead];
 #pragma unroll
-                for (int x = 1; x < kMostRows; ++x) r += x < m && k >= x * each;
-                const int i = k - r * each;
-                const int many = __shfl_sync(0xffffffffu, mine, r);
-                const int top = __shfl_sync(0xffffffffu, pos, r) >> g.ps_shift;
-                if (i < many) {
-                    const int e = sel[r * next_row + i];
-                    if (e < -1 || e > top) {
+                for (int j = 0; j < kAhead; ++j) {
+                    const int k = k0 + j * size + me;
+                    int r = 0;
+#pragma unroll
+                    for (int x = 1; x < kMostRows; ++x) r += x < m && k >= x * each;
+                    const int i = k - r * each;
+                    const int many = __shfl_sync(0xffffffffu, mine, r);
+                    of[j] = r;
+                    e[j] = i < many ? sel[r * next_row + i] : -1;
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int top = __shfl_sync(0xffffffffu, pos, of[j]) >> g.ps_shift;
+                    if (e[j] < -1 || e[j] > top) {
                         flag_error(err, PA_DEV_BAD_LENGTHS);
-                    } else if (e >= p0 && e < p0 + span) {
-                        const int at = e - p0;
-                        atomicOr(&s_rows[warp][at >> 2], 1u << (8 * (at & 3) + r));
+                        e[j] = -1;
                     }
                 }
+                f(e, of);
             }
-            __syncwarp();
-            for (int i0 = 0; i0 < span; i0 += 128) {
-                const int i = i0 + 4 * lane;
-                uint32_t w = i < span ? s_rows[warp][i >> 2] : 0u;
-                int here = 0;
+        };
+        int n = 0;
+        for (int64_t p0 = 0; p0 <= last; p0 += chunk) {
+            const int first = (int)p0, span = (int)min(chunk, last + 1 - p0);
+            for (int i = me; i < (span + 15) / 16; i += size)
+                reinterpret_cast<uint4*>(rows_of)[i] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(any)[me] = make_uint4(0u, 0u, 0u, 0u);
+            team_sync();
+            entries([&](const auto& e, const auto& of) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) here += (w >> (8 * j) & 255u) != 0;
-                const int upto = warp_inclusive(here, lane);
-                int k = n + upto - here;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t rows = w >> (8 * j) & 255u;
-                    if (rows == 0) continue;
-                    const int s = p0 + i + j;
-                    const int page = P.table[(int64_t)seq * g.mpps + s];
-                    const bool ok = (uint32_t)page < (uint32_t)g.num_pages;
-                    if (!ok) flag_error(err, PA_DEV_BAD_PAGE);
-                    to[k++] = make_int2(ok ? page : -1, (int)((uint32_t)s | rows << kRowBits));
+                for (int j = 0; j < (int)(sizeof(e) / sizeof(int)); ++j) {
+                    const int at = e[j] - first;
+                    if (e[j] < first || at >= span) continue;
+                    atomicOr(&rows_of[at >> 2], 1u << (8 * (at & 3) + of[j]));
+                    atomicOr(&any[at >> 5], 1u << (at & 31));
                 }
-                n += __shfl_sync(0xffffffffu, upto, 31);
+            });
+            team_sync();
+            // how many pages there are before each word of `any`
+            static_assert(kJoinPages / 32 == 4 * 32, "four words a lane");
+            const uint4 w = reinterpret_cast<const uint4*>(any)[me];
+            const int c0 = __popc(w.x), c1 = c0 + __popc(w.y), c2 = c1 + __popc(w.z);
+            const int here = c2 + __popc(w.w), upto = warp_inclusive(here, lane);
+            if (lane == 31) s_sum[warp] = upto;
+            team_sync();
+            int from = n + upto - here;
+            for (int x = team * S; x < (team + 1) * S; ++x) {
+                const int y = s_sum[x];
+                if (x < warp) from += y;
+                n += y;
             }
-            __syncwarp();
+            reinterpret_cast<int4*>(before_word)[me] = make_int4(from, from + c0, from + c1,
+                                                                 from + c2);
+            team_sync();
+            // the first row that listed a page writes it
+            entries([&](const auto& e, const auto& of) {
+                constexpr int K = (int)(sizeof(e) / sizeof(int));
+                uint32_t rows[K];
+                int page[K];
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    const int at = e[j] - first;
+                    rows[j] = 0u;
+                    if (e[j] >= first && at < span) {
+                        const uint32_t x = rows_of[at >> 2] >> (8 * (at & 3)) & 255u;
+                        if ((x & (0u - x)) == 1u << of[j]) rows[j] = x;
+                    }
+                    page[j] = rows[j] != 0 ? P.table[(int64_t)seq * g.mpps + e[j]] : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    if (rows[j] == 0) continue;
+                    const int at = e[j] - first;
+                    const int k =
+                        before_word[at >> 5] + __popc(any[at >> 5] & ((1u << (at & 31)) - 1u));
+                    const bool ok = (uint32_t)page[j] < (uint32_t)g.num_pages;
+                    if (!ok) flag_error(err, PA_DEV_BAD_PAGE);
+                    to[k] = make_int2(ok ? page[j] : -1,
+                                      (int)((uint32_t)e[j] | rows[j] << kRowBits));
+                }
+            });
+            team_sync();
         }
-        if (n == 0) {                  // the rows' results are written all the same
-            if (lane == 0) to[0] = make_int2(-1, 0);
-            n = 1;
+        if (there && me == 0) {
+            if (n == 0) {              // the rows' results are written all the same
+                to[0] = make_int2(-1, 0);
+                n = 1;
+            }
+            P.unit_entries[(int64_t)t * g.Hkv + hk] = n;
+            tiles += tiles_of(g, n);
         }
-        if (lane == 0) P.unit_entries[(int64_t)t * g.Hkv + hk] = n;
-        tiles += tiles_of(g, n);
     }
-    if (lane == 0) s_tiles[warp] = tiles;
+    if (me == 0) s_tiles[team] = tiles;
     __syncthreads();
     if (threadIdx.x == 0) {
-        int all = 0;
-        for (int w = 0; w < kJoinWarps; ++w) all += s_tiles[w];
+        int sum = 0;
+        for (int x = 0; x < teams; ++x) sum += s_tiles[x];
         P.row_lead[t] = m;
-        P.row_tiles[t] = all;
+        P.row_tiles[t * parts + c] = sum;
     }
 }
 
@@ -360,7 +428,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     }
     const int64_t upto = before(mine);
     const int64_t C = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel - 1) / kMinShareSel);
+    const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel(NT) - 1) / kMinShareSel(NT));
     const int cta = blockIdx.x;
     if (cta >= N) return;
     const int64_t lo = quotient(C * cta, N), hi = quotient(C * (cta + 1), N);
@@ -925,34 +993,47 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 __threadfence();
                 uint32_t ends = __ballot_sync(0xffffffffu, last);
                 __syncwarp();                    // (a vote orders no memory)
-                {
+                // part c of the unit is in slot 2 c (the first in 2 c + 1)
+                auto part_row = [&](int c, int r) {
+                    return (int64_t)(2 * c + (c == c_first ? 1 : 0)) * Cfg::kRows + r;
+                };
+                // K of those rows, whose first B parts are under way together, and their lse
+                // (one a lane); the weights of 32 parts at a time
+                auto join_rows = [&](auto rows, auto batch) {
+                    constexpr int K = decltype(rows)::value, B = decltype(batch)::value;
                     constexpr int DPL = D / 32;
-                    for (; ends != 0; ends &= ends - 1) {
-                        const int r = warp + W * (__ffs(ends) - 1);
-                        // part c of the unit is in slot 2 c (the first in 2 c + 1); 32
-                        // parts' lse at a time, one a lane
-                        auto part_row = [&](int c) {
-                            return (int64_t)(2 * c + (c == c_first ? 1 : 0)) * Cfg::kRows + r;
-                        };
-                        // the first sixteen parts are under way while the lse are looked at
-                        constexpr int B = 16;
-                        float x[B][DPL];
-                        auto load_parts = [&](int c0) {
+                    int row_in[K];
+                    bool there[K];
+                    float x[K][B][DPL], lse[K];
+                    auto load_parts = [&](int i, int c0) {
 #pragma unroll
-                            for (int j = 0; j < B; ++j) {
-                                const float* src =
-                                    P.part_o + part_row(min(c0 + j, c_last)) * D + lane * DPL;
+                        for (int j = 0; j < B; ++j) {
+                            const float* src =
+                                P.part_o + part_row(min(c0 + j, c_last), row_in[i]) * D + lane * DPL;
 #pragma unroll
-                                for (int e = 0; e < DPL; e += 2)
-                                    *reinterpret_cast<float2*>(x[j] + e) =
-                                        __ldcg(reinterpret_cast<const float2*>(src + e));
-                            }
-                        };
-                        load_parts(c_first);
-                        float M = -INFINITY;
-                        bool poison = false;
-                        for (int c = c_first + lane; c <= c_last; c += 32) {
-                            const float y = __ldcg(P.part_lse + part_row(c));
+                            for (int e = 0; e < DPL; e += 2)
+                                *reinterpret_cast<float2*>(x[i][j] + e) =
+                                    __ldcg(reinterpret_cast<const float2*>(src + e));
+                        }
+                    };
+                    auto load_lse = [&](int i, int c) {
+                        return c <= c_last ? __ldcg(P.part_lse + part_row(c, row_in[i])) : -INFINITY;
+                    };
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        there[i] = ends != 0;
+                        row_in[i] = there[i] ? warp + W * (__ffs(ends) - 1) : row_in[0];
+                        ends &= ends - 1;
+                        lse[i] = load_lse(i, c_first + lane);
+                        load_parts(i, c_first);
+                    }
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        if (!there[i]) continue;
+                        float M = lse[i];
+                        bool poison = M != M;
+                        for (int c = c_first + lane + 32; c <= c_last; c += 32) {
+                            const float y = load_lse(i, c);
                             poison |= y != y;
                             M = fmaxf(M, y);
                         }
@@ -964,25 +1045,28 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 #pragma unroll
                         for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
 #pragma unroll 1
-                        for (int c0 = c_first; c0 <= c_last; c0 += B) {
-                            if (c0 > c_first) load_parts(c0);
-                            float y = 0.f;
-                            if (lane < B && c0 + lane <= c_last) {
-                                const float v = __ldcg(P.part_lse + part_row(c0 + lane));
-                                y = poison ? NAN : v == -INFINITY ? 0.f : ex2((v - M) * kLog2e);
-                            }
+                        for (int cb = c_first; cb <= c_last; cb += 32) {
+                            const float v = cb == c_first ? lse[i] : load_lse(i, cb + lane);
+                            const float y = cb + lane > c_last ? 0.f
+                                            : poison           ? NAN
+                                            : v == -INFINITY   ? 0.f
+                                                               : ex2((v - M) * kLog2e);
+#pragma unroll 1
+                            for (int c0 = cb; c0 <= min(c_last, cb + 31); c0 += B) {
+                                if (c0 > c_first) load_parts(i, c0);
 #pragma unroll
-                            for (int j = 0; j < B; ++j) {
-                                const float w = __shfl_sync(0xffffffffu, y, j);
-                                den += w;
+                                for (int j = 0; j < B; ++j) {
+                                    const float w = __shfl_sync(0xffffffffu, y, c0 - cb + j);
+                                    den += w;
 #pragma unroll
-                                for (int e = 0; e < DPL; ++e)
-                                    if (w != 0.f) acc[e] = fmaf(w, x[j][e], acc[e]);
+                                    for (int e = 0; e < DPL; ++e)
+                                        if (w != 0.f) acc[e] = fmaf(w, x[i][j][e], acc[e]);
+                                }
                             }
                         }
                         const bool none = den == 0.f;
                         const float inv = none ? 0.f : 1.f / den;
-                        const int64_t row = out_row(r);
+                        const int64_t row = out_row(row_in[i]);
                         if (row >= 0) {
                             __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
@@ -993,6 +1077,14 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         if (P.lse != nullptr && lane == 0 && row >= 0)
                             P.lse[row] = none ? -INFINITY : M + lg2(den) * kLn2;
                     }
+                };
+                while (ends != 0) {
+                    if (NT > 1 && others < 4)
+                        join_rows(Const<4>{}, Const<4>{});
+                    else if (others < 8)
+                        join_rows(Const<2>{}, Const<8>{});
+                    else
+                        join_rows(Const<1>{}, Const<16>{});
                 }
             }
         }
@@ -1031,10 +1123,19 @@ int selected_row_tiles(int D, int rows) {
 }
 int selected_ctas_per_sm() { return SelCfg<128, 1>::kCtas; }
 
-cudaError_t launch_decode_selected(const SelectedParams& P, int rows, int nt, int grid,
+cudaError_t launch_decode_selected(const SelectedParams& P0, int rows, int nt, int grid, int sms,
                                    cudaStream_t stream) {
+    SelectedParams P = P0;
     if (rows > 1) {
-        const cudaError_t e = launch_dependent(join_lists_kernel, dim3(P.g.total_q),
+        // a row's heads among CTAs until there is one an SM, and a CTA's warps among its heads
+        int parts = 1, teams = 1;
+        while (parts < kMostJoinParts && 2 * parts <= P.g.Hkv &&
+               (int64_t)P.g.total_q * 2 * parts <= sms)
+            parts *= 2;
+        while (teams < kJoinWarps && teams * parts < P.g.Hkv) teams *= 2;
+        P.join_parts = parts;
+        P.join_team = kJoinWarps / teams;
+        const cudaError_t e = launch_dependent(join_lists_kernel, dim3(P.g.total_q, parts),
                                                dim3(32 * kJoinWarps), 0, stream, P, rows);
         if (e != cudaSuccess) return e;
     }

@@ -72,7 +72,7 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
     L.off_entries = L.off_list = L.total = L.off_lead;
     if (L.together > 1) {
         const int64_t units = (int64_t)g.total_q * g.Hkv;
-        L.off_entries = align256(L.off_lead + (int64_t)g.total_q * 8);
+        L.off_entries = align256(L.off_lead + (int64_t)g.total_q * (1 + kMostJoinParts) * 4);
         L.off_list = align256(L.off_entries + units * 4);
         L.total = align256(L.off_list + units * budget * 8);
     }
@@ -340,7 +340,11 @@ pa_status pa_decode_selected(const pa_problem* problem, int32_t budget, const vo
     P.row_tiles = P.row_lead + g.total_q;
     P.unit_entries = reinterpret_cast<int32_t*>(base + L.off_entries);
     P.list = reinterpret_cast<int2*>(base + L.off_list);
-    return status_of(launch_decode_selected(P, L.together, L.nt, L.grid, (cudaStream_t)stream));
+    P.join_parts = P.join_team = 1;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    return status_of(
+        launch_decode_selected(P, L.together, L.nt, L.grid, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -59,13 +59,17 @@ struct SelectedParams {
     int32_t unit_cost;   // fixed cost of a unit, in tiles
     int32_t once;        // the rows of a sequence are one unit at most
     // rows of a sequence joined to units: per row, how many it leads (0: none) and its
-    // units' tiles; per row and KV head, the entries of the joined list; and the lists
+    // units' tiles (by each of the CTAs that joined them); per row and KV head, the entries of
+    // the joined list; and the lists
     int32_t* row_lead;
     int32_t* row_tiles;
     int32_t* unit_entries;
     int2* list;          // page number, index in the sequence and rows
+    int32_t join_parts;  // CTAs of a row that join its heads' lists, at most kMostJoinParts
+    int32_t join_team;   // warps of a head
 };
 
+constexpr int kMostJoinParts = 8;
 constexpr int kSelDoneRows = 64;     // query rows of a unit of pa_decode_selected, at most
 
 cudaError_t launch_pages_take(const CacheGeom& g, const int32_t* seq_lens, const int32_t* q_lens,
@@ -85,7 +89,7 @@ cudaError_t launch_select(const SelectParams& P, int sms, cudaStream_t stream);
 int selected_rows(int heads, int max_q_len);
 int selected_row_tiles(int D, int rows);
 int selected_ctas_per_sm();
-cudaError_t launch_decode_selected(const SelectedParams& P, int rows, int nt, int grid,
+cudaError_t launch_decode_selected(const SelectedParams& P, int rows, int nt, int grid, int sms,
                                    cudaStream_t stream);
 
 }  // namespace pa
