@@ -49,17 +49,19 @@ struct SelCfg {
     static constexpr int kStage = 2 * kStep * kRow;
     static constexpr int kRows = 8 * NT;                   // q heads a unit has room for
     static constexpr int kQRow = 2 * D + 16;               // (ldmatrix: rows on other banks)
-    static constexpr int kMergeRows = 4;                   // rows merged at a time
-    static constexpr int kMergeRow = D + 4;                // floats
-    static constexpr int kMergeWarp = kMergeRows * kMergeRow + 2 * kMergeRows;
-    // eight rows: every warp has their queries in registers, and merges alternate between
-    // two buffers, so that a unit costs one barrier
+    // eight rows: every warp has their queries in registers, and merges of four alternate
+    // between two buffers, so that a unit costs one barrier or two.  More: merges of sixteen in
+    // the ring's stage that is free just then
     static constexpr bool kQInRegs = NT == 1;
+    static constexpr int kMergeRows = NT == 1 ? 4 : 16;    // rows merged at a time
     static constexpr int kBuffers = NT == 1 ? 2 : 1;
-    static constexpr int kMergeFloats = kWarps * kMergeWarp;
     static constexpr int kOffQ = kWarps * kStages * kStage;
-    static constexpr int kOffMerge = kOffQ + (kQInRegs ? 0 : kRows * kQRow);
-    static constexpr int kSmem = kOffMerge + kBuffers * kMergeFloats * 4;
+    static constexpr int kOffMl = kOffQ + (kQInRegs ? 0 : kRows * kQRow);     // max and sum
+    static constexpr int kOffFree = kOffMl + kBuffers * kWarps * kMergeRows * 8;   // free stages
+    static constexpr int kOffMerge = kOffFree + 16;
+    static constexpr int kMergeWarp = kMergeRows * D * 4;
+    static constexpr int kSmem = kOffMerge + (NT == 1 ? kBuffers * kWarps * kMergeWarp : 0);
+    static_assert(NT == 1 || kMergeWarp <= kStage, "a warp's rows in a stage");
     static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
     static_assert(kOffQ % 16 == 0 && kOffMerge % 16 == 0, "alignment");
 };
@@ -475,7 +477,6 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
 
     const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::kStage;
     const uint32_t qbase = smem_u32(smem + Cfg::kOffQ);
-    float* merge = reinterpret_cast<float*>(smem + Cfg::kOffMerge);
 
     // ---- the load side runs ST - 1 steps ahead, over unit boundaries
     constexpr int CH = ROW / 16, RPI = 32 / CH;   // pieces of a row, rows an instruction
@@ -893,57 +894,68 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                 return (int64_t)u.row * g.Hq + (int64_t)u.hk * g.G + r;
             };
             const int part = c_first == c_last ? -1 : 2 * cta + (cta == c_first ? 1 : 0);
+            // (the stage that the next load goes to: what was in it has been used)
+            int* s_free = reinterpret_cast<int*>(smem + Cfg::kOffFree);
+            if (NT > 1 && lane == 0) s_free[warp] = stage == 0 ? ST - 1 : stage - 1;
 #pragma unroll
             for (int r0 = 0; r0 < Cfg::kRows; r0 += MR) {
                 if (r0 >= R) break;
-                const int nt = r0 / 8;
-                float* area = merge + (Cfg::kBuffers > 1 ? buffer * Cfg::kMergeFloats : 0);
-                float* mw = area + warp * Cfg::kMergeWarp;
-                // rows r0 .. r0 + 3 are with the lanes whose pairs are these columns
-                const bool mine = t4 / 2 == (r0 % 8) / 4;
+                // row r is at r * D of a warp's area, its columns in eights turned by r / 2
+                auto area = [&](int w) {
+                    return reinterpret_cast<float*>(
+                        NT == 1 ? smem + Cfg::kOffMerge + (buffer * W + w) * Cfg::kMergeWarp
+                                : smem + (w * ST + s_free[w]) * Cfg::kStage);
+                };
+                float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffMl) + buffer * W * MR;
+                float* mw = NT == 1 ? area(warp)
+                                    : reinterpret_cast<float*>(
+                                          smem + (warp * ST + (stage == 0 ? ST - 1 : stage - 1)) *
+                                                     Cfg::kStage);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = l[nt][e];
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    x += __shfl_xor_sync(0xffffffffu, x, 8);
-                    x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    const int r = (2 * t4 + e) % MR;
-                    if (mine) {
-                        if (gr == 0) {
-                            mw[MR * Cfg::kMergeRow + r] = m[nt][e];
-                            mw[MR * Cfg::kMergeRow + MR + r] = x;
-                        }
+                for (int nt = r0 / 8; nt < NT && nt * 8 < r0 + MR; ++nt) {
+                    if (8 * nt >= R) break;
+                    // (of eight rows the four of r0 are with half of the lanes)
+                    const bool mine = MR >= 8 || t4 / 2 == (r0 % 8) / 4;
 #pragma unroll
-                        for (int i = 0; i < OT; ++i) {
-                            mw[r * Cfg::kMergeRow + 16 * i + gr] = o[i][nt][e];
-                            mw[r * Cfg::kMergeRow + 16 * i + 8 + gr] = o[i][nt][e + 2];
+                    for (int e = 0; e < 2; ++e) {
+                        float x = l[nt][e];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        const int r = (8 * nt + 2 * t4 + e) % MR;
+                        if (mine) {
+                            if (gr == 0) ml[warp * MR + r] = make_float2(m[nt][e], x);
+                            float* to = mw + r * D + gr;
+#pragma unroll
+                            for (int i = 0; i < OT; ++i) {
+                                to[(16 * i) ^ (8 * t4)] = o[i][nt][e];
+                                to[(16 * i + 8) ^ (8 * t4)] = o[i][nt][e + 2];
+                            }
                         }
                     }
                 }
                 __syncthreads();
-                // a warp a row
-                static_assert(MR == W, "a warp a row");
-                if (r0 + warp < R) {
-                    const int mr = warp, r = r0 + warp;
+                // a row a warp
+#pragma unroll
+                for (int rr = warp; rr < MR; rr += W) {
+                    const int r = r0 + rr;
+                    if (r >= R) break;
                     constexpr int DPL = D / 32;
                     float M = kUnseen;
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        M = fmaxf(M, area[w * Cfg::kMergeWarp + MR * Cfg::kMergeRow + mr]);
+                    for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * MR + rr].x);
                     float den = 0.f, acc[DPL];
 #pragma unroll
                     for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        const float* b = area + w * Cfg::kMergeWarp;
-                        const float mv = b[MR * Cfg::kMergeRow + mr];
-                        const float lv = b[MR * Cfg::kMergeRow + MR + mr];
-                        if (mv == kUnseen && lv == 0.f) continue;     // saw nothing
-                        const float x = mv == kUnseen ? 1.f : ex2(mv - M);
-                        den += x * lv;
+                        const float2 z = ml[w * MR + rr];
+                        const float* b = area(w) + rr * D + (lane * DPL ^ (8 * (r / 2 & 3)));
+                        if (z.x == kUnseen && z.y == 0.f) continue;   // saw nothing
+                        const float x = z.x == kUnseen ? 1.f : ex2(z.x - M);
+                        den += x * z.y;
 #pragma unroll
-                        for (int e = 0; e < DPL; ++e)
-                            acc[e] += x * b[mr * Cfg::kMergeRow + lane * DPL + e];
+                        for (int e = 0; e < DPL; ++e) acc[e] += x * b[e];
                     }
                     // (a NaN sum is not "no visible key")
                     const bool none = den == 0.f;
