@@ -1135,3 +1135,16 @@ def test_tensors_on_the_host_are_refused():
             B.pa_rope_append(*args[:i], args[i].cpu(), *args[i + 1:])
     torch.cuda.synchronize()
     no_error(err)
+
+
+@pytest.mark.parametrize("Hkv,page,budget,ctx,ql", [
+    (8, 16, 6, [70000, 200], [5, 155]),        # more pages than a warp looks at together
+    (8, 16, 40, [70000], [5]),                 # a CTA a head
+    (12, 16, 7, [5000, 60], [3, 20]), (5, 32, 9, [300, 60], [30, 20]), (9, 16, 3, [400], [2]),
+    (1, 16, 300, [9000, 5000], [6, 4]), (3, 16, 70, [2000], [75]),
+])
+def test_attention_of_rows_of_one_sequence_by_heads(Hkv, page, budget, ctx, ql):
+    """A row's heads in one CTA, or shared out among several; a warp a head, or more."""
+    test_attention_of_rows_of_one_sequence(64, 2, Hkv, page, 0, 0, budget, ctx, ql, "plain", 0)
+    if len(ctx) == 1:
+        test_attention_of_rows_of_one_sequence(64, 2, Hkv, page, 0, 90, budget, ctx, ql, "holes", 0)
