@@ -695,16 +695,21 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         };
 
 #pragma unroll 1
-        for (int tok = sh.a; tok < sh.z; tok += 16) {
+        for (int tok = sh.a; tok < sh.z;) {
             cp_async_wait<ST - 2>();
             __syncwarp();
             const uint32_t mt = __shfl_sync(0xffffffffu, meta, stage);
             const int at = JOINED ? __shfl_sync(0xffffffffu, meta_at, stage) : 0;
-            const int a = (int)(mt & 31u), z = (int)((mt >> 5) & 31u);
             issue(stage == 0 ? ST - 1 : stage - 1);   // into the stage the last step left
             const uint32_t sk = ring + stage * Cfg::kStage, sv = sk + 16 * ROW;
             stage = stage + 1 == ST ? 0 : stage + 1;
-            if (z == a) continue;                     // no key of the step is there
+            tok += 16;
+            // (taken out of mt again where they are needed: kept, they and tok cost the widest
+            // forms registers that they then spill; 128 sequences of 3 rows, 64 q heads 208 us,
+            // so 204)
+            auto first_key = [&]() { return (int)(mt & 31u); };
+            auto end_key = [&]() { return (int)((mt >> 5) & 31u); };
+            if (first_key() == end_key()) continue;   // no key of the step is there
 
             // ---- scores of 16 keys
             float s[NT][4];
@@ -743,8 +748,9 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         for (int e = 0; e < 4; ++e) s[nt][e] += s1[nt][e];
                 }
             }
-            const bool part_seen = JOINED ? !(mt >> 16 & 1u) : a > 0 || z < 16;
+            const bool part_seen = JOINED ? !(mt >> 16 & 1u) : first_key() > 0 || end_key() < 16;
             if (part_seen) {
+                const int a = first_key(), z = end_key();
                 if constexpr (JOINED) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -845,6 +851,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
             } else if constexpr (JOINED) {
                 // row by row of the sequence: the keys it does not see are zeros in V, and
                 // the product is added to its own columns only
+                const int a = first_key(), z = end_key();
                 for (int i0 = 0; i0 < u.rows; ++i0) {
                     const int p = __shfl_sync(0xffffffffu, upos, i0);
                     auto word = [&](int key) -> uint32_t {
