@@ -1046,60 +1046,75 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                         lse[i] = load_lse(i, c_first + lane);
                         load_parts(i, c_first);
                     }
+                    float M[K], den[K], acc[K][DPL];
+                    bool poison[K];
 #pragma unroll
                     for (int i = 0; i < K; ++i) {
-                        if (!there[i]) continue;
-                        float M = lse[i];
-                        bool poison = M != M;
+                        M[i] = lse[i];
+                        poison[i] = M[i] != M[i];
                         for (int c = c_first + lane + 32; c <= c_last; c += 32) {
                             const float y = load_lse(i, c);
-                            poison |= y != y;
-                            M = fmaxf(M, y);
+                            poison[i] |= y != y;
+                            M[i] = fmaxf(M[i], y);
                         }
 #pragma unroll
                         for (int y = 16; y > 0; y >>= 1)
-                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
-                        poison = __any_sync(0xffffffffu, poison);
-                        float den = 0.f, acc[DPL];
+                            M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], y));
+                        poison[i] = __any_sync(0xffffffffu, poison[i]);
+                        den[i] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
+                        for (int e = 0; e < DPL; ++e) acc[i][e] = 0.f;
+                    }
 #pragma unroll 1
-                        for (int cb = c_first; cb <= c_last; cb += 32) {
+                    for (int cb = c_first; cb <= c_last; cb += 32) {
+                        float y[K];
+#pragma unroll
+                        for (int i = 0; i < K; ++i) {
                             const float v = cb == c_first ? lse[i] : load_lse(i, cb + lane);
-                            const float y = cb + lane > c_last ? 0.f
-                                            : poison           ? NAN
-                                            : v == -INFINITY   ? 0.f
-                                                               : ex2((v - M) * kLog2e);
+                            y[i] = cb + lane > c_last ? 0.f
+                                   : poison[i]        ? NAN
+                                   : v == -INFINITY   ? 0.f
+                                                      : ex2((v - M[i]) * kLog2e);
+                        }
 #pragma unroll 1
-                            for (int c0 = cb; c0 <= min(c_last, cb + 31); c0 += B) {
-                                if (c0 > c_first) load_parts(i, c0);
+                        for (int c0 = cb; c0 <= min(c_last, cb + 31); c0 += B) {
+                            if (c0 > c_first)
+#pragma unroll
+                                for (int i = 0; i < K; ++i) load_parts(i, c0);
+#pragma unroll
+                            for (int i = 0; i < K; ++i)
 #pragma unroll
                                 for (int j = 0; j < B; ++j) {
-                                    const float w = __shfl_sync(0xffffffffu, y, c0 - cb + j);
-                                    den += w;
+                                    const float w = __shfl_sync(0xffffffffu, y[i], c0 - cb + j);
+                                    den[i] += w;
 #pragma unroll
                                     for (int e = 0; e < DPL; ++e)
-                                        if (w != 0.f) acc[e] = fmaf(w, x[i][j][e], acc[e]);
+                                        if (w != 0.f) acc[i][e] = fmaf(w, x[i][j][e], acc[i][e]);
                                 }
-                            }
                         }
-                        const bool none = den == 0.f;
-                        const float inv = none ? 0.f : 1.f / den;
+                    }
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        if (!there[i]) continue;
+                        const bool none = den[i] == 0.f;
+                        const float inv = none ? 0.f : 1.f / den[i];
                         const int64_t row = out_row(row_in[i]);
                         if (row >= 0) {
                             __nv_bfloat16* dst = P.out + row * D + lane * DPL;
 #pragma unroll
                             for (int e = 0; e < DPL; e += 2)
                                 *reinterpret_cast<uint32_t*>(dst + e) =
-                                    pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+                                    pack_bf16x2(acc[i][e] * inv, acc[i][e + 1] * inv);
                         }
                         if (P.lse != nullptr && lane == 0 && row >= 0)
-                            P.lse[row] = none ? -INFINITY : M + lg2(den) * kLn2;
+                            P.lse[row] = none ? -INFINITY : M[i] + lg2(den[i]) * kLn2;
                     }
                 };
                 while (ends != 0) {
                     if (NT > 1 && others < 4)
                         join_rows(Const<4>{}, Const<4>{});
+                    else if (NT > 2)           // (O had the registers; with 16 rows it spills)
+                        join_rows(Const<4>{}, Const<8>{});
                     else if (others < 8)
                         join_rows(Const<2>{}, Const<8>{});
                     else
