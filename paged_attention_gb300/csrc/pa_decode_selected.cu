@@ -27,9 +27,9 @@
 // whether V is finite, and multiplies row by row where it is not.
 //
 // Measured (head_dim 128, 8 KV heads): 64 rows of up to 32 pages of 64, 32 q heads, 60 us
-// for 54.5 of HBM time; 128 sequences of 3 rows, 64 q heads, 40 pages, 210 us for 194
+// for 54.5 of HBM time; 128 sequences of 3 rows, 64 q heads, 40 pages, 204 us for 194
 // (each row by itself: 540).  With 32 query rows a unit the products and the softmax set
-// the pace: 64 sequences of 4 rows, 64 q heads, 103 us for 56.
+// the pace: 64 sequences of 4 rows, 64 q heads, 90 us for 56.
 #include <algorithm>
 #include <type_traits>
 
@@ -70,8 +70,9 @@ namespace {
 
 // No CTA takes less than this of the flat line: joining a unit's parts costs more
 // than the tiles it would spread (one sequence of 131071 tokens, 256 pages of 16, 8
-// heads: 15.7 us with 2, 14.5 with 3, 13.7 with 4).
-constexpr int kMinShareSel(int nt) { return nt == 1 ? 4 : 4; }
+// heads: 13.1 us with 2, 12.7 with 3, 12.2 with 4, 12.1 with 6; four rows of it 28.9 with 4,
+// 30.2 with 12).
+constexpr int kMinShareSel = 4;
 
 constexpr int kDoneRows = kSelDoneRows;       // counters of a CTA: one a query row
 constexpr int kMostRows = 6;                  // of a unit: what an entry has bits for
@@ -197,7 +198,8 @@ __device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, in
 // ---- joins the lists of rows of one sequence (the CTAs (t, c) of row t; only a unit's first
 // row's go on).  P.join_team warps a KV head, some pages at a time: the set of rows of every
 // page, and a bit for the pages that have any, in shared memory; the bits before a page tell
-// its place.  Where rows are few their heads are shared out among P.join_parts CTAs.
+// its place.  Where rows are few their heads are shared out among P.join_parts CTAs (one
+// sequence of 131071 tokens, 4 rows, attention and all: a CTA with a warp a head 50 us, 29 so).
 constexpr int kJoinWarps = 8;
 constexpr int kJoinPages = 4096;             // a warp
 
@@ -430,7 +432,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     }
     const int64_t upto = before(mine);
     const int64_t C = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel(NT) - 1) / kMinShareSel(NT));
+    const int64_t N = min((int64_t)gridDim.x, (C + kMinShareSel - 1) / kMinShareSel);
     const int cta = blockIdx.x;
     if (cta >= N) return;
     const int64_t lo = quotient(C * cta, N), hi = quotient(C * (cta + 1), N);

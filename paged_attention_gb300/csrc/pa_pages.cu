@@ -11,7 +11,7 @@
 // another: the stack is read below its top only, and the table at pages that were
 // there before.  Bound by latency (a chain of length, sums, page number, slot): both
 // calls of a decode step of 64 sequences 5.3 us in a graph, of 190149 new rows of 256
-// prompts 7.2, 11 from the host.
+// prompts 7.2, 12 from the host.
 #include <algorithm>
 
 #include "pa_step_common.cuh"

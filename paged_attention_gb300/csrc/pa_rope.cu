@@ -13,7 +13,7 @@
 // lanes.  A lane has two pieces of 16 bytes, the pairs' both halves, so a row is
 // read and written once, in whole sectors.  Bound by HBM on long prompts (15237
 // rows of 32 + 8 + 8 heads: 58.5 us for 56.3 of HBM time), by latency on a decode step
-// (64 rows: 2.6 us in a graph, 8 from the host).
+// (64 rows: 2.6 us in a graph, 9 from the host).
 #include <algorithm>
 
 #include "pa_step_common.cuh"

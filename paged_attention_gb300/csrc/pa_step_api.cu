@@ -12,8 +12,9 @@ namespace {
 constexpr int kMaxGridSel = 1024;        // CTAs of pa_decode_selected
 // A unit's fixed cost (its first loads, its warps' merge), in 64-key tiles, which are half
 // the bytes with head_dim 64.  64 rows of up to 32 pages of 64: 61 us with 1 to 8, 62 with
-// 12; head_dim 64 46.8 with 1, 38.9 with 6; 64 sequences of 4 rows (16 query rows a
-// unit) 85 with 3, 80 with 6; 128 sequences of 3 rows (24) 223, 215 with 6, 213 with 12.
+// 12; head_dim 64 46.8 with 1, 40.2 with 3, 38.0 with 6; 64 sequences of 4 rows (16 query rows a
+// unit) 75.2 with 3, 72.7 with 6, 75.5 with 12; of 64 q heads (32) 109 with 4, 89 with 8 and 10;
+// 128 sequences of 3 rows (24) 211 with 3, 207 with 6, 206 with 10 and 12.
 constexpr int sel_unit_cost(int D, int rows) {
     return (rows > 16 ? 10 : rows > 8 ? 6 : 3) * 128 / D;
 }
