@@ -98,7 +98,9 @@ pa_status geometry(const pa_problem* pp, bool queries, CacheGeom& g) {
     g.total_q = p.total_q_tokens;
     g.max_q_len = p.max_q_len;
     g.max_ctx = p.max_context_len;
-    g.window = p.window;
+    // a window no shorter than any context hides nothing; a shorter one is below 2^30, so that
+    // position - window - position stays within 32 bits
+    g.window = p.window < p.max_context_len ? p.window : 0;
     g.tok_rows = p.layout == PA_NHD ? p.num_kv_heads : 1;
     g.head_rows = p.layout == PA_NHD ? 1 : p.page_size;
     g.sm_scale = p.sm_scale;

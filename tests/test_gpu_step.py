@@ -1148,3 +1148,22 @@ def test_attention_of_rows_of_one_sequence_by_heads(Hkv, page, budget, ctx, ql):
     test_attention_of_rows_of_one_sequence(64, 2, Hkv, page, 0, 0, budget, ctx, ql, "plain", 0)
     if len(ctx) == 1:
         test_attention_of_rows_of_one_sequence(64, 2, Hkv, page, 0, 90, budget, ctx, ql, "holes", 0)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30 + 1, 41])
+@pytest.mark.parametrize("D,G,page,ctx,ql", [(128, 4, 16, [18, 35, 16], [6, 5, 6]),
+                                             (64, 2, 32, [50, 17], [6, 3]),
+                                             (64, 5, 16, [34], [6])])
+def test_a_window_of_the_whole_context_hides_nothing(D, G, page, ctx, ql, window):
+    """Windows no shorter than any context, up to the largest number there is: every bit as with
+    none, rows of a sequence on both sides of a step's first key among them."""
+    window = max(window, max(ctx))
+    pages, table, seq, pos, k, v, q = attend_case(D, G, 2, page, 0, ctx, ql, 3)
+    budget = R.up(max(ctx), page)
+    sel = lists(seq, pos, 2, budget, page, 0, 5)
+    kw = dict(num_seqs=len(ctx), num_q_heads=2 * G, head_dim=D, page_size=page, num_pages=pages,
+              max_pages_per_seq=len(table[0]), total_q_tokens=len(seq), max_q_len=max(ql),
+              max_context_len=max(ctx))
+    none = check_attend(problem(**kw), budget, table, seq, pos, k, v, q, sel)
+    got = check_attend(problem(window=window, **kw), budget, table, seq, pos, k, v, q, sel)
+    assert torch.equal(got[0], none[0]) and torch.equal(got[1], none[1])
