@@ -18,6 +18,12 @@ inline bool cache_ok(const pa_problem& p, const void* cache, const void* scale) 
     if (!cache || !aligned(cache, 16)) return false;
     return p.kv_dtype != PA_MX4 || (scale && aligned(scale, 16));
 }
+// Whether a kernel can count a call's work on one line: a unit of up to `tiles` tiles and its
+// fixed cost in 32 bits, and all units, times the CTAs of a grid (2^10 at most), in 64.
+inline bool line_fits(int64_t units, int64_t tiles, int unit_cost) {
+    const int64_t each = tiles + unit_cost;
+    return each <= 0x7fffffff && (units <= 0 || each <= ((int64_t)1 << 52) / units);
+}
 inline bool ints_ok(const void* p) { return p && aligned(p, 4); }
 inline bool lens_ok(const int32_t* table, const int32_t* ctx, const int32_t* ql) {
     return ints_ok(table) && ints_ok(ctx) && ints_ok(ql);

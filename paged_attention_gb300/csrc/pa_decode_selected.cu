@@ -440,8 +440,14 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
     {
         const int src = __ffs(__ballot_sync(0xffffffffu, upto > lo)) - 1;
         u.start = __shfl_sync(0xffffffffu, upto - mine, src);
-        // the row among that lane's, then the head among the row's
+        // the row among that lane's, then the head among the row's.  (Neither is missed but where
+        // another call writes to the workspace at the same time.)
+        auto missed = [&](bool past) {
+            if (past) flag_error(P.header + H_ERROR, PA_DEV_BAD_WORKSPACE);
+            return past;
+        };
         for (int t0 = src * run;; t0 += 32) {
+            if (missed(t0 >= g.total_q)) return;
             const int64_t c = t0 + lane < g.total_q ? row_cost<JOINED>(P, t0 + lane) : 0;
             const int64_t to = u.start + before(c);
             const uint32_t past = __ballot_sync(0xffffffffu, to > lo);
@@ -455,6 +461,7 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
         load_row<JOINED>(P, u);
         if constexpr (JOINED) {
             for (int h0 = 0;; h0 += 32) {
+                if (missed(h0 >= g.Hkv)) return;
                 const int64_t c =
                     h0 + lane < g.Hkv
                         ? tiles_of(g, P.unit_entries[(int64_t)u.row * g.Hkv + h0 + lane]) + cost

@@ -1,5 +1,6 @@
 // pa_step_api.cu -- the entry points of pa_step.h: argument checks and launches, and
 // the frequencies of rotary positions, which are worked out on the host.
+#include <algorithm>
 #include <cmath>
 
 #include "pa_cache_host.cuh"
@@ -66,6 +67,12 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
     L.unit_cost = pp->unit_cost > 0   ? pp->unit_cost
                   : pp->unit_cost < 0 ? 0
                                       : sel_unit_cost(g.D, 8 * L.nt);
+    // (a unit's list has no page twice, nor more than its rows' lists together)
+    const int64_t pages = std::min(((int64_t)g.max_ctx + g.ps - 1) >> g.ps_shift,
+                                   (int64_t)L.together * budget);
+    if (!line_fits((int64_t)g.total_q * g.Hkv,
+                   ((pages << g.ps_shift) + kDecodeTile - 1) / kDecodeTile, L.unit_cost))
+        return PA_ERR_UNSUPPORTED;
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
     L.off_part = align256(L.off_done + (int64_t)kMaxGridSel * kSelDoneRows * 4);

@@ -56,7 +56,7 @@ struct SelectedParams {
     float* part_lse;     // [2 * grid][rows]
     __nv_bfloat16* out;
     float* lse;
-    int32_t unit_cost;   // fixed cost of a unit, in tiles
+    int32_t unit_cost;   // fixed cost of a unit, in tiles (line_fits)
     int32_t once;        // the rows of a sequence are one unit at most
     // rows of a sequence joined to units: per row, how many it leads (0: none) and its
     // units' tiles (by each of the CTAs that joined them); per row and KV head, the entries of

@@ -205,6 +205,26 @@ def test_more_rows_than_are_counted_are_refused(lib, name):
     assert call(lib, name, problem(total_q_tokens=(1 << 30) + 1)) == B.PA_ERR_UNSUPPORTED
 
 
+def test_unit_costs_that_cannot_be_counted_are_refused(lib):
+    """A kernel would count a unit's tiles and its cost in 32 bits, and all units' times the
+    CTAs in 64."""
+    d, most = "pa_decode_selected", 2 ** 31 - 1
+    size = lambda budget=4, **kw: B.pa_selected_workspace_size(problem(**kw), budget)  # noqa: E731
+    # a list of 4 pages of 16 is one tile, of 10 pages three; rows together list twice as many
+    for kw, budget, tiles in ((dict(), 4, 1), (dict(), 10, 3), (dict(), 1 << 20, 3),
+                              (dict(max_q_len=2), 4, 2)):
+        assert size(budget, unit_cost=most - tiles, **kw) > 0
+        for cost in (most - tiles + 1, most):
+            assert size(budget, unit_cost=cost, **kw) == 0
+            args = [budget] + GOOD[d][1:]
+            assert call(lib, d, problem(unit_cost=cost, **kw), args) == B.PA_ERR_UNSUPPORTED
+    rows = 1 << 27                            # 2^28 rows and heads
+    assert size(total_q_tokens=rows, unit_cost=(1 << 24) - 1) > 0
+    assert size(total_q_tokens=rows, unit_cost=1 << 24) == 0
+    assert call(lib, d, problem(total_q_tokens=rows, unit_cost=1 << 24)) == B.PA_ERR_UNSUPPORTED
+    assert size(unit_cost=-2 ** 31) > 0       # none
+
+
 def test_queries_in_place_are_dense(lib):
     r = "pa_rope_append"
     for stride in (1032, 1536):
