@@ -102,7 +102,9 @@ PA_API pa_status pa_kv_expand(const pa_problem* problem, const void* k_cache, co
  * head_dim 128, 64 for head_dim 64) in one kernel launch.  The cache's length
  * is split over the GPU inside the kernel, and the parts of a split unit are
  * joined by the last CTA to finish one: no task map is built or read.
- * num_ctas and unit_cost have their pa.h meaning (num_ctas at most 1024);
+ * num_ctas and unit_cost have their pa.h meaning (num_ctas at most 1024; a unit_cost that,
+ * added to the 64-token tiles of max_context_len, is 2^31 or more, or over all sequences,
+ * KV heads and blocks of rows (two at most) more than 2^52: PA_ERR_UNSUPPORTED);
  * balance_rows is not used.
  * The scores and the products with V are taken in f16 by the tensor cores with
  * fp32 sums; the block scales of K are applied in fp32.  What f16 rounds:

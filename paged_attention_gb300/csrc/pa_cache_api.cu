@@ -132,6 +132,10 @@ pa_status mx4_layout(const pa_problem* pp, CacheGeom& g, Mx4Layout& L) {
         if (L.grid > kMaxGrid) L.grid = kMaxGrid;
     }
     L.unit_cost = pp->unit_cost > 0 ? pp->unit_cost : pp->unit_cost < 0 ? 0 : mx4_unit_cost(8 * L.nt);
+    // (two blocks of rows are two units)
+    if (!line_fits((int64_t)2 * g.B * g.Hkv, (g.max_ctx + kDecodeTile - 1) / kDecodeTile,
+                   L.unit_cost))
+        return PA_ERR_UNSUPPORTED;
     L.rows = 8 * L.nt;
     L.off_done = kHeaderWords * 4;
     L.off_part = align256(L.off_done + (int64_t)kMaxGrid * 4);

@@ -51,7 +51,7 @@ struct Mx4Params {
     float* part_lse;     // [2 * grid][rows]
     __nv_bfloat16* out;
     float* lse;
-    int32_t unit_cost;   // fixed cost of a unit, in tiles
+    int32_t unit_cost;   // fixed cost of a unit, in tiles (line_fits)
 };
 
 // No CTA takes less than this of the flat line: joining a unit's parts costs more

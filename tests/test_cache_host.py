@@ -149,6 +149,22 @@ def test_attention_entry_points_refuse_a_4_bit_cache(lib):
     assert B.pa_static_workspace_size(p, 0) == 0
 
 
+def test_unit_costs_that_cannot_be_counted_are_refused(lib):
+    """pa_decode_mx4 counts a unit's tiles and its cost in 32 bits, and all units' times the
+    CTAs in 64."""
+    d, most = "pa_decode_mx4", 2 ** 31 - 1
+    size = lambda **kw: B.pa_mx4_workspace_size(problem(**kw))  # noqa: E731
+    assert size(unit_cost=most - 3) > 0       # 160 tokens are three tiles
+    for cost in (most - 2, most):
+        assert size(unit_cost=cost) == 0
+        assert call(lib, d, problem(unit_cost=cost)) == B.PA_ERR_UNSUPPORTED
+    many = dict(num_seqs=1 << 28)             # 2^30 blocks of rows
+    assert size(unit_cost=(1 << 22) - 3, **many) > 0
+    assert size(unit_cost=(1 << 22) - 2, **many) == 0
+    assert call(lib, d, problem(unit_cost=(1 << 22) - 2, **many)) == B.PA_ERR_UNSUPPORTED
+    assert size(unit_cost=-2 ** 31) > 0       # none
+
+
 def test_binding_checks_new_rows():
     p = problem()
     ok = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
