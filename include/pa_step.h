@@ -105,7 +105,9 @@ PA_API pa_status pa_pages_return(const pa_problem* problem, const int32_t* seq_l
  *   NTK     the base times factor^(rotary_dim / (rotary_dim - 2));
  *   YARN    pairs that make more than high_turns turns over original_context
  *           tokens as they are, fewer than low_turns divided by factor, between
- *           them a line over the pair's index; cos and sin times 0.1 ln(factor) + 1;
+ *           them a line over the pair's index (from the whole index at or before the
+ *           first end, at least 0, to that at or behind the second, at most
+ *           rotary_dim - 1); cos and sin times 0.1 ln(factor) + 1;
  *   BANDS   the same two ends, between them a line over the number of turns. */
 enum { PA_ROPE_NONE = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3, PA_ROPE_BANDS = 4 };
 

@@ -172,7 +172,14 @@ pa_status pa_rope_inv_freq(const pa_rope_scaling* s, double* inv_freq, double* c
     if (s->kind == PA_ROPE_YARN) {
         lo = std::fmax(0.0, std::floor(index_of(s->high_turns)));
         hi = std::fmin(d - 1.0, std::ceil(index_of(s->low_turns)));
-        if (hi == lo) hi = lo + 0.001;
+        // (where no pair makes more than low_turns, or all make more than high_turns, the ends
+        // as they were cut would meet or cross: all pairs are divided, or none)
+        if (hi <= 0.0) {
+            lo = -1.0;
+            hi = 0.0;
+        } else if (hi <= lo) {
+            hi = lo + 0.001;
+        }
     }
     for (int i = 0; i < d / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / d);

@@ -276,6 +276,54 @@ def test_frequencies(lib):
                 assert math.isclose(float(ratio[i]), 1 - r + r / 4, rel_tol=1e-12)
 
 
+@pytest.mark.parametrize("dim", [2, 16, 64, 128])
+def test_frequencies_at_the_ends_of_what_is_accepted(lib, dim):
+    """Pairs above high_turns as they are, below low_turns divided, whatever the parameters: all
+    of them above, all below, all between, and each kind of mixture."""
+    kinds = set()
+    for base in (1.001, 4.0, 10.0, 1e4, 1e6, 1e30):
+        for context in (1.0, 4.0, 6.3, 32.0, 300.0, 4096.0, 1e5, 1e9, 1e300):
+            for high, low in ((32.0, 1.0), (32.0, 8.0), (1.5, 1.0), (1e6, 1e-6)):
+                for kind in (B.PA_ROPE_YARN, B.PA_ROPE_BANDS):
+                    f, _ = B.pa_rope_inv_freq(scaling(kind, dim, base=base, high_turns=high,
+                                                      original_context=context, low_turns=low))
+                    plain = [base ** (-2 * i / dim) for i in range(dim // 2)]
+                    of = []
+                    for i, (x, y) in enumerate(zip(f.tolist(), plain)):
+                        turns = context * y / (2 * math.pi)
+                        # (indices and turns are taken by logarithms: near an end either is right)
+                        if turns > high * (1 + 1e-9):
+                            assert math.isclose(x, y, rel_tol=1e-12), (base, context, high, low, i)
+                            of.append("above")
+                        elif turns < low * (1 - 1e-9):
+                            assert math.isclose(x, y / 4, rel_tol=1e-12), (base, context, high, low, i)
+                            of.append("below")
+                        else:
+                            assert y / 4 * (1 - 1e-12) <= x <= y * (1 + 1e-12)
+                            of.append("between")
+                    kinds.add(tuple(sorted(set(of))))
+    assert {("above",), ("below",), ("between",)} <= kinds
+    if dim > 2:
+        assert ("above", "below", "between") in kinds
+
+
+@pytest.mark.parametrize("dim", [16, 32, 64, 128])
+def test_yarn_frequencies_are_the_published_ones(lib, dim):
+    """Where the published ends do not meet: its line between them, cut to [0, dim - 1]."""
+    for base in (1e4, 1.5e5, 5e5, 1e6):
+        for context in (300.0, 2048.0, 4096.0, 8192.0, 32768.0, 262144.0, 1e6):
+            for high, low in ((32.0, 1.0), (64.0, 1.0), (32.0, 2.0)):
+                at = lambda t: dim * math.log(context / (t * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731,E501
+                lo, hi = max(0.0, math.floor(at(high))), min(dim - 1.0, math.ceil(at(low)))
+                assert 0 <= lo < hi
+                f, _ = B.pa_rope_inv_freq(scaling(B.PA_ROPE_YARN, dim, base=base, high_turns=high,
+                                                  original_context=context, low_turns=low))
+                for i, x in enumerate(f.tolist()):
+                    r = min(1.0, max(0.0, (i - lo) / (hi - lo)))
+                    y = base ** (-2 * i / dim)
+                    assert math.isclose(x, y / 4 * r + y * (1 - r), rel_tol=1e-13)
+
+
 def test_frequencies_that_are_refused(lib):
     for kind, dim, kw in ((5, 64, {}), (-1, 64, {}), (0, 0, {}), (0, 63, {}), (0, 130, {}),
                           (0, 64, dict(base=1.0)), (0, 64, dict(base=math.nan)),
