@@ -65,9 +65,10 @@ enum { PA_DEV_NO_PAGES = 16 };
  *   max_context_len]).  Its q_lens, cut to [0, max_q_len], still count in where the
  *   rows of the sequences after it are.
  *   kv_dtype may be any.  num_pages * page_size at most 2^31 - 1.
- *   context_lens and free_left must not overlap any input; page numbers outside
- *   the pool on the stack are passed on as they are, with PA_DEV_BAD_PAGE, and
- *   slots of -1.
+ *   free_pages: int32 [num_pages].  Page numbers outside the pool on it are passed on as
+ *   they are, with PA_DEV_BAD_PAGE, and slots of -1.
+ *   What is written (block_table, context_lens, row_seq, positions, slots, free_left) must
+ *   overlap neither an input nor each other: PA_ERR_INVALID_ARG.
  */
 PA_API pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_lens,
                                const int32_t* q_lens, int32_t* block_table,
@@ -84,8 +85,9 @@ PA_API pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_len
  *   free_pages: int32 [num_pages]; what is below *free_count (cut to [0, num_pages],
  *     with PA_DEV_BAD_LENGTHS, where it is outside) is left alone.  A push past its
  *     end is not done (PA_DEV_BAD_LENGTHS).
- *   free_left: int32 [1], written: the new number of pages on the stack; must not
- *     overlap an input.
+ *   free_left: int32 [1], written: the new number of pages on the stack.
+ *   free_pages and free_left must overlap neither an input nor each other:
+ *     PA_ERR_INVALID_ARG.
  *   block_table is only read; an entry outside the pool is put back as -1
  *     (PA_DEV_BAD_PAGE).  A page that several sequences share goes back once for
  *     each of them: keep such pages out of the call.

@@ -20,10 +20,27 @@ constexpr int sel_unit_cost(int D, int rows) {
     return (rows > 16 ? 10 : rows > 8 ? 6 : 3) * 128 / D;
 }
 
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    const char* x = static_cast<const char*>(a);
-    const char* y = static_cast<const char*>(b);
-    return x < y + b_bytes && y < x + a_bytes;
+// Memory that a call reads, or writes.
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// Whether one of the first `outputs` spans overlaps any other.
+template <int N>
+bool overlap(const Span (&s)[N], int outputs) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (overlap(s[i], s[j])) return true;
+    return false;
+}
+
+// (no more than addresses have room for)
+int64_t table_bytes(const CacheGeom& g) {
+    return std::min((int64_t)g.B * g.mpps, (int64_t)1 << 56) * 4;
 }
 
 // Pages are pages whatever they hold: E4M3 caches have them too.
@@ -112,13 +129,19 @@ pa_status pa_pages_take(const pa_problem* problem, const int32_t* seq_lens, cons
         (rows && (!ints_ok(row_seq) || !ints_ok(positions) || !ints_ok(slots))) ||
         !aligned(device_error, 4))
         return PA_ERR_INVALID_ARG;
-    // every CTA reads what the first one would overwrite
-    const int64_t n = (int64_t)g.B * 4;
-    if (overlap(context_lens, n, seq_lens, n) || overlap(context_lens, n, q_lens, n) ||
-        overlap(free_left, 4, free_count, 4) || overlap(free_left, 4, seq_lens, n) ||
-        overlap(free_left, 4, q_lens, n) || overlap(context_lens, n, free_count, 4) ||
-        overlap(free_left, 4, context_lens, n))
-        return PA_ERR_INVALID_ARG;
+    // every CTA reads what others would overwrite, rounds of sequences after it has written rows
+    const int64_t n = (int64_t)g.B * 4, t = (int64_t)g.total_q * 4;
+    const Span spans[] = {{context_lens, n},
+                          {free_left, 4},
+                          {row_seq, t},
+                          {positions, t},
+                          {slots, t},
+                          {block_table, table_bytes(g)},
+                          {seq_lens, n},
+                          {q_lens, n},
+                          {free_pages, (int64_t)g.num_pages * 4},
+                          {free_count, 4}};
+    if (overlap(spans, 6)) return PA_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     return status_of(launch_pages_take(g, seq_lens, q_lens, block_table, free_pages, free_count,
@@ -138,9 +161,13 @@ pa_status pa_pages_return(const pa_problem* problem, const int32_t* seq_lens,
         !aligned(device_error, 4))
         return PA_ERR_INVALID_ARG;
     const int64_t n = (int64_t)g.B * 4;
-    if (overlap(free_left, 4, free_count, 4) || overlap(free_left, 4, seq_lens, n) ||
-        overlap(free_left, 4, keep_lens, n))
-        return PA_ERR_INVALID_ARG;
+    const Span spans[] = {{free_pages, (int64_t)g.num_pages * 4},
+                          {free_left, 4},
+                          {block_table, table_bytes(g)},
+                          {seq_lens, n},
+                          {keep_lens, n},
+                          {free_count, 4}};
+    if (overlap(spans, 2)) return PA_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     return status_of(launch_pages_return(g, seq_lens, keep_lens, block_table, free_pages,

@@ -1167,3 +1167,33 @@ def test_a_window_of_the_whole_context_hides_nothing(D, G, page, ctx, ql, window
     none = check_attend(problem(**kw), budget, table, seq, pos, k, v, q, sel)
     got = check_attend(problem(window=window, **kw), budget, table, seq, pos, k, v, q, sel)
     assert torch.equal(got[0], none[0]) and torch.equal(got[1], none[1])
+
+
+def test_pages_of_one_buffer():
+    """Every tensor of the two calls a slice of one buffer, back to back: no overlap."""
+    seq, q, page, pages, width, rows = [5, 0, 31], [12, 1, 1], 16, 9, 4, 15
+    sizes = dict(seq=3, table=3 * width, ctx=3, free=pages, left=1, q=3, count=1, rs=rows, pos=rows,
+                 slots=rows, err=1)
+    arena, at, s = ints([-9] * sum(sizes.values())), 0, {}
+    for name, n in sizes.items():
+        s[name] = arena[at:at + n]
+        at += n
+    table = [[0, -1, -1, -1], [-1] * 4, [1, 2, -1, -1]]
+    stack = [3, 4, 5, 6, 7, 8, -1, -1, -1]
+    for name, x in (("seq", seq), ("q", q), ("table", sum(table, [])), ("free", stack),
+                    ("count", [6]), ("err", [0])):
+        s[name].copy_(ints(x))
+    p = problem(num_seqs=3, page_size=page, num_pages=pages, max_pages_per_seq=width,
+                total_q_tokens=rows, max_q_len=12, max_context_len=width * page)
+    t = s["table"].view(3, width)
+    B.pa_pages_take(p, s["seq"], s["q"], t, s["free"], s["count"], s["ctx"], s["rs"], s["pos"],
+                    s["slots"], s["left"], s["err"])
+    want = R.take(seq, q, table, stack, 6, page=page, pages=pages, rows=rows, max_q=12,
+                  max_ctx=width * page)
+    maps = list(zip(s["rs"].tolist(), s["pos"].tolist(), s["slots"].tolist()))
+    assert (t.tolist(), s["ctx"].tolist(), maps, int(s["left"]), int(s["err"])) == want
+    s["count"].copy_(s["left"])
+    s["q"].zero_()                            # the lengths that stay
+    B.pa_pages_return(p, s["ctx"], s["q"], t, s["free"], s["count"], s["left"], s["err"])
+    assert int(s["left"]) == pages and sorted(s["free"].tolist()) == list(range(pages))
+    no_error(s["err"])

@@ -225,6 +225,21 @@ def test_unit_costs_that_cannot_be_counted_are_refused(lib):
     assert size(unit_cost=-2 ** 31) > 0       # none
 
 
+@pytest.mark.parametrize("name,outputs,sizes", [
+    # 3 sequences, 3 rows, 50 pages, a table of 3 x 10; in the arguments' order
+    ("pa_pages_take", {2, 5, 6, 7, 8, 9}, [12, 12, 120, 200, 4, 12, 12, 12, 12, 4]),
+    ("pa_pages_return", {3, 5}, [12, 12, 120, 200, 4, 4]),
+])
+def test_outputs_of_the_page_operators_stay_off_everything_else(lib, name, outputs, sizes):
+    """Each output on the first and on the last word of every other argument."""
+    for i in outputs:
+        for j in set(range(len(sizes))) - {i}:
+            first = GOOD[name][j].value
+            for at_byte in (first, first + sizes[j] - 4, first - sizes[i] + 4):
+                args = swap(name, i, ctypes.c_void_p(at_byte))
+                assert call(lib, name, problem(), args) == B.PA_ERR_INVALID_ARG, (i, j, at_byte)
+
+
 def test_queries_in_place_are_dense(lib):
     r = "pa_rope_append"
     for stride in (1032, 1536):
