@@ -154,8 +154,9 @@ typedef struct pa_rope {
  *   q: bf16 [total_q_tokens][Hq][D], tokens q_stride elements apart, or NULL with
  *     q_out NULL; k_new, v_new as pa_kv_append's.  Strides: multiples of 8, at
  *     least a token's rows: the three may be slices of a fused projection's output.
- *   q_out: bf16 [total_q_tokens][Hq][D], dense; may be q itself where q is dense (where not:
- *     PA_ERR_INVALID_ARG).
+ *   q_out: bf16 [total_q_tokens][Hq][D], dense; may be q itself where q is dense.  Any other
+ *     overlap with the memory from the first to the last of q, k_new or v_new:
+ *     PA_ERR_INVALID_ARG.
  *   positions: any int32 >= 0 (max_context_len does not bound them).
  *   A row whose slot is -1 is not cached and its q not written; other slots outside
  *   the pool: neither, and PA_DEV_BAD_PAGE; a negative position: neither, and

@@ -261,6 +261,16 @@ pa_status pa_rope_append(const pa_problem* problem, const pa_rope* rope, const u
         !aligned(q_out, 16) || (q != nullptr && (q_stride < qd || q_stride % 8 != 0)) ||
         (q != nullptr && q == q_out && q_stride != qd && g.total_q > 1))
         return PA_ERR_INVALID_ARG;
+    if (q != nullptr) {
+        // q is read row by row while others are written; in place a lane reads what it writes
+        auto rows = [&](const void* x, int64_t stride, int64_t width) -> Span {
+            return {x, ((g.total_q - 1) * stride + width) * 2};
+        };
+        const Span out = {q_out, g.total_q * qd * 2};
+        if ((q != q_out && overlap(out, rows(q, q_stride, qd))) ||
+            overlap(out, rows(k_new, k_stride, kv)) || overlap(out, rows(v_new, v_stride, kv)))
+            return PA_ERR_INVALID_ARG;
+    }
     P.rotary = rope->rotary_dim;
     P.interleaved = rope->interleaved;
     P.scale = rope->cos_sin_scale;

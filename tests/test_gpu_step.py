@@ -1197,3 +1197,33 @@ def test_pages_of_one_buffer():
     B.pa_pages_return(p, s["ctx"], s["q"], t, s["free"], s["count"], s["left"], s["err"])
     assert int(s["left"]) == pages and sorted(s["free"].tolist()) == list(range(pages))
     no_error(s["err"])
+
+
+@pytest.mark.parametrize("T,stride", [(1, 0), (1, 24), (9, 0), (9, 24)])
+def test_rope_within_one_buffer(T, stride):
+    """q, k_new, v_new and q_out back to back in one buffer; and the only token of a fused
+    projection turned in place."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    p, q, k, v, slots, kc, vc, _ = rope_case(T, Hq, Hkv, D, page, 0, B.PA_BF16, strided=False, seed=3)
+    steps, rope = B.pa_rope_steps(freq_of(D)).cuda(), B.PaRope(D, 0, 1.0)
+    pos, err = ints([50 + 3 * i for i in range(T)]), ints([0])
+    want = torch.zeros_like(q)
+    B.pa_rope_append(p, rope, steps, q, k, v, pos, slots, want, kc, None, vc, None, err)
+    width = (Hq + 2 * Hkv) * D + stride
+    arena = torch.zeros(T * width + T * Hq * D, dtype=BF16, device="cuda")
+    fused = arena[:T * width].view(T, width)
+    qs, ks, vs = (fused[:, a * D:b * D].unflatten(1, (-1, D))
+                  for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    for to, x in ((qs, q), (ks, k), (vs, v)):
+        to.copy_(x)
+    out = arena[T * width:].view(T, Hq, D)
+    k2, v2 = torch.full_like(kc, math.nan), torch.full_like(vc, math.nan)
+    call = lambda o: B.pa_rope_append(p, rope, steps, qs, ks, vs, pos, slots, o, k2, None, v2,  # noqa: E731,E501
+                                      None, err)
+    call(out)
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    assert same(out, want) and same(k2, kc) and same(v2, vc)
+    if T == 1:
+        call(arena[:Hq * D].view(T, Hq, D))
+        assert same(arena[:Hq * D].view(T, Hq, D), want)
+    no_error(err)

@@ -248,6 +248,26 @@ def test_queries_in_place_are_dense(lib):
         assert call(lib, r, problem(), args) == B.PA_ERR_INVALID_ARG
 
 
+def test_queries_are_written_where_nothing_is_read(lib):
+    """q_out a little before or behind q, or on new keys or values."""
+    r, out, word = "pa_rope_append", 10, 16
+    args = GOOD[r]
+    bad = [args[2].value + word, args[2].value - word,                   # q, all but in place
+           args[2].value + 3 * 2048 - word, args[2].value - 3 * 2048 + word]
+    for i in (3, 4):                          # k_new, v_new: 3 tokens of 512 bytes
+        bad += [args[i].value, args[i].value + 3 * 512 - word, args[i].value - 3 * 2048 + word]
+    for x in bad:
+        assert call(lib, r, problem(), swap(r, out, ctypes.c_void_p(x))) == B.PA_ERR_INVALID_ARG
+    # strided tokens: up to the last one's end
+    args = swap(r, 5, 4096)
+    args[out] = ctypes.c_void_p(args[2].value + 2 * 8192 + 2048 - word)
+    assert call(lib, r, problem(), args) == B.PA_ERR_INVALID_ARG
+    # a fused projection's only token turned in place is beside its keys, not on them
+    args = swap(r, out, args[2])
+    args[3] = ctypes.c_void_p(args[2].value + 2048 - word)
+    assert call(lib, r, problem(total_q_tokens=1), args) == B.PA_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------- frequencies
 
 def scaling(kind, dim, **kw):
