@@ -246,6 +246,7 @@ PA_API pa_status pa_select_pages(const pa_problem* problem, int32_t budget, int3
  *   product with V (2^-8 of each); num_ctas and unit_cost have their pa.h meaning
  *   (num_ctas at most 1024; a unit_cost that, added to a unit's 64-token tiles, is 2^31 or
  *   more, or over all rows and KV heads more than 2^52: PA_ERR_UNSUPPORTED).
+ *   With max_q_len > 1 rows * KV heads * budget is at most 2^56 (more: PA_ERR_UNSUPPORTED).
  *   ws: >= pa_selected_workspace_size bytes, 256-byte aligned, zero-filled before
  *     its first use; the rules of pa_decode_mx4's, whose workspace it must not be
  *     while either runs.  device errors: pa_last_device_error(ws).

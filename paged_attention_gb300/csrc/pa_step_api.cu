@@ -97,6 +97,8 @@ pa_status sel_layout(const pa_problem* pp, int budget, CacheGeom& g, SelLayout& 
     L.off_entries = L.off_list = L.total = L.off_lead;
     if (L.together > 1) {
         const int64_t units = (int64_t)g.total_q * g.Hkv;
+        // (a size that 64 bits hold: below 2^60)
+        if (units > 0 && budget > ((int64_t)1 << 56) / units) return PA_ERR_UNSUPPORTED;
         L.off_entries = align256(L.off_lead + (int64_t)g.total_q * (1 + kMostJoinParts) * 4);
         L.off_list = align256(L.off_entries + units * 4);
         L.total = align256(L.off_list + units * budget * 8);

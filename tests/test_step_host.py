@@ -225,6 +225,17 @@ def test_unit_costs_that_cannot_be_counted_are_refused(lib):
     assert size(unit_cost=-2 ** 31) > 0       # none
 
 
+def test_lists_that_no_size_holds_are_refused(lib):
+    """2^30 + 2 rows and heads of 2^31 - 1 entries of 8 bytes: 2^35 bytes past 2^64."""
+    d, budget = "pa_decode_selected", 2 ** 31 - 1
+    kw = dict(total_q_tokens=(1 << 29) + 1, max_q_len=2)
+    assert B.pa_selected_workspace_size(problem(**kw), budget) == 0
+    assert call(lib, d, problem(**kw), [budget] + GOOD[d][1:]) == B.PA_ERR_UNSUPPORTED
+    most = (1 << 56) // ((1 << 30) + 2)
+    assert B.pa_selected_workspace_size(problem(**kw), most) > 8 * most * (1 << 30)
+    assert B.pa_selected_workspace_size(problem(**kw), most + 1) == 0
+
+
 @pytest.mark.parametrize("name,outputs,sizes", [
     # 3 sequences, 3 rows, 50 pages, a table of 3 x 10; in the arguments' order
     ("pa_pages_take", {2, 5, 6, 7, 8, 9}, [12, 12, 120, 200, 4, 12, 12, 12, 12, 4]),
