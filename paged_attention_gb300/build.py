@@ -72,9 +72,8 @@ def _sources():
 
 def _fingerprint() -> str:
     h = hashlib.sha256()
-    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(INCLUDE, "pa.h"), os.path.join(INCLUDE, "pa_cache.h"),
-        os.path.abspath(__file__)]
+    files = (_sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+             + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)])
     for f in files:
         with open(f, "rb") as fh:
             h.update(f.encode() + fh.read())

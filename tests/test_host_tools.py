@@ -1,6 +1,7 @@
 """Host-side helpers: the counter fingerprint (comment edits keep measured
 counters valid, code edits do not) and the bench's launch count per step."""
 import os
+import shutil
 import sys
 
 import pytest
@@ -22,6 +23,18 @@ def test_code_only_strips_comments_not_strings():
     assert '"// kept"' in got and '"q\\"//still"' in got and "'/'" in got
     assert build_mod._code_only(src.replace("// one", "// two")) == got
     assert build_mod._code_only(src.replace("a = 1", "a = 2")) != got
+
+
+@pytest.mark.parametrize("header", sorted(os.listdir(build_mod.INCLUDE)))
+def test_every_header_is_part_of_the_build(header, monkeypatch, tmp_path):
+    """An edit of any public header makes the library be built again."""
+    for f in os.listdir(build_mod.INCLUDE):
+        shutil.copy(os.path.join(build_mod.INCLUDE, f), tmp_path)
+    monkeypatch.setattr(build_mod, "INCLUDE", str(tmp_path))
+    before = build_mod._fingerprint()
+    with open(tmp_path / header, "a") as f:
+        f.write("/* another line */")
+    assert build_mod._fingerprint() != before
 
 
 def test_kernel_fingerprints_are_stable_and_distinct():
