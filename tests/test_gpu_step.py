@@ -1227,3 +1227,96 @@ def test_rope_within_one_buffer(T, stride):
         call(arena[:Hq * D].view(T, Hq, D))
         assert same(arena[:Hq * D].view(T, Hq, D), want)
     no_error(err)
+
+
+# ------------------------------------- rows of one sequence: errors, and non-finite values
+
+@pytest.mark.parametrize("ctas", [0, 5, 700])
+@pytest.mark.parametrize("D,G,Hkv,page,layout", [(128, 4, 2, 16, 0), (64, 5, 3, 32, 1),
+                                                 (128, 11, 1, 16, 1), (64, 1, 9, 16, 0)])
+def test_rows_of_one_sequence_past_bad_entries(D, G, Hkv, page, layout, ctas):
+    """A row that cannot be among good ones, a unit of none but such, sequences that are none;
+    entries and pages that are none, listed by one row or by several."""
+    budget = 7
+    pages, table, seq, pos, k, v, q = attend_case(D, G, Hkv, page, layout, [300, 200, 64],
+                                                  [5, 3, 2], 9)
+    sel = lists(seq, pos, Hkv, budget, page, 0, 5)
+    p = problem(num_seqs=3, num_q_heads=G * Hkv, num_kv_heads=Hkv, head_dim=D, page_size=page,
+                num_pages=pages, max_pages_per_seq=len(table[0]), layout=layout,
+                total_q_tokens=15, max_q_len=5, max_context_len=300, num_ctas=ctas)
+    q = torch.cat((q, q[:5]))
+    more = dict(seq=seq + [-1] + [3, 3] + [1, 1], pos=pos + [0] + [7, 8] + [9, 10])
+    sel = sel + sel[:1] + sel[8:10] + lists([1, 1], [9, 10], Hkv, budget, page, 0, 6)
+    run = lambda code, s=sel, t=table, **kw: check_attend(  # noqa: E731
+        p, budget, t, k=k, v=v, q=q, sel=s, code=code, repeat=2, **{**more, **kw})
+    run(1)                                    # a sequence that is none
+    good = dict(seq=[b if b < 3 else -1 for b in more["seq"]])
+    run(0, **good)
+    for bad in (300, -1, 2 ** 31 - 1, -2 ** 31):
+        at = list(more["pos"])
+        at[1] = bad                           # among rows 0 .. 4
+        run(1, pos=at, **good)
+        at = list(more["pos"])
+        at[8] = at[9] = bad                   # both rows of sequence 2
+        run(1, pos=at, **good)
+    for entry in (pos[0] // page + 1, 2 ** 31 - 1, 2 ** 26, -2, -2 ** 31):
+        s = [[list(x) for x in r] for r in sel]
+        s[0][0][2] = s[6][Hkv - 1][1] = entry
+        s[1][0][2] = entry                    # the same one by two rows
+        run(1, s=s, **good)
+    t = [list(r) for r in table]
+    t[0][sel[2][0][1]], t[1][sel[5][0][0]], t[2][0] = -1, pages, 2 ** 31 - 1
+    run(2, t=t, **good)
+    run(0, s=[[[-1] * budget] * Hkv] * 15, **good)
+
+
+@pytest.mark.parametrize("ctas", [0, 5, 700])
+@pytest.mark.parametrize("D,G,page,rows", [(128, 4, 16, 4), (64, 3, 32, 6), (128, 16, 16, 2),
+                                           (64, 8, 16, 4)])
+def test_non_finite_values_in_units_that_are_split(D, G, page, rows, ctas):
+    """An infinity or NaN of K or V in a page that one row of several lists, in lists long enough
+    for several CTAs: the others' results are right, and its own column (V) or row (a NaN in K)
+    is not finite."""
+    ctx = 2600
+    pages, table, seq, pos, k, v, q = attend_case(D, G, 1, page, 0, [ctx], [rows], 9)
+    n = R.up(ctx, page)
+    budget = n // 2
+    g = torch.Generator().manual_seed(4)
+    # (the first pages of all but the last row's list are common to the others', one is its own)
+    own = n - 9
+    rest = [s for s in range(n - 5) if s != own]
+    sel = []
+    for r in range(rows):
+        pick = [rest[i] for i in torch.randperm(len(rest), generator=g)[:budget - 1].tolist()]
+        sel.append([sorted(pick + [own if r == 1 else n - 7 if n - 7 not in pick else n - 5])])
+    p = problem(num_q_heads=G, num_kv_heads=1, head_dim=D, page_size=page, num_pages=pages,
+                max_pages_per_seq=n, total_q_tokens=rows, max_q_len=rows, max_context_len=ctx,
+                num_ctas=ctas)
+    ws = torch.zeros(B.pa_selected_workspace_size(p, budget), dtype=torch.uint8, device="cuda")
+    check_attend(p, budget, table, seq, pos, k, v, q, sel)
+    for value in (math.inf, -math.inf, math.nan):
+        for which in "kv":
+            k2, v2 = k.clone(), v.clone()
+            (k2 if which == "k" else v2)[table[0][own], 3, 0, 7] = value
+            out = torch.zeros((rows, G, D), dtype=BF16, device="cuda")
+            lse = torch.zeros((rows, G), device="cuda")
+            B.pa_decode_selected(p, budget, q.cuda(), k2.cuda(), v2.cuda(), ints(table), ints(seq),
+                                 ints(pos), ints(sel), ws, out, lse)
+            assert B.pa_last_device_error(ws) == 0
+            for r in range(rows):
+                if r == 1:
+                    continue
+                at = [x for s in sel[r][0] for x in range(s * page, s * page + page)]
+                kk, vv = (torch.cat([x[table[0][s], :, 0] for s in sel[r][0]]) for x in (k, v))
+                o, L, size, big = R.attend(q[r], kk, vv, at, pos[r], 0, p.sm_scale)
+                ds = (D + 16) * 2.0 ** -24 * big[:, None] + 2.0 ** -20
+                tol = (HALF + 2 * ds) * size * 1.01 + HALF * (o.abs() + HALF * size)
+                assert torch.all((out[r].cpu().double() - o).abs() <= tol), (value, which, r)
+                far = (lse[r].cpu().double() - L).abs()
+                assert torch.all(far <= ds[:, 0] + 2.0 ** -22 * (1 + L.abs()))
+            if which == "v":
+                bad = ~torch.isfinite(out[1])
+                assert bad[:, 7].all() and not bad[:, :7].any() and not bad[:, 8:].any()
+                assert torch.isfinite(lse[1]).all()
+            elif value != value:
+                assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
