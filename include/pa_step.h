@@ -10,8 +10,9 @@
  *   A step's new tokens are the rows 0 .. total_q_tokens-1, those of a sequence
  *   together, in order.  pa_pages_take writes, and the others read, int32
  *   [total_q_tokens] each:
- *     row_seq    the row's sequence, or -1: a row of padding, behind the last
- *                sequence's rows.  Every operator leaves its outputs as they are.
+ *     row_seq    the row's sequence, or -1: a row of padding (behind the last
+ *                sequence's rows, and where a sequence's would be that got no
+ *                pages).  Every operator leaves its outputs as they are.
  *     positions  its position in the sequence.  The row's query sees the keys
  *                j <= position (and > position - window), so no lengths are needed.
  *     slots      page * page_size + slot of its K and V rows in the cache, or -1:

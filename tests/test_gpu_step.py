@@ -1320,3 +1320,36 @@ def test_non_finite_values_in_units_that_are_split(D, G, page, rows, ctas):
                 assert torch.isfinite(lse[1]).all()
             elif value != value:
                 assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,layout", [(8, 2, 128, 16, 0), (6, 3, 64, 32, 1)])
+def test_a_step_with_a_sequence_that_gets_no_pages(Hq, Hkv, D, page, layout):
+    """Its rows become padding in the middle of the step's; the others' results are those of a
+    step without it."""
+    def two_steps(ql):
+        L = Loop(3, Hq, Hkv, D, page, layout, 3, 40, 4 * page, seed=2)
+        g = torch.Generator().manual_seed(4)
+        L.fused.copy_(torch.randn(L.fused.shape, generator=g).to(BF16))
+        L.ql.copy_(ints([5, page, 3]))
+        L.step()
+        no_error(L.err)
+        L.count.fill_(0)                      # somebody else has the rest of the pool
+        new = torch.randn((3, 2, L.fused.shape[1]), generator=g).to(BF16).cuda()
+        L.fused[:sum(ql)].copy_(torch.cat([new[b, :n] for b, n in enumerate(ql)]))
+        L.ql.copy_(ints(ql))
+        for x, fill in ((L.out, 7.0), (L.lse, 7.0), (L.qr, 7.0), (L.sel, -9)):
+            x.fill_(fill)
+        L.step()
+        return L
+
+    a, b = two_steps([1, 2, 2]), two_steps([1, 0, 2])
+    assert int(a.err) == B.PA_DEV_NO_PAGES and int(b.err) == 0
+    assert B.pa_last_device_error(a.ws) == 0
+    assert a.seq.tolist() == [0, -1, -1, 2, 2] + [-1] * 35
+    assert a.lens.tolist() == b.lens.tolist() == [6, page, 5]
+    for x, y, fill in ((a.out, b.out, 7.0), (a.lse, b.lse, 7.0), (a.qr, b.qr, 7.0),
+                       (a.sel, b.sel, -9)):
+        assert torch.equal(x[[0, 3, 4]], y[:3]) and torch.isfinite(x[:5].float()).all()
+        assert torch.all(x[1:3] == fill) and torch.all(x[5:] == fill)
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.sc, b.sc), (a.bnd, b.bnd)):
+        assert torch.equal(x.view(torch.int8), y.view(torch.int8))
