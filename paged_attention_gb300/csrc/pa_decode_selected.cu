@@ -27,8 +27,9 @@
 // whether V is finite, and multiplies row by row where it is not.
 //
 // Measured (head_dim 128, 8 KV heads): 64 rows of up to 32 pages of 64, 32 q heads, 60 us
-// for 54.5 of HBM time; 128 sequences of 3 rows, 64 q heads, 40 pages, 204 us for 194
-// (each row by itself: 540).  With 32 query rows a unit the products and the softmax set
+// for 54.5 of HBM time; 128 sequences of 3 rows, 64 q heads, 40 pages, 205 to 210 us for 194
+// (each row by itself: 540), and where half of every row's list is its own 335 us for the 301
+// that the pages together take.  With 32 query rows a unit the products and the softmax set
 // the pace: 64 sequences of 4 rows, 64 q heads, 90 us for 56.
 #include <algorithm>
 #include <type_traits>
@@ -149,7 +150,7 @@ __device__ __forceinline__ void load_row(const SelectedParams& P, SelUnit& u) {
 
 // The unit after u (every lane the same); false past the share's end.  (That is looked
 // at first: rows of padding behind the last sequence's are not stepped through.  64 rows
-// and 192 of padding 60 us, else 84; and 960 of padding 68, else 208.)
+// and 192 of padding 61 us, else 84; and 960 of padding 69, else 208.)
 template <bool JOINED>
 __device__ __forceinline__ bool next_unit(const SelectedParams& P, SelUnit& u, int64_t hi) {
     u.start += P.unit_cost + u.n;
@@ -820,7 +821,12 @@ decode_selected_kernel(const __grid_constant__ SelectedParams P) {
                     }
                 exponents();
             }
-            // ---- probabilities, and their transposes as the B operand
+            // ---- probabilities, and their transposes as the B operand: rounded to bf16 (2^-8 of
+            // each at most), since a product's operands are of one type, V's.  Their sum keeps 32
+            // bits, for lse.  The roundings of different keys are independent: results are off by
+            // 0.0023 of their rms, where rounding them to bf16 alone gives 0.0017.  A second
+            // product, of what the first rounding left, would double the work that sets the pace
+            // from 24 rows on.
             uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
