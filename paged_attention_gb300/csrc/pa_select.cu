@@ -130,8 +130,9 @@ select_kernel(const __grid_constant__ SelectParams P) {
     const int n = (pos >> g.ps_shift) + 1 - first;
     int32_t* out = P.selected + (int64_t)unit * P.budget;
     if (n <= P.budget) {
-        for (int i = rank * kThreads + tid; i < P.budget; i += C * kThreads)
-            out[i] = i < n ? first + i : -1;
+        // (a budget near 2^31: one step further needs the 32nd bit)
+        for (uint32_t i = rank * kThreads + tid; i < (uint32_t)P.budget; i += C * kThreads)
+            out[i] = i < (uint32_t)n ? first + (int)i : -1;
         return;
     }
 

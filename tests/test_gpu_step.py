@@ -1353,3 +1353,18 @@ def test_a_step_with_a_sequence_that_gets_no_pages(Hq, Hkv, D, page, layout):
         assert torch.all(x[1:3] == fill) and torch.all(x[5:] == fill)
     for x, y in ((a.k, b.k), (a.v, b.v), (a.sc, b.sc), (a.bnd, b.bnd)):
         assert torch.equal(x.view(torch.int8), y.view(torch.int8))
+
+
+def test_selection_with_the_largest_budget_there_is():
+    """All pages, and -1 behind them up to entry 2^31 - 2; nothing behind that."""
+    budget, pos, page = 2 ** 31 - 1, 100, 16
+    p = problem(num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=page)
+    sel = torch.full((budget + 33,), -7, dtype=torch.int32, device="cuda")
+    bnd, sc = torch.zeros((8, 1, 2, 64), dtype=torch.int8).cuda(), torch.ones((8, 1)).cuda()
+    err = ints([0])
+    B.pa_select_pages(p, budget, 0, 0, torch.zeros((1, 1, 64), dtype=BF16, device="cuda"), bnd, sc,
+                      ints([list(range(8))]), ints([0]), ints([pos]), sel, err)
+    no_error(err)
+    assert sel[:7].tolist() == list(range(7))
+    assert int(sel[7:budget].max()) == -1 == int(sel[7:budget].min())
+    assert sel[budget:].tolist() == [-7] * 33
